@@ -19,6 +19,9 @@ Entry points (same names as the C ABI):
   16-bit output-layer baseline).
 * ``fp8_mx_quant_weights(w)``, ``fp8_mx_quant_act(x)``, ``fp8_mx_gemm(...)``:
   the native block-scaled (MX) variant, one UE8M0 scale per 32 K.
+* ``fp4_quant_weights(w, fmt)``, ``fp4_quant_act(x, fmt)``, ``fp4_gemm(...)``,
+  ``fp4_gemm_fused(x, ...)``, ``fp4_dequant_weights(...)``: microscaled 4-bit
+  weights and activations (FP4_NV or FP4_MX).
 * ``fp8_blockscaled_gemm_workspace_size``, ``make_workspace``,
   ``workspace_status``, ``split_plan``, ``gemm_schedule``, ``fused_route``:
   workspace and schedule queries.
@@ -35,6 +38,7 @@ FLAG_OVERLAP_PREV = 1
 FLAG_WEIGHTS_TILED = 2
 FLAG_PROLOGUE_CAST = 4
 F32, BF16 = 0, 1
+FP4_NV, FP4_MX = 0, 1  # 4-bit formats: 16-wide E4M3 scales and fp32 row scales; 32-wide powers of two
 
 _lib = None
 
@@ -106,6 +110,12 @@ def _load(path):
         "fp8_mx_quant_weights": [vp, i, i, i, vp, vp, vp],
         "fp8_mx_quant_act": [vp, i, i, i, vp, vp, u, vp],
         "fp8_mx_gemm_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "fp4_quant_weights": [vp, i, i, i, i, vp, vp, vp, vp],
+        "fp4_dequant_weights": [vp, vp, vp, i, i, i, vp, i, vp],
+        "fp4_quant_act": [vp, i, i, i, i, vp, vp, vp, u, vp],
+        "fp4_gemm_workspace_size": [i, i, i, i, ctypes.POINTER(sz)],
+        "fp4_gemm": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, sz, u, vp],
+        "fp4_gemm_fused": [vp, i, vp, vp, vp, vp, i, i, i, i, vp, sz, u, vp],
         "fp8_mx_gemm": [vp, vp, vp, vp, vp, i, i, i, vp, sz, u, vp],
     }
     for name, args in sigs.items():
@@ -434,6 +444,139 @@ def fp8_mx_gemm(aq, as_atoms, wq, ws_atoms, n, y=None, workspace=None, flags=0):
         workspace = make_workspace(fp8_mx_gemm_workspace_size(M, N, K), aq.device)
     _check("fp8_mx_gemm", lib().fp8_mx_gemm(_ptr(aq), _ptr(as_atoms), _ptr(wq), _ptr(ws_atoms), _ptr(y), M, N, K,
                                             _ptr(workspace), workspace.numel(), flags, _stream()))
+    return y
+
+
+# ------------------------------------------------------------- 4-bit layers
+def _fp4_tiles(N, K):
+    return ((N + 127) // 128) * ((K + 255) // 256)
+
+
+def _fp4_atoms(fmt):
+    """Scale atoms per 128 rows and 256 K."""
+    if fmt not in (FP4_NV, FP4_MX):
+        raise ValueError("fmt must be FP4_NV or FP4_MX")
+    return 4 if fmt == FP4_NV else 2
+
+
+def _fp4_operand(codes, atoms, rows, n_codes, n_atoms, n_rows, what):
+    """Checks of one packed 4-bit operand (rows may be None: all 1, FP4_MX only)."""
+    torch = _torch()
+    _need(codes, torch.uint8, what, ndim=codes.dim())
+    _need(atoms, torch.uint8, what + " scale atoms", ndim=atoms.dim())
+    if rows is not None:
+        _need(rows, torch.float32, what + " row scales", ndim=1)
+    if codes.numel() != n_codes or atoms.numel() != n_atoms or (rows is not None and rows.numel() != n_rows):
+        raise ValueError("operand shapes do not agree")
+    if not (codes.is_contiguous() and atoms.is_contiguous() and (rows is None or rows.is_contiguous())):
+        raise ValueError("%s must be contiguous" % what)
+
+
+def _out(t, shape, dtype, device, name):
+    """`t` checked as an output of that shape (contiguous), or a new one."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name, ndim=len(shape))
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be contiguous of shape %s" % (name, tuple(shape)))
+    return t
+
+
+def fp4_quant_weights(w, fmt=FP4_NV, wq=None, ws_atoms=None, w_rows=None):
+    """fp32 or bf16 W [N, K] (K % 32 == 0) -> (wq uint8 [ceil(N/128) *
+    ceil(K/256), 128, 128] tiled codes, two to a byte, ws_atoms uint8 [tiles *
+    4 or 2, 512] scale atoms, w_rows fp32 [N] row scales (all 1 for FP4_MX))."""
+    torch = _torch()
+    if w.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("w must be float32 or bfloat16")
+    _need(w, w.dtype, "w")
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    N, K = w.shape
+    tiles = _fp4_tiles(N, K)
+    wq = _out(wq, (tiles, 128, 128), torch.uint8, w.device, "wq")
+    ws_atoms = _out(ws_atoms, (tiles * _fp4_atoms(fmt), 512), torch.uint8, w.device, "ws_atoms")
+    w_rows = _out(w_rows, (N,), torch.float32, w.device, "w_rows")
+    wt = BF16 if w.dtype == torch.bfloat16 else F32
+    _check("fp4_quant_weights", lib().fp4_quant_weights(_ptr(w), wt, N, K, fmt, _ptr(wq), _ptr(ws_atoms),
+                                                        _ptr(w_rows), _stream()))
+    return wq, ws_atoms, w_rows
+
+
+def fp4_dequant_weights(wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, w=None, dtype=None):
+    """The values [n, k] (fp32, or bf16 with dtype=torch.bfloat16) that packed
+    4-bit weights stand for (w_rows None: all 1, FP4_MX only)."""
+    torch = _torch()
+    N, K = int(n), int(k)
+    tiles = _fp4_tiles(N, K)
+    _fp4_operand(wq, ws_atoms, w_rows, tiles * 16384, tiles * _fp4_atoms(fmt) * 512, N, "wq")
+    dtype = dtype or (w.dtype if w is not None else torch.float32)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("w must be float32 or bfloat16")
+    w = _out(w, (N, K), dtype, wq.device, "w")
+    wt = BF16 if dtype == torch.bfloat16 else F32
+    _check("fp4_dequant_weights", lib().fp4_dequant_weights(_ptr(wq), _ptr(ws_atoms), _ptr(w_rows), N, K, fmt,
+                                                            _ptr(w), wt, _stream()))
+    return w
+
+
+def fp4_quant_act(x, fmt=FP4_NV, xq=None, xs_atoms=None, x_rows=None, flags=0):
+    """bf16 X [M, K] (M <= 512, K % 32 == 0; row stride may exceed K) -> (xq
+    uint8 [M, ceil(K/256) * 128], xs_atoms uint8 [ceil(M/128) * ceil(K/256) *
+    4 or 2, 512], x_rows fp32 [M])."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x")
+    _rows_contiguous(x, "x")
+    M, K = x.shape
+    kt = (K + 255) // 256
+    xq = _out(xq, (M, kt * 128), torch.uint8, x.device, "xq")
+    xs_atoms = _out(xs_atoms, ((M + 127) // 128 * kt * _fp4_atoms(fmt), 512), torch.uint8, x.device, "xs_atoms")
+    x_rows = _out(x_rows, (M,), torch.float32, x.device, "x_rows")
+    _check("fp4_quant_act", lib().fp4_quant_act(_ptr(x), M, K, x.stride(0), fmt, _ptr(xq), _ptr(xs_atoms),
+                                                _ptr(x_rows), flags, _stream()))
+    return xq, xs_atoms, x_rows
+
+
+def fp4_gemm_workspace_size(M, N, K, fmt=FP4_NV):
+    n = ctypes.c_size_t(0)
+    _check("fp4_gemm_workspace_size", lib().fp4_gemm_workspace_size(M, N, K, fmt, ctypes.byref(n)))
+    return n.value
+
+
+def fp4_gemm(aq, as_atoms, a_rows, wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, y=None, workspace=None, flags=0):
+    """Y[M, n] bf16 from 4-bit operands (fp4_quant_act / fp4_quant_weights;
+    n = the number of weight rows, k = the unpadded K)."""
+    torch = _torch()
+    M, N, K = aq.shape[0], int(n), int(k)
+    kt = (K + 255) // 256
+    s = _fp4_atoms(fmt)
+    _fp4_operand(aq, as_atoms, a_rows, M * kt * 128, (M + 127) // 128 * kt * s * 512, M, "aq")
+    _fp4_operand(wq, ws_atoms, w_rows, _fp4_tiles(N, K) * 16384, _fp4_tiles(N, K) * s * 512, N, "wq")
+    y = _out(y, (M, N), torch.bfloat16, aq.device, "y")
+    if workspace is None:
+        workspace = make_workspace(fp4_gemm_workspace_size(M, N, K, fmt), aq.device)
+    _check("fp4_gemm", lib().fp4_gemm(_ptr(aq), _ptr(as_atoms), _ptr(a_rows), _ptr(wq), _ptr(ws_atoms), _ptr(w_rows),
+                                      _ptr(y), M, N, K, fmt, _ptr(workspace), workspace.numel(), flags, _stream()))
+    return y
+
+
+def fp4_gemm_fused(x, wq, ws_atoms, w_rows, n, fmt=FP4_NV, y=None, workspace=None, flags=0):
+    """Y[M, n] bf16 from bf16 activations (row stride may exceed K) and packed
+    4-bit weights: the cast into the workspace, then the product."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x")
+    _rows_contiguous(x, "x")
+    M, K = x.shape
+    N = int(n)
+    tiles = _fp4_tiles(N, K)
+    _fp4_operand(wq, ws_atoms, w_rows, tiles * 16384, tiles * _fp4_atoms(fmt) * 512, N, "wq")
+    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    if workspace is None:
+        workspace = make_workspace(fp4_gemm_workspace_size(M, N, K, fmt), x.device)
+    _check("fp4_gemm_fused", lib().fp4_gemm_fused(_ptr(x), x.stride(0), _ptr(wq), _ptr(ws_atoms), _ptr(w_rows),
+                                                  _ptr(y), M, N, K, fmt, _ptr(workspace), workspace.numel(), flags,
+                                                  _stream()))
     return y
 
 

@@ -129,11 +129,22 @@ WorkspaceLayout workspace_layout(const GemmShape &sh, int M, int K)
     return w;
 }
 
+Fp4Workspace fp4_workspace(const GemmShape &sh, int M, int sf_atoms)
+{
+    auto up256 = [](size_t b) { return (b + 255) / 256 * 256; };
+    Fp4Workspace w;
+    w.codes_off = workspace_layout(sh, M, 0).act_off;
+    w.atoms_off = w.codes_off + up256(static_cast<size_t>(M) * sh.kg * 128);
+    w.rows_off = w.atoms_off + static_cast<size_t>((M + 127) / 128) * sh.kg * sf_atoms * 512;
+    w.total = w.rows_off + up256(static_cast<size_t>(M) * 4);
+    return w;
+}
+
 GemmShape gemm_shape(int mode, int M, int N, int K, int sms)
 {
     GemmShape s{};
     s.m = M; // read by the fused route choice whatever the schedule below
-    s.kg = mode == 2 ? K / 64 : K / 128;
+    s.kg = mode == 2 ? K / 64 : mode == 4 ? (K + 255) / 256 : K / 128;
     s.ntiles = (N + 127) / 128;
     s.units = static_cast<long long>(s.ntiles) * s.kg;
     s.npad = token_pad(M);
@@ -170,8 +181,8 @@ GemmShape gemm_shape(int mode, int M, int N, int K, int sms)
     // a weight tile read it from L2 after the first.  (256-token tiles
     // promote 15% slower per token than 128-token ones and are not used.)
     for (int tt : {128, 64, 32}) {
-        if (mode == 3 && tt != 128)
-            break; // MX: the token scale atoms hold 128-token tiles
+        if ((mode == 3 || mode == 4) && tt != 128)
+            break; // MX, 4-bit: the token scale atoms hold 128-token tiles
         const int tiles_m = (M + tt - 1) / tt;
         const long long pairs = static_cast<long long>(s.ntiles) * tiles_m;
         if (pairs <= sms && pairs * (s.kg + 16) >= static_cast<long long>(sms) * s.kg) {
@@ -256,7 +267,8 @@ fp8bs_status run_gemm(GemmLaunch &L)
     if (L.sms <= 0)
         L.sms = dev.sms;
     const GemmShape sh = gemm_shape(L.mode, L.M, L.N, L.K, L.sms);
-    if (L.workspace_bytes < workspace_layout(sh, L.M, L.K).total)
+    const size_t need = L.mode == 4 ? fp4_workspace(sh, L.M, L.sf_atoms).total : workspace_layout(sh, L.M, L.K).total;
+    if (L.workspace_bytes < need)
         return FP8BS_ERR_WORKSPACE_TOO_SMALL;
     switch (L.mode) {
     case 0:
@@ -265,9 +277,61 @@ fp8bs_status run_gemm(GemmLaunch &L)
         return launch_gemm_fused(L, dev);
     case 3:
         return launch_gemm_mx(L, dev);
+    case 4:
+        return launch_gemm_fp4(L, dev);
     default:
         return launch_gemm_bf16(L, dev);
     }
+}
+
+bool bad_fp4_format(int fmt) { return fmt != FP8BS_FP4_NV && fmt != FP8BS_FP4_MX; }
+
+// Scale atoms per 128 rows and 256 K.
+int fp4_atoms(int fmt) { return fmt == FP8BS_FP4_NV ? 4 : 2; }
+
+// K in whole 32-wide blocks, and the packed codes' rows (128 per tile of 128
+// weight rows x 256 K) within the tensor maps' 31-bit coordinates.
+fp8bs_status fp4_weight_shape(int N, int K)
+{
+    if (K % 32 != 0 || N > (1 << 30) || K > (1 << 30) ||
+        static_cast<long long>((N + 127) / 128) * ((K + 255) / 256) >= (1ll << 24))
+        return FP8BS_ERR_UNSUPPORTED_SHAPE;
+    return FP8BS_OK;
+}
+
+fp8bs_status check_fp4_weights(const void *w, int wtype, int N, int K, int fmt, const void *wq, const void *ws_atoms,
+                               const void *w_rows)
+{
+    if (!w || !wq || !ws_atoms || N < 1 || K < 1 || (wtype != FP8BS_F32 && wtype != FP8BS_BF16) ||
+        bad_fp4_format(fmt) || (fmt == FP8BS_FP4_NV && !w_rows))
+        return FP8BS_ERR_INVALID_ARG;
+    if (fp4_weight_shape(N, K) != FP8BS_OK)
+        return FP8BS_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(w, 16) || !aligned(wq, 16) || !aligned(ws_atoms, 16) || !aligned(w_rows, 4))
+        return FP8BS_ERR_MISALIGNED;
+    return FP8BS_OK;
+}
+
+GemmLaunch fp4_launch(const uint8_t *wq, const uint8_t *ws_atoms, const float *w_rows, void *y, int M, int N, int K,
+                      int fmt, void *workspace, size_t workspace_bytes, unsigned flags, void *stream)
+{
+    GemmLaunch L = {};
+    L.mode = 4;
+    L.M = M;
+    L.N = N;
+    L.K = K;
+    L.w = wq;
+    L.sfa = ws_atoms;
+    L.sf_atoms = fp4_atoms(fmt);
+    L.row_w = w_rows;
+    L.y = y;
+    L.workspace = workspace;
+    L.workspace_bytes = workspace_bytes;
+    L.flags = flags | FP8BS_FLAG_WEIGHTS_TILED; // the 4-bit weight codes are always tiled
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.test_skip_unit = -1;
+    L.timeout_ns = kDefaultTimeoutNs;
+    return L;
 }
 
 } // namespace
@@ -654,6 +718,134 @@ fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, const uint8
     L.flags = flags | FP8BS_FLAG_WEIGHTS_TILED; // the MX weight codes are always tiled
     L.stream = static_cast<cudaStream_t>(stream);
     L.timeout_ns = kDefaultTimeoutNs;
+    return run_gemm(L);
+}
+
+fp8bs_status fp4_quant_weights(const void *w, fp8bs_dtype wtype, int N, int K, fp8bs_fp4_format fmt, uint8_t *wq,
+                               uint8_t *ws_atoms, float *w_rows, void *stream)
+{
+    fp8bs_status st = check_fp4_weights(w, wtype, N, K, fmt, wq, ws_atoms, w_rows);
+    if (st != FP8BS_OK)
+        return st;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != FP8BS_OK)
+        return st;
+    return launch_fp4_quant_weights(w, wtype, N, K, fmt, wq, ws_atoms, w_rows, static_cast<cudaStream_t>(stream), dev);
+}
+
+fp8bs_status fp4_dequant_weights(const uint8_t *wq, const uint8_t *ws_atoms, const float *w_rows, int N, int K,
+                                 fp8bs_fp4_format fmt, void *w, fp8bs_dtype wtype, void *stream)
+{
+    fp8bs_status st = check_fp4_weights(w, wtype, N, K, fmt, wq, ws_atoms, w_rows);
+    if (st != FP8BS_OK)
+        return st;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != FP8BS_OK)
+        return st;
+    return launch_fp4_dequant_weights(wq, ws_atoms, w_rows, N, K, fmt, w, wtype, static_cast<cudaStream_t>(stream), dev);
+}
+
+fp8bs_status fp4_quant_act(const void *x, int M, int K, int ldx, fp8bs_fp4_format fmt, uint8_t *xq, uint8_t *xs_atoms,
+                           float *x_rows, unsigned flags, void *stream)
+{
+    if (!x || !xq || !xs_atoms || M < 1 || K < 1 || ldx < K || bad_fp4_format(fmt) || (fmt == FP8BS_FP4_NV && !x_rows))
+        return FP8BS_ERR_INVALID_ARG;
+    if (check_flags(flags, FP8BS_FLAG_OVERLAP_PREV) != FP8BS_OK)
+        return FP8BS_ERR_INVALID_ARG;
+    if (M > kMaxTokens || K % 32 != 0 || K > (1 << 30))
+        return FP8BS_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(xq, 16) || !aligned(xs_atoms, 16) || !aligned(x_rows, 4))
+        return FP8BS_ERR_MISALIGNED;
+    DeviceInfo dev;
+    fp8bs_status st = current_device(&dev);
+    if (st != FP8BS_OK)
+        return st;
+    return launch_fp4_quant_act(x, M, K, ldx, fmt, xq, xs_atoms, x_rows, (flags & FP8BS_FLAG_OVERLAP_PREV) != 0,
+                                static_cast<cudaStream_t>(stream), dev);
+}
+
+fp8bs_status fp4_gemm_workspace_size(int M, int N, int K, fp8bs_fp4_format fmt, size_t *bytes)
+{
+    if (!bytes)
+        return FP8BS_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (bad_fp4_format(fmt))
+        return FP8BS_ERR_INVALID_ARG;
+    fp8bs_status st = check_gemm_shape(M, N, K, 32);
+    if (st == FP8BS_OK)
+        st = fp4_weight_shape(N, K);
+    if (st != FP8BS_OK)
+        return st;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != FP8BS_OK)
+        return st;
+    *bytes = fp4_workspace(gemm_shape(4, M, N, K, dev.sms), M, fp4_atoms(fmt)).total;
+    return FP8BS_OK;
+}
+
+fp8bs_status fp4_gemm(const uint8_t *aq, const uint8_t *as_atoms, const float *a_rows, const uint8_t *wq,
+                      const uint8_t *ws_atoms, const float *w_rows, void *y, int M, int N, int K,
+                      fp8bs_fp4_format fmt, void *workspace, size_t workspace_bytes, unsigned flags, void *stream)
+{
+    if (!aq || !as_atoms || !wq || !ws_atoms || !y || !workspace || bad_fp4_format(fmt) ||
+        (fmt == FP8BS_FP4_NV && (!a_rows || !w_rows)))
+        return FP8BS_ERR_INVALID_ARG;
+    fp8bs_status st = check_gemm_shape(M, N, K, 32);
+    if (st == FP8BS_OK)
+        st = fp4_weight_shape(N, K);
+    if (st != FP8BS_OK)
+        return st;
+    if (check_flags(flags, FP8BS_FLAG_OVERLAP_PREV) != FP8BS_OK)
+        return FP8BS_ERR_INVALID_ARG;
+    if (!aligned(aq, 16) || !aligned(as_atoms, 16) || !aligned(a_rows, 4) || !aligned(wq, 16) ||
+        !aligned(ws_atoms, 16) || !aligned(w_rows, 4) || !aligned(y, 2) || !aligned(workspace, 256))
+        return FP8BS_ERR_MISALIGNED;
+    GemmLaunch L = fp4_launch(wq, ws_atoms, w_rows, y, M, N, K, fmt, workspace, workspace_bytes, flags, stream);
+    L.a = aq;
+    L.sfb = as_atoms;
+    L.row_a = a_rows;
+    return run_gemm(L);
+}
+
+fp8bs_status fp4_gemm_fused(const void *x, int ldx, const uint8_t *wq, const uint8_t *ws_atoms, const float *w_rows,
+                            void *y, int M, int N, int K, fp8bs_fp4_format fmt, void *workspace,
+                            size_t workspace_bytes, unsigned flags, void *stream)
+{
+    if (!x || !wq || !ws_atoms || !y || !workspace || bad_fp4_format(fmt) || (fmt == FP8BS_FP4_NV && !w_rows))
+        return FP8BS_ERR_INVALID_ARG;
+    fp8bs_status st = check_gemm_shape(M, N, K, 32);
+    if (st == FP8BS_OK)
+        st = fp4_weight_shape(N, K);
+    if (st != FP8BS_OK)
+        return st;
+    if (ldx < K || check_flags(flags, FP8BS_FLAG_OVERLAP_PREV) != FP8BS_OK)
+        return FP8BS_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(wq, 16) || !aligned(ws_atoms, 16) || !aligned(w_rows, 4) ||
+        !aligned(y, 2) || !aligned(workspace, 256))
+        return FP8BS_ERR_MISALIGNED;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != FP8BS_OK)
+        return st;
+    const Fp4Workspace fw = fp4_workspace(gemm_shape(4, M, N, K, dev.sms), M, fp4_atoms(fmt));
+    if (workspace_bytes < fw.total)
+        return FP8BS_ERR_WORKSPACE_TOO_SMALL;
+    uint8_t *const wsb = static_cast<uint8_t *>(workspace);
+    // MX needs no row scales: the product then skips them
+    float *const rows = fmt == FP8BS_FP4_NV ? reinterpret_cast<float *>(wsb + fw.rows_off) : nullptr;
+    st = launch_fp4_quant_act(x, M, K, ldx, fmt, wsb + fw.codes_off, wsb + fw.atoms_off, rows,
+                              (flags & FP8BS_FLAG_OVERLAP_PREV) != 0, static_cast<cudaStream_t>(stream), dev);
+    if (st != FP8BS_OK)
+        return st;
+    // the product's early launch is ordered after the cast by its dependency wait
+    GemmLaunch L = fp4_launch(wq, ws_atoms, w_rows, y, M, N, K, fmt, workspace, workspace_bytes,
+                              flags | FP8BS_FLAG_OVERLAP_PREV, stream);
+    L.a = wsb + fw.codes_off;
+    L.sfb = wsb + fw.atoms_off;
+    L.row_a = rows;
     return run_gemm(L);
 }
 

@@ -77,11 +77,13 @@ enum GemmMode : int {
     kModeFp8Fused = 1, // bf16 activations quantised in the kernel prologue
     kModeBf16 = 2,     // bf16 x bf16, no block scales
     kModeMx = 3,       // E4M3 x E4M3 with one UE8M0 scale per 32 K per row, applied by the tensor core
+    kModeFp4 = 4,      // E2M1 x E2M1 with one UE4M3 scale per 16 K or one UE8M0 scale per 32 K per row,
+                       // applied by the tensor core, and fp32 row scales applied at the end
 };
 
 struct GemmParams {
     int M, N, K;
-    int kg;          // K blocks per tile (K/128 for FP8, K/64 for bf16)
+    int kg;          // K blocks per tile (K/128 for FP8, K/64 for bf16, ceil(K/256) for 4-bit)
     int ntiles;      // ceil(N / 128) weight tiles
     int ttiles;      // token tiles
     long long units; // token tiles * ntiles * kg: unit u is K block u % kg of
@@ -93,6 +95,10 @@ struct GemmParams {
     const float *ws;         // FP8: s_w [ntiles][K/128]
     const uint8_t *sfa;      // MX: weight scale atoms [ntiles][K/128][512]
     const uint8_t *sfb;      // MX: activation scale atoms [K/128][512]
+    int sf_atoms;            // 4-bit: scale atoms per row tile and unit: 4 (UE4M3 per 16 K) or 2 (UE8M0 per 32 K);
+                             // sfa / sfb are then [row tile][unit][sf_atoms][512]
+    const float *row_w;      // 4-bit: fp32 scale per weight row [N], or nullptr (all 1)
+    const float *row_a;      // 4-bit: fp32 scale per token [M], or nullptr (all 1)
     const uint16_t *x;       // fused: bf16 activations [M][ldx]
     int ldx;
     uint16_t *y;             // bf16 [M][N]
@@ -139,12 +145,16 @@ template <int NPAD, int MODE> struct GemmCfg {
     // MX: the stage also carries the unit's two 512-byte scale-factor atoms
     // (weights, tokens), copied into tensor memory by the MMA thread.
     static constexpr bool kMx = MODE == kModeMx;
-    static constexpr int kSfBytes = kMx ? 1024 : 0;
+    // 4-bit: up to four atoms a side.
+    static constexpr bool kFp4 = MODE == kModeFp4;
+    static constexpr int kSfBytes = kMx ? 1024 : kFp4 ? 4096 : 0;
     static constexpr int kStageBytes = kWBytes + (MODE == kModeFp8Fused ? 0 : kBBytes) + kSfBytes;
-    // bf16 and MX accumulate a whole tile segment in tensor memory (no
+    // bf16, MX and 4-bit accumulate a whole tile segment in tensor memory (no
     // per-K-block scale to apply on CUDA cores).
-    static constexpr bool kTileAcc = MODE == kModeBf16 || kMx;
-    static constexpr int kMaxStages = 12;
+    static constexpr bool kTileAcc = MODE == kModeBf16 || kMx || kFp4;
+    // (4-bit: as many stages as the scale-factor columns below leave room for,
+    // with two CTAs of the 16-token tile sharing the 512 columns)
+    static constexpr int kMaxStages = !kFp4 ? 12 : NPAD == 16 ? 6 : 8;
     // Accumulators in tensor memory (512 fp32 columns per SM, two CTAs of
     // the 16-token tile sharing them): eight for the 16-token tile, so the
     // MMA runs up to eight units ahead of an epilogue that stalls (for
@@ -155,11 +165,14 @@ template <int NPAD, int MODE> struct GemmCfg {
     // for the 32- to 64-token tiles within +-0.7 % (not taken).
     // (MX at 128 tokens: two, each a whole tile segment's sum, so that they
     // and the scale-factor columns fit the 512 columns.)
-    static constexpr int kAcc = NPAD == 16 ? 8 : (NPAD == 256 || (MODE == kModeMx && NPAD == 128)) ? 2 : 4;
-    // MX: after the accumulators, 8 columns of scale factors per ring stage
-    // (4 for the weight atom, 4 for the token atom).
+    // (4-bit: whole segments' sums, so four serve the 16-token tile too.)
+    static constexpr int kAcc = kFp4 ? (NPAD == 128 ? 2 : 4)
+                                     : NPAD == 16 ? 8 : (NPAD == 256 || (MODE == kModeMx && NPAD == 128)) ? 2 : 4;
+    // MX and 4-bit: after the accumulators, the scale factors' columns of
+    // each ring stage, four per atom (weight atoms, then token atoms).
     static constexpr int kSfCol = kAcc * NPAD;
-    static constexpr int kTmemNeed = kAcc * NPAD + (kMx ? kMaxStages * 8 : 0);
+    static constexpr int kSfStageCols = kMx ? 8 : kFp4 ? 32 : 0;
+    static constexpr int kTmemNeed = kAcc * NPAD + kMaxStages * kSfStageCols;
     static_assert(kTmemNeed <= 512, "tensor memory has 512 columns");
     static constexpr int kTmemCols =
         kTmemNeed <= 32 ? 32 : kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
@@ -224,7 +237,7 @@ template <int NPAD, int MODE> struct GemmCfg {
     // its two CTAs' rings.  Net, decode pass: 1 / 4 / 8 / 16 tokens 0.4 /
     // 0.4 / 0.9 / 1.5 % faster, 32 / 48 / 64 tokens 1.9 / 2.4 / 1.5 %, 128 /
     // 256 / 512 tokens 2.0-2.2 %.
-    static constexpr bool kYTma = MODE == kModeFp8 || MODE == kModeMx;
+    static constexpr bool kYTma = MODE == kModeFp8 || MODE == kModeMx || kFp4;
     static constexpr int kYStageBytes = kYTma ? kTileRows * NPAD * 2 : 0;
     static constexpr int kHeader = 1024;                    // barriers and flags
     // the mbarriers, the TMEM address and two flags end below the greedy keys at 512
@@ -254,8 +267,8 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
     using C = GemmCfg<NPAD, MODE>;
     static_assert(!GREEDY || NPAD <= 64, "the greedy choice keeps one key per token for at most 64 tokens");
     static_assert(MODE != kModeFp8Fused || NPAD <= 64, "the fused cast serves at most 64 tokens");
-    static_assert(MODE != kModeMx || ((NPAD <= 64 || NPAD == 128) && !GREEDY),
-                  "the MX layer: tiles of up to 64 tokens, or 128-token tiles (whose atoms hold 128 tokens)");
+    static_assert((MODE != kModeMx && MODE != kModeFp4) || ((NPAD <= 64 || NPAD == 128) && !GREEDY),
+                  "the MX and 4-bit layers: tiles of up to 64 tokens, or 128-token tiles (whose atoms hold 128 tokens)");
     // Instantiations that only ever run one token tile (the 16-token decode
     // tile, the fused cast and the greedy choice serve at most 64 tokens):
     // pair index == weight tile, and no token-tile stepping is compiled in.
@@ -347,7 +360,8 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_first();
             const uint64_t pol_b = l2_policy_evict_last();
-            const uint32_t tx = C::kStageBytes;
+            const uint32_t tx = C::kFp4 ? C::kWBytes + C::kBBytes + p.sf_atoms * 1024 : C::kStageBytes;
+            const uint32_t sf_bytes = p.sf_atoms * 512; // 4-bit: scale atoms of one side of a unit
             uint32_t armed_mask = 0, armed_parity = 0;
             const int pre = p.prefetch_before_wait ? (nunits < S ? nunits : S) : 0;
             // Per-unit state (K block, weight tile, first token row) advances
@@ -392,6 +406,9 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                 if constexpr (C::kMx)
                     bulk_load_1d(ring + i * C::kStageBytes + C::kWBytes + C::kBBytes,
                                  p.sfa + (static_cast<long long>(wt) * kg + kb) * 512, 512, &full[i], pol_w);
+                if constexpr (C::kFp4)
+                    bulk_load_1d(ring + i * C::kStageBytes + C::kWBytes + C::kBBytes,
+                                 p.sfa + (static_cast<long long>(wt) * kg + kb) * sf_bytes, sf_bytes, &full[i], pol_w);
             }
             grid_dependency_wait();
             if (MODE != kModeFp8Fused) {
@@ -405,6 +422,10 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         bulk_load_1d(ring + i * C::kStageBytes + C::kWBytes + C::kBBytes + 512,
                                      p.sfb + (static_cast<long long>(trow_b / 128) * kg + kb_b) * 512, 512, &full[i],
                                      pol_b);
+                    if constexpr (C::kFp4)
+                        bulk_load_1d(ring + i * C::kStageBytes + C::kWBytes + C::kBBytes + 2048,
+                                     p.sfb + (static_cast<long long>(trow_b / 128) * kg + kb_b) * sf_bytes, sf_bytes,
+                                     &full[i], pol_b);
                 }
             }
             int s = pre % S;
@@ -433,6 +454,13 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         bulk_load_1d(sf, p.sfa + (static_cast<long long>(wt) * kg + kb) * 512, 512, &full[s], pol_w);
                         bulk_load_1d(sf + 512, p.sfb + (static_cast<long long>(trow / 128) * kg + kb) * 512, 512,
                                      &full[s], pol_b);
+                    }
+                    if constexpr (C::kFp4) {
+                        uint8_t *sf = ring + s * C::kStageBytes + C::kWBytes + C::kBBytes;
+                        bulk_load_1d(sf, p.sfa + (static_cast<long long>(wt) * kg + kb) * sf_bytes, sf_bytes, &full[s],
+                                     pol_w);
+                        bulk_load_1d(sf + 2048, p.sfb + (static_cast<long long>(trow / 128) * kg + kb) * sf_bytes,
+                                     sf_bytes, &full[s], pol_b);
                     }
                 }
                 if (++s == S) {
@@ -512,6 +540,27 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         mma_mxf8f6f4(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
                                      idesc_mx_e4m3(C::kTileRows, NPAD, static_cast<uint32_t>(k), static_cast<uint32_t>(k)),
                                      sf, sf + 4, (k > 0 || !fresh) ? 1u : 0u);
+                } else if constexpr (C::kFp4) {
+                    // as MX: this unit's atoms to its stage's columns, then
+                    // four MMAs of 64 K
+                    const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfCol + s * C::kSfStageCols);
+                    const uint32_t sf_smem = smem_u32(ring + s * C::kStageBytes + C::kWBytes + C::kBBytes);
+                    for (int j = 0; j < p.sf_atoms; ++j) {
+                        tmem_cp_sf_atom(sf + 4 * j, sf_atom_desc(sf_smem + 512 * j));
+                        tmem_cp_sf_atom(sf + 16 + 4 * j, sf_atom_desc(sf_smem + 2048 + 512 * j));
+                    }
+                    if (p.sf_atoms == 4) {
+#pragma unroll
+                        for (int k = 0; k < C::kMmaSteps; ++k)
+                            mma_nvf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc_fp4(C::kTileRows, NPAD, 0u, 0u),
+                                     sf + 4 * k, sf + 16 + 4 * k, (k > 0 || !fresh) ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < C::kMmaSteps; ++k)
+                            mma_mxf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
+                                     idesc_fp4(C::kTileRows, NPAD, 1u, static_cast<uint32_t>(2 * (k & 1))),
+                                     sf + 4 * (k >> 1), sf + 16 + 4 * (k >> 1), (k > 0 || !fresh) ? 1u : 0u);
+                    }
                 } else {
 #pragma unroll
                     for (int k = 0; k < C::kMmaSteps; ++k) {
@@ -692,6 +741,15 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
             // Final values of the tile (weight tile wt, token tile ttile): by TMA
             // from the staging tile where the launch set it up, else per row.
             // Every epilogue warp calls it (it holds named barriers).
+            // 4-bit: the finished sums times their weight row's and token's fp32 scales
+            auto apply_rows = [&](int n) {
+                if constexpr (C::kFp4) {
+                    const float rw = p.row_w != nullptr && n < p.N ? p.row_w[n] : 1.0f;
+#pragma unroll
+                    for (int m = 0; m < C::kCols; ++m)
+                        acc[m] *= p.row_a != nullptr && m < mcnt ? rw * p.row_a[tok0 + m] : rw;
+                }
+            };
             bool y_pending = false; // warp 2 lane 0: a TMA store may still read the staging tile
             auto store_y = [&](int n) {
                 if constexpr (kYStage) {
@@ -897,6 +955,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                 const int n = wt * C::kTileRows + row;
                 const bool whole_tile = (seg_first_kb == 0) && (kb == kg - 1);
                 if (whole_tile) {
+                    apply_rows(n);
                     store_y(n);
                 } else {
                     // K-split tile: publish this CTA's partial, and the last
@@ -991,6 +1050,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                                             acc[mc + q] += v[j][q];
                             }
                         }
+                        apply_rows(n);
                         store_y(n);
                         if (warp == 2 && lane == 0)
                             counters_y[tile] = 0u; // ready for the next call

@@ -79,6 +79,12 @@ fp8bs_status launch_gemm_npad(const GemmLaunch &L, const DeviceInfo &dev, const 
         if (st == FP8BS_OK)
             st = make_tmap_2d(&tm_b, L.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, static_cast<uint64_t>(L.M),
                               static_cast<uint64_t>(L.K), static_cast<uint64_t>(L.lda) * 2, 64, NPAD);
+    } else if (MODE == kModeFp4) {
+        // codes as bytes, two to a byte: 128 bytes per row and unit
+        st = make_tmap_2d(&tm_w, L.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, tiled_rows, 128, 128, 128, 128);
+        if (st == FP8BS_OK)
+            st = make_tmap_2d(&tm_b, L.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, static_cast<uint64_t>(L.M),
+                              static_cast<uint64_t>(sh.kg) * 128, static_cast<uint64_t>(sh.kg) * 128, 128, NPAD);
     } else {
         if (tiled)
             st = make_tmap_2d(&tm_w, L.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, tiled_rows, 128, 128, 128, 128);
@@ -95,7 +101,7 @@ fp8bs_status launch_gemm_npad(const GemmLaunch &L, const DeviceInfo &dev, const 
     }
     if (st != FP8BS_OK)
         return st;
-    // Y by TMA store (plain FP8 and MX layers): the tensor map needs a
+    // Y by TMA store (plain FP8, MX and 4-bit layers): the tensor map needs a
     // 16-byte aligned base and a row pitch that is a multiple of 16 bytes;
     // otherwise the epilogue stores rows itself.
     CUtensorMap tm_y = tm_w; // not read unless y_tma
@@ -126,6 +132,9 @@ fp8bs_status launch_gemm_npad(const GemmLaunch &L, const DeviceInfo &dev, const 
     p.ws = L.ws;
     p.sfa = L.sfa;
     p.sfb = L.sfb;
+    p.sf_atoms = L.sf_atoms;
+    p.row_w = L.row_w;
+    p.row_a = L.row_a;
     p.x = static_cast<const uint16_t *>(MODE == kModeFp8Fused ? L.a : nullptr);
     p.ldx = L.lda;
     p.y = static_cast<uint16_t *>(L.y);

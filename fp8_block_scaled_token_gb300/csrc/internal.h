@@ -59,15 +59,18 @@ struct GemmShape;
 WorkspaceLayout workspace_layout(const GemmShape &sh, int M, int K);
 
 struct GemmLaunch {
-    int mode;                 // GemmMode (0 FP8, 1 FP8 fused cast, 2 bf16, 3 MX)
+    int mode;                 // GemmMode (0 FP8, 1 FP8 fused cast, 2 bf16, 3 MX, 4 4-bit)
     int M, N, K;
     const void *a;            // mode 0: Aq u8 [M][K]; mode 1: X bf16 [M][ldx]; mode 2: X bf16 [M][K]
     int lda;                  // row stride of `a` in elements
     const float *as;          // mode 0
     const void *w;            // mode 0/1: Wq u8 [N][K]; mode 2: W bf16 [N][K]
     const float *ws;          // mode 0/1
-    const uint8_t *sfa;       // mode 3: weight scale atoms
-    const uint8_t *sfb;       // mode 3: activation scale atoms
+    const uint8_t *sfa;       // mode 3, 4: weight scale atoms
+    const uint8_t *sfb;       // mode 3, 4: activation scale atoms
+    int sf_atoms = 0;         // mode 4: scale atoms per row tile and 256 K (4: 16-wide blocks, 2: 32-wide)
+    const float *row_w = nullptr; // mode 4: scale per weight row, or nullptr
+    const float *row_a = nullptr; // mode 4: scale per token, or nullptr
     void *y;
     void *workspace;
     size_t workspace_bytes;
@@ -105,6 +108,7 @@ fp8bs_status launch_gemm_fp8(const GemmLaunch &L, const DeviceInfo &dev);
 fp8bs_status launch_gemm_fused(const GemmLaunch &L, const DeviceInfo &dev);
 fp8bs_status launch_gemm_bf16(const GemmLaunch &L, const DeviceInfo &dev);
 fp8bs_status launch_gemm_mx(const GemmLaunch &L, const DeviceInfo &dev);
+fp8bs_status launch_gemm_fp4(const GemmLaunch &L, const DeviceInfo &dev);
 fp8bs_status launch_mx_quant_weights(const void *w, int wtype, int N, int K, uint8_t *wq, uint8_t *sf,
                                      cudaStream_t stream, const DeviceInfo &dev);
 fp8bs_status launch_mx_quant_act(const void *x, int M, int K, int ldx, uint8_t *xq, uint8_t *sf, bool pdl,
@@ -116,6 +120,19 @@ fp8bs_status launch_quant_weight(const void *w, int wtype, int N, int K, uint8_t
                                  cudaStream_t stream, const DeviceInfo &dev);
 fp8bs_status launch_pack_bf16_tiled(const void *w, int N, int K, void *wt, cudaStream_t stream,
                                     const DeviceInfo &dev);
+
+// 4-bit: activations [M][kg * 128] codes, [ceil(M/128)][kg * sf_atoms][512]
+// atoms and [M] row scales at these offsets of the workspace of fp4_gemm_fused.
+struct Fp4Workspace {
+    size_t codes_off, atoms_off, rows_off, total;
+};
+Fp4Workspace fp4_workspace(const GemmShape &sh, int M, int sf_atoms);
+fp8bs_status launch_fp4_quant_weights(const void *w, int wtype, int N, int K, int fmt, uint8_t *wq, uint8_t *sf,
+                                      float *rows, cudaStream_t stream, const DeviceInfo &dev);
+fp8bs_status launch_fp4_quant_act(const void *x, int M, int K, int ldx, int fmt, uint8_t *xq, uint8_t *sf,
+                                  float *rows, bool pdl, cudaStream_t stream, const DeviceInfo &dev);
+fp8bs_status launch_fp4_dequant_weights(const uint8_t *wq, const uint8_t *sf, const float *rows, int N, int K,
+                                        int fmt, void *w, int wtype, cudaStream_t stream, const DeviceInfo &dev);
 
 constexpr unsigned long long kDefaultTimeoutNs = 1000000000ull; // one second
 

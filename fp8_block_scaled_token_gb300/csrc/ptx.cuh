@@ -493,6 +493,45 @@ __host__ __device__ constexpr uint32_t idesc_mx_e4m3(int m, int n, uint32_t a_sf
            (static_cast<uint32_t>(m >> 7) << 27) | (a_sf_id << 29);
 }
 
+// ------------------------------------------------------- 4-bit operands
+// E2M1 operands, two to a byte (the lower K in the lower four bits): a
+// 128-byte K-major row holds 256 values, four MMAs of 64.  The scale factors
+// use the atoms above, read four blocks of K to an atom:
+//   scale_vec::4X (one UE4M3 factor per 16 K): an atom covers 64 K, one MMA;
+//     its four bytes per row are the MMA's four factors (scale factor id 0);
+//   scale_vec::2X (one UE8M0 factor per 32 K): an atom covers 128 K, two
+//     MMAs, which take the byte pairs 0-1 and 2-3 (scale factor ids 0, 2).
+__device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
+// Instruction descriptor of kind::mxf4 / kind::mxf4nvf4: as idesc_mx_e4m3,
+// with A and B format 1 (E2M1), scale format 0 = UE4M3, 1 = UE8M0, and bit 31
+// = 0 (64 K per dense MMA).
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, uint32_t ue8m0, uint32_t sf_id)
+{
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (ue8m0 << 23) |
+           (static_cast<uint32_t>(m >> 7) << 27) | (sf_id << 29);
+}
+
 // Named barrier over `nthreads` threads (ids 1..15; 0 is __syncthreads).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads)
 {

@@ -327,6 +327,69 @@ FP8BS_API fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, c
                                    size_t workspace_bytes, unsigned flags, void *stream);
 
 /*
+ * Microscaled 4-bit floating point: E2M1 weights and activations (magnitudes
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6) with block scales that the tensor core applies
+ * (tcgen05.mma kind::mxf4nvf4 / kind::mxf4, block_scale).  Two formats:
+ *   FP8BS_FP4_NV  every 16 consecutive values along K share one E4M3 scale,
+ *     and every weight row and token has one fp32 scale:
+ *       r    = fl32(amax_row / 2688)   (2688 = 6 * 448; 1 where that is below 2^-126)
+ *       b    = e4m3_rn(fl32(fl32(amax_16 / 6) / r)),  d = fl32(dec(b) * r)
+ *       code = e2m1_rn_satfinite(fl32(v / d)), 0 where b is 0
+ *   FP8BS_FP4_MX  every 32 consecutive values share one power of two 2^e:
+ *       e    = floor(log2(amax_32)) - 2, clamped to [-127, 127] (0 for zeros)
+ *       code = e2m1_rn_satfinite(v / 2^e)   (exact scaling); r = 1
+ * Divisions are IEEE fp32.  Inputs must be finite.
+ *
+ * K is a multiple of 32, padded inside the packed operands to kt = ceil(K/256)
+ * blocks of 256 with zero codes and zero scale bytes.  Two codes to a byte,
+ * the lower k in the lower four bits.  Scale bytes in 512-byte atoms as in the
+ * MX variant above, four consecutive blocks of K per atom: the byte of row r
+ * (0..127) and block j (0..3) at 16 * (r % 32) + 4 * (r / 32) + j; a 256-wide
+ * unit has S = 4 atoms (NV) or 2 (MX).
+ *
+ * fp4_quant_weights: w fp32|bf16 [N][K] ->
+ *   wq       ceil(N/128) * kt * 16384 bytes: row r of tile nb, unit kb at
+ *            ((nb * kt + kb) * 128 + r) * 128; rows past N zero;
+ *   ws_atoms ceil(N/128) * kt * S * 512 bytes, atom (nb, kb, s) at
+ *            ((nb * kt + kb) * S + s) * 512; rows past N zero;
+ *   w_rows   fp32 [N], r (may be NULL for MX, where every r is 1).
+ * fp4_dequant_weights: the values back, w[n][k] = fl32(code * fl32(scale * r)),
+ *   as fp32 or (rounded to nearest even) bf16.
+ * fp4_quant_act: x bf16, M rows (1..512), row stride ldx (>= K, % 8 == 0) ->
+ *   xq [M][kt * 128] bytes, xs_atoms ceil(M/128) * kt * S * 512 bytes laid out
+ *   as ws_atoms (bytes of rows past M are not written), x_rows fp32 [M] (may be
+ *   NULL for MX).  flags: 0 or FP8BS_FLAG_OVERLAP_PREV.
+ * fp4_gemm: y bf16 [M][N],
+ *   y[m,n] = bf16_rn(r_a[m] r_w[n] sum over blocks of s_a s_w sum of code products)
+ *   with fp32 accumulation, 1 <= M <= 512; a_rows / w_rows NULL means 1 (MX
+ *   only).  Same pipeline, schedule rules (fp8_mx_gemm's, with 256-wide units),
+ *   Y alignment rule, workspace contract and flags as fp8_mx_gemm.  Bitwise
+ *   reproducible.
+ * fp4_gemm_fused: fp4_quant_act into the workspace followed by fp4_gemm, the
+ *   same bits as the two calls.
+ * w, wq, ws_atoms, x, xq, xs_atoms: 16-byte aligned; row scales 4-byte.
+ */
+typedef enum fp8bs_fp4_format {
+    FP8BS_FP4_NV = 0,
+    FP8BS_FP4_MX = 1
+} fp8bs_fp4_format;
+
+FP8BS_API fp8bs_status fp4_quant_weights(const void *w, fp8bs_dtype wtype, int N, int K, fp8bs_fp4_format fmt,
+                                         uint8_t *wq, uint8_t *ws_atoms, float *w_rows, void *stream);
+FP8BS_API fp8bs_status fp4_dequant_weights(const uint8_t *wq, const uint8_t *ws_atoms, const float *w_rows, int N,
+                                           int K, fp8bs_fp4_format fmt, void *w, fp8bs_dtype wtype, void *stream);
+FP8BS_API fp8bs_status fp4_quant_act(const void *x, int M, int K, int ldx, fp8bs_fp4_format fmt, uint8_t *xq,
+                                     uint8_t *xs_atoms, float *x_rows, unsigned flags, void *stream);
+FP8BS_API fp8bs_status fp4_gemm_workspace_size(int M, int N, int K, fp8bs_fp4_format fmt, size_t *bytes);
+FP8BS_API fp8bs_status fp4_gemm(const uint8_t *aq, const uint8_t *as_atoms, const float *a_rows, const uint8_t *wq,
+                                const uint8_t *ws_atoms, const float *w_rows, void *y, int M, int N, int K,
+                                fp8bs_fp4_format fmt, void *workspace, size_t workspace_bytes, unsigned flags,
+                                void *stream);
+FP8BS_API fp8bs_status fp4_gemm_fused(const void *x, int ldx, const uint8_t *wq, const uint8_t *ws_atoms,
+                                      const float *w_rows, void *y, int M, int N, int K, fp8bs_fp4_format fmt,
+                                      void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
  * 16-bit comparison GEMM for the output layer [P2 "The output layer, which
  * did run": the layer "still 16-bit" before conversion]:
  *   y[m*N + n] = bf16_rn( sum_k x[m,k] * w[n,k] )   (fp32 accumulation)

@@ -1,0 +1,196 @@
+"""GPU parity of the 4-bit layers (FP4_NV: 16-wide E4M3 scales under an fp32
+row scale; FP4_MX: 32-wide powers of two) against the definition in numpy.
+
+Codes, scale bytes, row scales and values read back must be equal bit for bit
+(the definition names every rounding; a zero code's sign is free).  Y must
+meet the layers' bound |y - y64| <= 4e-3 * sum|a w| + 1e-6, which covers its
+one bf16 rounding (2^-9 of |y|) and fp32 accumulation, and repeat bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_scaled_token_gb300 as fb
+from fp8_block_scaled_token_gb300 import synth
+from tests import fp4_reference as ref
+from tests.gpu_helpers import Ran, check_y, runs_gemm
+
+pytestmark = pytest.mark.gpu
+
+MODE_FP4 = 4
+RUNS_FP4_QUANT_WEIGHT, RUNS_FP4_QUANT_ACT, RUNS_FP4_DEQUANT = 5, 6, 7
+FORMATS = [fb.FP4_NV, fb.FP4_MX]
+
+
+def _f32(t):
+    return t.float().cpu().numpy()
+
+
+def _check_packed(wq, wa, wr, v, fmt, tiled):
+    codes, byte, r = ref.quantise(v, fmt)
+    assert np.array_equal(ref.without_zero_signs(wq.cpu().numpy()), ref.pack_codes(codes, tiled))
+    R = v.shape[0]
+    atoms = ref.pack_atoms(byte, v.shape[1], fmt)
+    got = wa.cpu().numpy()
+    if not tiled:  # bytes of rows past M are not written
+        live = ref.pack_atoms(np.ones_like(byte), v.shape[1], fmt) + ref.pack_atoms(
+            np.ones((R, atoms.shape[0] // -(-R // 128) * 4), np.uint8), v.shape[1], fmt) > 0
+        got, atoms = got[live], atoms[live]
+    assert np.array_equal(got, atoms)
+    assert np.array_equal(wr.cpu().numpy(), r)
+    return codes, byte, r
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("N,K,dtype", [(256, 512, torch.float32), (300, 1280, torch.bfloat16), (1, 32, torch.float32),
+                                       (129, 288, torch.float32), (7, 4128, torch.bfloat16), (640, 5120, torch.float32)])
+def test_weights_bit_exact_and_read_back(fmt, N, K, dtype):
+    w = synth.weights(N, K, seed=N + K, outlier_p=0.01).to(dtype)
+    with Ran() as run:
+        wq, wa, wr = fb.fp4_quant_weights(w.cuda(), fmt)
+        back = fb.fp4_dequant_weights(wq, wa, wr, N, K, fmt)
+        back16 = fb.fp4_dequant_weights(wq, wa, wr, N, K, fmt, dtype=torch.bfloat16)
+    assert run.launched() == {RUNS_FP4_QUANT_WEIGHT: 1, RUNS_FP4_DEQUANT: 2}
+    codes, byte, r = _check_packed(wq, wa, wr, _f32(w), fmt, True)
+    want = ref.values(codes, byte, r, fmt, np.float32)
+    assert np.array_equal(back.cpu().numpy(), want)  # -0 equals 0
+    assert torch.equal(back16.cpu().float(), torch.from_numpy(want).to(torch.bfloat16).float())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K", [(1, 32), (8, 5120), (13, 1312), (64, 2048), (129, 256), (512, 512), (3, 17408)])
+def test_activations_bit_exact(fmt, M, K):
+    x = synth.activations(M, K, seed=M + K, outlier_p=0.001)
+    with Ran() as run:
+        xq, xa, xr = fb.fp4_quant_act(x.cuda(), fmt)
+    assert run.launched() == {RUNS_FP4_QUANT_ACT: 1}
+    _check_packed(xq, xa, xr, _f32(x), fmt, False)
+
+
+def _edge_rows(K=256):
+    rows = [np.zeros(K), np.full(K, 2.0 ** -130), np.full(K, 2.0 ** -149), np.full(K, 3e38)]
+    t = np.zeros(K)
+    t[5] = 1e-20                                               # one value, every other block's scale byte is 0
+    rows.append(t)
+    t = np.full(K, 1e-6)
+    t[0] = 1e6                                                 # small blocks vanish under the row's largest (NV)
+    rows.append(t)
+    t = np.tile([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], K // 8)  # ties of the codes (MX: scale 1)
+    t[1::2] *= -1
+    rows += [t, t * 2.0 ** -40, t * 2.0 ** 100]
+    rows.append(np.array([2.0 ** (j % 60 - 30) for j in range(K)]))
+    z = np.zeros(K)
+    z[1::2] = -0.0
+    z[::64] = -3.0
+    rows.append(z)
+    rows.append(np.where(np.arange(K) == 3, 2688.0 * 2.0 ** -126, 0.0))  # the least row with a scale of its own
+    rows.append(np.where(np.arange(K) == 3, 2687.0 * 2.0 ** -126, 0.0))
+    return np.stack(rows).astype(np.float32)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_edge_values(fmt):
+    v = _edge_rows()
+    w = torch.from_numpy(v)
+    wq, wa, wr = fb.fp4_quant_weights(w.cuda(), fmt)
+    codes, byte, r = _check_packed(wq, wa, wr, v, fmt, True)
+    back = fb.fp4_dequant_weights(wq, wa, wr, v.shape[0], v.shape[1], fmt)
+    assert np.array_equal(back.cpu().numpy(), ref.values(codes, byte, r, fmt, np.float32))
+    xb = w.to(torch.bfloat16)
+    _check_packed(*fb.fp4_quant_act(xb.cuda(), fmt), _f32(xb), fmt, False)
+
+
+def _layer(M, N, K, fmt, seed):
+    x = synth.activations(M, K, seed=seed, outlier_p=0.001)
+    w = synth.weights(N, K, seed=seed + 1000, outlier_p=0.01)
+    packed = fb.fp4_quant_weights(w.cuda(), fmt)
+    a = ref.values(*ref.quantise(_f32(x), fmt), fmt)
+    b = ref.values(*ref.quantise(w.numpy(), fmt), fmt)
+    return x.cuda(), packed, a @ b.T, np.abs(a) @ np.abs(b).T
+
+
+def _npad(M):
+    return 16 if M <= 16 else 32 if M <= 32 else 48 if M <= 48 else 64 if M <= 64 else 128
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(8, 128, 256), (1, 1, 32), (8, 256, 512), (1, 640, 1024), (13, 300, 1312),
+                                   (33, 1000, 2080), (48, 257, 544), (64, 384, 1024), (8, 5120, 5120), (8, 512, 17408),
+                                   (65, 640, 1024), (128, 1001, 2048), (300, 2560, 1056), (512, 640, 512),
+                                   (256, 7168, 1024)])
+def test_product_matches_64_bits(M, N, K, fmt):
+    x, packed, y_ref, bound = _layer(M, N, K, fmt, seed=M + N)
+    work = fb.make_workspace(fb.fp4_gemm_workspace_size(M, N, K, fmt))
+    with Ran() as run:
+        y = fb.fp4_gemm_fused(x, *packed, N, fmt, workspace=work)
+    assert run.launched() == {RUNS_FP4_QUANT_ACT: 1, runs_gemm(MODE_FP4, _npad(M)): 1}
+    assert fb.workspace_status(work) == 0
+    check_y(y, y_ref, bound, "fp4 M=%d N=%d K=%d" % (M, N, K))
+    y2 = fb.fp4_gemm(*fb.fp4_quant_act(x, fmt), *packed, N, K, fmt, workspace=work)
+    assert torch.equal(y.view(torch.int16), y2.view(torch.int16)), "the fused call and the two calls differ"
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_strided_input_other_stream_and_garbage_workspace_rows(fmt):
+    """Rows of a wider matrix, on a stream of its own, with the activations'
+    region of the workspace full of NaN bytes: nothing of it may reach Y."""
+    M, N, K = 5, 384, 1056
+    x, packed, y_ref, bound = _layer(M, N, K, fmt, seed=9)
+    wide = torch.full((M, K + 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, :K] = x
+    work = fb.make_workspace(fb.fp4_gemm_workspace_size(M, N, K, fmt))
+    kt = (K + 255) // 256
+    act = M * kt * 128 + kt * 4 * 512
+    work[-act:] = 0x7F
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y = fb.fp4_gemm_fused(wide[:, :K], *packed, N, fmt, workspace=work)
+    s.synchronize()
+    check_y(y, y_ref, bound, "strided")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(8, 5120, 5120), (300, 1024, 4096)])
+def test_reruns_bitwise(M, N, K, fmt):
+    x, packed, _, _ = _layer(M, N, K, fmt, seed=3)
+    work = fb.make_workspace(fb.fp4_gemm_workspace_size(M, N, K, fmt))
+    outs = [fb.fp4_gemm_fused(x, *packed, N, fmt, workspace=work, flags=(fb.FLAG_OVERLAP_PREV if i % 2 else 0))
+            for i in range(10)]
+    torch.cuda.synchronize()
+    for o in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+    assert fb.workspace_status(work) == 0
+
+
+def test_row_scales_may_be_left_out_for_mx_only():
+    M, N, K = 4, 256, 512
+    x, (wq, wa, wr), y_ref, bound = _layer(M, N, K, fb.FP4_MX, seed=4)
+    check_y(fb.fp4_gemm_fused(x, wq, wa, None, N, fb.FP4_MX), y_ref, bound, "no row scales")
+    with pytest.raises(fb.Fp8bsError) as e:
+        fb.fp4_gemm_fused(x, *fb.fp4_quant_weights(torch.zeros(N, K, device="cuda"))[:2], None, N, fb.FP4_NV)
+    assert e.value.code == 1
+
+
+def test_refusals():
+    x = synth.activations(513, 256, seed=1).cuda()
+    with pytest.raises(fb.Fp8bsError) as e:
+        fb.fp4_quant_act(x)
+    assert e.value.code == 2                                     # more than 512 tokens
+    with pytest.raises(fb.Fp8bsError) as e:
+        fb.fp4_gemm_workspace_size(8, 256, 40)
+    assert e.value.code == 2                                     # K % 32
+    w = torch.zeros(256, 512, device="cuda")
+    packed = fb.fp4_quant_weights(w)
+    with pytest.raises(ValueError):
+        fb.fp4_gemm_fused(x[:8], *packed, 256)                   # K of x is not the weights'
+    with pytest.raises(ValueError):
+        fb.fp4_quant_weights(w.t())
+    with pytest.raises(TypeError):
+        fb.fp4_quant_weights(w.half())
+    with pytest.raises(ValueError):
+        fb.fp4_quant_act(x[:8], fmt=5)
+    with pytest.raises(fb.Fp8bsError) as e:
+        fb.fp4_gemm_fused(synth.activations(8, 512, seed=1).cuda(), *packed, 256,
+                          workspace=fb.make_workspace(1024))
+    assert e.value.code == 4
