@@ -19,6 +19,9 @@ Entry points (same names as the C ABI):
   16-bit output-layer baseline).
 * ``fp8_mx_quant_weights(w)``, ``fp8_mx_quant_act(x)``, ``fp8_mx_gemm(...)``:
   the native block-scaled (MX) variant, one UE8M0 scale per 32 K.
+* ``moe_route(x, wr, top_k)`` -> (ids, weights), ``fp8_moe_experts(x, ids,
+  weights, w13, s13, w2, s2)`` -> Y and ``fp8_moe_layer(x, wr, top_k, w13, s13,
+  w2, s2)`` -> (Y, ids, weights): a mixture-of-experts layer (M up to 64).
 * ``fp4_quant_weights(w, fmt)``, ``fp4_quant_act(x, fmt)``, ``fp4_gemm(...)``,
   ``fp4_gemm_fused(x, ...)``, ``fp4_dequant_weights(...)``: microscaled 4-bit
   weights and activations (FP4_NV or FP4_MX).
@@ -110,6 +113,11 @@ def _load(path):
         "fp8_mx_quant_weights": [vp, i, i, i, vp, vp, vp],
         "fp8_mx_quant_act": [vp, i, i, i, vp, vp, u, vp],
         "fp8_mx_gemm_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "moe_route_workspace_size": [i, i, ctypes.POINTER(sz)],
+        "moe_route": [vp, i, vp, i, i, i, i, i, i, vp, vp, vp, sz, u, vp],
+        "fp8_moe_workspace_size": [i, i, i, i, i, ctypes.POINTER(sz)],
+        "fp8_moe_experts": [vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, u, vp],
+        "fp8_moe_layer": [vp, i, vp, i, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, u, vp],
         "fp4_quant_weights": [vp, i, i, i, i, vp, vp, vp, vp],
         "fp4_dequant_weights": [vp, vp, vp, i, i, i, vp, i, vp],
         "fp4_quant_act": [vp, i, i, i, i, vp, vp, vp, u, vp],
@@ -445,6 +453,127 @@ def fp8_mx_gemm(aq, as_atoms, wq, ws_atoms, n, y=None, workspace=None, flags=0):
     _check("fp8_mx_gemm", lib().fp8_mx_gemm(_ptr(aq), _ptr(as_atoms), _ptr(wq), _ptr(ws_atoms), _ptr(y), M, N, K,
                                             _ptr(workspace), workspace.numel(), flags, _stream()))
     return y
+
+
+# ------------------------------------------------------------ expert layers
+def moe_route_workspace_size(M, E):
+    n = ctypes.c_size_t(0)
+    _check("moe_route_workspace_size", lib().moe_route_workspace_size(M, E, ctypes.byref(n)))
+    return n.value
+
+
+def fp8_moe_workspace_size(M, H, I, E, top_k):
+    n = ctypes.c_size_t(0)
+    _check("fp8_moe_workspace_size", lib().fp8_moe_workspace_size(M, H, I, E, top_k, ctypes.byref(n)))
+    return n.value
+
+
+def _router(x, wr):
+    """(M, H, E, dtype code) of activations and router weights."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x")
+    _rows_contiguous(x, "x")
+    if wr.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("wr must be float32 or bfloat16")
+    _need(wr, wr.dtype, "wr")
+    if not wr.is_contiguous():
+        raise ValueError("wr must be contiguous")
+    if wr.shape[1] != x.shape[1]:
+        raise ValueError("operand shapes do not agree")
+    return x.shape[0], x.shape[1], wr.shape[0], BF16 if wr.dtype == torch.bfloat16 else F32
+
+
+def _experts(w13, s13, w2, s2, H, E):
+    """(E, I, flag) of the experts' weights: w13 [E, 2I, H] and w2 [E, H, I],
+    or both tiled [tiles, 128, 128]; E (None: from a row-major w13) settles the
+    tiled form."""
+    torch = _torch()
+    for t, nm in ((w13, "w13"), (w2, "w2")):
+        _need(t, torch.uint8, nm, ndim=3)
+    for t, nm in ((s13, "s13"), (s2, "s2")):
+        _need(t, torch.float32, nm)
+    for t, nm in ((w13, "w13"), (w2, "w2"), (s13, "s13"), (s2, "s2")):
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % nm)
+    kg = H // 128
+    if E is None:
+        if w13.shape[2] != H:
+            raise ValueError("w13 is tiled: pass experts= (the number of experts)")
+        E = w13.shape[0]
+    E = int(E)
+    rows = s13.shape[0] // (2 * E) if E > 0 else 0  # 128-row tiles of I
+    I = rows * 128
+    if rows < 1 or tuple(s13.shape) != (2 * E * rows, kg) or tuple(s2.shape) != (E * kg, rows):
+        raise ValueError("operand shapes do not agree")
+    if tuple(w13.shape) == (E, 2 * I, H) and tuple(w2.shape) == (E, H, I):
+        return E, I, 0
+    if tuple(w13.shape) == (2 * E * rows * kg, 128, 128) and tuple(w2.shape) == (E * kg * rows, 128, 128):
+        return E, I, FLAG_WEIGHTS_TILED
+    raise ValueError("operand shapes do not agree")
+
+
+def moe_route(x, wr, top_k, renormalize=True, ids=None, weights=None, workspace=None, flags=0):
+    """The experts of each token: x bf16 [M, H] (row stride may exceed H), wr
+    fp32 or bf16 [E, H] -> (ids int32 [M, top_k] by descending logit, weights
+    fp32 [M, top_k], softmax over the chosen or, with renormalize=False, over
+    all experts)."""
+    torch = _torch()
+    M, H, E, wt = _router(x, wr)
+    ids = _out(ids, (M, top_k), torch.int32, x.device, "ids")
+    weights = _out(weights, (M, top_k), torch.float32, x.device, "weights")
+    if workspace is None:
+        workspace = make_workspace(moe_route_workspace_size(M, E), x.device)
+    _check("moe_route", lib().moe_route(_ptr(x), x.stride(0), _ptr(wr), wt, M, H, E, top_k, 1 if renormalize else 0,
+                                        _ptr(ids), _ptr(weights), _ptr(workspace), workspace.numel(), flags, _stream()))
+    return ids, weights
+
+
+def fp8_moe_experts(x, ids, weights, w13, s13, w2, s2, experts=None, y=None, workspace=None, flags=0):
+    """Y bf16 [M, H] of the experts that ids int32 [M, top_k] names, weighted
+    by weights fp32 [M, top_k] (an id outside [0, experts) is skipped); w13
+    [experts, 2I, H] and w2 [experts, H, I] E4M3 row-major, or both tiled
+    (fp8_quant_weight_blocks of the matrices with the experts' rows stacked)
+    with experts= given; s13, s2 their block scales."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x")
+    _rows_contiguous(x, "x")
+    M, H = x.shape
+    E, I, tf = _experts(w13, s13, w2, s2, H, experts)
+    _need(ids, torch.int32, "ids")
+    _need(weights, torch.float32, "weights")
+    k = ids.shape[1]
+    if ids.shape[0] != M or tuple(weights.shape) != (M, k):
+        raise ValueError("operand shapes do not agree")
+    if not (ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError("ids and weights must be contiguous")
+    y = _out(y, (M, H), torch.bfloat16, x.device, "y")
+    if workspace is None:
+        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, k), x.device)
+    _check("fp8_moe_experts",
+           lib().fp8_moe_experts(_ptr(x), x.stride(0), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(s13), _ptr(w2),
+                                 _ptr(s2), _ptr(y), M, H, I, E, k, _ptr(workspace), workspace.numel(), flags | tf,
+                                 _stream()))
+    return y
+
+
+def fp8_moe_layer(x, wr, top_k, w13, s13, w2, s2, renormalize=True, y=None, ids=None, weights=None, workspace=None,
+                  flags=0):
+    """The whole layer, moe_route and fp8_moe_experts in three kernels: (y
+    bf16 [M, H], ids int32 [M, top_k], weights fp32 [M, top_k]); w13 and w2 as
+    in fp8_moe_experts, row-major or tiled."""
+    torch = _torch()
+    M, H, E, wt = _router(x, wr)
+    _, I, tf = _experts(w13, s13, w2, s2, H, E)
+    y = _out(y, (M, H), torch.bfloat16, x.device, "y")
+    ids = _out(ids, (M, top_k), torch.int32, x.device, "ids")
+    weights = _out(weights, (M, top_k), torch.float32, x.device, "weights")
+    if workspace is None:
+        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, top_k), x.device)
+    _check("fp8_moe_layer",
+           lib().fp8_moe_layer(_ptr(x), x.stride(0), _ptr(wr), wt, 1 if renormalize else 0, _ptr(w13), _ptr(s13),
+                               _ptr(w2), _ptr(s2), _ptr(y), _ptr(ids), _ptr(weights), M, H, I, E, top_k,
+                               _ptr(workspace), workspace.numel(), flags | tf, _stream()))
+    return y, ids, weights
 
 
 # ------------------------------------------------------------- 4-bit layers

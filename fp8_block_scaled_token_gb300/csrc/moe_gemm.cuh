@@ -1,0 +1,632 @@
+// moe_gemm.cuh -- the two grouped products of an expert layer for up to 64
+// tokens, E4M3 with 128x128 weight-block and 1x128 activation scales.
+//
+//   up:   g, u = W13[e] a   (gate rows 0..I-1, up rows I..2I-1 of expert e),
+//         h = g / (1 + exp(-g)) * u, one fp32 scale per token and 128 of I,
+//         E4M3 codes
+//   down: y = sum over chosen experts of w * W2[e] h
+//
+// A few tokens choose from many experts, so nearly every expert product has
+// one to a few rows and the layer's time is the active experts' weight bytes.
+// Both products therefore multiply every active expert's weights by ALL the
+// tokens (16, 32 or 64 columns of the MMA's N, which cost no memory traffic
+// worth counting): no gather, no padding per expert, every weight byte is read
+// once, and a token that did not choose an expert has weight 0 there.
+//   up   is one product with N concatenated over the active experts:
+//        unit = (active expert a, 128 of I, 128 of H), a gate tile and an up
+//        tile of weights a unit;
+//   down is one product with K concatenated over the active experts:
+//        unit = (128 of H, active expert a, 128 of I); the experts' sum is
+//        the K sum, with the token's weight folded into the scale of its
+//        intermediate, so nothing is combined afterwards.
+// Units are dealt to the CTAs in equal contiguous ranges (stream-K, plan.cuh)
+// over the number of active experts, which the kernels read on the device.  A
+// tile shared by CTAs is summed in contributor order by the last one to
+// arrive: results repeat bit for bit, and no CTA waits for another.
+//
+// Warp 0 streams the tiles (TMA), warp 1 issues tcgen05.mma, the others
+// promote each unit's accumulators by their scales into fp32 registers, as in
+// gemm_kernel.cuh.  Every wait is bounded.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "fp8bs_testing.h"
+#include "moe.h"
+#include "plan.cuh"
+#include "ptx.cuh"
+#include "quant_math.cuh"
+
+namespace fp8bs {
+
+enum MoePhase : int { kMoeUp = 0, kMoeDown = 1 };
+
+struct MoeGemmParams {
+    int M, H, I, E;
+    int stages;
+    const int *active;     // number of active experts, then their numbers
+    const float *wtok;     // [E][NPAD]
+    const float *ws;       // weight block scales: s13 [E][2I/128][H/128] or s2 [E][H/128][I/128]
+    const float *xs;       // up: activation scales [H/128][M]
+    uint8_t *hq;           // up: codes out, [active][NPAD][I]
+    float *hs;             // scales times weights, [active][I/128][NPAD]: up writes, down reads
+    uint16_t *y;           // down: bf16 [M][H]
+    unsigned *status, *counters;
+    float *slots;          // [2 * grid][tiles a unit][NPAD * 128]
+    int w_tiled;
+    int max_active;
+    int test_skip_unit;
+    unsigned long long timeout_ns;
+    unsigned long long *runs;
+};
+
+template <int NPAD, int PHASE> struct MoeCfg {
+    static_assert(NPAD == 16 || NPAD == 32 || NPAD == 64, "token tile");
+    static constexpr int kTiles = PHASE == kMoeUp ? 2 : 1;  // weight tiles a unit
+    static constexpr int kWBytes = 128 * 128;
+    static constexpr int kBBytes = NPAD * 128;
+    static constexpr int kStageBytes = kTiles * kWBytes + kBBytes;
+    static constexpr int kMaxStages = 12;
+    static constexpr int kAcc = PHASE == kMoeDown && NPAD == 16 ? 8 : 4;
+    static constexpr int kAccCols = kTiles * NPAD;
+    static constexpr int kTmemCols = kAcc * kAccCols; // 128 (16 tokens), 256 / 128 (32), 512 / 256 (64)
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
+    // As in the dense GEMM: two CTAs per SM at 16 tokens, so that the next
+    // kernel's CTA streams its first weights while this one finishes, and two
+    // groups of epilogue warps at 64.
+    static constexpr int kMinBlocks = NPAD == 16 ? 2 : 1;
+    static constexpr int kColGroups = NPAD == 64 ? 2 : 1;
+    static constexpr int kCols = NPAD / kColGroups;
+    static_assert(kCols <= 32, "a lane holds one token's scale");
+    static constexpr int kEpiWarps = 4 * kColGroups;
+    static constexpr int kThreads = 32 * (2 + kEpiWarps);
+    static constexpr int kMaxRegs = kMinBlocks == 2 ? 160 : kEpiWarps == 4 ? 255 : 168;
+    // barriers and flags, [1024, 3072) active experts, [3072, 4096) amax exchange
+    static constexpr int kHeader = 4096;
+    static constexpr int kProdFloats = kEpiWarps * 2 * kTiles * kCols; // per warp, by unit parity
+    static constexpr uint32_t kIdesc = idesc_e4m3_f32(128, NPAD);
+    static_assert((2 * kMaxStages + 2 * kAcc + 1) * 8 + 12 <= 1024, "header layout");
+    static constexpr int smem_bytes(int stages)
+    {
+        return 1024 + kHeader + stages * kStageBytes + kProdFloats * 4;
+    }
+};
+
+template <int NPAD, int PHASE>
+__global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
+    moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_b,
+                    const MoeGemmParams p)
+{
+    using C = MoeCfg<NPAD, PHASE>;
+    constexpr bool kUp = PHASE == kMoeUp;
+    constexpr int kTriggerLead = 6; // as in gemm_kernel.cuh
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem);
+    uint64_t *empty = full + C::kMaxStages;
+    uint64_t *tfull = empty + C::kMaxStages;
+    uint64_t *tempty = tfull + C::kAcc;
+    uint64_t *mma_done = tempty + C::kAcc;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *last_flag = abort_flag + 1;
+    int *act = reinterpret_cast<int *>(smem + 1024);            // [kMoeMaxExperts]
+    float *amax_x = reinterpret_cast<float *>(smem + 3072);     // [4][NPAD]
+    const int S = p.stages;
+    uint8_t *ring = smem + C::kHeader;
+    float *prod = reinterpret_cast<float *>(ring + S * C::kStageBytes);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    if (threadIdx.x == 0) {
+        if (cta == 0)
+            atomicAdd(p.runs + FP8BS_RUNS_MOE_GEMM(PHASE, NPAD), 1ull);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < C::kAcc; ++a) {
+            mbar_init(&tfull[a], 1);
+            mbar_init(&tempty[a], C::kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        *last_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+    }
+    // The list of active experts comes from the routing kernel: the up
+    // product's predecessor, which it waits for here, and the down product's
+    // predecessor's, complete because every CTA of the up product has passed
+    // this wait before it lets this grid start.
+    if (kUp)
+        grid_dependency_wait();
+    int A = __ldcg(p.active);
+    A = A < 0 ? 0 : A > p.max_active ? p.max_active : A;
+    for (int i = threadIdx.x; i < A; i += C::kThreads)
+        act[i] = __ldcg(p.active + 1 + i);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+
+    // K blocks of one expert, tiles of 128 output rows (up: of one expert's I)
+    const int kg1 = kUp ? p.H / 128 : p.I / 128;
+    const int nj = kUp ? p.I / 128 : p.H / 128;
+    const int kg = kUp ? kg1 : A * kg1;           // units per output tile
+    const int tiles = kUp ? A * nj : nj;
+    const long long units = static_cast<long long>(tiles) * kg;
+    const int ctas = plan_ctas(units, gridDim.x); // CTAs past the units have none
+    const bool has = cta < ctas;
+    const long long u0 = has ? plan_begin(units, ctas, cta) : 0;
+    const int nunits = has ? static_cast<int>(plan_begin(units, ctas, cta + 1) - u0) : 0;
+    const int tile0 = has ? static_cast<int>(u0 / kg) : 0;
+    const int ku0 = has ? static_cast<int>(u0 % kg) : 0; // unit within the tile
+
+    // A unit's place: output tile, active expert, K block of that expert.
+    struct Unit {
+        int ku, a, j, kb; // unit within the tile, active expert, tile of 128 rows within its matrix, K block
+    };
+    auto first_unit = [&]() {
+        Unit u;
+        u.ku = ku0;
+        u.a = kUp ? tile0 / nj : ku0 / kg1;
+        u.j = kUp ? tile0 % nj : tile0;
+        u.kb = kUp ? ku0 : ku0 % kg1;
+        return u;
+    };
+    auto step = [&](Unit &u) {
+        if (kUp) {
+            u.kb = ++u.ku;
+            if (u.ku == kg) {
+                u.ku = u.kb = 0;
+                if (++u.j == nj) {
+                    u.j = 0;
+                    ++u.a;
+                }
+            }
+        } else {
+            ++u.ku;
+            if (++u.kb == kg1) {
+                u.kb = 0;
+                ++u.a;
+            }
+            if (u.ku == kg) {
+                u.ku = u.a = 0;
+                ++u.j;
+            }
+        }
+    };
+    // Weight tile of a unit (its t-th), counted in 128-row tiles from the start of the weights.
+    auto weight_tile = [&](const Unit &u, int t) {
+        const long long e = act[u.a];
+        return kUp ? e * 2 * nj + t * nj + u.j : e * nj + u.j;
+    };
+    auto unit_ok = [&](const Unit &u) {
+        return FP8BS_CHECK(u.a >= 0 && u.a < A && u.j >= 0 && u.j < nj && u.kb >= 0 && u.kb < kg1 && act[u.a] >= 0 &&
+                           act[u.a] < p.E);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint64_t pol_w = l2_policy_evict_first();
+            const uint64_t pol_b = l2_policy_evict_last();
+            uint32_t armed_mask = 0, armed_parity = 0;
+            auto load_w = [&](int s, const Unit &u) {
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t) {
+                    const long long wt = weight_tile(u, t);
+                    const int wx = p.w_tiled ? 0 : u.kb * 128;
+                    const int wy = static_cast<int>(p.w_tiled ? (wt * kg1 + u.kb) * 128 : wt * 128);
+                    tma_load_2d(ring + s * C::kStageBytes + t * C::kWBytes, &tm_w, &full[s], wx, wy, pol_w);
+                }
+            };
+            auto load_b = [&](int s, const Unit &u) {
+                tma_load_2d(ring + s * C::kStageBytes + C::kTiles * C::kWBytes, &tm_b, &full[s], u.kb * 128,
+                            kUp ? 0 : u.a * NPAD, pol_b);
+            };
+            Unit u = first_unit();
+            const int pre = nunits < S ? nunits : S;
+            for (int i = 0; i < pre; ++i, step(u)) {
+                if (i == p.test_skip_unit || !unit_ok(u))
+                    continue;
+                mbar_arrive_expect_tx(&full[i], C::kStageBytes);
+                armed_mask |= 1u << i;
+                load_w(i, u);
+            }
+            if (!kUp)
+                grid_dependency_wait(); // the intermediate
+            Unit ub = first_unit();
+            for (int i = 0; i < pre; ++i, step(ub))
+                if (armed_mask & (1u << i))
+                    load_b(i, ub);
+            int s = pre % S;
+            uint32_t ph = static_cast<uint32_t>(pre / S) & 1u;
+            bool triggered = false;
+            for (int i = pre; i < nunits; ++i) {
+                if (!triggered && i >= nunits - kTriggerLead) {
+                    grid_launch_dependents();
+                    triggered = true;
+                }
+                if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kErrTimeoutProducer, p.timeout_ns))
+                    break;
+                if (i != p.test_skip_unit && unit_ok(u)) {
+                    mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+                    armed_mask |= 1u << s;
+                    armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                    load_w(s, u);
+                    load_b(s, u);
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                step(u);
+            }
+            if (!triggered)
+                grid_launch_dependents();
+            // Nothing may still be landing in shared memory when the CTA exits.
+            for (int i = 0; i < S; ++i) {
+                if (!(armed_mask & (1u << i)))
+                    continue;
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_test(&full[i], (armed_parity >> i) & 1u)) {
+                    if (globaltimer_ns() - t0 > p.timeout_ns) {
+                        atomicOr(p.status, kErrTimeoutDrain);
+                        break;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int acc = 0, s = 0;
+            uint32_t acc_ph = 0, ph = 0;
+            for (int i = 0; i < nunits; ++i) {
+                if (!mbar_wait(&tempty[acc], acc_ph ^ 1u, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
+                    break;
+                if (!mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
+                    break;
+                tc_fence_after_sync();
+                const uint8_t *stage = ring + s * C::kStageBytes;
+                const uint64_t b_desc = sw128_kmajor_desc(smem_u32(stage + C::kTiles * C::kWBytes));
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t) {
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAccCols + t * NPAD);
+                    const uint64_t a_desc = sw128_kmajor_desc(smem_u32(stage + t * C::kWBytes));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f8f6f4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, C::kIdesc, k > 0 ? 1u : 0u);
+                }
+                mma_commit(&empty[s]);
+                mma_commit(&tfull[acc]);
+                if (++acc == C::kAcc) {
+                    acc = 0;
+                    acc_ph ^= 1u;
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            // every MMA complete before the tensor memory is released
+            mma_commit(mma_done);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_test(mma_done, 0)) {
+                if (globaltimer_ns() - t0 > p.timeout_ns) {
+                    atomicOr(p.status, kErrTimeoutDrain);
+                    break;
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------ promotion / epilogue
+        const int quarter = warp & 3; // TMEM lanes this warp may read
+        const int row = quarter * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        const int col0 = ((warp - 2) >> 2) * C::kCols; // this thread's token columns
+        const int mcnt = p.M - col0;                   // of them that exist (may exceed kCols)
+        float acc[C::kTiles][C::kCols];
+#pragma unroll
+        for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+            for (int m = 0; m < C::kCols; ++m)
+                acc[t][m] = 0.0f;
+        int accb = 0;
+        uint32_t acc_ph = 0;
+        Unit u = first_unit();
+        int tile = tile0, seg_first = ku0;
+        // Contributors of the (at most two) tiles this CTA shares, as in gemm_kernel.cuh.
+        struct SplitPlan {
+            int c_first, c_last, slot_first;
+        };
+        auto make_plan = [&](int t) {
+            const long long tf = static_cast<long long>(t) * kg;
+            SplitPlan sp;
+            sp.c_first = plan_owner(units, ctas, tf);
+            sp.c_last = plan_owner(units, ctas, tf + kg - 1);
+            sp.slot_first = 2 * sp.c_first + (plan_begin(units, ctas, sp.c_first) == tf ? 0 : 1);
+            return sp;
+        };
+        const int tile_b = has ? static_cast<int>((u0 + nunits - 1) / kg) : 0;
+        SplitPlan plan_a = {0, 0, 0}, plan_b = {0, 0, 0};
+        if (nunits > 0) {
+            plan_a = make_plan(tile0);
+            plan_b = tile_b != tile0 ? make_plan(tile_b) : plan_a;
+        }
+        if (!kUp)
+            grid_dependency_wait();
+        // Scales of the next unit to promote, loaded one unit ahead: the
+        // weight blocks', and this lane's token's.
+        float nx_w[C::kTiles], nx_a = 0.0f;
+        auto load_scales = [&](const Unit &v) {
+            if (!unit_ok(v))
+                return;
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t)
+                nx_w[t] = p.ws[weight_tile(v, t) * kg1 + v.kb];
+            nx_a = 0.0f;
+            if (lane < C::kCols && lane < mcnt)
+                nx_a = kUp ? __ldcg(p.xs + v.kb * p.M + col0 + lane)
+                           : __ldcg(p.hs + (static_cast<long long>(v.a) * kg1 + v.kb) * NPAD + col0 + lane);
+        };
+#pragma unroll
+        for (int t = 0; t < C::kTiles; ++t)
+            nx_w[t] = 0.0f;
+        if (nunits > 0)
+            load_scales(u);
+        float *const wprod = prod + (warp - 2) * 2 * C::kTiles * C::kCols;
+
+        // Finished sums of one output tile (thread = row `row` of it).
+        auto finish = [&]() {
+            if constexpr (!kUp) {
+                const int n = u.j * 128 + row;
+#pragma unroll
+                for (int m = 0; m < C::kCols; ++m)
+                    if (m < mcnt)
+                        p.y[static_cast<long long>(col0 + m) * p.H + n] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][m]));
+            } else {
+                // h in fp32, 0 for tokens that did not choose this expert;
+                // the scale is over the tile's 128 rows, which the four
+                // quarter warps of a column group hold
+                const float *wt = p.wtok + static_cast<long long>(act[u.a]) * NPAD + col0;
+                const float w_l = lane < C::kCols && lane < mcnt ? __ldcg(wt + lane) : 0.0f;
+                // (the 0 is written out, not multiplied in: an unchosen
+                // expert's sums may be infinite)
+                const uint32_t chosen = __ballot_sync(0xffffffffu, w_l != 0.0f);
+#pragma unroll
+                for (int m = 0; m < C::kCols; ++m) {
+                    const float g = acc[0][m];
+                    const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[1][m];
+                    acc[0][m] = (chosen >> m & 1u) ? h : 0.0f;
+                    const float am = warp_max(fabsf(acc[0][m]));
+                    if (lane == m)
+                        amax_x[quarter * NPAD + col0 + m] = am;
+                }
+                named_bar_sync(1, 32 * C::kEpiWarps);
+                const long long hrow = static_cast<long long>(u.a) * NPAD + col0;
+#pragma unroll
+                for (int m = 0; m < C::kCols; ++m) {
+                    if (m < mcnt) {
+                        const float *ax = amax_x + col0 + m;
+                        const float s = group_scale(fmaxf(fmaxf(ax[0], ax[NPAD]), fmaxf(ax[2 * NPAD], ax[3 * NPAD])));
+                        const float q = __fdiv_rn(acc[0][m], s);
+                        p.hq[(hrow + m) * p.I + u.j * 128 + row] = static_cast<uint8_t>(e4m3x4(q, 0.0f, 0.0f, 0.0f));
+                        if (quarter == 0 && lane == m)
+                            __stcg(p.hs + (static_cast<long long>(u.a) * nj + u.j) * NPAD + col0 + m, s * w_l);
+                    }
+                }
+                named_bar_sync(1, 32 * C::kEpiWarps); // amax_x may be written again
+            }
+        };
+
+        for (int i = 0; i < nunits; ++i) {
+            const bool seg_end = (i == nunits - 1) || (u.ku == kg - 1);
+            // s_w * s_a of this unit's tokens, per warp (double-buffered by
+            // parity: rewritten only after every lane passed the next __syncwarp)
+            float *pr = wprod + (i & 1) * C::kTiles * C::kCols;
+            if (lane < C::kCols) {
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t)
+                    pr[t * C::kCols + lane] = nx_w[t] * nx_a;
+            }
+            __syncwarp();
+            Unit nu = u;
+            step(nu);
+            if (i + 1 < nunits)
+                load_scales(nu);
+            mbar_wait(&tfull[accb], acc_ph, abort_flag, p.status, kErrTimeoutEpilogue, p.timeout_ns);
+            // (a wait that gave up carries on in bounds, as in gemm_kernel.cuh)
+            tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + lane_addr + static_cast<uint32_t>(accb * C::kAccCols + col0);
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) {
+                uint32_t r[C::kCols];
+                tmem_issue(taddr + t * NPAD, r);
+                tmem_wait(r);
+#pragma unroll
+                for (int q = 0; q < C::kCols / 4; ++q) {
+                    const float4 sc = reinterpret_cast<const float4 *>(pr + t * C::kCols)[q];
+                    fma2(acc[t][4 * q], acc[t][4 * q + 1], sc.x, sc.y, __uint_as_float(r[4 * q]),
+                         __uint_as_float(r[4 * q + 1]));
+                    fma2(acc[t][4 * q + 2], acc[t][4 * q + 3], sc.z, sc.w, __uint_as_float(r[4 * q + 2]),
+                         __uint_as_float(r[4 * q + 3]));
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&tempty[accb]);
+            if (++accb == C::kAcc) {
+                accb = 0;
+                acc_ph ^= 1u;
+            }
+            if (seg_end) {
+                if (seg_first == 0 && u.ku == kg - 1) {
+                    finish();
+                } else {
+                    // shared tile: publish this CTA's partial; the last
+                    // contributor to arrive sums all of them in order
+                    const SplitPlan &pl = tile == tile0 ? plan_a : plan_b;
+                    auto slot_of = [&](int c) { return c == pl.c_first ? pl.slot_first : 2 * c; };
+                    const bool ex_ok =
+                        FP8BS_CHECK(pl.c_first >= 0 && pl.c_first <= cta && cta <= pl.c_last && pl.c_last < ctas &&
+                                    slot_of(cta) < 2 * static_cast<int>(gridDim.x) && tile >= 0 && tile < tiles);
+                    constexpr int kSlot = C::kTiles * NPAD * 128;
+                    float *mine = p.slots + static_cast<long long>(slot_of(cta)) * kSlot + col0 * 128 + row;
+#pragma unroll
+                    for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                        for (int m = 0; m < C::kCols; ++m)
+                            if (m < mcnt && ex_ok)
+                                __stcg(mine + (t * NPAD + m) * 128, acc[t][m]);
+                    named_bar_sync(1, 32 * C::kEpiWarps);
+                    if (warp == 2 && lane == 0) {
+                        const unsigned prev = ex_ok ? atomic_add_acq_rel_gpu(&p.counters[tile], 1u) : 0u;
+                        *last_flag = (ex_ok && prev == static_cast<unsigned>(pl.c_last - pl.c_first)) ? 1 : 0;
+                    }
+                    named_bar_sync(1, 32 * C::kEpiWarps);
+                    if (*last_flag) {
+#pragma unroll
+                        for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                            for (int m = 0; m < C::kCols; ++m)
+                                acc[t][m] = 0.0f;
+                        for (int c = pl.c_first; c <= pl.c_last; ++c) {
+                            const float *src = p.slots + static_cast<long long>(slot_of(c)) * kSlot + col0 * 128 + row;
+                            float v[C::kTiles][C::kCols];
+#pragma unroll
+                            for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                                for (int m = 0; m < C::kCols; ++m)
+                                    v[t][m] = m < mcnt ? __ldcg(src + (t * NPAD + m) * 128) : 0.0f;
+#pragma unroll
+                            for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                                for (int m = 0; m < C::kCols; ++m)
+                                    acc[t][m] += v[t][m];
+                        }
+                        finish();
+                        if (warp == 2 && lane == 0)
+                            p.counters[tile] = 0u; // ready for the next call
+                    }
+                    named_bar_sync(1, 32 * C::kEpiWarps); // last_flag may be written again
+                }
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                    for (int m = 0; m < C::kCols; ++m)
+                        acc[t][m] = 0.0f;
+                ++tile;
+                seg_first = 0;
+            }
+            u = nu;
+        }
+        // No token chose any expert: the layer's output is zero.
+        if (!kUp && A == 0) {
+            const long long n = static_cast<long long>(p.M) * p.H;
+            for (long long i = static_cast<long long>(cta) * (32 * C::kEpiWarps) + (threadIdx.x - 64); i < n;
+                 i += static_cast<long long>(gridDim.x) * (32 * C::kEpiWarps))
+                p.y[i] = 0;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, C::kTmemCols);
+    }
+}
+
+template <int NPAD, int PHASE>
+fp8bs_status launch_moe_gemm(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev)
+{
+    using C = MoeCfg<NPAD, PHASE>;
+    static unsigned long long attr_done = 0;
+    constexpr bool kUp = PHASE == kMoeUp;
+    constexpr int kSmemLimit = 227 * 1024;
+    auto kernel = moe_gemm_kernel<NPAD, PHASE>;
+    int stages = (C::kMinBlocks == 2 ? 104 * 1024 : 204 * 1024) / C::kStageBytes;
+    stages = stages > C::kMaxStages ? C::kMaxStages : stages;
+    const int smem = C::smem_bytes(stages);
+    fp8bs_status st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kSmemLimit, dev.device, &attr_done);
+    if (st != FP8BS_OK)
+        return st;
+    const int max_active = L.E < L.M * L.top_k ? L.E : L.M * L.top_k;
+    const uint64_t rows = static_cast<uint64_t>(L.E) * (kUp ? 2 * L.I : L.H);
+    const uint64_t cols = static_cast<uint64_t>(kUp ? L.H : L.I);
+    CUtensorMap tm_w, tm_b;
+    const void *wp = kUp ? L.w13 : L.w2;
+    if (L.flags & FP8BS_FLAG_WEIGHTS_TILED)
+        st = make_tmap_2d(&tm_w, wp, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows / 128 * cols, 128, 128, 128, 128);
+    else
+        st = make_tmap_2d(&tm_w, wp, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, cols, cols, 128, 128);
+    if (st == FP8BS_OK)
+        st = kUp ? make_tmap_2d(&tm_b, L.workspace + w.xq_off, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
+                                static_cast<uint64_t>(L.M), cols, cols, 128, NPAD)
+                 : make_tmap_2d(&tm_b, L.workspace + w.hq_off, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
+                                static_cast<uint64_t>(max_active) * NPAD, cols, cols, 128, NPAD);
+    if (st != FP8BS_OK)
+        return st;
+    MoeGemmParams p = {};
+    p.M = L.M;
+    p.H = L.H;
+    p.I = L.I;
+    p.E = L.E;
+    p.stages = stages;
+    p.active = reinterpret_cast<const int *>(L.workspace + w.active_off);
+    p.wtok = reinterpret_cast<const float *>(L.workspace + w.wtok_off);
+    p.ws = kUp ? L.s13 : L.s2;
+    p.xs = reinterpret_cast<const float *>(L.workspace + w.xs_off);
+    p.hq = L.workspace + w.hq_off;
+    p.hs = reinterpret_cast<float *>(L.workspace + w.hs_off);
+    p.y = static_cast<uint16_t *>(L.y);
+    p.status = reinterpret_cast<unsigned *>(L.workspace);
+    p.counters = reinterpret_cast<unsigned *>(L.workspace + (kUp ? w.counters_up_off : w.counters_down_off));
+    p.slots = reinterpret_cast<float *>(L.workspace + w.slots_off);
+    p.w_tiled = (L.flags & FP8BS_FLAG_WEIGHTS_TILED) ? 1 : 0;
+    p.max_active = max_active;
+    p.test_skip_unit = L.test_skip_unit;
+    p.timeout_ns = L.timeout_ns;
+    p.runs = dev.runs;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.sms), 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1; // follows this layer's own kernel, and waits for it
+    return launch_status(cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_b, p));
+}
+
+template <int PHASE> fp8bs_status launch_moe_phase(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev)
+{
+    switch (moe_token_pad(L.M)) {
+    case 16:
+        return launch_moe_gemm<16, PHASE>(L, w, dev);
+    case 32:
+        return launch_moe_gemm<32, PHASE>(L, w, dev);
+    default:
+        return launch_moe_gemm<64, PHASE>(L, w, dev);
+    }
+}
+
+} // namespace fp8bs

@@ -327,6 +327,62 @@ FP8BS_API fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, c
                                    size_t workspace_bytes, unsigned flags, void *stream);
 
 /*
+ * A mixture-of-experts layer for a few tokens (a decode or speculative-verify
+ * batch, M = 1..64), its experts in E4M3 with one fp32 scale per 128x128 block:
+ *   l[m,e]  = sum_h x[m,h] * wr[e,h]                       (fp32)
+ *   ids[m]  = the top_k experts of largest l, in descending order, ties to the
+ *             lowest expert (a NaN logit orders below every number)
+ *   w[m,j]  = exp(l_j - l_max) / sum exp(l - l_max), the sum over the chosen
+ *             experts (renormalize != 0) or over all E
+ *   a       = fp8_quant_act(x)
+ *   g, u    = rows 0..I-1 and I..2I-1 of W13[e] . a   (promoted per 128-wide K
+ *             block by s_a * s_w into fp32, as fp8_blockscaled_gemm)
+ *   h       = g / (1 + exp(-g)) * u in fp32, cast per 128 of I as
+ *             fp8_quant_act casts (scale fl32(amax/448), 1 for zeros), without
+ *             a rounding to bf16 in between
+ *   y[m]    = bf16_rn( sum over the chosen e of w * W2[e] . h )   (fp32; the
+ *             weight multiplies the scale of h)
+ * Only the active experts' weights are read, each byte once.  Bitwise
+ * reproducible: no sum's order depends on timing.  A token with NaN or
+ * infinite values gives NaN in its own row of y only.
+ *
+ * x: bf16 [M][ldx], 16-byte aligned, ldx % 8 == 0, ldx >= H.
+ * wr: router weights fp32 or bf16 [E][H], 16-byte aligned.
+ * w13: E4M3 [E][2I][H], w2: E4M3 [E][H][I], 16-byte aligned; with
+ *   FP8BS_FLAG_WEIGHTS_TILED in the layout fp8_quant_weight_blocks_tiled writes
+ *   for the matrices [E * 2I][H] and [E * H][I].  s13: fp32 [E * 2I/128][H/128],
+ *   s2: fp32 [E * H/128][I/128].
+ * ids: int32 [M][top_k], weights: fp32 [M][top_k].  moe_route and fp8_moe_layer
+ *   write them (fp8_moe_layer: either may be NULL); fp8_moe_experts reads them:
+ *   an id outside [0, E) is skipped (a token with no expert left gets zeros),
+ *   an expert named twice by a token gets the sum of both weights, and a weight
+ *   of 0 counts as not chosen.
+ * y: bf16 [M][H], 2-byte aligned.
+ * 1 <= M <= 64, 1 <= E <= 512, 1 <= top_k <= min(16, E), H and I multiples of
+ * 128, E * 2I * H below 2^38.
+ * workspace: 256-byte aligned, of moe_route_workspace_size (moe_route alone) or
+ * fp8_moe_workspace_size; the same contract as the GEMMs' workspace (zero-filled
+ * once, clean after every call, one call at a time; fp8bs_workspace_status
+ * reports a time-out).
+ * flags: FP8BS_FLAG_OVERLAP_PREV (the layer's first kernel may be set up while
+ * the previous kernel on the stream finishes; it waits for it before reading
+ * anything) and, for the layers, FP8BS_FLAG_WEIGHTS_TILED.
+ */
+FP8BS_API fp8bs_status moe_route_workspace_size(int M, int E, size_t *bytes);
+FP8BS_API fp8bs_status moe_route(const void *x, int ldx, const void *wr, fp8bs_dtype wr_type, int M, int H, int E,
+                                 int top_k, int renormalize, int32_t *ids, float *weights, void *workspace,
+                                 size_t workspace_bytes, unsigned flags, void *stream);
+FP8BS_API fp8bs_status fp8_moe_workspace_size(int M, int H, int I, int E, int top_k, size_t *bytes);
+FP8BS_API fp8bs_status fp8_moe_experts(const void *x, int ldx, const int32_t *ids, const float *weights,
+                                       const uint8_t *w13, const float *s13, const uint8_t *w2, const float *s2,
+                                       void *y, int M, int H, int I, int E, int top_k, void *workspace,
+                                       size_t workspace_bytes, unsigned flags, void *stream);
+FP8BS_API fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8bs_dtype wr_type, int renormalize,
+                                     const uint8_t *w13, const float *s13, const uint8_t *w2, const float *s2, void *y,
+                                     int32_t *ids, float *weights, int M, int H, int I, int E, int top_k,
+                                     void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
  * Microscaled 4-bit floating point: E2M1 weights and activations (magnitudes
  * 0, 0.5, 1, 1.5, 2, 3, 4, 6) with block scales that the tensor core applies
  * (tcgen05.mma kind::mxf4nvf4 / kind::mxf4, block_scale).  Two formats:

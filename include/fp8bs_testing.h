@@ -37,6 +37,11 @@ extern "C" {
  * the instantiation with the greedy-choice epilogue. */
 #define FP8BS_RUNS_NPAD_INDEX(npad) ((npad) <= 64 ? (npad) / 16 - 1 : (npad) == 128 ? 4 : 5)
 #define FP8BS_RUNS_GEMM(mode, npad, greedy) (8 + (mode) * 16 + FP8BS_RUNS_NPAD_INDEX(npad) * 2 + (greedy))
+/* Expert layer: routing, the plan of a given choice, and the grouped
+ * products (phase 0 = gate/up, 1 = down; npad 16, 32 or 64). */
+#define FP8BS_RUNS_MOE_ROUTE 88
+#define FP8BS_RUNS_MOE_PLAN 89
+#define FP8BS_RUNS_MOE_GEMM(phase, npad) (90 + (phase) * 3 + ((npad) == 16 ? 0 : (npad) == 32 ? 1 : 2))
 #define FP8BS_RUNS_SLOTS 128
 
 /*
