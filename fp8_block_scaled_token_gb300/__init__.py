@@ -146,9 +146,15 @@ def _check(fn, code):
 
 
 # ---------------------------------------------------------------- helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 # The helpers below run on every call: an eager decode pass makes hundreds of
@@ -172,6 +178,8 @@ def _ptr(t):
 
 def _need(t, dtype, name, ndim=2):
     torch = _torch()
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.dim() == ndim:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:

@@ -25,7 +25,7 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     w.hq_off = w.xs_off + up256(static_cast<size_t>(M) * (H / 128) * 4);
     w.hs_off = w.hq_off + up256(active * npad * I);
     w.slots_off = w.hs_off + up256(active * (I / 128) * npad * 4);
-    w.total = w.slots_off + static_cast<size_t>(2) * sms * 2 * npad * 128 * 4;
+    w.total = w.slots_off + static_cast<size_t>(3) * sms * 2 * npad * 128 * 4;
     return w;
 }
 

@@ -28,7 +28,7 @@ struct MoeWorkspace {
     size_t wtok_off;          // [E][NPAD] weight of each token for each expert, 0 where not chosen
     size_t xq_off, xs_off;    // activations: codes [M][H], scales [H/128][M]
     size_t hq_off, hs_off;    // intermediate: codes [active][NPAD][I], scales times weights [active][I/128][NPAD]
-    size_t slots_off;         // K-split partials, [2 * SMs][2][NPAD * 128] fp32
+    size_t slots_off;         // partials, [3 * SMs][2][NPAD * 128] fp32
     size_t total;
 };
 

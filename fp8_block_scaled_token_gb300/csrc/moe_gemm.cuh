@@ -52,7 +52,7 @@ struct MoeGemmParams {
     float *hs;             // scales times weights, [active][I/128][NPAD]: up writes, down reads
     uint16_t *y;           // down: bf16 [M][H]
     unsigned *status, *counters;
-    float *slots;          // [2 * grid][tiles a unit][NPAD * 128]
+    float *slots;          // [2 * grid (up: 3 * grid)][tiles a unit][NPAD * 128]
     int w_tiled;
     int max_active;
     int test_skip_unit;
@@ -81,8 +81,7 @@ template <int NPAD, int PHASE> struct MoeCfg {
     static constexpr int kEpiWarps = 4 * kColGroups;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
     static constexpr int kMaxRegs = kMinBlocks == 2 ? 160 : kEpiWarps == 4 ? 255 : 168;
-    // barriers and flags, [1024, 3072) active experts, [3072, 4096) amax exchange
-    static constexpr int kHeader = 4096;
+    static constexpr int kHeader = 3072; // barriers and flags, then [1024, 3072) the active experts
     static constexpr int kProdFloats = kEpiWarps * 2 * kTiles * kCols; // per warp, by unit parity
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(128, NPAD);
     static_assert((2 * kMaxStages + 2 * kAcc + 1) * 8 + 12 <= 1024, "header layout");
@@ -112,7 +111,6 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
     int *act = reinterpret_cast<int *>(smem + 1024);            // [kMoeMaxExperts]
-    float *amax_x = reinterpret_cast<float *>(smem + 3072);     // [4][NPAD]
     const int S = p.stages;
     uint8_t *ring = smem + C::kHeader;
     float *prod = reinterpret_cast<float *>(ring + S * C::kStageBytes);
@@ -387,48 +385,108 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         if (nunits > 0)
             load_scales(u);
         float *const wprod = prod + (warp - 2) * 2 * C::kTiles * C::kCols;
+        // up: the tokens' weights for the unit's expert, this lane's tokens
+        // lane and lane + 32; read when the expert changes, used at a tile's end
+        float w_tok[2] = {0.0f, 0.0f};
+        auto load_weights = [&](int a) {
+            const float *wt = p.wtok + static_cast<long long>(act[a]) * NPAD;
+#pragma unroll
+            for (int q = 0; q < (NPAD + 31) / 32; ++q)
+                w_tok[q] = lane + 32 * q < p.M ? __ldcg(wt + lane + 32 * q) : 0.0f;
+        };
+        if (kUp && nunits > 0 && unit_ok(u))
+            load_weights(u.a);
 
-        // Finished sums of one output tile (thread = row `row` of it).
-        auto finish = [&]() {
-            if constexpr (!kUp) {
-                const int n = u.j * 128 + row;
+        // down: finished sums of one output tile (thread = row `row` of it)
+        auto store_y = [&]() {
+            const int n = u.j * 128 + row;
 #pragma unroll
-                for (int m = 0; m < C::kCols; ++m)
-                    if (m < mcnt)
-                        p.y[static_cast<long long>(col0 + m) * p.H + n] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][m]));
-            } else {
-                // h in fp32, 0 for tokens that did not choose this expert;
-                // the scale is over the tile's 128 rows, which the four
-                // quarter warps of a column group hold
-                const float *wt = p.wtok + static_cast<long long>(act[u.a]) * NPAD + col0;
-                const float w_l = lane < C::kCols && lane < mcnt ? __ldcg(wt + lane) : 0.0f;
-                // (the 0 is written out, not multiplied in: an unchosen
-                // expert's sums may be infinite)
-                const uint32_t chosen = __ballot_sync(0xffffffffu, w_l != 0.0f);
-#pragma unroll
-                for (int m = 0; m < C::kCols; ++m) {
-                    const float g = acc[0][m];
-                    const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[1][m];
-                    acc[0][m] = (chosen >> m & 1u) ? h : 0.0f;
-                    const float am = warp_max(fabsf(acc[0][m]));
-                    if (lane == m)
-                        amax_x[quarter * NPAD + col0 + m] = am;
-                }
-                named_bar_sync(1, 32 * C::kEpiWarps);
-                const long long hrow = static_cast<long long>(u.a) * NPAD + col0;
-#pragma unroll
-                for (int m = 0; m < C::kCols; ++m) {
-                    if (m < mcnt) {
-                        const float *ax = amax_x + col0 + m;
-                        const float s = group_scale(fmaxf(fmaxf(ax[0], ax[NPAD]), fmaxf(ax[2 * NPAD], ax[3 * NPAD])));
-                        const float q = __fdiv_rn(acc[0][m], s);
-                        p.hq[(hrow + m) * p.I + u.j * 128 + row] = static_cast<uint8_t>(e4m3x4(q, 0.0f, 0.0f, 0.0f));
-                        if (quarter == 0 && lane == m)
-                            __stcg(p.hs + (static_cast<long long>(u.a) * nj + u.j) * NPAD + col0 + m, s * w_l);
+            for (int m = 0; m < C::kCols; ++m)
+                if (m < mcnt)
+                    p.y[static_cast<long long>(col0 + m) * p.H + n] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(acc[0][m]));
+        };
+        // up: one pair of tiles from its contributors' partials in the slots:
+        // h, its scale and codes, a warp a token (128 rows, four a lane).  The
+        // chosen tokens are dealt to the warps in turn, two at a time; the
+        // others get zero codes (written, not multiplied in: an unchosen
+        // expert's sums may be infinite).  The loops stay rolled: this code
+        // runs once or twice a CTA, and unrolled over the tokens its
+        // instruction fetches alone took 11 us.
+        constexpr int kSlot = C::kTiles * NPAD * 128;
+        auto finish_up = [&](int c_first, int c_last, int slot_first) {
+            const int ew = warp - 2;
+            unsigned long long chosen = __ballot_sync(0xffffffffu, w_tok[0] != 0.0f);
+            if constexpr (NPAD > 32)
+                chosen |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, w_tok[1] != 0.0f)) << 32;
+            const long long hrow = static_cast<long long>(u.a) * NPAD;
+            float *const hs = p.hs + (static_cast<long long>(u.a) * nj + u.j) * NPAD;
+            uint8_t *const hq = p.hq + hrow * p.I + u.j * 128 + 4 * lane;
+#pragma unroll 1
+            for (int m = ew; m < p.M; m += C::kEpiWarps) {
+                if (chosen >> m & 1ull)
+                    continue;
+                *reinterpret_cast<uint32_t *>(hq + static_cast<long long>(m) * p.I) = 0u;
+                if (lane == 0)
+                    __stcg(hs + m, 0.0f);
+            }
+            // the warp's chosen tokens: numbers ew, ew + kEpiWarps, ... of the set bits
+            int rank = 0;
+#pragma unroll 1
+            while (chosen != 0ull) {
+                int m0 = -1, m1 = -1;
+#pragma unroll 1
+                while (chosen != 0ull && m1 < 0) {
+                    const int m = __ffsll(static_cast<long long>(chosen)) - 1;
+                    chosen &= chosen - 1ull;
+                    if (rank++ % C::kEpiWarps == ew) {
+                        if (m0 < 0)
+                            m0 = m;
+                        else
+                            m1 = m;
                     }
                 }
-                named_bar_sync(1, 32 * C::kEpiWarps); // amax_x may be written again
+                if (m0 < 0)
+                    break;
+                const int n = m1 < 0 ? 1 : 2;
+                float4 g[2], uu[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    g[b] = uu[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+                for (int c = c_first; c <= c_last; ++c) {
+                    const float *src = p.slots + static_cast<long long>(c == c_first ? slot_first : 2 * c) * kSlot + 4 * lane;
+                    float4 vg[2], vu[2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int m = b == 0 || n == 1 ? m0 : m1;
+                        vg[b] = __ldcg(reinterpret_cast<const float4 *>(src + m * 128));
+                        vu[b] = __ldcg(reinterpret_cast<const float4 *>(src + (NPAD + m) * 128));
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        add2(g[b].x, g[b].y, vg[b].x, vg[b].y);
+                        add2(g[b].z, g[b].w, vg[b].z, vg[b].w);
+                        add2(uu[b].x, uu[b].y, vu[b].x, vu[b].y);
+                        add2(uu[b].z, uu[b].w, vu[b].z, vu[b].w);
+                    }
+                }
+#pragma unroll 1
+                for (int b = 0; b < n; ++b) {
+                    const int m = b ? m1 : m0;
+                    float h[4] = {b ? g[1].x : g[0].x, b ? g[1].y : g[0].y, b ? g[1].z : g[0].z, b ? g[1].w : g[0].w};
+                    const float up[4] = {b ? uu[1].x : uu[0].x, b ? uu[1].y : uu[0].y, b ? uu[1].z : uu[0].z,
+                                         b ? uu[1].w : uu[0].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        h[q] = __fdiv_rn(h[q], 1.0f + expf(-h[q])) * up[q];
+                    const float s = group_scale(warp_max(abs_max4(h[0], h[1], h[2], h[3])));
+                    *reinterpret_cast<uint32_t *>(hq + static_cast<long long>(m) * p.I) =
+                        quantize4(h[0], h[1], h[2], h[3], s);
+                    const float w = __shfl_sync(0xffffffffu, NPAD > 32 && m >= 32 ? w_tok[1] : w_tok[0], m & 31);
+                    if (lane == 0)
+                        __stcg(hs + m, s * w);
+                }
             }
         };
 
@@ -474,17 +532,20 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                 acc_ph ^= 1u;
             }
             if (seg_end) {
-                if (seg_first == 0 && u.ku == kg - 1) {
-                    finish();
+                const bool whole = seg_first == 0 && u.ku == kg - 1;
+                if (!kUp && whole) {
+                    store_y();
                 } else {
                     // shared tile: publish this CTA's partial; the last
-                    // contributor to arrive sums all of them in order
-                    const SplitPlan &pl = tile == tile0 ? plan_a : plan_b;
+                    // contributor to arrive sums all of them in order (up:
+                    // also for a whole tile, by way of a slot of its own)
+                    SplitPlan pl = tile == tile0 ? plan_a : plan_b;
+                    if (kUp && whole)
+                        pl.c_first = pl.c_last = cta, pl.slot_first = 2 * static_cast<int>(gridDim.x) + cta;
                     auto slot_of = [&](int c) { return c == pl.c_first ? pl.slot_first : 2 * c; };
                     const bool ex_ok =
                         FP8BS_CHECK(pl.c_first >= 0 && pl.c_first <= cta && cta <= pl.c_last && pl.c_last < ctas &&
-                                    slot_of(cta) < 2 * static_cast<int>(gridDim.x) && tile >= 0 && tile < tiles);
-                    constexpr int kSlot = C::kTiles * NPAD * 128;
+                                    slot_of(cta) < (kUp ? 3 : 2) * static_cast<int>(gridDim.x) && tile >= 0 && tile < tiles);
                     float *mine = p.slots + static_cast<long long>(slot_of(cta)) * kSlot + col0 * 128 + row;
 #pragma unroll
                     for (int t = 0; t < C::kTiles; ++t)
@@ -493,12 +554,19 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                             if (m < mcnt && ex_ok)
                                 __stcg(mine + (t * NPAD + m) * 128, acc[t][m]);
                     named_bar_sync(1, 32 * C::kEpiWarps);
-                    if (warp == 2 && lane == 0) {
-                        const unsigned prev = ex_ok ? atomic_add_acq_rel_gpu(&p.counters[tile], 1u) : 0u;
-                        *last_flag = (ex_ok && prev == static_cast<unsigned>(pl.c_last - pl.c_first)) ? 1 : 0;
+                    if (!(kUp && whole)) {
+                        if (warp == 2 && lane == 0) {
+                            const unsigned prev = ex_ok ? atomic_add_acq_rel_gpu(&p.counters[tile], 1u) : 0u;
+                            *last_flag = (ex_ok && prev == static_cast<unsigned>(pl.c_last - pl.c_first)) ? 1 : 0;
+                        }
+                        named_bar_sync(1, 32 * C::kEpiWarps);
                     }
-                    named_bar_sync(1, 32 * C::kEpiWarps);
-                    if (*last_flag) {
+                    if (kUp && (whole || *last_flag)) {
+                        if (ex_ok)
+                            finish_up(pl.c_first, pl.c_last, pl.slot_first);
+                        if (warp == 2 && lane == 0 && !whole)
+                            p.counters[tile] = 0u; // ready for the next call
+                    } else if (!kUp && *last_flag) {
 #pragma unroll
                         for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
@@ -518,11 +586,11 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                                 for (int m = 0; m < C::kCols; ++m)
                                     acc[t][m] += v[t][m];
                         }
-                        finish();
+                        store_y();
                         if (warp == 2 && lane == 0)
-                            p.counters[tile] = 0u; // ready for the next call
+                            p.counters[tile] = 0u;
                     }
-                    named_bar_sync(1, 32 * C::kEpiWarps); // last_flag may be written again
+                    named_bar_sync(1, 32 * C::kEpiWarps); // last_flag and the whole tiles' slot may be written again
                 }
 #pragma unroll
                 for (int t = 0; t < C::kTiles; ++t)
@@ -531,6 +599,8 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                         acc[t][m] = 0.0f;
                 ++tile;
                 seg_first = 0;
+                if (kUp && i + 1 < nunits && nu.a != u.a && unit_ok(nu))
+                    load_weights(nu.a);
             }
             u = nu;
         }

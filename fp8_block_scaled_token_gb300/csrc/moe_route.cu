@@ -9,10 +9,13 @@
 //   w[m, j] = exp(l_j - l_max) / sum exp(l - l_max), the sum over the chosen
 //             experts (renormalised) or over all of them
 //
-// Grid: one CTA per (expert, group of 8 tokens), then one CTA per four (token,
+// Grid: one CTA per (expert, group of 8 tokens), then one CTA per eight (token,
 // 128 of H) groups of the cast.  The last CTA of a token group chooses for its
 // eight tokens, and the last group's CTA lists the active experts; arrivals
-// are counted, nobody waits.
+// are counted, nobody waits.  A few microseconds of latency, not bandwidth:
+// loads are issued for all eight tokens at once, and the choice keeps its
+// loops rolled (unrolled code run once costs more in instruction fetches than
+// it saves).
 #include <cuda_bf16.h>
 
 #include "fp8bs_testing.h"
@@ -22,9 +25,10 @@
 
 namespace fp8bs {
 
-constexpr int kRouteThreads = 128;
+constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kTG = kMoeTokenGroup;
+static_assert(kRouteWarps == kTG, "one warp chooses for each token of a group");
 
 struct RouteParams {
     int M, H, E, top_k, npad;
@@ -53,78 +57,75 @@ __device__ __forceinline__ uint32_t route_key(float v)
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// The active experts of the bit mask, ascending, and the mask back to zero
-// (one warp, after every bit is set).
-__device__ __forceinline__ void list_active(unsigned *mask, int E, int *active)
+// The active experts of the bit mask (this lane's word in `m`), ascending (one warp).
+__device__ __forceinline__ void list_active(unsigned m, int E, int *active)
 {
     const int lane = threadIdx.x & 31;
     const int words = (E + 31) / 32;
-    const unsigned m = lane < words ? atomicExch(mask + lane, 0u) : 0u;
     int before = 0, total = 0;
+#pragma unroll 1
     for (int i = 0; i < words; ++i) {
         const int c = __popc(__shfl_sync(0xffffffffu, m, i));
         before += i < lane ? c : 0;
         total += c;
     }
+#pragma unroll 1
     for (unsigned rest = m; rest != 0u; rest &= rest - 1u)
         active[1 + before++] = lane * 32 + __ffs(rest) - 1;
     if (lane == 0)
         active[0] = total;
 }
 
-// One warp: the choice for one token.
-__device__ __forceinline__ void choose(const RouteParams &p, int m)
+// One warp: the choice for token m; `l` its E logits, `mask` the experts' bit
+// mask (shared or global).
+__device__ __forceinline__ void choose(const RouteParams &p, int m, float *l, unsigned *mask)
 {
-    constexpr int kPer = kMoeMaxExperts / 32;
     const int lane = threadIdx.x & 31;
-    float l[kPer];
-    uint32_t key[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = i * 32 + lane;
-        l[i] = e < p.E ? __ldcg(p.logits + static_cast<long long>(m) * p.E + e) : 0.0f;
-        key[i] = e < p.E ? route_key(l[i]) : 0u;
-    }
-    float lmax = 0.0f, sum = 0.0f, mine_l = 0.0f;
-    int mine_e = -1;
-    unsigned taken = 0; // bit i: this lane's expert i * 32 + lane is chosen
-    for (int j = 0; j < p.top_k; ++j) {
-        // this lane's best remaining expert, then the warp's
-        uint32_t k = 0;
-        int e = 0x7fffffff;
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int ei = i * 32 + lane;
-            if (ei < p.E && !(taken >> i & 1u) && (e == 0x7fffffff || key[i] > k)) {
-                k = key[i];
-                e = ei;
-                v = l[i];
+    float mine_l = 0.0f, lmax = 0.0f;
+    int mine_e = 0;
+    // Each lane keeps the best of its experts lane, lane + 32, ... that are
+    // not taken yet (ties to the lowest); only the lane whose expert is taken
+    // looks again.
+    unsigned taken = 0; // bit i: expert 32 i + lane
+    uint32_t k = 0;
+    int e = 0x7fffffff;
+    auto look = [&]() {
+        k = 0;
+        e = 0x7fffffff;
+#pragma unroll 1
+        for (int i = 0; 32 * i + lane < p.E; ++i) {
+            const uint32_t key = route_key(l[32 * i + lane]);
+            if (!(taken >> i & 1u) && (e == 0x7fffffff || key > k)) {
+                k = key;
+                e = 32 * i + lane;
             }
         }
+    };
+    look();
+#pragma unroll 1
+    for (int j = 0; j < p.top_k; ++j) {
         const uint32_t kmax = __reduce_max_sync(0xffffffffu, k);
-        const uint32_t emin = __reduce_min_sync(0xffffffffu, k == kmax ? static_cast<uint32_t>(e) : 0xffffffffu);
-        const int owner = static_cast<int>(emin & 31u);
-        v = __shfl_sync(0xffffffffu, v, owner);
-        if (lane == owner)
-            taken |= 1u << (emin >> 5);
+        const int best = static_cast<int>(__reduce_min_sync(0xffffffffu, k == kmax ? static_cast<uint32_t>(e) : 0x7fffffffu));
+        const float v = l[best];
         if (j == 0)
             lmax = v;
         if (lane == j) {
-            mine_e = static_cast<int>(emin);
+            mine_e = best;
             mine_l = v;
         }
+        if (lane == (best & 31)) {
+            taken |= 1u << (best >> 5);
+            look();
+        }
     }
-    // p = exp(l - lmax); where the largest is infinite the difference is NaN,
-    // as the formula gives
+    // exp(l - lmax) / sum; an infinite largest logit gives NaN, as the formula does
     float pj = lane < p.top_k ? expf(mine_l - lmax) : 0.0f;
-    if (p.renorm) {
-        sum = pj;
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (i * 32 + lane < p.E)
-                sum += expf(l[i] - lmax);
+    float sum = pj;
+    if (!p.renorm) {
+        sum = 0.0f;
+#pragma unroll 1
+        for (int i = lane; i < p.E; i += 32)
+            sum += expf(l[i] - lmax);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -135,7 +136,7 @@ __device__ __forceinline__ void choose(const RouteParams &p, int m)
         p.topw[static_cast<long long>(m) * p.top_k + lane] = pj;
         if (p.wtok != nullptr) {
             p.wtok[static_cast<long long>(mine_e) * p.npad + m] = pj;
-            atomicOr(p.group_done + kMoeMaxTokens / kTG + 1 + (mine_e >> 5), 1u << (mine_e & 31));
+            atomicOr(mask + (mine_e >> 5), 1u << (mine_e & 31));
         }
     }
 }
@@ -161,6 +162,8 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
 {
     __shared__ float part[kRouteWarps][kTG];
     __shared__ unsigned arrived;
+    __shared__ unsigned smask[kMoeMaxExperts / 32];
+    __shared__ float logit[kTG][kMoeMaxExperts];
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(p.runs + FP8BS_RUNS_MOE_ROUTE, 1ull);
     grid_launch_dependents();
@@ -175,45 +178,55 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     const int e = blockIdx.x % p.E, tg = blockIdx.x / p.E;
     const int t0 = tg * kTG;
     const int nt = p.M - t0 < kTG ? p.M - t0 : kTG;
-    // the 128-value blocks of H, dealt to the warps in turn, four values a lane
+    // eight values of H a thread and step, all tokens' loads in flight at once
+    // (tokens past the last re-read it; their sums are not used)
     float acc[kTG];
 #pragma unroll
     for (int t = 0; t < kTG; ++t)
         acc[t] = 0.0f;
-    for (int h = warp * 128 + lane * 4; h < p.H; h += kRouteThreads * 4) {
-        float w[4];
+    const uint16_t *const x0 = p.x + static_cast<long long>(t0) * p.ldx;
+#pragma unroll 1
+    for (int h = threadIdx.x * 8; h < p.H; h += kRouteThreads * 8) {
+        float w[8];
         if (kBf16) {
-            const uint2 r = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.wr) +
+            const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.wr) +
                                                              static_cast<long long>(e) * p.H + h);
-            w[0] = bf16_lo(r.x);
-            w[1] = bf16_hi(r.x);
-            w[2] = bf16_lo(r.y);
-            w[3] = bf16_hi(r.y);
+            const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[2 * i] = bf16_lo(rw[i]);
+                w[2 * i + 1] = bf16_hi(rw[i]);
+            }
         } else {
-            const float4 r = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.wr) +
+            const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.wr) +
                                                                static_cast<long long>(e) * p.H + h);
-            w[0] = r.x;
-            w[1] = r.y;
-            w[2] = r.z;
-            w[3] = r.w;
+            const float4 a = r[0], b = r[1];
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+            w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
         }
+        uint4 xr[kTG];
+#pragma unroll
+        for (int t = 0; t < kTG; ++t)
+            xr[t] = *reinterpret_cast<const uint4 *>(x0 + static_cast<long long>(t < nt ? t : nt - 1) * p.ldx + h);
 #pragma unroll
         for (int t = 0; t < kTG; ++t) {
-            if (t < nt) {
-                const uint2 r = *reinterpret_cast<const uint2 *>(p.x + static_cast<long long>(t0 + t) * p.ldx + h);
-                acc[t] = fmaf(bf16_lo(r.x), w[0], acc[t]);
-                acc[t] = fmaf(bf16_hi(r.x), w[1], acc[t]);
-                acc[t] = fmaf(bf16_lo(r.y), w[2], acc[t]);
-                acc[t] = fmaf(bf16_hi(r.y), w[3], acc[t]);
+            const uint32_t xw[4] = {xr[t].x, xr[t].y, xr[t].z, xr[t].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[t] = fmaf(bf16_lo(xw[i]), w[2 * i], acc[t]);
+                acc[t] = fmaf(bf16_hi(xw[i]), w[2 * i + 1], acc[t]);
             }
         }
     }
 #pragma unroll
-    for (int t = 0; t < kTG; ++t) {
+    for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int t = 0; t < kTG; ++t)
             acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-        if (lane == 0)
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int t = 0; t < kTG; ++t)
             part[warp][t] = acc[t];
     }
     __syncthreads();
@@ -229,26 +242,43 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     __syncthreads();
     if (threadIdx.x == 0)
         arrived = atomic_add_acq_rel_gpu(p.group_done + tg, 1u);
+    if (threadIdx.x < kMoeMaxExperts / 32)
+        smask[threadIdx.x] = 0u;
     __syncthreads();
     if (arrived != static_cast<unsigned>(p.E - 1))
         return;
     __threadfence(); // the other CTAs' logits and zeroed weights, for every thread of this one
-    for (int t = warp; t < nt; t += kRouteWarps)
-        choose(p, t0 + t);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        p.group_done[tg] = 0u;
-        __threadfence();
-        arrived = p.wtok != nullptr ? atomic_add_acq_rel_gpu(p.group_done + kMoeMaxTokens / kTG, 1u) : 0xffffffffu;
+    // one group of tokens: the mask stays in shared memory
+    unsigned *const gmask = p.group_done + kMoeMaxTokens / kTG + 1;
+    unsigned *const mask = groups == 1 ? smask : gmask;
+    if (warp < nt) {
+        float *const l = logit[warp];
+        for (int i = lane; i < p.E; i += 32)
+            l[i] = __ldcg(p.logits + static_cast<long long>(t0 + warp) * p.E + i);
+        __syncwarp();
+        choose(p, t0 + warp, l, mask);
     }
-    __syncthreads();
-    if (arrived != static_cast<unsigned>(groups - 1) || p.wtok == nullptr)
-        return;
-    __threadfence();
-    if (warp == 0)
-        list_active(p.group_done + kMoeMaxTokens / kTG + 1, p.E, p.active);
     if (threadIdx.x == 0)
-        p.group_done[kMoeMaxTokens / kTG] = 0u;
+        p.group_done[tg] = 0u;
+    __syncthreads();
+    if (p.wtok == nullptr)
+        return;
+    if (groups > 1) {
+        if (threadIdx.x == 0) {
+            __threadfence();
+            arrived = atomic_add_acq_rel_gpu(p.group_done + kMoeMaxTokens / kTG, 1u);
+        }
+        __syncthreads();
+        if (arrived != static_cast<unsigned>(groups - 1))
+            return;
+        __threadfence();
+        if (threadIdx.x == 0)
+            p.group_done[kMoeMaxTokens / kTG] = 0u;
+    }
+    if (warp == 0) {
+        const bool word = lane < (p.E + 31) / 32;
+        list_active(!word ? 0u : groups == 1 ? smask[lane] : atomicExch(gmask + lane, 0u), p.E, p.active);
+    }
 }
 
 // The same bookkeeping for a choice that the caller made: one CTA per expert
@@ -291,8 +321,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_plan_kernel(const RoutePara
     if (arrived != static_cast<unsigned>(p.E - 1))
         return;
     __threadfence();
-    if (warp == 0)
-        list_active(p.group_done + kMoeMaxTokens / kTG + 1, p.E, p.active);
+    if (warp == 0) {
+        unsigned *mask = p.group_done + kMoeMaxTokens / kTG + 1;
+        const int lane = threadIdx.x & 31;
+        list_active(lane < (p.E + 31) / 32 ? atomicExch(mask + lane, 0u) : 0u, p.E, p.active);
+    }
     if (threadIdx.x == 0)
         p.group_done[0] = 0u;
 }
