@@ -481,14 +481,17 @@ def _router(x, wr):
     torch = _torch()
     _need(x, torch.bfloat16, "x")
     _rows_contiguous(x, "x")
-    if wr.dtype not in (torch.float32, torch.bfloat16):
+    wt = wr.dtype
+    if wt is not torch.bfloat16 and wt is not torch.float32:
         raise TypeError("wr must be float32 or bfloat16")
-    _need(wr, wr.dtype, "wr")
+    _need(wr, wt, "wr")
     if not wr.is_contiguous():
         raise ValueError("wr must be contiguous")
-    if wr.shape[1] != x.shape[1]:
+    M, H = x.shape
+    E, Hr = wr.shape
+    if H != Hr:
         raise ValueError("operand shapes do not agree")
-    return x.shape[0], x.shape[1], wr.shape[0], BF16 if wr.dtype == torch.bfloat16 else F32
+    return M, H, E, BF16 if wt is torch.bfloat16 else F32
 
 
 def _experts(w13, s13, w2, s2, H, E):
@@ -496,27 +499,28 @@ def _experts(w13, s13, w2, s2, H, E):
     or both tiled [tiles, 128, 128]; E (None: from a row-major w13) settles the
     tiled form."""
     torch = _torch()
-    for t, nm in ((w13, "w13"), (w2, "w2")):
-        _need(t, torch.uint8, nm, ndim=3)
-    for t, nm in ((s13, "s13"), (s2, "s2")):
-        _need(t, torch.float32, nm)
-    for t, nm in ((w13, "w13"), (w2, "w2"), (s13, "s13"), (s2, "s2")):
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % nm)
+    _need(w13, torch.uint8, "w13", 3)
+    _need(w2, torch.uint8, "w2", 3)
+    _need(s13, torch.float32, "s13")
+    _need(s2, torch.float32, "s2")
+    if not (w13.is_contiguous() and w2.is_contiguous() and s13.is_contiguous() and s2.is_contiguous()):
+        raise ValueError("w13, s13, w2 and s2 must be contiguous")
     kg = H // 128
+    shape13, shape2 = w13.shape, w2.shape
     if E is None:
-        if w13.shape[2] != H:
+        if shape13[2] != H:
             raise ValueError("w13 is tiled: pass experts= (the number of experts)")
-        E = w13.shape[0]
+        E = shape13[0]
     E = int(E)
-    rows = s13.shape[0] // (2 * E) if E > 0 else 0  # 128-row tiles of I
+    rows, kg2 = s2.shape[1], s2.shape[0]  # rows: 128-row tiles of I
     I = rows * 128
-    if rows < 1 or tuple(s13.shape) != (2 * E * rows, kg) or tuple(s2.shape) != (E * kg, rows):
+    if rows < 1 or E < 1 or kg2 != E * kg or s13.shape != (2 * E * rows, kg):
         raise ValueError("operand shapes do not agree")
-    if tuple(w13.shape) == (E, 2 * I, H) and tuple(w2.shape) == (E, H, I):
-        return E, I, 0
-    if tuple(w13.shape) == (2 * E * rows * kg, 128, 128) and tuple(w2.shape) == (E * kg * rows, 128, 128):
+    tiles = E * rows * kg
+    if shape13 == (2 * tiles, 128, 128) and shape2 == (tiles, 128, 128):
         return E, I, FLAG_WEIGHTS_TILED
+    if shape13 == (E, 2 * I, H) and shape2 == (E, H, I):
+        return E, I, 0
     raise ValueError("operand shapes do not agree")
 
 
@@ -599,24 +603,27 @@ def _fp4_atoms(fmt):
 def _fp4_operand(codes, atoms, rows, n_codes, n_atoms, n_rows, what):
     """Checks of one packed 4-bit operand (rows may be None: all 1, FP4_MX only)."""
     torch = _torch()
-    _need(codes, torch.uint8, what, ndim=codes.dim())
-    _need(atoms, torch.uint8, what + " scale atoms", ndim=atoms.dim())
-    if rows is not None:
-        _need(rows, torch.float32, what + " row scales", ndim=1)
-    if codes.numel() != n_codes or atoms.numel() != n_atoms or (rows is not None and rows.numel() != n_rows):
+    _need(codes, torch.uint8, what, codes.dim())
+    _need(atoms, torch.uint8, what, atoms.dim())
+    if codes.numel() != n_codes or atoms.numel() != n_atoms:
         raise ValueError("operand shapes do not agree")
-    if not (codes.is_contiguous() and atoms.is_contiguous() and (rows is None or rows.is_contiguous())):
+    if not (codes.is_contiguous() and atoms.is_contiguous()):
         raise ValueError("%s must be contiguous" % what)
+    if rows is not None:
+        _need(rows, torch.float32, what, 1)
+        if rows.numel() != n_rows:
+            raise ValueError("operand shapes do not agree")
+        if not rows.is_contiguous():
+            raise ValueError("%s must be contiguous" % what)
 
 
 def _out(t, shape, dtype, device, name):
     """`t` checked as an output of that shape (contiguous), or a new one."""
-    torch = _torch()
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, name, ndim=len(shape))
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be contiguous of shape %s" % (name, tuple(shape)))
+        return _torch().empty(shape, dtype=dtype, device=device)
+    _need(t, dtype, name, len(shape))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous of shape %s" % (name, shape))
     return t
 
 

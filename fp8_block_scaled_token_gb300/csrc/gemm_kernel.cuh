@@ -177,6 +177,12 @@ template <int NPAD, int MODE> struct GemmCfg {
     static constexpr int kTmemCols =
         kTmemNeed <= 32 ? 32 : kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
     static constexpr int kQuantWarps = MODE == kModeFp8Fused ? 4 : 0;
+    // 4-bit: four warps move each unit's scale factors from shared to tensor
+    // memory, every warp the 32 lines of each atom to its own 32 lanes.  (The
+    // tensor core's own copy, one 512-byte atom an instruction, takes about 40
+    // ns each in the MMA thread's queue, 0.3 us for the eight atoms of a unit:
+    // 34,816 x 5,120 at M = 16 / 512 runs in 32.8 / 118 us with it.)
+    static constexpr int kSfWarps = kFp4 ? 4 : 0;
     // Up to 16 tokens the non-fused kernels run two CTAs per SM (a ~100 KB
     // ring each): the next GEMM's CTA, launched early by programmatic
     // dependent launch, then shares the SM and streams its weights while this
@@ -191,7 +197,9 @@ template <int NPAD, int MODE> struct GemmCfg {
     // wider tiles need more than a second resident CTA (measured in a chain
     // of layers: 64-token tiles 7-16% faster than with one group, 128-token
     // tiles 1-13%), and a thread keeps at most 128 accumulators in registers.
-    static constexpr int kColGroups = NPAD >= 64 ? 2 : 1;
+    // (4-bit: nothing to promote, so two groups only where one would hold 128
+    // columns in registers.)
+    static constexpr int kColGroups = kFp4 ? (NPAD == 128 ? 2 : 1) : NPAD >= 64 ? 2 : 1;
     static constexpr int kCols = NPAD / kColGroups;         // token columns per epilogue thread
     static constexpr int kEpiWarps = 4 * kColGroups;
     // From 32 tokens up, the per-unit scale products s_w * s_a[m] of a
@@ -213,7 +221,7 @@ template <int NPAD, int MODE> struct GemmCfg {
     static constexpr bool kProducts = NPAD >= 32 && !kTileAcc;
     static constexpr int kProdPerLane = (kCols + 31) / 32; // token columns per lane
     static constexpr int kProdBytes = kProducts ? kEpiWarps * 2 * kCols * 4 : 0; // per warp, by unit parity
-    static constexpr int kThreads = 32 * (2 + kEpiWarps + kQuantWarps);
+    static constexpr int kThreads = 32 * (2 + kEpiWarps + kQuantWarps + kSfWarps);
     // Registers per thread.  An SM's register file is four 16,384-register
     // banks, one per scheduler, and a CTA's warps are spread over the four:
     // with W resident warps a bank holds ceil(W / 4) of them, so a thread may
@@ -225,7 +233,7 @@ template <int NPAD, int MODE> struct GemmCfg {
     // CTA landed (decode pass 5.31 -> 5.27 ms at M = 8).
     static constexpr int kWarpsPerBank = (kMinBlocks * (kThreads / 32) + 3) / 4;
     static constexpr int kRegSplit = (16384 / (32 * kWarpsPerBank)) & ~7;
-    static constexpr int kMaxRegs = kMinBlocks == 2 ? 160 : kRegSplit > 255 ? 255 : kRegSplit;
+    static constexpr int kMaxRegs = kMinBlocks == 2 ? (kRegSplit < 160 ? kRegSplit : 160) : kRegSplit > 255 ? 255 : kRegSplit;
     static_assert(kMaxRegs <= kRegSplit || kRegSplit > 255, "the CTAs must fit in the register file");
     // Plain FP8 and MX layers (not the greedy output layer): a finished Y
     // tile (128 weight rows x NPAD tokens, bf16) is staged in shared memory as
@@ -295,6 +303,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
     unsigned long long *cta_best = reinterpret_cast<unsigned long long *>(smem + 512); // [64] greedy keys
+    uint64_t *sf_ready = reinterpret_cast<uint64_t *>(smem + 512); // 4-bit (no greedy choice): [kMaxStages]
     const int S = p.stages;
     uint8_t *ring = smem + C::kHeader;
     uint16_t *ystage = reinterpret_cast<uint16_t *>(ring + S * C::kStageBytes); // [NPAD][128] bf16
@@ -329,8 +338,13 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
         *abort_flag = 0;
         *last_flag = 0;
     }
-    if (threadIdx.x < 64)
+    if constexpr (C::kFp4) {
+        if (threadIdx.x == 0)
+            for (int s = 0; s < S; ++s)
+                mbar_init(&sf_ready[s], C::kSfWarps);
+    } else if (threadIdx.x < 64) {
         cta_best[threadIdx.x] = 0ull;
+    }
     if (threadIdx.x == 0) {
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -518,6 +532,8 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                     break;
                 if (!mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
                     break;
+                if (C::kFp4 && !mbar_wait(&sf_ready[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
+                    break;
                 if (MODE == kModeFp8Fused && !FP8BS_CHECK(slot < p.act_chunks))
                     break;
                 tc_fence_after_sync();
@@ -541,14 +557,8 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                                      idesc_mx_e4m3(C::kTileRows, NPAD, static_cast<uint32_t>(k), static_cast<uint32_t>(k)),
                                      sf, sf + 4, (k > 0 || !fresh) ? 1u : 0u);
                 } else if constexpr (C::kFp4) {
-                    // as MX: this unit's atoms to its stage's columns, then
-                    // four MMAs of 64 K
+                    // four MMAs of 64 K, this unit's atoms in its stage's columns
                     const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfCol + s * C::kSfStageCols);
-                    const uint32_t sf_smem = smem_u32(ring + s * C::kStageBytes + C::kWBytes + C::kBBytes);
-                    for (int j = 0; j < p.sf_atoms; ++j) {
-                        tmem_cp_sf_atom(sf + 4 * j, sf_atom_desc(sf_smem + 512 * j));
-                        tmem_cp_sf_atom(sf + 16 + 4 * j, sf_atom_desc(sf_smem + 2048 + 512 * j));
-                    }
                     if (p.sf_atoms == 4) {
 #pragma unroll
                         for (int k = 0; k < C::kMmaSteps; ++k)
@@ -588,6 +598,42 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                 if (globaltimer_ns() - t0 > p.timeout_ns) {
                     atomicOr(p.status, kErrTimeoutDrain);
                     break;
+                }
+            }
+        }
+    } else if (C::kSfWarps > 0 && warp >= 2 + C::kEpiWarps) {
+        // ------------------------------------------------ scale factors to tensor memory
+        if constexpr (C::kFp4) {
+            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = 0; i < nunits; ++i) {
+                const bool ok = mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                // line `lane` of the weight atoms, then of the token atoms
+                // (with two atoms a side, the other columns' values are not used)
+                const uint4 *line = reinterpret_cast<const uint4 *>(ring + s * C::kStageBytes + C::kWBytes + C::kBBytes) + lane;
+                uint32_t r[32];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 v = line[32 * j];
+                    r[4 * j] = v.x;
+                    r[4 * j + 1] = v.y;
+                    r[4 * j + 2] = v.z;
+                    r[4 * j + 3] = v.w;
+                }
+                // the stage's columns are free: its previous MMAs completed
+                // before the ring stage could be filled again
+                tc_fence_after_sync();
+                tmem_store32(tmem_base + lanes + static_cast<uint32_t>(C::kSfCol + s * C::kSfStageCols), r);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sf_ready[s]);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
         }
@@ -1023,7 +1069,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         // Otherwise issue every contributor's loads for a chunk of
                         // tokens at once (one L2 round trip per chunk), then add
                         // them in contributor order.
-                        constexpr int kMaxC = NPAD > 64 ? 2 : 6;
+                        constexpr int kMaxC = NPAD > 64 ? 2 : C::kFp4 && NPAD == 16 ? 3 : 6;
                         constexpr int kMC = NPAD <= 16 ? 16 : NPAD > 64 ? 32 : 8;
                         for (int c0 = bulk ? c_last + 1 : c_first; c0 <= c_last; c0 += kMaxC) {
                             const int nc = c_last - c0 + 1 < kMaxC ? c_last - c0 + 1 : kMaxC;
