@@ -958,7 +958,15 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                                      __uint_as_float(r[j + 1]));
                         }
                     };
-                    if constexpr (kLd < 64 && kNLd > 1) {
+                    if constexpr (C::kFp4 && NPAD == 128) {
+                        // a whole segment's sums: no second set of registers
+#pragma unroll
+                        for (int c = 0; c < kNLd; ++c) {
+                            uint32_t r[kLd];
+                            tmem_load32(taddr + c * kLd, r);
+                            promote(c, r);
+                        }
+                    } else if constexpr (kLd < 64 && kNLd > 1) {
                         // chunk c + 1 in flight while chunk c is promoted
                         uint32_t ra[kLd], rb[kLd];
                         tmem_issue(taddr, ra);
@@ -1070,7 +1078,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         // tokens at once (one L2 round trip per chunk), then add
                         // them in contributor order.
                         constexpr int kMaxC = NPAD > 64 ? 2 : C::kFp4 && NPAD == 16 ? 3 : 6;
-                        constexpr int kMC = NPAD <= 16 ? 16 : NPAD > 64 ? 32 : 8;
+                        constexpr int kMC = NPAD <= 16 ? 16 : NPAD > 64 && !C::kFp4 ? 32 : 8;
                         for (int c0 = bulk ? c_last + 1 : c_first; c0 <= c_last; c0 += kMaxC) {
                             const int nc = c_last - c0 + 1 < kMaxC ? c_last - c0 + 1 : kMaxC;
                             const float *src[kMaxC];

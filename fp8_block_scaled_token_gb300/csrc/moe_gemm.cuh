@@ -84,7 +84,7 @@ template <int NPAD, int PHASE> struct MoeCfg {
     static constexpr int kHeader = 3072; // barriers and flags, then [1024, 3072) the active experts
     static constexpr int kProdFloats = kEpiWarps * 2 * kTiles * kCols; // per warp, by unit parity
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(128, NPAD);
-    static_assert((2 * kMaxStages + 2 * kAcc + 1) * 8 + 12 <= 1024, "header layout");
+    static_assert((2 * kMaxStages + 2 * kAcc + 2) * 8 + 12 <= 1024, "header layout");
     static constexpr int smem_bytes(int stages)
     {
         return 1024 + kHeader + stages * kStageBytes + kProdFloats * 4;
@@ -107,7 +107,8 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     uint64_t *tfull = empty + C::kMaxStages;
     uint64_t *tempty = tfull + C::kAcc;
     uint64_t *mma_done = tempty + C::kAcc;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    uint64_t *red_ready = mma_done + 1; // down: bulk copies of the exchange slots (last segment)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_ready + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
     int *act = reinterpret_cast<int *>(smem + 1024);            // [kMoeMaxExperts]
@@ -129,6 +130,7 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
             mbar_init(&tempty[a], C::kEpiWarps);
         }
         mbar_init(mma_done, 1);
+        mbar_init(red_ready, 1);
         *abort_flag = 0;
         *last_flag = 0;
         fence_mbar_init();
@@ -148,10 +150,12 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     // this wait before it lets this grid start.
     if (kUp)
         grid_dependency_wait();
+    // (the count and the list in one round trip: entries past the count are
+    // whatever the workspace holds, and never used)
     int A = __ldcg(p.active);
-    A = A < 0 ? 0 : A > p.max_active ? p.max_active : A;
-    for (int i = threadIdx.x; i < A; i += C::kThreads)
+    for (int i = threadIdx.x; i < p.max_active; i += C::kThreads)
         act[i] = __ldcg(p.active + 1 + i);
+    A = A < 0 ? 0 : A > p.max_active ? p.max_active : A;
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -345,6 +349,7 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         uint32_t acc_ph = 0;
         Unit u = first_unit();
         int tile = tile0, seg_first = ku0;
+        bool bulk_issued = false; // warp 2 lane 0: slot copies into the ring
         // Contributors of the (at most two) tiles this CTA shares, as in gemm_kernel.cuh.
         struct SplitPlan {
             int c_first, c_last, slot_first;
@@ -408,7 +413,7 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         };
         // up: one pair of tiles from its contributors' partials in the slots:
         // h, its scale and codes, a warp a token (128 rows, four a lane).  The
-        // chosen tokens are dealt to the warps in turn, two at a time; the
+        // chosen tokens are dealt to the warps in turn; the
         // others get zero codes (written, not multiplied in: an unchosen
         // expert's sums may be infinite).  The loops stay rolled: this code
         // runs once or twice a CTA, and unrolled over the tokens its
@@ -430,63 +435,45 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                 if (lane == 0)
                     __stcg(hs + m, 0.0f);
             }
-            // the warp's chosen tokens: numbers ew, ew + kEpiWarps, ... of the set bits
+            // the warp's chosen tokens: numbers ew, ew + kEpiWarps, ... of the
+            // set bits; four contributors' partials in flight at a time
             int rank = 0;
 #pragma unroll 1
-            while (chosen != 0ull) {
-                int m0 = -1, m1 = -1;
+            for (; chosen != 0ull; chosen &= chosen - 1ull) {
+                if (rank++ % C::kEpiWarps != ew)
+                    continue;
+                const int m = __ffsll(static_cast<long long>(chosen)) - 1;
+                float h[4] = {0.0f, 0.0f, 0.0f, 0.0f}, up[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float *const src = p.slots + m * 128 + 4 * lane;
 #pragma unroll 1
-                while (chosen != 0ull && m1 < 0) {
-                    const int m = __ffsll(static_cast<long long>(chosen)) - 1;
-                    chosen &= chosen - 1ull;
-                    if (rank++ % C::kEpiWarps == ew) {
-                        if (m0 < 0)
-                            m0 = m;
-                        else
-                            m1 = m;
-                    }
-                }
-                if (m0 < 0)
-                    break;
-                const int n = m1 < 0 ? 1 : 2;
-                float4 g[2], uu[2];
+                for (int c0 = c_first; c0 <= c_last; c0 += 4) {
+                    float4 vg[4], vu[4];
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    g[b] = uu[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-                for (int c = c_first; c <= c_last; ++c) {
-                    const float *src = p.slots + static_cast<long long>(c == c_first ? slot_first : 2 * c) * kSlot + 4 * lane;
-                    float4 vg[2], vu[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int m = b == 0 || n == 1 ? m0 : m1;
-                        vg[b] = __ldcg(reinterpret_cast<const float4 *>(src + m * 128));
-                        vu[b] = __ldcg(reinterpret_cast<const float4 *>(src + (NPAD + m) * 128));
+                    for (int q = 0; q < 4; ++q) {
+                        const int c = c0 + q <= c_last ? c0 + q : c_last;
+                        const float *s = src + static_cast<long long>(c == c_first ? slot_first : 2 * c) * kSlot;
+                        vg[q] = __ldcg(reinterpret_cast<const float4 *>(s));
+                        vu[q] = __ldcg(reinterpret_cast<const float4 *>(s + NPAD * 128));
                     }
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        add2(g[b].x, g[b].y, vg[b].x, vg[b].y);
-                        add2(g[b].z, g[b].w, vg[b].z, vg[b].w);
-                        add2(uu[b].x, uu[b].y, vu[b].x, vu[b].y);
-                        add2(uu[b].z, uu[b].w, vu[b].z, vu[b].w);
+                    for (int q = 0; q < 4; ++q) {
+                        if (c0 + q <= c_last) {
+                            add2(h[0], h[1], vg[q].x, vg[q].y);
+                            add2(h[2], h[3], vg[q].z, vg[q].w);
+                            add2(up[0], up[1], vu[q].x, vu[q].y);
+                            add2(up[2], up[3], vu[q].z, vu[q].w);
+                        }
                     }
                 }
-#pragma unroll 1
-                for (int b = 0; b < n; ++b) {
-                    const int m = b ? m1 : m0;
-                    float h[4] = {b ? g[1].x : g[0].x, b ? g[1].y : g[0].y, b ? g[1].z : g[0].z, b ? g[1].w : g[0].w};
-                    const float up[4] = {b ? uu[1].x : uu[0].x, b ? uu[1].y : uu[0].y, b ? uu[1].z : uu[0].z,
-                                         b ? uu[1].w : uu[0].w};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        h[q] = __fdiv_rn(h[q], 1.0f + expf(-h[q])) * up[q];
-                    const float s = group_scale(warp_max(abs_max4(h[0], h[1], h[2], h[3])));
-                    *reinterpret_cast<uint32_t *>(hq + static_cast<long long>(m) * p.I) =
-                        quantize4(h[0], h[1], h[2], h[3], s);
-                    const float w = __shfl_sync(0xffffffffu, NPAD > 32 && m >= 32 ? w_tok[1] : w_tok[0], m & 31);
-                    if (lane == 0)
-                        __stcg(hs + m, s * w);
-                }
+                for (int q = 0; q < 4; ++q)
+                    h[q] = __fdiv_rn(h[q], 1.0f + expf(-h[q])) * up[q];
+                const float s = group_scale(warp_max(abs_max4(h[0], h[1], h[2], h[3])));
+                *reinterpret_cast<uint32_t *>(hq + static_cast<long long>(m) * p.I) =
+                    quantize4(h[0], h[1], h[2], h[3], s);
+                const float w = __shfl_sync(0xffffffffu, NPAD > 32 && m >= 32 ? w_tok[1] : w_tok[0], m & 31);
+                if (lane == 0)
+                    __stcg(hs + m, s * w);
             }
         };
 
@@ -572,19 +559,61 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
 #pragma unroll
                             for (int m = 0; m < C::kCols; ++m)
                                 acc[t][m] = 0.0f;
-                        for (int c = pl.c_first; c <= pl.c_last; ++c) {
-                            const float *src = p.slots + static_cast<long long>(slot_of(c)) * kSlot + col0 * 128 + row;
-                            float v[C::kTiles][C::kCols];
+                        if constexpr (!kUp) {
+                            // as in gemm_kernel.cuh: at the range's last segment
+                            // from 32 tokens up the weight ring is idle and takes
+                            // every contributor's slot by bulk copy, one round
+                            // trip; otherwise through registers, six
+                            // contributors' loads in flight
+                            constexpr int kSlotBytes = kSlot * 4;
+                            const int ncon = pl.c_last - pl.c_first + 1;
+                            const bool bulk = NPAD >= 32 && i == nunits - 1 && ncon * kSlotBytes <= S * C::kStageBytes;
+                            if (bulk) {
+                                if (warp == 2 && lane == 0) {
+                                    fence_proxy_async_global(); // the partials were stored by generic writes
+                                    mbar_arrive_expect_tx(red_ready, static_cast<uint32_t>(ncon * kSlotBytes));
+                                    const uint64_t pol = l2_policy_evict_first();
+                                    for (int j = 0; j < ncon; ++j)
+                                        bulk_load_1d(ring + j * kSlotBytes,
+                                                     p.slots + static_cast<long long>(slot_of(pl.c_first + j)) * kSlot,
+                                                     kSlotBytes, red_ready, pol);
+                                    bulk_issued = true;
+                                }
+                                mbar_wait(red_ready, 0, abort_flag, p.status, kErrTimeoutEpilogue, p.timeout_ns);
+                                const float *sm = reinterpret_cast<const float *>(ring) + col0 * 128 + row;
+                                for (int j = 0; j < ncon; ++j)
 #pragma unroll
-                            for (int t = 0; t < C::kTiles; ++t)
+                                    for (int m = 0; m < C::kCols; m += 2)
+                                        if (m < mcnt) // (column m + 1 >= M is never stored)
+                                            add2(acc[0][m], acc[0][m + 1], sm[j * kSlot + m * 128],
+                                                 sm[j * kSlot + (m + 1) * 128]);
+                            }
+                            constexpr int kMaxC = 6, kMC = NPAD == 16 ? 16 : 8;
+                            for (int c0 = bulk ? pl.c_last + 1 : pl.c_first; c0 <= pl.c_last; c0 += kMaxC) {
+                                const int nc = pl.c_last - c0 + 1 < kMaxC ? pl.c_last - c0 + 1 : kMaxC;
+                                const float *src[kMaxC];
 #pragma unroll
-                                for (int m = 0; m < C::kCols; ++m)
-                                    v[t][m] = m < mcnt ? __ldcg(src + (t * NPAD + m) * 128) : 0.0f;
+                                for (int j = 0; j < kMaxC; ++j)
+                                    src[j] = p.slots + static_cast<long long>(slot_of(c0 + (j < nc ? j : 0))) * kSlot +
+                                             col0 * 128 + row;
 #pragma unroll
-                            for (int t = 0; t < C::kTiles; ++t)
+                                for (int mc = 0; mc < C::kCols; mc += kMC) {
+                                    if (mc >= mcnt)
+                                        break;
+                                    float v[kMaxC][kMC];
 #pragma unroll
-                                for (int m = 0; m < C::kCols; ++m)
-                                    acc[t][m] += v[t][m];
+                                    for (int j = 0; j < kMaxC; ++j)
+#pragma unroll
+                                        for (int q = 0; q < kMC; ++q)
+                                            v[j][q] = (j < nc && mc + q < mcnt) ? __ldcg(src[j] + (mc + q) * 128) : 0.0f;
+#pragma unroll
+                                    for (int j = 0; j < kMaxC; ++j)
+#pragma unroll
+                                        for (int q = 0; q < kMC; ++q)
+                                            if (j < nc)
+                                                acc[0][mc + q] += v[j][q];
+                                }
+                            }
                         }
                         store_y();
                         if (warp == 2 && lane == 0)
@@ -603,6 +632,16 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                     load_weights(nu.a);
             }
             u = nu;
+        }
+        // the slot copies have landed before the CTA exits, also when the wait gave up
+        if (bulk_issued) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_test(red_ready, 0)) {
+                if (globaltimer_ns() - t0 > p.timeout_ns) {
+                    atomicOr(p.status, kErrTimeoutEpilogue);
+                    break;
+                }
+            }
         }
         // No token chose any expert: the layer's output is zero.
         if (!kUp && A == 0) {

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     for (int t = 0; t < kTG; ++t)
         acc[t] = 0.0f;
     const uint16_t *const x0 = p.x + static_cast<long long>(t0) * p.ldx;
-#pragma unroll 1
+#pragma unroll 2
     for (int h = threadIdx.x * 8; h < p.H; h += kRouteThreads * 8) {
         float w[8];
         if (kBf16) {

@@ -97,6 +97,19 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1)
         : "f"(a0), "f"(a1));
 }
 
+// d0 = a0 * b, d1 = a1 * b as one packed instruction (mul.rn.f32x2, the same
+// result as two fp32 multiplications).
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b)
+{
+    asm("{\n\t.reg .b64 ra, rb;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %4};\n\t"
+        "mul.rn.f32x2 ra, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b));
+}
+
 // Orders this thread's view of global memory (generic proxy) before its later
 // bulk copies from global memory (async proxy).
 __device__ __forceinline__ void fence_proxy_async_global()
