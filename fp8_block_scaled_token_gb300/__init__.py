@@ -463,158 +463,44 @@ def fp8_mx_gemm(aq, as_atoms, wq, ws_atoms, n, y=None, workspace=None, flags=0):
     return y
 
 
-# ------------------------------------------------------------ expert layers
-def moe_route_workspace_size(M, E):
-    n = ctypes.c_size_t(0)
-    _check("moe_route_workspace_size", lib().moe_route_workspace_size(M, E, ctypes.byref(n)))
-    return n.value
+# ------------------------------------------------- expert and 4-bit layers
+# Each tensor is checked and turned into its address in one short call: a
+# decode step makes many of these calls, and between kernel launches every
+# attribute that Python reads costs a tenth of a microsecond or more.
+def _addr(t, dtype, numel, name):
+    """Address of a contiguous CUDA tensor of that type and number of elements."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == numel:
+        return t.data_ptr()
+    _need(t, dtype, name, t.dim())
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("operand shapes do not agree (%s has %d elements, not %d)" % (name, t.numel(), numel))
 
 
-def fp8_moe_workspace_size(M, H, I, E, top_k):
-    n = ctypes.c_size_t(0)
-    _check("fp8_moe_workspace_size", lib().fp8_moe_workspace_size(M, H, I, E, top_k, ctypes.byref(n)))
-    return n.value
-
-
-def _router(x, wr):
-    """(M, H, E, dtype code) of activations and router weights."""
+def _act(x):
+    """(M, K, row stride, address) of bf16 activations [M, K]."""
     torch = _torch()
-    _need(x, torch.bfloat16, "x")
-    _rows_contiguous(x, "x")
-    wt = wr.dtype
-    if wt is not torch.bfloat16 and wt is not torch.float32:
-        raise TypeError("wr must be float32 or bfloat16")
-    _need(wr, wt, "wr")
-    if not wr.is_contiguous():
-        raise ValueError("wr must be contiguous")
-    M, H = x.shape
-    E, Hr = wr.shape
-    if H != Hr:
-        raise ValueError("operand shapes do not agree")
-    return M, H, E, BF16 if wt is torch.bfloat16 else F32
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 2:
+        _need(x, torch.bfloat16, "x")
+    M, K = x.shape
+    ld, unit = x.stride()
+    if unit != 1:
+        raise ValueError("x must have unit stride along K")
+    return M, K, ld, x.data_ptr()
 
 
-def _experts(w13, s13, w2, s2, H, E):
-    """(E, I, flag) of the experts' weights: w13 [E, 2I, H] and w2 [E, H, I],
-    or both tiled [tiles, 128, 128]; E (None: from a row-major w13) settles the
-    tiled form."""
+def _matrix(w, name):
+    """(rows, K, dtype code, address) of a contiguous fp32 or bf16 matrix."""
     torch = _torch()
-    _need(w13, torch.uint8, "w13", 3)
-    _need(w2, torch.uint8, "w2", 3)
-    _need(s13, torch.float32, "s13")
-    _need(s2, torch.float32, "s2")
-    if not (w13.is_contiguous() and w2.is_contiguous() and s13.is_contiguous() and s2.is_contiguous()):
-        raise ValueError("w13, s13, w2 and s2 must be contiguous")
-    kg = H // 128
-    shape13, shape2 = w13.shape, w2.shape
-    if E is None:
-        if shape13[2] != H:
-            raise ValueError("w13 is tiled: pass experts= (the number of experts)")
-        E = shape13[0]
-    E = int(E)
-    rows, kg2 = s2.shape[1], s2.shape[0]  # rows: 128-row tiles of I
-    I = rows * 128
-    if rows < 1 or E < 1 or kg2 != E * kg or s13.shape != (2 * E * rows, kg):
-        raise ValueError("operand shapes do not agree")
-    tiles = E * rows * kg
-    if shape13 == (2 * tiles, 128, 128) and shape2 == (tiles, 128, 128):
-        return E, I, FLAG_WEIGHTS_TILED
-    if shape13 == (E, 2 * I, H) and shape2 == (E, H, I):
-        return E, I, 0
-    raise ValueError("operand shapes do not agree")
-
-
-def moe_route(x, wr, top_k, renormalize=True, ids=None, weights=None, workspace=None, flags=0):
-    """The experts of each token: x bf16 [M, H] (row stride may exceed H), wr
-    fp32 or bf16 [E, H] -> (ids int32 [M, top_k] by descending logit, weights
-    fp32 [M, top_k], softmax over the chosen or, with renormalize=False, over
-    all experts)."""
-    torch = _torch()
-    M, H, E, wt = _router(x, wr)
-    ids = _out(ids, (M, top_k), torch.int32, x.device, "ids")
-    weights = _out(weights, (M, top_k), torch.float32, x.device, "weights")
-    if workspace is None:
-        workspace = make_workspace(moe_route_workspace_size(M, E), x.device)
-    _check("moe_route", lib().moe_route(_ptr(x), x.stride(0), _ptr(wr), wt, M, H, E, top_k, 1 if renormalize else 0,
-                                        _ptr(ids), _ptr(weights), _ptr(workspace), workspace.numel(), flags, _stream()))
-    return ids, weights
-
-
-def fp8_moe_experts(x, ids, weights, w13, s13, w2, s2, experts=None, y=None, workspace=None, flags=0):
-    """Y bf16 [M, H] of the experts that ids int32 [M, top_k] names, weighted
-    by weights fp32 [M, top_k] (an id outside [0, experts) is skipped); w13
-    [experts, 2I, H] and w2 [experts, H, I] E4M3 row-major, or both tiled
-    (fp8_quant_weight_blocks of the matrices with the experts' rows stacked)
-    with experts= given; s13, s2 their block scales."""
-    torch = _torch()
-    _need(x, torch.bfloat16, "x")
-    _rows_contiguous(x, "x")
-    M, H = x.shape
-    E, I, tf = _experts(w13, s13, w2, s2, H, experts)
-    _need(ids, torch.int32, "ids")
-    _need(weights, torch.float32, "weights")
-    k = ids.shape[1]
-    if ids.shape[0] != M or tuple(weights.shape) != (M, k):
-        raise ValueError("operand shapes do not agree")
-    if not (ids.is_contiguous() and weights.is_contiguous()):
-        raise ValueError("ids and weights must be contiguous")
-    y = _out(y, (M, H), torch.bfloat16, x.device, "y")
-    if workspace is None:
-        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, k), x.device)
-    _check("fp8_moe_experts",
-           lib().fp8_moe_experts(_ptr(x), x.stride(0), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(s13), _ptr(w2),
-                                 _ptr(s2), _ptr(y), M, H, I, E, k, _ptr(workspace), workspace.numel(), flags | tf,
-                                 _stream()))
-    return y
-
-
-def fp8_moe_layer(x, wr, top_k, w13, s13, w2, s2, renormalize=True, y=None, ids=None, weights=None, workspace=None,
-                  flags=0):
-    """The whole layer, moe_route and fp8_moe_experts in three kernels: (y
-    bf16 [M, H], ids int32 [M, top_k], weights fp32 [M, top_k]); w13 and w2 as
-    in fp8_moe_experts, row-major or tiled."""
-    torch = _torch()
-    M, H, E, wt = _router(x, wr)
-    _, I, tf = _experts(w13, s13, w2, s2, H, E)
-    y = _out(y, (M, H), torch.bfloat16, x.device, "y")
-    ids = _out(ids, (M, top_k), torch.int32, x.device, "ids")
-    weights = _out(weights, (M, top_k), torch.float32, x.device, "weights")
-    if workspace is None:
-        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, top_k), x.device)
-    _check("fp8_moe_layer",
-           lib().fp8_moe_layer(_ptr(x), x.stride(0), _ptr(wr), wt, 1 if renormalize else 0, _ptr(w13), _ptr(s13),
-                               _ptr(w2), _ptr(s2), _ptr(y), _ptr(ids), _ptr(weights), M, H, I, E, top_k,
-                               _ptr(workspace), workspace.numel(), flags | tf, _stream()))
-    return y, ids, weights
-
-
-# ------------------------------------------------------------- 4-bit layers
-def _fp4_tiles(N, K):
-    return ((N + 127) // 128) * ((K + 255) // 256)
-
-
-def _fp4_atoms(fmt):
-    """Scale atoms per 128 rows and 256 K."""
-    if fmt not in (FP4_NV, FP4_MX):
-        raise ValueError("fmt must be FP4_NV or FP4_MX")
-    return 4 if fmt == FP4_NV else 2
-
-
-def _fp4_operand(codes, atoms, rows, n_codes, n_atoms, n_rows, what):
-    """Checks of one packed 4-bit operand (rows may be None: all 1, FP4_MX only)."""
-    torch = _torch()
-    _need(codes, torch.uint8, what, codes.dim())
-    _need(atoms, torch.uint8, what, atoms.dim())
-    if codes.numel() != n_codes or atoms.numel() != n_atoms:
-        raise ValueError("operand shapes do not agree")
-    if not (codes.is_contiguous() and atoms.is_contiguous()):
-        raise ValueError("%s must be contiguous" % what)
-    if rows is not None:
-        _need(rows, torch.float32, what, 1)
-        if rows.numel() != n_rows:
-            raise ValueError("operand shapes do not agree")
-        if not rows.is_contiguous():
-            raise ValueError("%s must be contiguous" % what)
+    t = w.dtype
+    if t is not torch.bfloat16 and t is not torch.float32:
+        raise TypeError("%s must be float32 or bfloat16" % name)
+    if not w.is_cuda or w.dim() != 2:
+        _need(w, t, name)
+    if not w.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    rows, K = w.shape
+    return rows, K, BF16 if t is torch.bfloat16 else F32, w.data_ptr()
 
 
 def _out(t, shape, dtype, device, name):
@@ -627,24 +513,151 @@ def _out(t, shape, dtype, device, name):
     return t
 
 
+def _work(workspace):
+    """(address, bytes) of a workspace."""
+    if workspace.dtype is not _torch().uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor of bytes (make_workspace)")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def moe_route_workspace_size(M, E):
+    n = ctypes.c_size_t(0)
+    _check("moe_route_workspace_size", lib().moe_route_workspace_size(M, E, ctypes.byref(n)))
+    return n.value
+
+
+def fp8_moe_workspace_size(M, H, I, E, top_k):
+    n = ctypes.c_size_t(0)
+    _check("fp8_moe_workspace_size", lib().fp8_moe_workspace_size(M, H, I, E, top_k, ctypes.byref(n)))
+    return n.value
+
+
+def _experts(w13, s13, w2, s2, H, E):
+    """(I, flag, addresses of w13, s13, w2, s2) of E experts' weights: w13 [E,
+    2I, H] and w2 [E, H, I], or both tiled [tiles, 128, 128]."""
+    torch = _torch()
+    kg = H // 128
+    if E < 1 or s2.dim() != 2 or s13.dim() != 2:
+        raise ValueError("operand shapes do not agree")
+    rows = s2.shape[1]  # 128-row tiles of I
+    tiles = E * rows * kg
+    I = rows * 128
+    if tiles < 1 or s2.shape[0] != E * kg or s13.shape != (2 * E * rows, kg):
+        raise ValueError("operand shapes do not agree")
+    shape13, shape2 = w13.shape, w2.shape
+    if shape13 == (2 * tiles, 128, 128) and shape2 == (tiles, 128, 128):
+        flag = FLAG_WEIGHTS_TILED
+    elif shape13 == (E, 2 * I, H) and shape2 == (E, H, I):
+        flag = 0
+    else:
+        raise ValueError("operand shapes do not agree")
+    u8, f32 = torch.uint8, torch.float32
+    return (I, flag, _addr(w13, u8, 2 * tiles * 16384, "w13"), _addr(s13, f32, 2 * tiles, "s13"),
+            _addr(w2, u8, tiles * 16384, "w2"), _addr(s2, f32, tiles, "s2"))
+
+
+def moe_route(x, wr, top_k, renormalize=True, ids=None, weights=None, workspace=None, flags=0):
+    """The experts of each token: x bf16 [M, H] (row stride may exceed H), wr
+    fp32 or bf16 [E, H] -> (ids int32 [M, top_k] by descending logit, weights
+    fp32 [M, top_k], softmax over the chosen or, with renormalize=False, over
+    all experts)."""
+    torch = _torch()
+    M, H, ldx, xp = _act(x)
+    E, Hr, wt, wrp = _matrix(wr, "wr")
+    if H != Hr:
+        raise ValueError("operand shapes do not agree")
+    ids = _out(ids, (M, top_k), torch.int32, x.device, "ids")
+    weights = _out(weights, (M, top_k), torch.float32, x.device, "weights")
+    if workspace is None:
+        workspace = make_workspace(moe_route_workspace_size(M, E), x.device)
+    wsp, wsn = _work(workspace)
+    _check("moe_route", lib().moe_route(xp, ldx, wrp, wt, M, H, E, top_k, 1 if renormalize else 0, ids.data_ptr(),
+                                        weights.data_ptr(), wsp, wsn, flags, _stream()))
+    return ids, weights
+
+
+def fp8_moe_experts(x, ids, weights, w13, s13, w2, s2, experts=None, y=None, workspace=None, flags=0):
+    """Y bf16 [M, H] of the experts that ids int32 [M, top_k] names, weighted
+    by weights fp32 [M, top_k] (an id outside [0, experts) is skipped); w13
+    [experts, 2I, H] and w2 [experts, H, I] E4M3 row-major, or both tiled
+    (fp8_quant_weight_blocks of the matrices with the experts' rows stacked)
+    with experts= given; s13, s2 their block scales."""
+    torch = _torch()
+    M, H, ldx, xp = _act(x)
+    if experts is None:
+        if w13.dim() != 3 or w13.shape[2] != H:
+            raise ValueError("w13 is tiled: pass experts= (the number of experts)")
+        experts = w13.shape[0]
+    E = int(experts)
+    I, tf, w13p, s13p, w2p, s2p = _experts(w13, s13, w2, s2, H, E)
+    if ids.dim() != 2 or ids.shape[0] != M or ids.shape != weights.shape:
+        raise ValueError("operand shapes do not agree")
+    k = ids.shape[1]
+    idp, wp = _addr(ids, torch.int32, M * k, "ids"), _addr(weights, torch.float32, M * k, "weights")
+    y = _out(y, (M, H), torch.bfloat16, x.device, "y")
+    if workspace is None:
+        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, k), x.device)
+    wsp, wsn = _work(workspace)
+    _check("fp8_moe_experts", lib().fp8_moe_experts(xp, ldx, idp, wp, w13p, s13p, w2p, s2p, y.data_ptr(), M, H, I, E, k,
+                                                    wsp, wsn, flags | tf, _stream()))
+    return y
+
+
+def fp8_moe_layer(x, wr, top_k, w13, s13, w2, s2, renormalize=True, y=None, ids=None, weights=None, workspace=None,
+                  flags=0):
+    """The whole layer, moe_route and fp8_moe_experts in three kernels: (y
+    bf16 [M, H], ids int32 [M, top_k], weights fp32 [M, top_k]); w13 and w2 as
+    in fp8_moe_experts, row-major or tiled."""
+    torch = _torch()
+    M, H, ldx, xp = _act(x)
+    E, Hr, wt, wrp = _matrix(wr, "wr")
+    if H != Hr:
+        raise ValueError("operand shapes do not agree")
+    I, tf, w13p, s13p, w2p, s2p = _experts(w13, s13, w2, s2, H, E)
+    dev = x.device
+    y = _out(y, (M, H), torch.bfloat16, dev, "y")
+    ids = _out(ids, (M, top_k), torch.int32, dev, "ids")
+    weights = _out(weights, (M, top_k), torch.float32, dev, "weights")
+    if workspace is None:
+        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, top_k), dev)
+    wsp, wsn = _work(workspace)
+    _check("fp8_moe_layer", lib().fp8_moe_layer(xp, ldx, wrp, wt, 1 if renormalize else 0, w13p, s13p, w2p, s2p,
+                                                y.data_ptr(), ids.data_ptr(), weights.data_ptr(), M, H, I, E, top_k,
+                                                wsp, wsn, flags | tf, _stream()))
+    return y, ids, weights
+
+
+def _fp4_tiles(N, K):
+    return ((N + 127) // 128) * ((K + 255) // 256)
+
+
+def _fp4_atoms(fmt):
+    """Scale atoms per 128 rows and 256 K."""
+    if fmt != FP4_NV and fmt != FP4_MX:
+        raise ValueError("fmt must be FP4_NV or FP4_MX")
+    return 4 if fmt == FP4_NV else 2
+
+
+def _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt):
+    """Addresses of packed 4-bit weights (w_rows may be None: all 1, FP4_MX only)."""
+    torch = _torch()
+    u8, tiles = torch.uint8, _fp4_tiles(N, K)
+    return (_addr(wq, u8, tiles * 16384, "wq"), _addr(ws_atoms, u8, tiles * _fp4_atoms(fmt) * 512, "ws_atoms"),
+            _addr(w_rows, torch.float32, N, "w_rows") if w_rows is not None else None)
+
+
 def fp4_quant_weights(w, fmt=FP4_NV, wq=None, ws_atoms=None, w_rows=None):
     """fp32 or bf16 W [N, K] (K % 32 == 0) -> (wq uint8 [ceil(N/128) *
     ceil(K/256), 128, 128] tiled codes, two to a byte, ws_atoms uint8 [tiles *
     4 or 2, 512] scale atoms, w_rows fp32 [N] row scales (all 1 for FP4_MX))."""
     torch = _torch()
-    if w.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("w must be float32 or bfloat16")
-    _need(w, w.dtype, "w")
-    if not w.is_contiguous():
-        raise ValueError("w must be contiguous")
-    N, K = w.shape
-    tiles = _fp4_tiles(N, K)
-    wq = _out(wq, (tiles, 128, 128), torch.uint8, w.device, "wq")
-    ws_atoms = _out(ws_atoms, (tiles * _fp4_atoms(fmt), 512), torch.uint8, w.device, "ws_atoms")
-    w_rows = _out(w_rows, (N,), torch.float32, w.device, "w_rows")
-    wt = BF16 if w.dtype == torch.bfloat16 else F32
-    _check("fp4_quant_weights", lib().fp4_quant_weights(_ptr(w), wt, N, K, fmt, _ptr(wq), _ptr(ws_atoms),
-                                                        _ptr(w_rows), _stream()))
+    N, K, wt, wp = _matrix(w, "w")
+    tiles, dev = _fp4_tiles(N, K), w.device
+    wq = _out(wq, (tiles, 128, 128), torch.uint8, dev, "wq")
+    ws_atoms = _out(ws_atoms, (tiles * _fp4_atoms(fmt), 512), torch.uint8, dev, "ws_atoms")
+    w_rows = _out(w_rows, (N,), torch.float32, dev, "w_rows")
+    _check("fp4_quant_weights", lib().fp4_quant_weights(wp, wt, N, K, fmt, wq.data_ptr(), ws_atoms.data_ptr(),
+                                                        w_rows.data_ptr(), _stream()))
     return wq, ws_atoms, w_rows
 
 
@@ -653,15 +666,13 @@ def fp4_dequant_weights(wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, w=None, dtype=No
     4-bit weights stand for (w_rows None: all 1, FP4_MX only)."""
     torch = _torch()
     N, K = int(n), int(k)
-    tiles = _fp4_tiles(N, K)
-    _fp4_operand(wq, ws_atoms, w_rows, tiles * 16384, tiles * _fp4_atoms(fmt) * 512, N, "wq")
+    qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
     dtype = dtype or (w.dtype if w is not None else torch.float32)
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise TypeError("w must be float32 or bfloat16")
     w = _out(w, (N, K), dtype, wq.device, "w")
-    wt = BF16 if dtype == torch.bfloat16 else F32
-    _check("fp4_dequant_weights", lib().fp4_dequant_weights(_ptr(wq), _ptr(ws_atoms), _ptr(w_rows), N, K, fmt,
-                                                            _ptr(w), wt, _stream()))
+    _check("fp4_dequant_weights", lib().fp4_dequant_weights(qp, ap, rp, N, K, fmt, w.data_ptr(),
+                                                            BF16 if dtype is torch.bfloat16 else F32, _stream()))
     return w
 
 
@@ -670,15 +681,13 @@ def fp4_quant_act(x, fmt=FP4_NV, xq=None, xs_atoms=None, x_rows=None, flags=0):
     uint8 [M, ceil(K/256) * 128], xs_atoms uint8 [ceil(M/128) * ceil(K/256) *
     4 or 2, 512], x_rows fp32 [M])."""
     torch = _torch()
-    _need(x, torch.bfloat16, "x")
-    _rows_contiguous(x, "x")
-    M, K = x.shape
-    kt = (K + 255) // 256
-    xq = _out(xq, (M, kt * 128), torch.uint8, x.device, "xq")
-    xs_atoms = _out(xs_atoms, ((M + 127) // 128 * kt * _fp4_atoms(fmt), 512), torch.uint8, x.device, "xs_atoms")
-    x_rows = _out(x_rows, (M,), torch.float32, x.device, "x_rows")
-    _check("fp4_quant_act", lib().fp4_quant_act(_ptr(x), M, K, x.stride(0), fmt, _ptr(xq), _ptr(xs_atoms),
-                                                _ptr(x_rows), flags, _stream()))
+    M, K, ldx, xp = _act(x)
+    kt, dev = (K + 255) // 256, x.device
+    xq = _out(xq, (M, kt * 128), torch.uint8, dev, "xq")
+    xs_atoms = _out(xs_atoms, ((M + 127) // 128 * kt * _fp4_atoms(fmt), 512), torch.uint8, dev, "xs_atoms")
+    x_rows = _out(x_rows, (M,), torch.float32, dev, "x_rows")
+    _check("fp4_quant_act", lib().fp4_quant_act(xp, M, K, ldx, fmt, xq.data_ptr(), xs_atoms.data_ptr(),
+                                                x_rows.data_ptr(), flags, _stream()))
     return xq, xs_atoms, x_rows
 
 
@@ -694,14 +703,15 @@ def fp4_gemm(aq, as_atoms, a_rows, wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, y=Non
     torch = _torch()
     M, N, K = aq.shape[0], int(n), int(k)
     kt = (K + 255) // 256
-    s = _fp4_atoms(fmt)
-    _fp4_operand(aq, as_atoms, a_rows, M * kt * 128, (M + 127) // 128 * kt * s * 512, M, "aq")
-    _fp4_operand(wq, ws_atoms, w_rows, _fp4_tiles(N, K) * 16384, _fp4_tiles(N, K) * s * 512, N, "wq")
+    qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
+    aqp = _addr(aq, torch.uint8, M * kt * 128, "aq")
+    asp = _addr(as_atoms, torch.uint8, (M + 127) // 128 * kt * _fp4_atoms(fmt) * 512, "as_atoms")
+    arp = _addr(a_rows, torch.float32, M, "a_rows") if a_rows is not None else None
     y = _out(y, (M, N), torch.bfloat16, aq.device, "y")
     if workspace is None:
         workspace = make_workspace(fp4_gemm_workspace_size(M, N, K, fmt), aq.device)
-    _check("fp4_gemm", lib().fp4_gemm(_ptr(aq), _ptr(as_atoms), _ptr(a_rows), _ptr(wq), _ptr(ws_atoms), _ptr(w_rows),
-                                      _ptr(y), M, N, K, fmt, _ptr(workspace), workspace.numel(), flags, _stream()))
+    wsp, wsn = _work(workspace)
+    _check("fp4_gemm", lib().fp4_gemm(aqp, asp, arp, qp, ap, rp, y.data_ptr(), M, N, K, fmt, wsp, wsn, flags, _stream()))
     return y
 
 
@@ -709,17 +719,14 @@ def fp4_gemm_fused(x, wq, ws_atoms, w_rows, n, fmt=FP4_NV, y=None, workspace=Non
     """Y[M, n] bf16 from bf16 activations (row stride may exceed K) and packed
     4-bit weights: the cast into the workspace, then the product."""
     torch = _torch()
-    _need(x, torch.bfloat16, "x")
-    _rows_contiguous(x, "x")
-    M, K = x.shape
+    M, K, ldx, xp = _act(x)
     N = int(n)
-    tiles = _fp4_tiles(N, K)
-    _fp4_operand(wq, ws_atoms, w_rows, tiles * 16384, tiles * _fp4_atoms(fmt) * 512, N, "wq")
+    qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
     y = _out(y, (M, N), torch.bfloat16, x.device, "y")
     if workspace is None:
         workspace = make_workspace(fp4_gemm_workspace_size(M, N, K, fmt), x.device)
-    _check("fp4_gemm_fused", lib().fp4_gemm_fused(_ptr(x), x.stride(0), _ptr(wq), _ptr(ws_atoms), _ptr(w_rows),
-                                                  _ptr(y), M, N, K, fmt, _ptr(workspace), workspace.numel(), flags,
+    wsp, wsn = _work(workspace)
+    _check("fp4_gemm_fused", lib().fp4_gemm_fused(xp, ldx, qp, ap, rp, y.data_ptr(), M, N, K, fmt, wsp, wsn, flags,
                                                   _stream()))
     return y
 

@@ -241,14 +241,22 @@ __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float r, float
 template <bool kBf16, bool kNv, bool kTiled, int kRowThreads, int kHold>
 __global__ void __launch_bounds__(kRowThreads)
     fp4_quant_rows_kernel(const void *__restrict__ x, int rows, int K, long long ldx, int kg, uint8_t *__restrict__ xq,
-                          uint8_t *__restrict__ sf, float *__restrict__ row_scale, unsigned long long *runs)
+                          uint8_t *__restrict__ sf, float *__restrict__ row_scale, int overlap,
+                          unsigned long long *runs)
 {
     __shared__ float warp_amax[kRowThreads / 32];
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(runs + (kTiled ? FP8BS_RUNS_FP4_QUANT_WEIGHT : FP8BS_RUNS_FP4_QUANT_ACT), 1ull);
     if (!kTiled) {
-        grid_launch_dependents();
+        // Launched early behind whatever kernel is before it (its launch
+        // latency is then hidden); it touches nothing before the wait.  The
+        // product that follows may be let in before the wait only if the
+        // caller vouches for the weights, which it prefetches.
+        if (overlap)
+            grid_launch_dependents();
         grid_dependency_wait();
+        if (!overlap)
+            grid_launch_dependents();
     }
     const int row = blockIdx.x;
     const bool real = row < rows;
@@ -399,7 +407,7 @@ fp8bs_status launch_fp4_quant_weights(const void *w, int wtype, int N, int K, in
                             : (wide ? fp4_quant_rows_kernel<false, false, true, 256, 3>
                                     : fp4_quant_rows_kernel<false, false, true, 128, 2>));
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, w, N, K, static_cast<long long>(K), (K + 255) / 256, wq, sf,
-                                            rows, dev.runs));
+                                            rows, 0, dev.runs));
 }
 
 fp8bs_status launch_fp4_quant_act(const void *x, int M, int K, int ldx, int fmt, uint8_t *xq, uint8_t *sf,
@@ -413,11 +421,11 @@ fp8bs_status launch_fp4_quant_act(const void *x, int M, int K, int ldx, int fmt,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = 1;
     auto kernel = fmt == FP8BS_FP4_NV ? fp4_quant_rows_kernel<true, true, false, 512, 3>
                                       : fp4_quant_rows_kernel<true, false, false, 512, 3>;
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, x, M, K, static_cast<long long>(ldx), (K + 255) / 256, xq, sf,
-                                            rows, dev.runs));
+                                            rows, pdl ? 1 : 0, dev.runs));
 }
 
 fp8bs_status launch_fp4_dequant_weights(const uint8_t *wq, const uint8_t *sf, const float *rows, int N, int K,

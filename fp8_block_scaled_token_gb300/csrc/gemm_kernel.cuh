@@ -1077,8 +1077,8 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         // Otherwise issue every contributor's loads for a chunk of
                         // tokens at once (one L2 round trip per chunk), then add
                         // them in contributor order.
-                        constexpr int kMaxC = NPAD > 64 ? 2 : C::kFp4 && NPAD == 16 ? 3 : 6;
-                        constexpr int kMC = NPAD <= 16 ? 16 : NPAD > 64 && !C::kFp4 ? 32 : 8;
+                        constexpr int kMaxC = NPAD > 64 ? 2 : 6;
+                        constexpr int kMC = NPAD <= 16 && !C::kFp4 ? 16 : NPAD > 64 && !C::kFp4 ? 32 : 8;
                         for (int c0 = bulk ? c_last + 1 : c_first; c0 <= c_last; c0 += kMaxC) {
                             const int nc = c_last - c0 + 1 < kMaxC ? c_last - c0 + 1 : kMaxC;
                             const float *src[kMaxC];

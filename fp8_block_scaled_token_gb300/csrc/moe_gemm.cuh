@@ -224,14 +224,16 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
             const uint64_t pol_w = l2_policy_evict_first();
             const uint64_t pol_b = l2_policy_evict_last();
             uint32_t armed_mask = 0, armed_parity = 0;
+            auto weight_x = [&](const Unit &u) { return p.w_tiled ? 0 : u.kb * 128; };
+            auto weight_y = [&](const Unit &u, int t) {
+                const long long wt = weight_tile(u, t);
+                return static_cast<int>(p.w_tiled ? (wt * kg1 + u.kb) * 128 : wt * 128);
+            };
             auto load_w = [&](int s, const Unit &u) {
 #pragma unroll
-                for (int t = 0; t < C::kTiles; ++t) {
-                    const long long wt = weight_tile(u, t);
-                    const int wx = p.w_tiled ? 0 : u.kb * 128;
-                    const int wy = static_cast<int>(p.w_tiled ? (wt * kg1 + u.kb) * 128 : wt * 128);
-                    tma_load_2d(ring + s * C::kStageBytes + t * C::kWBytes, &tm_w, &full[s], wx, wy, pol_w);
-                }
+                for (int t = 0; t < C::kTiles; ++t)
+                    tma_load_2d(ring + s * C::kStageBytes + t * C::kWBytes, &tm_w, &full[s], weight_x(u),
+                                weight_y(u, t), pol_w);
             };
             auto load_b = [&](int s, const Unit &u) {
                 tma_load_2d(ring + s * C::kStageBytes + C::kTiles * C::kWBytes, &tm_b, &full[s], u.kb * 128,

@@ -9,7 +9,7 @@
 //   w[m, j] = exp(l_j - l_max) / sum exp(l - l_max), the sum over the chosen
 //             experts (renormalised) or over all of them
 //
-// Grid: one CTA per (expert, group of 8 tokens), then one CTA per eight (token,
+// Grid: one CTA per (one or four experts, group of 8 tokens), then one CTA per eight (token,
 // 128 of H) groups of the cast.  The last CTA of a token group chooses for its
 // eight tokens, and the last group's CTA lists the active experts; arrivals
 // are counted, nobody waits.  A few microseconds of latency, not bandwidth:
@@ -157,10 +157,13 @@ __device__ __forceinline__ void cast_group(const RouteParams &p, long long group
         p.xs[g * p.M + m] = s;
 }
 
-template <bool kBf16>
+// kEx experts a CTA: one where the CTAs then fill the GPU at most twice (each
+// reads its tokens' rows of x from L2: 42 MB at 64 tokens, 64 experts and H =
+// 5,120), four otherwise.
+template <bool kBf16, int kEx>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p)
 {
-    __shared__ float part[kRouteWarps][kTG];
+    __shared__ float part[kRouteWarps][kEx * kTG];
     __shared__ unsigned arrived;
     __shared__ unsigned smask[kMoeMaxExperts / 32];
     __shared__ float logit[kTG][kMoeMaxExperts];
@@ -170,74 +173,99 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (p.M + kTG - 1) / kTG;
-    const int routing = p.E * groups;
+    const int per_group = (p.E + kEx - 1) / kEx; // CTAs
+    const int routing = per_group * groups;
     if (static_cast<int>(blockIdx.x) >= routing) {
         cast_group(p, static_cast<long long>(blockIdx.x - routing) * kRouteWarps + warp);
         return;
     }
-    const int e = blockIdx.x % p.E, tg = blockIdx.x / p.E;
+    const int e0 = blockIdx.x % per_group * kEx, tg = blockIdx.x / per_group;
     const int t0 = tg * kTG;
     const int nt = p.M - t0 < kTG ? p.M - t0 : kTG;
     // eight values of H a thread and step, all tokens' loads in flight at once
-    // (tokens past the last re-read it; their sums are not used)
-    float acc[kTG];
+    // (tokens past the last and experts past E re-read the last; those sums
+    // are not used)
+    float acc[kEx][kTG];
 #pragma unroll
-    for (int t = 0; t < kTG; ++t)
-        acc[t] = 0.0f;
+    for (int q = 0; q < kEx; ++q)
+#pragma unroll
+        for (int t = 0; t < kTG; ++t)
+            acc[q][t] = 0.0f;
     const uint16_t *const x0 = p.x + static_cast<long long>(t0) * p.ldx;
-#pragma unroll 2
+#pragma unroll(kEx == 1 ? 2 : 1)
     for (int h = threadIdx.x * 8; h < p.H; h += kRouteThreads * 8) {
-        float w[8];
-        if (kBf16) {
-            const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.wr) +
-                                                             static_cast<long long>(e) * p.H + h);
-            const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[2 * i] = bf16_lo(rw[i]);
-                w[2 * i + 1] = bf16_hi(rw[i]);
-            }
-        } else {
-            const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.wr) +
-                                                               static_cast<long long>(e) * p.H + h);
-            const float4 a = r[0], b = r[1];
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-            w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        }
         uint4 xr[kTG];
 #pragma unroll
         for (int t = 0; t < kTG; ++t)
             xr[t] = *reinterpret_cast<const uint4 *>(x0 + static_cast<long long>(t < nt ? t : nt - 1) * p.ldx + h);
+        uint4 wr[kEx][kBf16 ? 1 : 2];
 #pragma unroll
-        for (int t = 0; t < kTG; ++t) {
-            const uint32_t xw[4] = {xr[t].x, xr[t].y, xr[t].z, xr[t].w};
+        for (int q = 0; q < kEx; ++q) {
+            const long long e = e0 + q < p.E ? e0 + q : p.E - 1;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.wr) +
+                                                               (e * p.H + h) * (kBf16 ? 2 : 4));
+            wr[q][0] = src[0];
+            if (!kBf16)
+                wr[q][kBf16 ? 0 : 1] = src[1];
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[t] = fmaf(bf16_lo(xw[i]), w[2 * i], acc[t]);
-                acc[t] = fmaf(bf16_hi(xw[i]), w[2 * i + 1], acc[t]);
+        for (int q = 0; q < kEx; ++q) {
+            float w[8];
+            if (kBf16) {
+                const uint32_t rw[4] = {wr[q][0].x, wr[q][0].y, wr[q][0].z, wr[q][0].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[2 * i] = bf16_lo(rw[i]);
+                    w[2 * i + 1] = bf16_hi(rw[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 r = wr[q][kBf16 ? 0 : i];
+                    w[4 * i] = __uint_as_float(r.x);
+                    w[4 * i + 1] = __uint_as_float(r.y);
+                    w[4 * i + 2] = __uint_as_float(r.z);
+                    w[4 * i + 3] = __uint_as_float(r.w);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < kTG; ++t) {
+                const uint32_t xw[4] = {xr[t].x, xr[t].y, xr[t].z, xr[t].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[q][t] = fmaf(bf16_lo(xw[i]), w[2 * i], acc[q][t]);
+                    acc[q][t] = fmaf(bf16_hi(xw[i]), w[2 * i + 1], acc[q][t]);
+                }
             }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
 #pragma unroll
-        for (int t = 0; t < kTG; ++t)
-            acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+        for (int q = 0; q < kEx; ++q)
+#pragma unroll
+            for (int t = 0; t < kTG; ++t)
+                acc[q][t] += __shfl_xor_sync(0xffffffffu, acc[q][t], o);
     }
     if (lane == 0) {
 #pragma unroll
-        for (int t = 0; t < kTG; ++t)
-            part[warp][t] = acc[t];
+        for (int q = 0; q < kEx; ++q)
+#pragma unroll
+            for (int t = 0; t < kTG; ++t)
+                part[warp][q * kTG + t] = acc[q][t];
     }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < nt) {
-        float s = part[0][threadIdx.x];
+    if (threadIdx.x < kEx * kTG) {
+        const int t = threadIdx.x % kTG, e = e0 + threadIdx.x / kTG;
+        if (t < nt && e < p.E) {
+            float s = part[0][threadIdx.x];
 #pragma unroll
-        for (int i = 1; i < kRouteWarps; ++i)
-            s += part[i][threadIdx.x];
-        __stcg(p.logits + static_cast<long long>(t0 + threadIdx.x) * p.E + e, s);
-        if (p.wtok != nullptr)
-            __stcg(p.wtok + static_cast<long long>(e) * p.npad + t0 + threadIdx.x, 0.0f);
+            for (int i = 1; i < kRouteWarps; ++i)
+                s += part[i][threadIdx.x];
+            __stcg(p.logits + static_cast<long long>(t0 + t) * p.E + e, s);
+            if (p.wtok != nullptr)
+                __stcg(p.wtok + static_cast<long long>(e) * p.npad + t0 + t, 0.0f);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0)
@@ -245,7 +273,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     if (threadIdx.x < kMoeMaxExperts / 32)
         smask[threadIdx.x] = 0u;
     __syncthreads();
-    if (arrived != static_cast<unsigned>(p.E - 1))
+    if (arrived != static_cast<unsigned>(per_group - 1))
         return;
     __threadfence(); // the other CTAs' logits and zeroed weights, for every thread of this one
     // one group of tokens: the mask stays in shared memory
@@ -354,8 +382,9 @@ fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const D
     p.runs = dev.runs;
     const long long cast = layer ? (static_cast<long long>(L.M) * (L.H / 128) + kRouteWarps - 1) / kRouteWarps : 0;
     const int groups = (L.M + kTG - 1) / kTG;
+    const bool four = L.E * groups > 2 * dev.sms; // experts a CTA
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cast + (L.wr != nullptr ? L.E * groups : L.E)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(cast + (L.wr == nullptr ? L.E : (four ? (L.E + 3) / 4 : L.E) * groups)), 1, 1);
     cfg.blockDim = dim3(kRouteThreads, 1, 1);
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[1];
@@ -364,8 +393,8 @@ fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const D
     cfg.attrs = attr;
     cfg.numAttrs = (L.flags & FP8BS_FLAG_OVERLAP_PREV) ? 1 : 0;
     auto kernel = L.wr == nullptr ? moe_plan_kernel
-                  : L.wr_type == FP8BS_BF16 ? moe_route_kernel<true>
-                                            : moe_route_kernel<false>;
+                  : L.wr_type == FP8BS_BF16 ? (four ? moe_route_kernel<true, 4> : moe_route_kernel<true, 1>)
+                                            : (four ? moe_route_kernel<false, 4> : moe_route_kernel<false, 1>);
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
