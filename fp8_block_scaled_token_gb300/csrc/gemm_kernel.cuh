@@ -502,7 +502,76 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if constexpr (C::kFp4) {
+            // The whole warp runs the loop and one lane issues: the loop's
+            // values are then uniform, which the tensor instructions' operands
+            // have to be, and the next stage's barrier is looked at before
+            // this stage's MMAs are issued.  A unit's MMAs take a quarter of
+            // the time that a chain of waits, operand moves and issues by a
+            // single thread does.  (sf_ready completes after full: the warps
+            // that store the scale factors wait for it.)
+            const bool leader = elect_one();
+            int acc = 0, s = 0, kb = kb0;
+            uint32_t acc_ph = 0, ph = 0;
+            bool ready = false;
+            for (int i = 0; i < nunits; ++i) {
+                const bool fresh = i == 0 || kb == 0;
+                const bool publish = i == nunits - 1 || kb == kg - 1;
+                bool ok = true;
+                if (fresh)
+                    ok = mbar_wait(&tempty[acc], acc_ph ^ 1u, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+                if (!ready)
+                    ok = ok && mbar_wait(&sf_ready[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+                if (!__all_sync(0xffffffffu, ok))
+                    break;
+                tc_fence_after_sync();
+                const int s1 = s + 1 == S ? 0 : s + 1;
+                const uint32_t ph1 = s + 1 == S ? ph ^ 1u : ph;
+                ready = __all_sync(0xffffffffu, i + 1 < nunits && mbar_peek(&sf_ready[s1], ph1));
+                if (leader) {
+                    const uint32_t stage = smem_u32(ring) + static_cast<uint32_t>(s * C::kStageBytes);
+                    const uint64_t a_desc = sw128_kmajor_desc(stage);
+                    const uint64_t b_desc = sw128_kmajor_desc(stage + C::kWBytes);
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * NPAD);
+                    // four MMAs of 64 K, this unit's atoms in its stage's columns
+                    const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfCol + s * C::kSfStageCols);
+                    if (p.sf_atoms == 4) {
+#pragma unroll
+                        for (int k = 0; k < C::kMmaSteps; ++k)
+                            mma_nvf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc_fp4(C::kTileRows, NPAD, 0u, 0u),
+                                     sf + 4 * k, sf + 16 + 4 * k, (k > 0 || !fresh) ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < C::kMmaSteps; ++k)
+                            mma_mxf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
+                                     idesc_fp4(C::kTileRows, NPAD, 1u, static_cast<uint32_t>(2 * (k & 1))),
+                                     sf + 4 * (k >> 1), sf + 16 + 4 * (k >> 1), (k > 0 || !fresh) ? 1u : 0u);
+                    }
+                    mma_commit(&empty[s]);
+                    if (publish)
+                        mma_commit(&tfull[acc]);
+                }
+                __syncwarp();
+                if (publish && ++acc == C::kAcc) {
+                    acc = 0;
+                    acc_ph ^= 1u;
+                }
+                s = s1;
+                ph = ph1;
+                if (++kb == kg)
+                    kb = 0;
+            }
+            if (leader) {
+                mma_commit(mma_done);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_test(mma_done, 0)) {
+                    if (globaltimer_ns() - t0 > p.timeout_ns) {
+                        atomicOr(p.status, kErrTimeoutDrain);
+                        break;
+                    }
+                }
+            }
+        } else if (lane == 0) {
             int acc = 0;
             uint32_t acc_ph = 0;
             bool ok = true;
@@ -532,8 +601,6 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                     break;
                 if (!mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
                     break;
-                if (C::kFp4 && !mbar_wait(&sf_ready[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
-                    break;
                 if (MODE == kModeFp8Fused && !FP8BS_CHECK(slot < p.act_chunks))
                     break;
                 tc_fence_after_sync();
@@ -556,21 +623,6 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         mma_mxf8f6f4(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
                                      idesc_mx_e4m3(C::kTileRows, NPAD, static_cast<uint32_t>(k), static_cast<uint32_t>(k)),
                                      sf, sf + 4, (k > 0 || !fresh) ? 1u : 0u);
-                } else if constexpr (C::kFp4) {
-                    // four MMAs of 64 K, this unit's atoms in its stage's columns
-                    const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfCol + s * C::kSfStageCols);
-                    if (p.sf_atoms == 4) {
-#pragma unroll
-                        for (int k = 0; k < C::kMmaSteps; ++k)
-                            mma_nvf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc_fp4(C::kTileRows, NPAD, 0u, 0u),
-                                     sf + 4 * k, sf + 16 + 4 * k, (k > 0 || !fresh) ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < C::kMmaSteps; ++k)
-                            mma_mxf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
-                                     idesc_fp4(C::kTileRows, NPAD, 1u, static_cast<uint32_t>(2 * (k & 1))),
-                                     sf + 4 * (k >> 1), sf + 16 + 4 * (k >> 1), (k > 0 || !fresh) ? 1u : 0u);
-                    }
                 } else {
 #pragma unroll
                     for (int k = 0; k < C::kMmaSteps; ++k) {
