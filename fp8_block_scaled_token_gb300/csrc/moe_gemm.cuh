@@ -294,36 +294,46 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            int acc = 0, s = 0;
-            uint32_t acc_ph = 0, ph = 0;
-            for (int i = 0; i < nunits; ++i) {
-                if (!mbar_wait(&tempty[acc], acc_ph ^ 1u, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
-                    break;
-                if (!mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns))
-                    break;
-                tc_fence_after_sync();
-                const uint8_t *stage = ring + s * C::kStageBytes;
-                const uint64_t b_desc = sw128_kmajor_desc(smem_u32(stage + C::kTiles * C::kWBytes));
+        // (the whole warp runs the loop and one lane issues, as the 4-bit
+        // product's: the operands' values are uniform, and the next stage's
+        // barrier is looked at before this one's MMAs are issued)
+        const bool leader = elect_one();
+        int acc = 0, s = 0;
+        uint32_t acc_ph = 0, ph = 0;
+        bool ready = false;
+        for (int i = 0; i < nunits; ++i) {
+            bool ok = mbar_wait(&tempty[acc], acc_ph ^ 1u, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+            if (!ready)
+                ok = ok && mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            tc_fence_after_sync();
+            const int s1 = s + 1 == S ? 0 : s + 1;
+            const uint32_t ph1 = s + 1 == S ? ph ^ 1u : ph;
+            ready = __all_sync(0xffffffffu, i + 1 < nunits && mbar_peek(&full[s1], ph1));
+            if (leader) {
+                const uint32_t stage = smem_u32(ring) + static_cast<uint32_t>(s * C::kStageBytes);
+                const uint64_t b_desc = sw128_kmajor_desc(stage + C::kTiles * C::kWBytes);
 #pragma unroll
                 for (int t = 0; t < C::kTiles; ++t) {
                     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAccCols + t * NPAD);
-                    const uint64_t a_desc = sw128_kmajor_desc(smem_u32(stage + t * C::kWBytes));
+                    const uint64_t a_desc = sw128_kmajor_desc(stage + t * C::kWBytes);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_f8f6f4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, C::kIdesc, k > 0 ? 1u : 0u);
                 }
                 mma_commit(&empty[s]);
                 mma_commit(&tfull[acc]);
-                if (++acc == C::kAcc) {
-                    acc = 0;
-                    acc_ph ^= 1u;
-                }
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1u;
-                }
             }
+            __syncwarp();
+            if (++acc == C::kAcc) {
+                acc = 0;
+                acc_ph ^= 1u;
+            }
+            s = s1;
+            ph = ph1;
+        }
+        if (leader) {
             // every MMA complete before the tensor memory is released
             mma_commit(mma_done);
             const uint64_t t0 = globaltimer_ns();
