@@ -113,6 +113,9 @@ def _load(path):
         "fp8_mx_quant_weights": [vp, i, i, i, vp, vp, vp],
         "fp8_mx_quant_act": [vp, i, i, i, vp, vp, u, vp],
         "fp8_mx_gemm_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "fp8bs_testhook_fp4_stall": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, sz, i, ctypes.c_ulonglong, vp],
+        "fp8bs_testhook_moe_stall": [vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, u, i, i,
+                                     ctypes.c_ulonglong, vp],
         "moe_route_workspace_size": [i, i, ctypes.POINTER(sz)],
         "moe_route": [vp, i, vp, i, i, i, i, i, i, vp, vp, vp, sz, u, vp],
         "fp8_moe_workspace_size": [i, i, i, i, i, ctypes.POINTER(sz)],

@@ -346,8 +346,8 @@ const char *fp8bs_status_string(fp8bs_status status)
     case FP8BS_ERR_INVALID_ARG:
         return "invalid argument (null pointer, size below 1, ldx below K, or unknown flag/dtype)";
     case FP8BS_ERR_UNSUPPORTED_SHAPE:
-        return "unsupported shape (GEMM M must be 1..512, 1..64 with the greedy choice, without a workspace or in "
-               "the MX variant; K must be a multiple of 128, or 64 for the bf16 GEMM)";
+        return "unsupported shape (a token or expert count or a size outside the entry point's limits, or K not a "
+               "multiple of what it needs; fp8bs.h states both)";
     case FP8BS_ERR_MISALIGNED:
         return "misaligned pointer or row stride";
     case FP8BS_ERR_WORKSPACE_TOO_SMALL:
@@ -905,6 +905,33 @@ extern "C" fp8bs_status fp8bs_testhook_gemm_stall(const uint8_t *aq, const float
     L.workspace_bytes = workspace_bytes;
     L.flags = 0;
     L.stream = static_cast<cudaStream_t>(stream);
+    L.test_skip_unit = skip_unit;
+    L.timeout_ns = timeout_ns;
+    return run_gemm(L);
+}
+
+// The same for the 4-bit product.
+extern "C" fp8bs_status fp8bs_testhook_fp4_stall(const uint8_t *aq, const uint8_t *as_atoms, const float *a_rows,
+                                                 const uint8_t *wq, const uint8_t *ws_atoms, const float *w_rows,
+                                                 void *y, int M, int N, int K, fp8bs_fp4_format fmt, void *workspace,
+                                                 size_t workspace_bytes, int skip_unit, unsigned long long timeout_ns,
+                                                 void *stream)
+{
+    if (!aq || !as_atoms || !a_rows || !wq || !ws_atoms || !w_rows || !y || !workspace || bad_fp4_format(fmt) ||
+        skip_unit < 0 || timeout_ns == 0 || timeout_ns > 10ull * kDefaultTimeoutNs)
+        return FP8BS_ERR_INVALID_ARG;
+    fp8bs_status st = check_gemm_shape(M, N, K, 32);
+    if (st == FP8BS_OK)
+        st = fp4_weight_shape(N, K);
+    if (st != FP8BS_OK)
+        return st;
+    if (!aligned(aq, 16) || !aligned(as_atoms, 16) || !aligned(a_rows, 4) || !aligned(wq, 16) ||
+        !aligned(ws_atoms, 16) || !aligned(w_rows, 4) || !aligned(y, 2) || !aligned(workspace, 256))
+        return FP8BS_ERR_MISALIGNED;
+    GemmLaunch L = fp4_launch(wq, ws_atoms, w_rows, y, M, N, K, fmt, workspace, workspace_bytes, 0, stream);
+    L.a = aq;
+    L.sfb = as_atoms;
+    L.row_a = a_rows;
     L.test_skip_unit = skip_unit;
     L.timeout_ns = timeout_ns;
     return run_gemm(L);

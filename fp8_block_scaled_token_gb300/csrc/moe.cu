@@ -189,6 +189,7 @@ fp8bs_status fp8_moe_experts(const void *x, int ldx, const int32_t *ids, const f
     L.ldx = ldx;
     L.ids = const_cast<int32_t *>(ids); // read only: no router weights
     L.topw = const_cast<float *>(weights);
+    L.test_skip_unit = -1;
     L.w13 = w13;
     L.s13 = s13;
     L.w2 = w2;
@@ -222,6 +223,7 @@ fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8bs_dtype w
     L.renorm = renormalize != 0;
     L.ids = ids;
     L.topw = weights;
+    L.test_skip_unit = -1;
     L.w13 = w13;
     L.s13 = s13;
     L.w2 = w2;
@@ -234,6 +236,41 @@ fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8bs_dtype w
     fp8bs_status st = check_layer(L);
     if (st == FP8BS_OK && !aligned(wr, 16))
         st = FP8BS_ERR_MISALIGNED;
+    return st != FP8BS_OK ? st : run_experts(L, workspace_bytes);
+}
+
+// Test hook (declared in include/fp8bs_testing.h).
+fp8bs_status fp8bs_testhook_moe_stall(const void *x, int ldx, const int32_t *ids, const float *weights,
+                                      const uint8_t *w13, const float *s13, const uint8_t *w2, const float *s2,
+                                      void *y, int M, int H, int I, int E, int top_k, void *workspace,
+                                      size_t workspace_bytes, unsigned flags, int phase, int skip_unit,
+                                      unsigned long long timeout_ns, void *stream)
+{
+    if (!ids || !weights || phase < 0 || phase > 1 || skip_unit < 0 || timeout_ns == 0 ||
+        timeout_ns > 10ull * kDefaultTimeoutNs)
+        return FP8BS_ERR_INVALID_ARG;
+    MoeLaunch L = {};
+    L.M = M;
+    L.H = H;
+    L.I = I;
+    L.E = E;
+    L.top_k = top_k;
+    L.x = x;
+    L.ldx = ldx;
+    L.ids = const_cast<int32_t *>(ids);
+    L.topw = const_cast<float *>(weights);
+    L.w13 = w13;
+    L.s13 = s13;
+    L.w2 = w2;
+    L.s2 = s2;
+    L.y = y;
+    L.workspace = static_cast<uint8_t *>(workspace);
+    L.flags = flags;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.timeout_ns = timeout_ns;
+    L.test_skip_unit = skip_unit;
+    L.test_skip_phase = phase;
+    fp8bs_status st = check_layer(L);
     return st != FP8BS_OK ? st : run_experts(L, workspace_bytes);
 }
 

@@ -48,7 +48,8 @@ struct MoeLaunch {
     unsigned flags;
     cudaStream_t stream;
     unsigned long long timeout_ns;
-    int test_skip_unit = -1;
+    int test_skip_unit = -1;  // -1, or a unit whose stage the producer of phase test_skip_phase never fills
+    int test_skip_phase = 0;  // 0 = gate/up, 1 = down
 };
 
 MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms);

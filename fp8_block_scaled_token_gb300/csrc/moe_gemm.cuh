@@ -721,7 +721,7 @@ fp8bs_status launch_moe_gemm(const MoeLaunch &L, const MoeWorkspace &w, const De
     p.slots = reinterpret_cast<float *>(L.workspace + w.slots_off);
     p.w_tiled = (L.flags & FP8BS_FLAG_WEIGHTS_TILED) ? 1 : 0;
     p.max_active = max_active;
-    p.test_skip_unit = L.test_skip_unit;
+    p.test_skip_unit = L.test_skip_phase == PHASE ? L.test_skip_unit : -1;
     p.timeout_ns = L.timeout_ns;
     p.runs = dev.runs;
 

@@ -9,8 +9,8 @@
 //   w[m, j] = exp(l_j - l_max) / sum exp(l - l_max), the sum over the chosen
 //             experts (renormalised) or over all of them
 //
-// Grid: one CTA per (one or four experts, group of 8 tokens), then one CTA per eight (token,
-// 128 of H) groups of the cast.  The last CTA of a token group chooses for its
+// Grid: one CTA per (one or four experts, group of 8 tokens), then the CTAs of
+// the cast, a warp per (token, 128 of H).  The last CTA of a token group chooses for its
 // eight tokens, and the last group's CTA lists the active experts; arrivals
 // are counted, nobody waits.  A few microseconds of latency, not bandwidth:
 // loads are issued for all eight tokens at once, and the choice keeps its
@@ -26,9 +26,9 @@
 namespace fp8bs {
 
 constexpr int kRouteThreads = 256;
-constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteWide = 1024; // at most, for long rows
 constexpr int kTG = kMoeTokenGroup;
-static_assert(kRouteWarps == kTG, "one warp chooses for each token of a group");
+static_assert(kRouteThreads / 32 == kTG, "one warp chooses for each token of a group");
 
 struct RouteParams {
     int M, H, E, top_k, npad;
@@ -160,10 +160,14 @@ __device__ __forceinline__ void cast_group(const RouteParams &p, long long group
 // kEx experts a CTA: one where the CTAs then fill the GPU at most twice (each
 // reads its tokens' rows of x from L2: 42 MB at 64 tokens, 64 experts and H =
 // 5,120), four otherwise.
-template <bool kBf16, int kEx>
-__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p)
+// kMost threads at most: kRouteThreads, or kRouteWide for one expert a CTA and
+// H above 4,096, where a thread for every eight values of H puts the whole
+// row's loads in flight at once (M = 8, 64 experts, H = 5,120: the layer 91.8
+// -> 90.9 us; at H = 2,048 the smaller register budget costs 0.2 us).
+template <bool kBf16, int kEx, int kMost>
+__global__ void __launch_bounds__(kMost) moe_route_kernel(const RouteParams p)
 {
-    __shared__ float part[kRouteWarps][kEx * kTG];
+    __shared__ float part[kMost / 32][kEx * kTG];
     __shared__ unsigned arrived;
     __shared__ unsigned smask[kMoeMaxExperts / 32];
     __shared__ float logit[kTG][kMoeMaxExperts];
@@ -172,11 +176,12 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     grid_launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
     const int groups = (p.M + kTG - 1) / kTG;
     const int per_group = (p.E + kEx - 1) / kEx; // CTAs
     const int routing = per_group * groups;
     if (static_cast<int>(blockIdx.x) >= routing) {
-        cast_group(p, static_cast<long long>(blockIdx.x - routing) * kRouteWarps + warp);
+        cast_group(p, static_cast<long long>(blockIdx.x - routing) * warps + warp);
         return;
     }
     const int e0 = blockIdx.x % per_group * kEx, tg = blockIdx.x / per_group;
@@ -192,8 +197,8 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
         for (int t = 0; t < kTG; ++t)
             acc[q][t] = 0.0f;
     const uint16_t *const x0 = p.x + static_cast<long long>(t0) * p.ldx;
-#pragma unroll(kEx == 1 ? 2 : 1)
-    for (int h = threadIdx.x * 8; h < p.H; h += kRouteThreads * 8) {
+#pragma unroll(kEx == 1 && kMost == kRouteThreads ? 2 : 1)
+    for (int h = threadIdx.x * 8; h < p.H; h += threads * 8) {
         uint4 xr[kTG];
 #pragma unroll
         for (int t = 0; t < kTG; ++t)
@@ -259,8 +264,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
         const int t = threadIdx.x % kTG, e = e0 + threadIdx.x / kTG;
         if (t < nt && e < p.E) {
             float s = part[0][threadIdx.x];
-#pragma unroll
-            for (int i = 1; i < kRouteWarps; ++i)
+            for (int i = 1; i < warps; ++i)
                 s += part[i][threadIdx.x];
             __stcg(p.logits + static_cast<long long>(t0 + t) * p.E + e, s);
             if (p.wtok != nullptr)
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_plan_kernel(const RoutePara
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5;
     if (static_cast<int>(blockIdx.x) >= p.E) {
-        cast_group(p, static_cast<long long>(blockIdx.x - p.E) * kRouteWarps + warp);
+        cast_group(p, static_cast<long long>(blockIdx.x - p.E) * (kRouteThreads / 32) + warp);
         return;
     }
     const int e = blockIdx.x;
@@ -380,21 +384,26 @@ fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const D
     p.xq = L.workspace + w.xq_off;
     p.xs = reinterpret_cast<float *>(L.workspace + w.xs_off);
     p.runs = dev.runs;
-    const long long cast = layer ? (static_cast<long long>(L.M) * (L.H / 128) + kRouteWarps - 1) / kRouteWarps : 0;
     const int groups = (L.M + kTG - 1) / kTG;
     const bool four = L.E * groups > 2 * dev.sms; // experts a CTA
+    const bool wide = L.wr != nullptr && !four && L.H > 4096;
+    const int threads = !wide ? kRouteThreads : L.H >= 8 * kRouteWide ? kRouteWide : (L.H / 8 + 31) / 32 * 32;
+    const int warps = threads / 32;
+    const long long cast = layer ? (static_cast<long long>(L.M) * (L.H / 128) + warps - 1) / warps : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cast + (L.wr == nullptr ? L.E : (four ? (L.E + 3) / 4 : L.E) * groups)), 1, 1);
-    cfg.blockDim = dim3(kRouteThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (L.flags & FP8BS_FLAG_OVERLAP_PREV) ? 1 : 0;
+    const bool bf = L.wr_type == FP8BS_BF16;
     auto kernel = L.wr == nullptr ? moe_plan_kernel
-                  : L.wr_type == FP8BS_BF16 ? (four ? moe_route_kernel<true, 4> : moe_route_kernel<true, 1>)
-                                            : (four ? moe_route_kernel<false, 4> : moe_route_kernel<false, 1>);
+                  : four ? (bf ? moe_route_kernel<true, 4, kRouteThreads> : moe_route_kernel<false, 4, kRouteThreads>)
+                  : wide ? (bf ? moe_route_kernel<true, 1, kRouteWide> : moe_route_kernel<false, 1, kRouteWide>)
+                         : (bf ? moe_route_kernel<true, 1, kRouteThreads> : moe_route_kernel<false, 1, kRouteThreads>);
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 

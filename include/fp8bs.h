@@ -67,8 +67,9 @@ typedef enum fp8bs_status {
     FP8BS_OK = 0,
     FP8BS_ERR_INVALID_ARG = 1,         /* null pointer, size < 1, ldx < K, bad enum */
     FP8BS_ERR_UNSUPPORTED_SHAPE = 2,   /* M above the entry point's limit (512 for the GEMMs, 64 with the
-                                          greedy choice or without a workspace), K not a multiple of 128
-                                          (64 for the bf16 GEMM), sizes beyond 2^30 */
+                                          greedy choice, without a workspace or for the expert layer), K not
+                                          a multiple of 128 (64 for the bf16 GEMM, 32 for 4 bits), more
+                                          experts than stated, sizes beyond 2^30 */
     FP8BS_ERR_MISALIGNED = 3,          /* a pointer or row stride breaks the alignment stated below */
     FP8BS_ERR_WORKSPACE_TOO_SMALL = 4, /* workspace_bytes below the *_workspace_size() answer */
     FP8BS_ERR_UNSUPPORTED_DEVICE = 5,  /* current device is not sm_103 */

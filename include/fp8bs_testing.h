@@ -68,6 +68,22 @@ FP8BS_API fp8bs_status fp8bs_testhook_gemm_stall(const uint8_t *aq, const float 
                                        int skip_unit, unsigned long long timeout_ns, void *stream);
 
 /*
+ * The same gap in fp4_gemm, and in one of fp8_moe_experts' two products (phase
+ * 0 = gate/up, 1 = down): after the call the status word is non-zero, the
+ * context usable, and the workspace to be zeroed.
+ */
+FP8BS_API fp8bs_status fp8bs_testhook_fp4_stall(const uint8_t *aq, const uint8_t *as_atoms, const float *a_rows,
+                                                const uint8_t *wq, const uint8_t *ws_atoms, const float *w_rows,
+                                                void *y, int M, int N, int K, fp8bs_fp4_format fmt, void *workspace,
+                                                size_t workspace_bytes, int skip_unit, unsigned long long timeout_ns,
+                                                void *stream);
+FP8BS_API fp8bs_status fp8bs_testhook_moe_stall(const void *x, int ldx, const int32_t *ids, const float *weights,
+                                                const uint8_t *w13, const float *s13, const uint8_t *w2,
+                                                const float *s2, void *y, int M, int H, int I, int E, int top_k,
+                                                void *workspace, size_t workspace_bytes, unsigned flags, int phase,
+                                                int skip_unit, unsigned long long timeout_ns, void *stream);
+
+/*
  * fp8_blockscaled_gemm_fused with the schedule planned for `num_sms` SMs
  * (1 .. 4096) instead of the device's: the CTA count, the K ranges of the
  * CTAs and hence the order of the K-split reduction change with it.  Used to

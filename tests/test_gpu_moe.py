@@ -53,7 +53,7 @@ class Layer:
 
 SHAPES = [(1, 1, 1, 128, 128), (1, 8, 2, 512, 256), (3, 5, 5, 128, 384), (8, 16, 4, 1024, 256), (13, 43, 3, 1408, 640),
           (16, 24, 4, 256, 384), (17, 33, 6, 640, 128), (32, 64, 8, 512, 256), (33, 12, 2, 256, 128),
-          (64, 96, 8, 384, 256), (64, 512, 16, 128, 128), (2, 160, 6, 2048, 128)]
+          (64, 96, 8, 384, 256), (64, 300, 16, 128, 128), (2, 160, 6, 2048, 128)]
 
 
 @pytest.mark.parametrize("renorm", [True, False])
