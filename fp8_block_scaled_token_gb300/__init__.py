@@ -652,15 +652,17 @@ def _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt):
 def fp4_quant_weights(w, fmt=FP4_NV, wq=None, ws_atoms=None, w_rows=None):
     """fp32 or bf16 W [N, K] (K % 32 == 0) -> (wq uint8 [ceil(N/128) *
     ceil(K/256), 128, 128] tiled codes, two to a byte, ws_atoms uint8 [tiles *
-    4 or 2, 512] scale atoms, w_rows fp32 [N] row scales (all 1 for FP4_MX))."""
+    4 or 2, 512] scale atoms, w_rows fp32 [N] row scales, None for FP4_MX unless
+    given (then all 1))."""
     torch = _torch()
     N, K, wt, wp = _matrix(w, "w")
     tiles, dev = _fp4_tiles(N, K), w.device
     wq = _out(wq, (tiles, 128, 128), torch.uint8, dev, "wq")
     ws_atoms = _out(ws_atoms, (tiles * _fp4_atoms(fmt), 512), torch.uint8, dev, "ws_atoms")
-    w_rows = _out(w_rows, (N,), torch.float32, dev, "w_rows")
+    if fmt == FP4_NV or w_rows is not None:
+        w_rows = _out(w_rows, (N,), torch.float32, dev, "w_rows")
     _check("fp4_quant_weights", lib().fp4_quant_weights(wp, wt, N, K, fmt, wq.data_ptr(), ws_atoms.data_ptr(),
-                                                        w_rows.data_ptr(), _stream()))
+                                                        _ptr(w_rows), _stream()))
     return wq, ws_atoms, w_rows
 
 
@@ -682,15 +684,16 @@ def fp4_dequant_weights(wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, w=None, dtype=No
 def fp4_quant_act(x, fmt=FP4_NV, xq=None, xs_atoms=None, x_rows=None, flags=0):
     """bf16 X [M, K] (M <= 512, K % 32 == 0; row stride may exceed K) -> (xq
     uint8 [M, ceil(K/256) * 128], xs_atoms uint8 [ceil(M/128) * ceil(K/256) *
-    4 or 2, 512], x_rows fp32 [M])."""
+    4 or 2, 512], x_rows fp32 [M], None for FP4_MX unless given)."""
     torch = _torch()
     M, K, ldx, xp = _act(x)
     kt, dev = (K + 255) // 256, x.device
     xq = _out(xq, (M, kt * 128), torch.uint8, dev, "xq")
     xs_atoms = _out(xs_atoms, ((M + 127) // 128 * kt * _fp4_atoms(fmt), 512), torch.uint8, dev, "xs_atoms")
-    x_rows = _out(x_rows, (M,), torch.float32, dev, "x_rows")
+    if fmt == FP4_NV or x_rows is not None:
+        x_rows = _out(x_rows, (M,), torch.float32, dev, "x_rows")
     _check("fp4_quant_act", lib().fp4_quant_act(xp, M, K, ldx, fmt, xq.data_ptr(), xs_atoms.data_ptr(),
-                                                x_rows.data_ptr(), flags, _stream()))
+                                                _ptr(x_rows), flags, _stream()))
     return xq, xs_atoms, x_rows
 
 

@@ -917,8 +917,8 @@ extern "C" fp8bs_status fp8bs_testhook_fp4_stall(const uint8_t *aq, const uint8_
                                                  size_t workspace_bytes, int skip_unit, unsigned long long timeout_ns,
                                                  void *stream)
 {
-    if (!aq || !as_atoms || !a_rows || !wq || !ws_atoms || !w_rows || !y || !workspace || bad_fp4_format(fmt) ||
-        skip_unit < 0 || timeout_ns == 0 || timeout_ns > 10ull * kDefaultTimeoutNs)
+    if (!aq || !as_atoms || !wq || !ws_atoms || !y || !workspace || bad_fp4_format(fmt) ||
+        (fmt == FP8BS_FP4_NV && (!a_rows || !w_rows)) || skip_unit < 0 || timeout_ns == 0 || timeout_ns > 10ull * kDefaultTimeoutNs)
         return FP8BS_ERR_INVALID_ARG;
     fp8bs_status st = check_gemm_shape(M, N, K, 32);
     if (st == FP8BS_OK)

@@ -152,8 +152,7 @@ template <int NPAD, int MODE> struct GemmCfg {
     // bf16, MX and 4-bit accumulate a whole tile segment in tensor memory (no
     // per-K-block scale to apply on CUDA cores).
     static constexpr bool kTileAcc = MODE == kModeBf16 || kMx || kFp4;
-    // (4-bit: as many stages as the scale-factor columns below leave room for,
-    // with two CTAs of the 16-token tile sharing the 512 columns)
+    // (4-bit: as many stages as the scale-factor columns below leave room for)
     static constexpr int kMaxStages = !kFp4 ? 12 : NPAD == 16 ? 6 : 8;
     // Accumulators in tensor memory (512 fp32 columns per SM, two CTAs of
     // the 16-token tile sharing them): eight for the 16-token tile, so the
@@ -191,7 +190,10 @@ template <int NPAD, int MODE> struct GemmCfg {
     // M = 32 and 48 it loses by 5% and 11% over a whole decode pass (cast
     // kernels included), although it wins by 2-5% in a chain of
     // pre-quantised layers.
-    static constexpr int kMinBlocks = (MODE != kModeFp8Fused && NPAD == 16) ? 2 : 1;
+    // (4-bit: one, with a ring of six stages.  Its units take half the bytes'
+    // time of FP8's while a stage's way round the ring takes as long, so the
+    // deeper ring counts for more: 34,816 x 5,120 at M = 16 24.2 -> 22.8 us.)
+    static constexpr int kMinBlocks = (MODE != kModeFp8Fused && !kFp4 && NPAD == 16) ? 2 : 1;
     // From 64 tokens up the columns of a token tile are split over two groups
     // of four epilogue warps: twice the threads promote each unit, which the
     // wider tiles need more than a second resident CTA (measured in a chain

@@ -382,25 +382,33 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         }
         if (!kUp)
             grid_dependency_wait();
-        // Scales of the next unit to promote, loaded one unit ahead: the
-        // weight blocks', and this lane's token's.
-        float nx_w[C::kTiles], nx_a = 0.0f;
+        // Scales of the units to promote, loaded kAhead units ahead: the weight
+        // blocks', and this lane's token's.
+        struct Scales {
+            float w[C::kTiles], a;
+        };
+        constexpr int kAhead = 2;
+        Scales nx[kAhead];
         auto load_scales = [&](const Unit &v) {
+            Scales r = {};
             if (!unit_ok(v))
-                return;
+                return r;
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t)
-                nx_w[t] = p.ws[weight_tile(v, t) * kg1 + v.kb];
-            nx_a = 0.0f;
+                r.w[t] = p.ws[weight_tile(v, t) * kg1 + v.kb];
             if (lane < C::kCols && lane < mcnt)
-                nx_a = kUp ? __ldcg(p.xs + v.kb * p.M + col0 + lane)
-                           : __ldcg(p.hs + (static_cast<long long>(v.a) * kg1 + v.kb) * NPAD + col0 + lane);
+                r.a = kUp ? __ldcg(p.xs + v.kb * p.M + col0 + lane)
+                          : __ldcg(p.hs + (static_cast<long long>(v.a) * kg1 + v.kb) * NPAD + col0 + lane);
+            return r;
         };
+        Unit un = u; // the unit whose scales are loaded next
 #pragma unroll
-        for (int t = 0; t < C::kTiles; ++t)
-            nx_w[t] = 0.0f;
-        if (nunits > 0)
-            load_scales(u);
+        for (int q = 0; q < kAhead; ++q) {
+            nx[q] = Scales{};
+            if (q < nunits)
+                nx[q] = load_scales(un);
+            step(un);
+        }
         float *const wprod = prod + (warp - 2) * 2 * C::kTiles * C::kCols;
         // up: the tokens' weights for the unit's expert, this lane's tokens
         // lane and lane + 32; read when the expert changes, used at a tile's end
@@ -497,13 +505,17 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
             if (lane < C::kCols) {
 #pragma unroll
                 for (int t = 0; t < C::kTiles; ++t)
-                    pr[t * C::kCols + lane] = nx_w[t] * nx_a;
+                    pr[t * C::kCols + lane] = nx[0].w[t] * nx[0].a;
             }
             __syncwarp();
             Unit nu = u;
             step(nu);
-            if (i + 1 < nunits)
-                load_scales(nu);
+#pragma unroll
+            for (int q = 0; q + 1 < kAhead; ++q)
+                nx[q] = nx[q + 1];
+            if (i + kAhead < nunits)
+                nx[kAhead - 1] = load_scales(un);
+            step(un);
             mbar_wait(&tfull[accb], acc_ph, abort_flag, p.status, kErrTimeoutEpilogue, p.timeout_ns);
             // (a wait that gave up carries on in bounds, as in gemm_kernel.cuh)
             tc_fence_after_sync();

@@ -30,7 +30,7 @@ def _fp4_stall(x, packed, N, fmt, work, skip, limit):
     M, K = x.shape
     y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
     a = fb.fp4_quant_act(x, fmt)
-    ptrs = [t.data_ptr() for t in (*a, *packed)]
+    ptrs = [t.data_ptr() if t is not None else None for t in (*a, *packed)]
     return fb.lib().fp8bs_testhook_fp4_stall(*ptrs, y.data_ptr(), M, N, K, fmt, work.data_ptr(), work.numel(), skip,
                                              limit, _stream())
 

@@ -37,7 +37,7 @@ def _check_packed(wq, wa, wr, v, fmt, tiled):
             np.ones((R, atoms.shape[0] // -(-R // 128) * 4), np.uint8), v.shape[1], fmt) > 0
         got, atoms = got[live], atoms[live]
     assert np.array_equal(got, atoms)
-    assert np.array_equal(wr.cpu().numpy(), r)
+    assert wr is None if fmt == fb.FP4_MX else np.array_equal(wr.cpu().numpy(), r)
     return codes, byte, r
 
 
@@ -166,7 +166,13 @@ def test_reruns_bitwise(M, N, K, fmt):
 def test_row_scales_may_be_left_out_for_mx_only():
     M, N, K = 4, 256, 512
     x, (wq, wa, wr), y_ref, bound = _layer(M, N, K, fb.FP4_MX, seed=4)
+    assert wr is None
     check_y(fb.fp4_gemm_fused(x, wq, wa, None, N, fb.FP4_MX), y_ref, bound, "no row scales")
+    rows = torch.linspace(0.5, 2, N, device="cuda")                # given ones count
+    scaled = rows.double().cpu().numpy()[None]
+    check_y(fb.fp4_gemm_fused(x, wq, wa, rows, N, fb.FP4_MX), y_ref * scaled, bound * scaled, "row scales")
+    assert torch.equal(fb.fp4_quant_weights(torch.zeros(N, K, device="cuda"), fb.FP4_MX, w_rows=rows)[2],
+                       torch.ones(N, device="cuda"))
     with pytest.raises(fb.Fp8bsError) as e:
         fb.fp4_gemm_fused(x, *fb.fp4_quant_weights(torch.zeros(N, K, device="cuda"))[:2], None, N, fb.FP4_NV)
     assert e.value.code == 1
