@@ -165,12 +165,21 @@ def _torch():
 # layers are short (measured: 17.3 us a fused call with the stream taken from
 # torch.cuda.current_stream() and the device from t.device, 10.1 us as here,
 # 4.8 us of it in the library).
+_raw_stream = None
+
+
 def _stream():
     """The current CUDA stream of the current device, as an integer handle."""
+    global _raw_stream
+    if _raw_stream is not None:
+        return _raw_stream[0](_raw_stream[1]())
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:
+        stream = raw(torch.cuda.current_device())  # (this initialises CUDA)
+        _raw_stream = (raw, device)
+        return stream
     return torch.cuda.current_stream().cuda_stream
 
 
