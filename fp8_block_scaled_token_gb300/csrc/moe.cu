@@ -16,8 +16,8 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     w.logits_off = 512;
     w.counters_up_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4);
     w.counters_down_off = w.counters_up_off + up256(active * (I / 128) * 4);
-    w.active_off = w.counters_down_off + up256(static_cast<size_t>(H / 128) * 4);
-    w.ids_off = w.active_off + up256((static_cast<size_t>(kMoeMaxExperts) + 1) * 4);
+    w.masks_off = w.counters_down_off + up256(static_cast<size_t>(H / 128) * 4);
+    w.ids_off = w.masks_off + static_cast<size_t>(kMoeMaxTokens / kMoeTokenGroup) * (kMoeMaxExperts / 32) * 4;
     w.topw_off = w.ids_off + up256(static_cast<size_t>(M) * top_k * 4);
     w.wtok_off = w.topw_off + up256(static_cast<size_t>(M) * top_k * 4);
     w.xq_off = w.wtok_off + up256(static_cast<size_t>(E) * npad * 4);
@@ -31,7 +31,8 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
 
 namespace {
 
-static_assert((kMoeMaxTokens / kMoeTokenGroup + 1 + kMoeMaxExperts / 32) * 4 <= 256, "routing words");
+static_assert((kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32) * 4 <= 256, "routing words");
+static_assert(kMoeMaxTokens / kMoeTokenGroup * (kMoeMaxExperts / 32) * 4 % 256 == 0, "masks");
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

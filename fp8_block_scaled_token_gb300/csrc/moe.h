@@ -17,12 +17,12 @@ inline int moe_token_pad(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 // words and the arrival counters are zero between calls.  The routing alone
 // uses what comes before counters_up_off.
 struct MoeWorkspace {
-    size_t route_off;         // kMoeMaxTokens / kMoeTokenGroup group counters, then the groups' counter,
-                              // then the experts' bit mask (kMoeMaxExperts / 32 words)
+    size_t route_off;         // arrival counters of the kMoeMaxTokens / kMoeTokenGroup groups of tokens, then a
+                              // bit mask of the experts (kMoeMaxExperts / 32 words) for a given choice
     size_t logits_off;        // [M][E] router logits
     size_t counters_up_off;   // arrival counters of the (active expert, 128 of I) pairs
     size_t counters_down_off; // arrival counters of the 128-row tiles of H
-    size_t active_off;        // number of active experts, then their numbers, ascending
+    size_t masks_off;         // [groups of tokens][kMoeMaxExperts / 32] bit masks of the experts they chose
     size_t ids_off;           // [M][top_k] chosen experts, where the caller keeps none
     size_t topw_off;          // [M][top_k] their weights
     size_t wtok_off;          // [E][NPAD] weight of each token for each expert, 0 where not chosen

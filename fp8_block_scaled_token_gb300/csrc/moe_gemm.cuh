@@ -44,7 +44,8 @@ enum MoePhase : int { kMoeUp = 0, kMoeDown = 1 };
 struct MoeGemmParams {
     int M, H, I, E;
     int stages;
-    const int *active;     // number of active experts, then their numbers
+    const unsigned *masks; // [groups][kMoeMaxExperts / 32] experts that each group of tokens chose
+    int groups;
     const float *wtok;     // [E][NPAD]
     const float *ws;       // weight block scales: s13 [E][2I/128][H/128] or s2 [E][H/128][I/128]
     const float *xs;       // up: activation scales [H/128][M]
@@ -84,7 +85,7 @@ template <int NPAD, int PHASE> struct MoeCfg {
     static constexpr int kHeader = 3072; // barriers and flags, then [1024, 3072) the active experts
     static constexpr int kProdFloats = kEpiWarps * 2 * kTiles * kCols; // per warp, by unit parity
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(128, NPAD);
-    static_assert((2 * kMaxStages + 2 * kAcc + 2) * 8 + 12 <= 1024, "header layout");
+    static_assert((2 * kMaxStages + 2 * kAcc + 2) * 8 + 16 <= 1024, "header layout");
     static constexpr int smem_bytes(int stages)
     {
         return 1024 + kHeader + stages * kStageBytes + kProdFloats * 4;
@@ -111,6 +112,7 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_ready + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
+    volatile int *active_count = last_flag + 1;
     int *act = reinterpret_cast<int *>(smem + 1024);            // [kMoeMaxExperts]
     const int S = p.stages;
     uint8_t *ring = smem + C::kHeader;
@@ -144,22 +146,36 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
     }
-    // The list of active experts comes from the routing kernel: the up
-    // product's predecessor, which it waits for here, and the down product's
-    // predecessor's, complete because every CTA of the up product has passed
-    // this wait before it lets this grid start.
+    // The list of active experts, ascending, from the masks that the routing
+    // kernel left: the up product's predecessor, which it waits for here, and
+    // the down product's predecessor's, complete because every CTA of the up
+    // product has passed this wait before it lets this grid start.
     if (kUp)
         grid_dependency_wait();
-    // (the count and the list in one round trip: entries past the count are
-    // whatever the workspace holds, and never used)
-    int A = __ldcg(p.active);
-    for (int i = threadIdx.x; i < p.max_active; i += C::kThreads)
-        act[i] = __ldcg(p.active + 1 + i);
-    A = A < 0 ? 0 : A > p.max_active ? p.max_active : A;
+    if (warp == 2) {
+        unsigned word = 0; // lane w: experts 32 w .. 32 w + 31
+        if (lane < (p.E + 31) / 32) {
+#pragma unroll
+            for (int g = 0; g < kMoeMaxTokens / kMoeTokenGroup; ++g)
+                word |= g < p.groups ? __ldcg(p.masks + g * (kMoeMaxExperts / 32) + lane) : 0u;
+        }
+        int before = 0; // active experts of the words so far
+#pragma unroll 1
+        for (int w = 0; 32 * w < p.E; ++w) {
+            const unsigned bits = __shfl_sync(0xffffffffu, word, w);
+            const int at = before + __popc(bits & ((1u << lane) - 1u));
+            if ((bits >> lane & 1u) && at < p.max_active)
+                act[at] = 32 * w + lane;
+            before += __popc(bits);
+        }
+        if (lane == 0)
+            *active_count = before < p.max_active ? before : p.max_active;
+    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
+    const int A = *active_count;
 
     // K blocks of one expert, tiles of 128 output rows (up: of one expert's I)
     const int kg1 = kUp ? p.H / 128 : p.I / 128;
@@ -169,10 +185,22 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     const long long units = static_cast<long long>(tiles) * kg;
     const int ctas = plan_ctas(units, gridDim.x); // CTAs past the units have none
     const bool has = cta < ctas;
-    const long long u0 = has ? plan_begin(units, ctas, cta) : 0;
-    const int nunits = has ? static_cast<int>(plan_begin(units, ctas, cta + 1) - u0) : 0;
-    const int tile0 = has ? static_cast<int>(u0 / kg) : 0;
-    const int ku0 = has ? static_cast<int>(u0 % kg) : 0; // unit within the tile
+    // plan.cuh's functions, in 32 bits where they fit (64-bit divisions on the
+    // way to the first load are most of a microsecond)
+    const bool narrow = units <= 0xffffffffll / static_cast<long long>(gridDim.x + 1);
+    const unsigned units32 = static_cast<unsigned>(units), ctas32 = static_cast<unsigned>(ctas);
+    auto range_begin = [&](int c) {
+        return narrow ? static_cast<long long>(units32 * static_cast<unsigned>(c) / ctas32) : plan_begin(units, ctas, c);
+    };
+    auto owner = [&](long long u) {
+        return narrow ? static_cast<int>(((static_cast<unsigned>(u) + 1u) * ctas32 + units32 - 1u) / units32) - 1
+                      : plan_owner(units, ctas, u);
+    };
+    const long long u0 = has ? range_begin(cta) : 0;
+    const int nunits = has ? static_cast<int>(range_begin(cta + 1) - u0) : 0;
+    const int tile0 = !has ? 0 : narrow ? static_cast<int>(static_cast<unsigned>(u0) / static_cast<unsigned>(kg))
+                                        : static_cast<int>(u0 / kg);
+    const int ku0 = has ? static_cast<int>(u0 - static_cast<long long>(tile0) * kg) : 0; // unit within the tile
 
     // A unit's place: output tile, active expert, K block of that expert.
     struct Unit {
@@ -369,16 +397,30 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         auto make_plan = [&](int t) {
             const long long tf = static_cast<long long>(t) * kg;
             SplitPlan sp;
-            sp.c_first = plan_owner(units, ctas, tf);
-            sp.c_last = plan_owner(units, ctas, tf + kg - 1);
-            sp.slot_first = 2 * sp.c_first + (plan_begin(units, ctas, sp.c_first) == tf ? 0 : 1);
+            sp.c_first = owner(tf);
+            sp.c_last = owner(tf + kg - 1);
+            sp.slot_first = 2 * sp.c_first + (range_begin(sp.c_first) == tf ? 0 : 1);
             return sp;
         };
-        const int tile_b = has ? static_cast<int>((u0 + nunits - 1) / kg) : 0;
+        const int tile_b = tile0 + (has ? (ku0 + nunits - 1) / kg : 0);
         SplitPlan plan_a = {0, 0, 0}, plan_b = {0, 0, 0};
         if (nunits > 0) {
             plan_a = make_plan(tile0);
             plan_b = tile_b != tile0 ? make_plan(tile_b) : plan_a;
+        }
+        // The weight blocks' scales of the first 32 units to L1 (a lane a unit):
+        // in a short range their first use would wait for memory unit by unit.
+        if (warp == 2 && lane < nunits) {
+            const int ku = ku0 + lane, t = tile0 + ku / kg, r = ku % kg;
+            Unit v;
+            v.ku = r;
+            v.a = kUp ? t / nj : r / kg1;
+            v.j = kUp ? t % nj : t;
+            v.kb = kUp ? r : r % kg1;
+            if (unit_ok(v))
+#pragma unroll
+                for (int q = 0; q < C::kTiles; ++q)
+                    prefetch_l1(p.ws + weight_tile(v, q) * kg1 + v.kb);
         }
         if (!kUp)
             grid_dependency_wait();
@@ -721,7 +763,8 @@ fp8bs_status launch_moe_gemm(const MoeLaunch &L, const MoeWorkspace &w, const De
     p.I = L.I;
     p.E = L.E;
     p.stages = stages;
-    p.active = reinterpret_cast<const int *>(L.workspace + w.active_off);
+    p.masks = reinterpret_cast<const unsigned *>(L.workspace + w.masks_off);
+    p.groups = L.wr != nullptr ? (L.M + kMoeTokenGroup - 1) / kMoeTokenGroup : 1; // (a given choice: one)
     p.wtok = reinterpret_cast<const float *>(L.workspace + w.wtok_off);
     p.ws = kUp ? L.s13 : L.s2;
     p.xs = reinterpret_cast<const float *>(L.workspace + w.xs_off);
