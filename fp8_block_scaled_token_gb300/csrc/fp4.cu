@@ -173,30 +173,39 @@ template <bool kBf16> __device__ __forceinline__ void values16(const Raw16<kBf16
     }
 }
 
-// Their largest magnitude.  For non-negative bf16 or fp32 numbers the bits
-// order like the values.
+// Their largest magnitude (fp32: the bits of non-negative numbers order like
+// the values).
 template <bool kBf16> __device__ __forceinline__ float abs_max16(const Raw16<kBf16> &r)
 {
+    if (kBf16) {
+        __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&r.w[0].x));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[q])));
+        }
+        return fmaxf(__low2float(m), __high2float(m));
+    }
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < (kBf16 ? 2 : 4); ++i) {
-        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            m = kBf16 ? __vmaxu2(m, w[q] & 0x7FFF7FFFu) : max(m, w[q] & 0x7FFFFFFFu);
-    }
-    return __uint_as_float(kBf16 ? max(m << 16, m & 0xFFFF0000u) : m);
+    for (int i = 0; i < (kBf16 ? 2 : 4); ++i)
+        m = max(max(m, max(r.w[i].x & 0x7FFFFFFFu, r.w[i].y & 0x7FFFFFFFu)),
+                max(r.w[i].z & 0x7FFFFFFFu, r.w[i].w & 0x7FFFFFFFu));
+    return __uint_as_float(m);
 }
 
 // Sixteen values -> two words of codes, and in `word` the scale bytes of the
 // lane's atom, each at its place; whole warps call it (the word is put
-// together from the lanes of one atom).  inv6: as nv_scale_code.
+// together from the lanes of one atom).  amax: their abs_max16; inv6: as
+// nv_scale_code.
 template <bool kBf16, bool kNv>
-__device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float r, float inv6, int c, bool live, uint32_t &word)
+__device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, float r, float inv6, int c, bool live,
+                                         uint32_t &word)
 {
     float v[16];
     values16<kBf16>(raw, v);
-    float amax = abs_max16<kBf16>(raw);
     uint2 codes = make_uint2(0u, 0u);
     if (kNv) {
         const uint32_t byte = nv_scale_code(amax, r, inv6);
@@ -274,11 +283,15 @@ __global__ void __launch_bounds__(kRowThreads)
             held[i] = load16<kBf16>(src, c * kFp4Chunk);
     }
     float r = 1.0f, inv6 = 0.0f;
+    float held_amax[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+        held_amax[i] = abs_max16<kBf16>(held[i]);
     if (kNv && real) {
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < kHold; ++i)
-            amax = fmaxf(amax, abs_max16<kBf16>(held[i]));
+            amax = fmaxf(amax, held_amax[i]);
 #pragma unroll 1
         for (int c = static_cast<int>(threadIdx.x) + kHold * kRowThreads; c < whole; c += kRowThreads)
             amax = fmaxf(amax, abs_max16<kBf16>(load16<kBf16>(src, c * kFp4Chunk)));
@@ -294,9 +307,9 @@ __global__ void __launch_bounds__(kRowThreads)
         row_scale[row] = r;
     const int tile = row >> 7, rt = row & 127;
     // whole warps take part in the shuffles of quant16, also past the last chunk
-    auto convert = [&](int c, const Raw16<kBf16> &raw) {
+    auto convert = [&](int c, const Raw16<kBf16> &raw, float amax) {
         uint32_t word;
-        const uint2 codes = quant16<kBf16, kNv>(raw, r, inv6, c, c < whole, word);
+        const uint2 codes = quant16<kBf16, kNv>(raw, amax, r, inv6, c, c < whole, word);
         if (c < chunks) {
             const int kb = c >> 4;
             const long long at = kTiled ? ((static_cast<long long>(tile) * kg + kb) * 128 + rt) * 128 + (c & 15) * 8
@@ -312,13 +325,13 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
         if (i * kRowThreads + (static_cast<int>(threadIdx.x) & ~31) < chunks)
-            convert(static_cast<int>(threadIdx.x) + i * kRowThreads, held[i]);
+            convert(static_cast<int>(threadIdx.x) + i * kRowThreads, held[i], held_amax[i]);
 #pragma unroll 1
     for (int c = static_cast<int>(threadIdx.x) + kHold * kRowThreads; (c & ~31) < chunks; c += kRowThreads) {
         Raw16<kBf16> raw = {};
         if (c < whole)
             raw = load16<kBf16>(src, c * kFp4Chunk);
-        convert(c, raw);
+        convert(c, raw, abs_max16<kBf16>(raw));
     }
 }
 
@@ -392,19 +405,19 @@ fp8bs_status launch_fp4_quant_weights(const void *w, int wtype, int N, int K, in
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((N + 127) / 128) * 128u, 1, 1);
     cfg.stream = stream;
-    // Threads a row: 128 hold 8,192 bf16 values, 256 hold 20,480 (quantising
-    // and reading back: K = 2,080 fp32 in 5.7 us with 128 and 6.8 with 256,
-    // K = 17,408 bf16 in 130 us with 128 and 124 with 256).
+    // Threads a row: 128 hold 8,192 bf16 values, 256 hold 16,384 (quantising
+    // and reading back: 1,000 x 2,080 fp32 in 5.7 us with 128 and 6.8 with
+    // 256, 5,120 x 17,408 bf16 in 130 us with 128 and 123 with 256).
     const bool wide = K > 8192, nv = fmt == FP8BS_FP4_NV;
     cfg.blockDim = dim3(wide ? 256 : 128, 1, 1);
     auto kernel = wtype == FP8BS_BF16
-                      ? (nv ? (wide ? fp4_quant_rows_kernel<true, true, true, 256, 5>
+                      ? (nv ? (wide ? fp4_quant_rows_kernel<true, true, true, 256, 4>
                                     : fp4_quant_rows_kernel<true, true, true, 128, 4>)
-                            : (wide ? fp4_quant_rows_kernel<true, false, true, 256, 5>
+                            : (wide ? fp4_quant_rows_kernel<true, false, true, 256, 4>
                                     : fp4_quant_rows_kernel<true, false, true, 128, 4>))
-                      : (nv ? (wide ? fp4_quant_rows_kernel<false, true, true, 256, 3>
+                      : (nv ? (wide ? fp4_quant_rows_kernel<false, true, true, 256, 2>
                                     : fp4_quant_rows_kernel<false, true, true, 128, 2>)
-                            : (wide ? fp4_quant_rows_kernel<false, false, true, 256, 3>
+                            : (wide ? fp4_quant_rows_kernel<false, false, true, 256, 2>
                                     : fp4_quant_rows_kernel<false, false, true, 128, 2>));
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, w, N, K, static_cast<long long>(K), (K + 255) / 256, wq, sf,
                                             rows, 0, dev.runs));
