@@ -121,8 +121,9 @@ WorkspaceLayout workspace_layout(const GemmShape &sh, int M, int K)
     auto up256 = [](size_t b) { return (b + 255) / 256 * 256; };
     WorkspaceLayout w;
     w.greedy_off = 256;
-    w.counters_off = 1024;
-    w.slots_off = w.counters_off + up256(static_cast<size_t>(sh.ttiles) * sh.ntiles * 4);
+    w.counters_off = kCountersOff;
+    w.counters_bytes = static_cast<size_t>(sh.ttiles) * sh.ntiles * 4;
+    w.slots_off = w.counters_off + counters_region(w.counters_bytes);
     w.act_off = w.slots_off + (sh.split ? static_cast<size_t>(2) * sh.ctas * sh.npad * 128 * 4 : 0);
     w.act_scale_off = w.act_off + up256(static_cast<size_t>(M) * K);
     w.total = w.act_scale_off + up256(static_cast<size_t>(M) * (K / 128) * 4);

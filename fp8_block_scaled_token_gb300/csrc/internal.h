@@ -48,13 +48,24 @@ inline int token_pad(int M)
 // Workspace layout shared by the GEMM launchers:
 //   [0, 256)                status word (+ padding)
 //   [256, 1024)             greedy choice: 64 64-bit keys, then the CTA counter
-//   [1024, 1024 + C)        ttiles * ntiles 32-bit arrival counters, C rounded up to 256
+//   [1024, 1024 + C)        ttiles * ntiles 32-bit arrival counters (counters_region bytes)
 //   slots                   ttiles * 2 * ctas slots of NPAD * 128 fp32 partials
 //   act, act_scale          M x K codes and M x K/128 scales, used only when the
 //                           fused entry point quantises in a separate kernel
 struct WorkspaceLayout {
-    size_t greedy_off, counters_off, slots_off, act_off, act_scale_off, total;
+    size_t greedy_off, counters_off, counters_bytes, slots_off, act_off, act_scale_off, total;
 };
+// What has to be zero between calls lies in the same place for every shape and
+// every operator, with no shape's data in it, so that calls of different
+// shapes may share a workspace: up to 16,384 counters (2 million weight rows at
+// one token tile) have a region of that size; a larger shape's region extends
+// over what others use for data, so it needs a workspace of its own.
+constexpr size_t kCountersOff = 1024;
+constexpr size_t kCountersRegion = 16384 * 4;
+inline size_t counters_region(size_t bytes)
+{
+    return bytes <= kCountersRegion ? kCountersRegion : (bytes + 255) / 256 * 256;
+}
 struct GemmShape;
 WorkspaceLayout workspace_layout(const GemmShape &sh, int M, int K);
 

@@ -12,11 +12,11 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     const size_t npad = static_cast<size_t>(moe_token_pad(M));
     const size_t active = static_cast<size_t>(E < M * top_k ? E : M * top_k);
     MoeWorkspace w;
-    w.route_off = 256;
-    w.logits_off = 512;
-    w.counters_up_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4);
-    w.counters_down_off = w.counters_up_off + up256(active * (I / 128) * 4);
-    w.masks_off = w.counters_down_off + up256(static_cast<size_t>(H / 128) * 4);
+    w.route_off = kMoeRouteOff;
+    w.counters_down_off = kCountersOff;
+    w.counters_up_off = w.counters_down_off + static_cast<size_t>(H / 128) * 4;
+    w.logits_off = kCountersOff + counters_region(static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4);
+    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4);
     w.ids_off = w.masks_off + static_cast<size_t>(kMoeMaxTokens / kMoeTokenGroup) * (kMoeMaxExperts / 32) * 4;
     w.topw_off = w.ids_off + up256(static_cast<size_t>(M) * top_k * 4);
     w.wtok_off = w.topw_off + up256(static_cast<size_t>(M) * top_k * 4);
@@ -31,7 +31,11 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
 
 namespace {
 
-static_assert((kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32) * 4 <= 256, "routing words");
+// The routing words lie behind the GEMMs' greedy keys and counter (64 64-bit
+// words and one 32-bit word from byte 256), which like them are zero between calls.
+static_assert(kMoeRouteOff >= 256 + 64 * 8 + 4 &&
+                  kMoeRouteOff + (kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32) * 4 <= kCountersOff,
+              "routing words");
 static_assert(kMoeMaxTokens / kMoeTokenGroup * (kMoeMaxExperts / 32) * 4 % 256 == 0, "masks");
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -115,7 +119,7 @@ fp8bs_status moe_route_workspace_size(int M, int E, size_t *bytes)
     fp8bs_status st = check_tokens(M, 128, E, 1);
     if (st != FP8BS_OK)
         return st;
-    *bytes = moe_workspace(M, 128, 128, E, 1, 1).counters_up_off;
+    *bytes = moe_workspace(M, 128, 128, E, 1, 1).masks_off;
     return FP8BS_OK;
 }
 
@@ -137,8 +141,8 @@ fp8bs_status moe_route(const void *x, int ldx, const void *wr, fp8bs_dtype wr_ty
     st = current_device(&dev);
     if (st != FP8BS_OK)
         return st;
-    const MoeWorkspace w = moe_workspace(M, H, 128, E, top_k, dev.sms);
-    if (workspace_bytes < w.counters_up_off)
+    const MoeWorkspace w = moe_workspace(M, 128, 128, E, 1, dev.sms); // the routing's part depends on M and E alone
+    if (workspace_bytes < w.masks_off)
         return FP8BS_ERR_WORKSPACE_TOO_SMALL;
     MoeLaunch L = {};
     L.M = M;

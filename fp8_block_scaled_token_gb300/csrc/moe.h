@@ -14,8 +14,10 @@ constexpr int kMoeTokenGroup = 8; // tokens that one routing CTA multiplies an e
 inline int moe_token_pad(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
 // Workspace of one expert layer.  [0, 256) the status word; the routing
-// words and the arrival counters are zero between calls.  The routing alone
-// uses what comes before counters_up_off.
+// words and the arrival counters are zero between calls and where no
+// operator's data lies (internal.h).  The routing alone uses what comes before
+// masks_off.
+constexpr size_t kMoeRouteOff = 832;
 struct MoeWorkspace {
     size_t route_off;         // arrival counters of the kMoeMaxTokens / kMoeTokenGroup groups of tokens, then a
                               // bit mask of the experts (kMoeMaxExperts / 32 words) for a given choice

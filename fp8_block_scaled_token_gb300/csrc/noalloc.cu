@@ -85,7 +85,7 @@ extern "C" fp8bs_status fp8_blockscaled_gemm_fused_noalloc(const void *x, int ld
     // The status word and arrival counters must start at zero; the array
     // keeps whatever the previous call left there.
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    e = cudaMemsetAsync(scratch, 0, wl.slots_off, s);
+    e = cudaMemsetAsync(scratch, 0, wl.counters_off + wl.counters_bytes, s);
     if (e != cudaSuccess)
         return launch_status(e);
 

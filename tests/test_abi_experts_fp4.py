@@ -84,5 +84,5 @@ def test_moe_validation(L):
     assert r(A16, 512, A16, 1, 8, 512, 8, 2, 1, A16, A16, A16, 1 << 20, 2, S) == INVALID    # no weights to be tiled
     sz = ctypes.c_size_t(3)
     assert L.moe_route_workspace_size(8, 600, ctypes.byref(sz)) == SHAPE and sz.value == 0
-    assert L.moe_route_workspace_size(8, 64, ctypes.byref(sz)) == OK and sz.value >= 512 + 8 * 64 * 4
+    assert L.moe_route_workspace_size(8, 64, ctypes.byref(sz)) == OK and sz.value >= 8 * 64 * 4
     assert L.fp8_moe_workspace_size(8, 512, 100, 8, 2, ctypes.byref(sz)) == SHAPE and sz.value == 0
