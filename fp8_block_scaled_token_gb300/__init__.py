@@ -498,6 +498,10 @@ def _act(x):
     ld, unit = x.stride()
     if unit != 1:
         raise ValueError("x must have unit stride along K")
+    if M == 1:
+        ld = K  # one row: whatever its stride says
+    elif ld > 0x7fffffff:
+        raise ValueError("x's row stride does not fit in 32 bits")
     return M, K, ld, x.data_ptr()
 
 

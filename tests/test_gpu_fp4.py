@@ -150,6 +150,14 @@ def test_strided_input_other_stream_and_garbage_workspace_rows(fmt):
     check_y(y, y_ref, bound, "strided")
 
 
+def test_single_row_of_any_stride():
+    """One row of a matrix whose rows overlap or lie far apart."""
+    M, N, K = 1, 256, 512
+    x, packed, y_ref, bound = _layer(M, N, K, fb.FP4_NV, seed=14)
+    for ld in (0, 8, 3 * K + 3):
+        check_y(fb.fp4_gemm_fused(x.as_strided((1, K), (ld, 1)), *packed, N), y_ref, bound, "stride %d" % ld)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K", [(8, 5120, 5120), (300, 1024, 4096)])
 def test_reruns_bitwise(M, N, K, fmt):
