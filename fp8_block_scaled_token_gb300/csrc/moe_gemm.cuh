@@ -24,6 +24,14 @@
 // tile shared by CTAs is summed in contributor order by the last one to
 // arrive: results repeat bit for bit, and no CTA waits for another.
 //
+// Measured (8 tokens, 64 experts, top 4, H = 5,120, I = 1,280): the up product
+// reads its 341 MB at 7.0 TB/s between its first and last MMA, the down
+// product 171 MB at 6.4; before, between and after them lie the routing (9 us
+// until the first weights can be named), 4 us and 3 us.  64 tokens and 64
+// experts of (5,120, 1,408): the layer 235-240 us, 0.85 of the measured copy
+// bandwidth; there one CTA fills an SM and the next product cannot start
+// early.
+//
 // Warp 0 streams the tiles (TMA), warp 1 issues tcgen05.mma, the others
 // promote each unit's accumulators by their scales into fp32 registers, as in
 // gemm_kernel.cuh.  Every wait is bounded.
