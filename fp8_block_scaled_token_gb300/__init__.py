@@ -153,9 +153,11 @@ _torch_module = None
 
 
 def _torch():
-    global _torch_module
+    """torch, imported at the first call that needs it."""
+    global _torch_module, _bf16, _f32, _i32, _u8, _empty
     if _torch_module is None:
         import torch
+        _bf16, _f32, _i32, _u8, _empty = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.empty
         _torch_module = torch
     return _torch_module
 
@@ -491,9 +493,10 @@ def _addr(t, dtype, numel, name):
 
 def _act(x):
     """(M, K, row stride, address) of bf16 activations [M, K]."""
-    torch = _torch()
-    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 2:
-        _need(x, torch.bfloat16, "x")
+    if _torch_module is None:
+        _torch()
+    if x.dtype is not _bf16 or not x.is_cuda or x.dim() != 2:
+        _need(x, _bf16, "x")
     M, K = x.shape
     ld, unit = x.stride()
     if unit != 1:
@@ -507,31 +510,32 @@ def _act(x):
 
 def _matrix(w, name):
     """(rows, K, dtype code, address) of a contiguous fp32 or bf16 matrix."""
-    torch = _torch()
+    if _torch_module is None:
+        _torch()
     t = w.dtype
-    if t is not torch.bfloat16 and t is not torch.float32:
+    if t is not _bf16 and t is not _f32:
         raise TypeError("%s must be float32 or bfloat16" % name)
     if not w.is_cuda or w.dim() != 2:
         _need(w, t, name)
     if not w.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     rows, K = w.shape
-    return rows, K, BF16 if t is torch.bfloat16 else F32, w.data_ptr()
+    return rows, K, BF16 if t is _bf16 else F32, w.data_ptr()
 
 
 def _out(t, shape, dtype, device, name):
-    """`t` checked as an output of that shape (contiguous), or a new one."""
+    """(tensor, address) of an output: `t` checked (that shape, contiguous), or a new one."""
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    _need(t, dtype, name, len(shape))
-    if t.shape != shape or not t.is_contiguous():
+        t = _empty(shape, dtype=dtype, device=device)
+    elif t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, name, len(shape))
         raise ValueError("%s must be contiguous of shape %s" % (name, shape))
-    return t
+    return t, t.data_ptr()
 
 
 def _work(workspace):
     """(address, bytes) of a workspace."""
-    if workspace.dtype is not _torch().uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+    if workspace.dtype is not _u8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor of bytes (make_workspace)")
     return workspace.data_ptr(), workspace.numel()
 
@@ -551,15 +555,14 @@ def fp8_moe_workspace_size(M, H, I, E, top_k):
 def _experts(w13, s13, w2, s2, H, E):
     """(I, flag, addresses of w13, s13, w2, s2) of E experts' weights: w13 [E,
     2I, H] and w2 [E, H, I], or both tiled [tiles, 128, 128]."""
-    torch = _torch()
     kg = H // 128
     if E < 1 or s2.dim() != 2 or s13.dim() != 2:
         raise ValueError("operand shapes do not agree")
-    rows = s2.shape[1]  # 128-row tiles of I
+    rows2, rows = s2.shape  # rows: 128-row tiles of I
     tiles = E * rows * kg
-    I = rows * 128
-    if tiles < 1 or s2.shape[0] != E * kg or s13.shape != (2 * E * rows, kg):
+    if tiles < 1 or rows2 != E * kg or s13.shape != (2 * E * rows, kg):
         raise ValueError("operand shapes do not agree")
+    I = rows * 128
     shape13, shape2 = w13.shape, w2.shape
     if shape13 == (2 * tiles, 128, 128) and shape2 == (tiles, 128, 128):
         flag = FLAG_WEIGHTS_TILED
@@ -567,9 +570,8 @@ def _experts(w13, s13, w2, s2, H, E):
         flag = 0
     else:
         raise ValueError("operand shapes do not agree")
-    u8, f32 = torch.uint8, torch.float32
-    return (I, flag, _addr(w13, u8, 2 * tiles * 16384, "w13"), _addr(s13, f32, 2 * tiles, "s13"),
-            _addr(w2, u8, tiles * 16384, "w2"), _addr(s2, f32, tiles, "s2"))
+    return (I, flag, _addr(w13, _u8, 2 * tiles * 16384, "w13"), _addr(s13, _f32, 2 * tiles, "s13"),
+            _addr(w2, _u8, tiles * 16384, "w2"), _addr(s2, _f32, tiles, "s2"))
 
 
 def moe_route(x, wr, top_k, renormalize=True, ids=None, weights=None, workspace=None, flags=0):
@@ -577,18 +579,17 @@ def moe_route(x, wr, top_k, renormalize=True, ids=None, weights=None, workspace=
     fp32 or bf16 [E, H] -> (ids int32 [M, top_k] by descending logit, weights
     fp32 [M, top_k], softmax over the chosen or, with renormalize=False, over
     all experts)."""
-    torch = _torch()
     M, H, ldx, xp = _act(x)
     E, Hr, wt, wrp = _matrix(wr, "wr")
     if H != Hr:
         raise ValueError("operand shapes do not agree")
-    ids = _out(ids, (M, top_k), torch.int32, x.device, "ids")
-    weights = _out(weights, (M, top_k), torch.float32, x.device, "weights")
+    ids, idp = _out(ids, (M, top_k), _i32, x.device, "ids")
+    weights, wp = _out(weights, (M, top_k), _f32, x.device, "weights")
     if workspace is None:
         workspace = make_workspace(moe_route_workspace_size(M, E), x.device)
     wsp, wsn = _work(workspace)
-    _check("moe_route", lib().moe_route(xp, ldx, wrp, wt, M, H, E, top_k, 1 if renormalize else 0, ids.data_ptr(),
-                                        weights.data_ptr(), wsp, wsn, flags, _stream()))
+    _check("moe_route", lib().moe_route(xp, ldx, wrp, wt, M, H, E, top_k, 1 if renormalize else 0, idp, wp,
+                                        wsp, wsn, flags, _stream()))
     return ids, weights
 
 
@@ -598,7 +599,6 @@ def fp8_moe_experts(x, ids, weights, w13, s13, w2, s2, experts=None, y=None, wor
     [experts, 2I, H] and w2 [experts, H, I] E4M3 row-major, or both tiled
     (fp8_quant_weight_blocks of the matrices with the experts' rows stacked)
     with experts= given; s13, s2 their block scales."""
-    torch = _torch()
     M, H, ldx, xp = _act(x)
     if experts is None:
         if w13.dim() != 3 or w13.shape[2] != H:
@@ -609,13 +609,13 @@ def fp8_moe_experts(x, ids, weights, w13, s13, w2, s2, experts=None, y=None, wor
     if ids.dim() != 2 or ids.shape[0] != M or ids.shape != weights.shape:
         raise ValueError("operand shapes do not agree")
     k = ids.shape[1]
-    idp, wp = _addr(ids, torch.int32, M * k, "ids"), _addr(weights, torch.float32, M * k, "weights")
-    y = _out(y, (M, H), torch.bfloat16, x.device, "y")
+    idp, wp = _addr(ids, _i32, M * k, "ids"), _addr(weights, _f32, M * k, "weights")
+    y, yp = _out(y, (M, H), _bf16, x.device, "y")
     if workspace is None:
         workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, k), x.device)
     wsp, wsn = _work(workspace)
-    _check("fp8_moe_experts", lib().fp8_moe_experts(xp, ldx, idp, wp, w13p, s13p, w2p, s2p, y.data_ptr(), M, H, I, E, k,
-                                                    wsp, wsn, flags | tf, _stream()))
+    _check("fp8_moe_experts", lib().fp8_moe_experts(xp, ldx, idp, wp, w13p, s13p, w2p, s2p, yp, M, H, I, E, k, wsp, wsn,
+                                                    flags | tf, _stream()))
     return y
 
 
@@ -624,22 +624,20 @@ def fp8_moe_layer(x, wr, top_k, w13, s13, w2, s2, renormalize=True, y=None, ids=
     """The whole layer, moe_route and fp8_moe_experts in three kernels: (y
     bf16 [M, H], ids int32 [M, top_k], weights fp32 [M, top_k]); w13 and w2 as
     in fp8_moe_experts, row-major or tiled."""
-    torch = _torch()
     M, H, ldx, xp = _act(x)
     E, Hr, wt, wrp = _matrix(wr, "wr")
     if H != Hr:
         raise ValueError("operand shapes do not agree")
     I, tf, w13p, s13p, w2p, s2p = _experts(w13, s13, w2, s2, H, E)
     dev = x.device
-    y = _out(y, (M, H), torch.bfloat16, dev, "y")
-    ids = _out(ids, (M, top_k), torch.int32, dev, "ids")
-    weights = _out(weights, (M, top_k), torch.float32, dev, "weights")
+    y, yp = _out(y, (M, H), _bf16, dev, "y")
+    ids, idp = _out(ids, (M, top_k), _i32, dev, "ids")
+    weights, wp = _out(weights, (M, top_k), _f32, dev, "weights")
     if workspace is None:
         workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, top_k), dev)
     wsp, wsn = _work(workspace)
     _check("fp8_moe_layer", lib().fp8_moe_layer(xp, ldx, wrp, wt, 1 if renormalize else 0, w13p, s13p, w2p, s2p,
-                                                y.data_ptr(), ids.data_ptr(), weights.data_ptr(), M, H, I, E, top_k,
-                                                wsp, wsn, flags | tf, _stream()))
+                                                yp, idp, wp, M, H, I, E, top_k, wsp, wsn, flags | tf, _stream()))
     return y, ids, weights
 
 
@@ -656,10 +654,11 @@ def _fp4_atoms(fmt):
 
 def _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt):
     """Addresses of packed 4-bit weights (w_rows may be None: all 1, FP4_MX only)."""
-    torch = _torch()
-    u8, tiles = torch.uint8, _fp4_tiles(N, K)
-    return (_addr(wq, u8, tiles * 16384, "wq"), _addr(ws_atoms, u8, tiles * _fp4_atoms(fmt) * 512, "ws_atoms"),
-            _addr(w_rows, torch.float32, N, "w_rows") if w_rows is not None else None)
+    if _torch_module is None:
+        _torch()
+    tiles = _fp4_tiles(N, K)
+    return (_addr(wq, _u8, tiles * 16384, "wq"), _addr(ws_atoms, _u8, tiles * _fp4_atoms(fmt) * 512, "ws_atoms"),
+            None if w_rows is None else _addr(w_rows, _f32, N, "w_rows"))
 
 
 def fp4_quant_weights(w, fmt=FP4_NV, wq=None, ws_atoms=None, w_rows=None):
@@ -667,30 +666,30 @@ def fp4_quant_weights(w, fmt=FP4_NV, wq=None, ws_atoms=None, w_rows=None):
     ceil(K/256), 128, 128] tiled codes, two to a byte, ws_atoms uint8 [tiles *
     4 or 2, 512] scale atoms, w_rows fp32 [N] row scales, None for FP4_MX unless
     given (then all 1))."""
-    torch = _torch()
     N, K, wt, wp = _matrix(w, "w")
     tiles, dev = _fp4_tiles(N, K), w.device
-    wq = _out(wq, (tiles, 128, 128), torch.uint8, dev, "wq")
-    ws_atoms = _out(ws_atoms, (tiles * _fp4_atoms(fmt), 512), torch.uint8, dev, "ws_atoms")
+    atoms = tiles * _fp4_atoms(fmt)
+    wq, qp = _out(wq, (tiles, 128, 128), _u8, dev, "wq")
+    ws_atoms, ap = _out(ws_atoms, (atoms, 512), _u8, dev, "ws_atoms")
+    rp = None
     if fmt == FP4_NV or w_rows is not None:
-        w_rows = _out(w_rows, (N,), torch.float32, dev, "w_rows")
-    _check("fp4_quant_weights", lib().fp4_quant_weights(wp, wt, N, K, fmt, wq.data_ptr(), ws_atoms.data_ptr(),
-                                                        _ptr(w_rows), _stream()))
+        w_rows, rp = _out(w_rows, (N,), _f32, dev, "w_rows")
+    _check("fp4_quant_weights", lib().fp4_quant_weights(wp, wt, N, K, fmt, qp, ap, rp, _stream()))
     return wq, ws_atoms, w_rows
 
 
 def fp4_dequant_weights(wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, w=None, dtype=None):
     """The values [n, k] (fp32, or bf16 with dtype=torch.bfloat16) that packed
     4-bit weights stand for (w_rows None: all 1, FP4_MX only)."""
-    torch = _torch()
     N, K = int(n), int(k)
     qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
-    dtype = dtype or (w.dtype if w is not None else torch.float32)
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+    if dtype is None:
+        dtype = _f32 if w is None else w.dtype
+    if dtype is not _f32 and dtype is not _bf16:
         raise TypeError("w must be float32 or bfloat16")
-    w = _out(w, (N, K), dtype, wq.device, "w")
-    _check("fp4_dequant_weights", lib().fp4_dequant_weights(qp, ap, rp, N, K, fmt, w.data_ptr(),
-                                                            BF16 if dtype is torch.bfloat16 else F32, _stream()))
+    w, op = _out(w, (N, K), dtype, wq.device, "w")
+    _check("fp4_dequant_weights", lib().fp4_dequant_weights(qp, ap, rp, N, K, fmt, op, BF16 if dtype is _bf16 else F32,
+                                                            _stream()))
     return w
 
 
@@ -698,15 +697,15 @@ def fp4_quant_act(x, fmt=FP4_NV, xq=None, xs_atoms=None, x_rows=None, flags=0):
     """bf16 X [M, K] (M <= 512, K % 32 == 0; row stride may exceed K) -> (xq
     uint8 [M, ceil(K/256) * 128], xs_atoms uint8 [ceil(M/128) * ceil(K/256) *
     4 or 2, 512], x_rows fp32 [M], None for FP4_MX unless given)."""
-    torch = _torch()
     M, K, ldx, xp = _act(x)
     kt, dev = (K + 255) // 256, x.device
-    xq = _out(xq, (M, kt * 128), torch.uint8, dev, "xq")
-    xs_atoms = _out(xs_atoms, ((M + 127) // 128 * kt * _fp4_atoms(fmt), 512), torch.uint8, dev, "xs_atoms")
+    atoms = (M + 127) // 128 * kt * _fp4_atoms(fmt)
+    xq, qp = _out(xq, (M, kt * 128), _u8, dev, "xq")
+    xs_atoms, ap = _out(xs_atoms, (atoms, 512), _u8, dev, "xs_atoms")
+    rp = None
     if fmt == FP4_NV or x_rows is not None:
-        x_rows = _out(x_rows, (M,), torch.float32, dev, "x_rows")
-    _check("fp4_quant_act", lib().fp4_quant_act(xp, M, K, ldx, fmt, xq.data_ptr(), xs_atoms.data_ptr(),
-                                                _ptr(x_rows), flags, _stream()))
+        x_rows, rp = _out(x_rows, (M,), _f32, dev, "x_rows")
+    _check("fp4_quant_act", lib().fp4_quant_act(xp, M, K, ldx, fmt, qp, ap, rp, flags, _stream()))
     return xq, xs_atoms, x_rows
 
 
@@ -719,33 +718,32 @@ def fp4_gemm_workspace_size(M, N, K, fmt=FP4_NV):
 def fp4_gemm(aq, as_atoms, a_rows, wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, y=None, workspace=None, flags=0):
     """Y[M, n] bf16 from 4-bit operands (fp4_quant_act / fp4_quant_weights;
     n = the number of weight rows, k = the unpadded K)."""
-    torch = _torch()
     M, N, K = aq.shape[0], int(n), int(k)
     kt = (K + 255) // 256
     qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
-    aqp = _addr(aq, torch.uint8, M * kt * 128, "aq")
-    asp = _addr(as_atoms, torch.uint8, (M + 127) // 128 * kt * _fp4_atoms(fmt) * 512, "as_atoms")
-    arp = _addr(a_rows, torch.float32, M, "a_rows") if a_rows is not None else None
-    y = _out(y, (M, N), torch.bfloat16, aq.device, "y")
+    aqp = _addr(aq, _u8, M * kt * 128, "aq")
+    asp = _addr(as_atoms, _u8, (M + 127) // 128 * kt * _fp4_atoms(fmt) * 512, "as_atoms")
+    arp = None if a_rows is None else _addr(a_rows, _f32, M, "a_rows")
+    y, yp = _out(y, (M, N), _bf16, aq.device, "y")
     if workspace is None:
         workspace = make_workspace(fp4_gemm_workspace_size(M, N, K, fmt), aq.device)
     wsp, wsn = _work(workspace)
-    _check("fp4_gemm", lib().fp4_gemm(aqp, asp, arp, qp, ap, rp, y.data_ptr(), M, N, K, fmt, wsp, wsn, flags, _stream()))
+    _check("fp4_gemm", lib().fp4_gemm(aqp, asp, arp, qp, ap, rp, yp, M, N, K, fmt, wsp, wsn, flags,
+                                      _stream()))
     return y
 
 
 def fp4_gemm_fused(x, wq, ws_atoms, w_rows, n, fmt=FP4_NV, y=None, workspace=None, flags=0):
     """Y[M, n] bf16 from bf16 activations (row stride may exceed K) and packed
     4-bit weights: the cast into the workspace, then the product."""
-    torch = _torch()
     M, K, ldx, xp = _act(x)
     N = int(n)
     qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
-    y = _out(y, (M, N), torch.bfloat16, x.device, "y")
+    y, yp = _out(y, (M, N), _bf16, x.device, "y")
     if workspace is None:
         workspace = make_workspace(fp4_gemm_workspace_size(M, N, K, fmt), x.device)
     wsp, wsn = _work(workspace)
-    _check("fp4_gemm_fused", lib().fp4_gemm_fused(xp, ldx, qp, ap, rp, y.data_ptr(), M, N, K, fmt, wsp, wsn, flags,
+    _check("fp4_gemm_fused", lib().fp4_gemm_fused(xp, ldx, qp, ap, rp, yp, M, N, K, fmt, wsp, wsn, flags,
                                                   _stream()))
     return y
 
