@@ -93,7 +93,7 @@ template <int NPAD, int PHASE> struct MoeCfg {
     static constexpr int kHeader = 3072; // barriers and flags, then [1024, 3072) the active experts
     static constexpr int kProdFloats = kEpiWarps * 2 * kTiles * kCols; // per warp, by unit parity
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(128, NPAD);
-    static_assert((2 * kMaxStages + 2 * kAcc + 2) * 8 + 16 <= 1024, "header layout");
+    static_assert((2 * kMaxStages + 2 * kAcc + 1) * 8 + 16 <= 1024, "header layout");
     static constexpr int smem_bytes(int stages)
     {
         return 1024 + kHeader + stages * kStageBytes + kProdFloats * 4;
@@ -116,8 +116,7 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     uint64_t *tfull = empty + C::kMaxStages;
     uint64_t *tempty = tfull + C::kAcc;
     uint64_t *mma_done = tempty + C::kAcc;
-    uint64_t *red_ready = mma_done + 1; // down: bulk copies of the exchange slots (last segment)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_ready + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
     volatile int *active_count = last_flag + 1;
@@ -140,7 +139,6 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
             mbar_init(&tempty[a], C::kEpiWarps);
         }
         mbar_init(mma_done, 1);
-        mbar_init(red_ready, 1);
         *abort_flag = 0;
         *last_flag = 0;
         fence_mbar_init();
@@ -191,7 +189,17 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     const int kg = kUp ? kg1 : A * kg1;           // units per output tile
     const int tiles = kUp ? A * nj : nj;
     const long long units = static_cast<long long>(tiles) * kg;
-    const int ctas = plan_ctas(units, gridDim.x); // CTAs past the units have none
+    // A tile's exchange takes time in proportion to its contributors n, its
+    // product kg / n: small layers use sqrt(kg) contributors a tile, not every
+    // SM.  Down, tokens x experts x (H, I), with the cap and without: 20 x 16 x
+    // (512, 256) 18.3 and 23.5 us, 50 x 24 x (896, 640) 32.5 and 35.0, one token
+    // and 2 experts of (2,048, 1,408) 17.8 and 18.8; large layers have fewer
+    // than that anyway.  Up: 40 x 8 x (1,280, 384) 20.8 and 22.7, but one token
+    // and 2 experts of (512, 256) 13.7 and 13.5: from 32 columns only.
+    const int contributors = static_cast<int>(ceilf(sqrtf(static_cast<float>(kg))));
+    const int most = (kUp && NPAD == 16) || tiles * contributors > static_cast<int>(gridDim.x)
+                         ? static_cast<int>(gridDim.x) : tiles * contributors;
+    const int ctas = plan_ctas(units, most); // CTAs past the units have none
     const bool has = cta < ctas;
     // plan.cuh's functions, in 32 bits where they fit (64-bit divisions on the
     // way to the first load are most of a microsecond)
@@ -397,7 +405,6 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         uint32_t acc_ph = 0;
         Unit u = first_unit();
         int tile = tile0, seg_first = ku0;
-        bool bulk_issued = false; // warp 2 lane 0: slot copies into the ring
         // Contributors of the (at most two) tiles this CTA shares, as in gemm_kernel.cuh.
         struct SplitPlan {
             int c_first, c_last, slot_first;
@@ -547,6 +554,63 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
             }
         };
 
+        // down: a tile's sum over its contributors, a warp a token (four rows
+        // a lane).  The time is the L2's round trips: kTok tokens of kCon
+        // contributors, up to 24 KB a warp, are in flight at a time, and the
+        // loops over more of either stay rolled.  (Thread = row, six
+        // contributors of eight tokens, took 41.6 us where this takes 35.0, a
+        // layer of 50 tokens with 22 contributors a tile; bulk copies into the
+        // idle ring, eight in flight, 40.6.)
+        auto finish_down = [&](int c_first, int c_last, int slot_first) {
+            constexpr int kTok = NPAD == 64 ? 2 : 4, kCon = NPAD == 16 ? 6 : 12;
+            const int ew = warp - 2;
+            uint16_t *const y = p.y + u.j * 128 + 4 * lane;
+            const bool y_wide = (reinterpret_cast<uintptr_t>(p.y) & 7u) == 0; // (the entry asks for two bytes)
+#pragma unroll 1
+            for (int m0 = ew; m0 < p.M; m0 += kTok * C::kEpiWarps) {
+                float sum[kTok][4] = {};
+#pragma unroll 1
+                for (int c0 = c_first; c0 <= c_last; c0 += kCon) {
+                    float4 v[kCon][kTok];
+#pragma unroll
+                    for (int q = 0; q < kCon; ++q) {
+                        const int c = c0 + q;
+                        const float *const src =
+                            p.slots + static_cast<long long>(c == c_first ? slot_first : 2 * c) * kSlot + 4 * lane;
+#pragma unroll
+                        for (int t = 0; t < kTok; ++t) {
+                            const int m = m0 + t * C::kEpiWarps;
+                            v[q][t] = c <= c_last && m < p.M ? __ldcg(reinterpret_cast<const float4 *>(src + m * 128))
+                                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < kCon; ++q)
+                        if (c0 + q <= c_last)
+#pragma unroll
+                            for (int t = 0; t < kTok; ++t) {
+                                add2(sum[t][0], sum[t][1], v[q][t].x, v[q][t].y);
+                                add2(sum[t][2], sum[t][3], v[q][t].z, v[q][t].w);
+                            }
+                }
+#pragma unroll
+                for (int t = 0; t < kTok; ++t) {
+                    if (m0 + t * C::kEpiWarps >= p.M)
+                        break;
+                    uint16_t *const to = y + static_cast<long long>(m0 + t * C::kEpiWarps) * p.H;
+                    ushort4 b;
+                    b.x = __bfloat16_as_ushort(__float2bfloat16_rn(sum[t][0]));
+                    b.y = __bfloat16_as_ushort(__float2bfloat16_rn(sum[t][1]));
+                    b.z = __bfloat16_as_ushort(__float2bfloat16_rn(sum[t][2]));
+                    b.w = __bfloat16_as_ushort(__float2bfloat16_rn(sum[t][3]));
+                    if (y_wide)
+                        *reinterpret_cast<ushort4 *>(to) = b;
+                    else
+                        to[0] = b.x, to[1] = b.y, to[2] = b.z, to[3] = b.w;
+                }
+            }
+        };
+
         for (int i = 0; i < nunits; ++i) {
             const bool seg_end = (i == nunits - 1) || (u.ku == kg - 1);
             // s_w * s_a of this unit's tokens, per warp (double-buffered by
@@ -628,68 +692,7 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                         if (warp == 2 && lane == 0 && !whole)
                             p.counters[tile] = 0u; // ready for the next call
                     } else if (!kUp && *last_flag) {
-#pragma unroll
-                        for (int t = 0; t < C::kTiles; ++t)
-#pragma unroll
-                            for (int m = 0; m < C::kCols; ++m)
-                                acc[t][m] = 0.0f;
-                        if constexpr (!kUp) {
-                            // as in gemm_kernel.cuh: at the range's last segment
-                            // from 32 tokens up the weight ring is idle and takes
-                            // every contributor's slot by bulk copy, one round
-                            // trip; otherwise through registers, six
-                            // contributors' loads in flight
-                            constexpr int kSlotBytes = kSlot * 4;
-                            const int ncon = pl.c_last - pl.c_first + 1;
-                            const bool bulk = NPAD >= 32 && i == nunits - 1 && ncon * kSlotBytes <= S * C::kStageBytes;
-                            if (bulk) {
-                                if (warp == 2 && lane == 0) {
-                                    fence_proxy_async_global(); // the partials were stored by generic writes
-                                    mbar_arrive_expect_tx(red_ready, static_cast<uint32_t>(ncon * kSlotBytes));
-                                    const uint64_t pol = l2_policy_evict_first();
-                                    for (int j = 0; j < ncon; ++j)
-                                        bulk_load_1d(ring + j * kSlotBytes,
-                                                     p.slots + static_cast<long long>(slot_of(pl.c_first + j)) * kSlot,
-                                                     kSlotBytes, red_ready, pol);
-                                    bulk_issued = true;
-                                }
-                                mbar_wait(red_ready, 0, abort_flag, p.status, kErrTimeoutEpilogue, p.timeout_ns);
-                                const float *sm = reinterpret_cast<const float *>(ring) + col0 * 128 + row;
-                                for (int j = 0; j < ncon; ++j)
-#pragma unroll
-                                    for (int m = 0; m < C::kCols; m += 2)
-                                        if (m < mcnt) // (column m + 1 >= M is never stored)
-                                            add2(acc[0][m], acc[0][m + 1], sm[j * kSlot + m * 128],
-                                                 sm[j * kSlot + (m + 1) * 128]);
-                            }
-                            constexpr int kMaxC = 6, kMC = NPAD == 16 ? 16 : 8;
-                            for (int c0 = bulk ? pl.c_last + 1 : pl.c_first; c0 <= pl.c_last; c0 += kMaxC) {
-                                const int nc = pl.c_last - c0 + 1 < kMaxC ? pl.c_last - c0 + 1 : kMaxC;
-                                const float *src[kMaxC];
-#pragma unroll
-                                for (int j = 0; j < kMaxC; ++j)
-                                    src[j] = p.slots + static_cast<long long>(slot_of(c0 + (j < nc ? j : 0))) * kSlot +
-                                             col0 * 128 + row;
-#pragma unroll
-                                for (int mc = 0; mc < C::kCols; mc += kMC) {
-                                    if (mc >= mcnt)
-                                        break;
-                                    float v[kMaxC][kMC];
-#pragma unroll
-                                    for (int j = 0; j < kMaxC; ++j)
-#pragma unroll
-                                        for (int q = 0; q < kMC; ++q)
-                                            v[j][q] = (j < nc && mc + q < mcnt) ? __ldcg(src[j] + (mc + q) * 128) : 0.0f;
-#pragma unroll
-                                    for (int j = 0; j < kMaxC; ++j)
-#pragma unroll
-                                        for (int q = 0; q < kMC; ++q)
-                                            if (j < nc)
-                                                acc[0][mc + q] += v[j][q];
-                                }
-                            }
-                        }
-                        store_y();
+                        finish_down(pl.c_first, pl.c_last, pl.slot_first);
                         if (warp == 2 && lane == 0)
                             p.counters[tile] = 0u;
                     }
@@ -706,16 +709,6 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                     load_weights(nu.a);
             }
             u = nu;
-        }
-        // the slot copies have landed before the CTA exits, also when the wait gave up
-        if (bulk_issued) {
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_test(red_ready, 0)) {
-                if (globaltimer_ns() - t0 > p.timeout_ns) {
-                    atomicOr(p.status, kErrTimeoutEpilogue);
-                    break;
-                }
-            }
         }
         // No token chose any expert: the layer's output is zero.
         if (!kUp && A == 0) {

@@ -84,6 +84,29 @@ def test_layer_matches_64_bits(M, E, k, H, I, renorm):
     assert torch.equal(y2.view(torch.int16), y.view(torch.int16))
 
 
+# few tiles of Y and many K blocks to each (7 to 41 contributors to a tile where
+# every SM takes part), and tokens that do not divide by the warps of the sum
+DEEP = [(50, 24, 6, 896, 640), (20, 16, 2, 512, 256), (29, 58, 8, 1024, 256), (64, 40, 8, 128, 1408),
+        (40, 8, 2, 1280, 384), (15, 60, 4, 384, 768), (1, 24, 8, 128, 1152)]
+
+
+@pytest.mark.parametrize("M,E,k,H,I", DEEP)
+def test_deep_tiles_and_an_output_at_any_two_byte_address(M, E, k, H, I):
+    t = Layer(M, E, k, H, I, seed=M + E)
+    ops, work = t.operands(), t.workspace()
+    y, ids, w = fb.fp8_moe_layer(t.x.cuda(), t.wr.cuda(), k, *ops, workspace=work)
+    y_ref, bound = ref.experts(t.x64(), ids.cpu().numpy(), w.cpu().numpy(), t.v13, t.v2)
+    check_y(y, y_ref, bound, "moe %s" % (t.dims,))
+    buf = torch.full((M * H + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    for first in (1, 2, 3, 4):
+        buf.fill_(7.0)
+        out = buf[first:first + M * H].view(M, H)
+        fb.fp8_moe_layer(t.x.cuda(), t.wr.cuda(), k, *ops, y=out, workspace=work)
+        assert torch.equal(out.view(torch.int16), y.view(torch.int16))
+        assert (buf[:first] == 7.0).all() and (buf[first + M * H:] == 7.0).all()
+    assert fb.workspace_status(work) == 0
+
+
 def test_row_major_weights_give_the_same_bits():
     t = Layer(9, 12, 3, 640, 384, seed=3)
     a = fb.fp8_moe_layer(t.x.cuda(), t.wr.cuda(), 3, *t.operands(True))[0]
