@@ -80,16 +80,18 @@ template <int NPAD, int PHASE> struct MoeCfg {
     static constexpr int kAccCols = kTiles * NPAD;
     static constexpr int kTmemCols = kAcc * kAccCols; // 128 (16 tokens), 256 / 128 (32), 512 / 256 (64)
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
-    // As in the dense GEMM: two CTAs per SM at 16 tokens, so that the next
-    // kernel's CTA streams its first weights while this one finishes, and two
-    // groups of epilogue warps at 64.
-    static constexpr int kMinBlocks = NPAD == 16 ? 2 : 1;
+    // Up to 32 tokens two CTAs per SM, so that the next kernel's CTA streams
+    // its first weights while this one finishes (32 tokens, 128 experts of
+    // (2,048, 768), top 8: 103.6 us, one CTA of twice the ring 106.3; 20 tokens,
+    // 16 of (512, 256), top 2: 17.0 and 17.9); at 64 two groups of epilogue
+    // warps, whose registers leave no room for a second CTA.
+    static constexpr int kMinBlocks = NPAD <= 32 ? 2 : 1;
     static constexpr int kColGroups = NPAD == 64 ? 2 : 1;
     static constexpr int kCols = NPAD / kColGroups;
     static_assert(kCols <= 32, "a lane holds one token's scale");
     static constexpr int kEpiWarps = 4 * kColGroups;
     static constexpr int kThreads = 32 * (2 + kEpiWarps);
-    static constexpr int kMaxRegs = kMinBlocks == 2 ? 160 : kEpiWarps == 4 ? 255 : 168;
+    static constexpr int kMaxRegs = NPAD == 16 ? 160 : 168;
     static constexpr int kHeader = 3072; // barriers and flags, then [1024, 3072) the active experts
     static constexpr int kProdFloats = kEpiWarps * 2 * kTiles * kCols; // per warp, by unit parity
     static constexpr uint32_t kIdesc = idesc_e4m3_f32(128, NPAD);
@@ -556,13 +558,14 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
 
         // down: a tile's sum over its contributors, a warp a token (four rows
         // a lane).  The time is the L2's round trips: kTok tokens of kCon
-        // contributors, up to 24 KB a warp, are in flight at a time, and the
-        // loops over more of either stay rolled.  (Thread = row, six
-        // contributors of eight tokens, took 41.6 us where this takes 35.0, a
-        // layer of 50 tokens with 22 contributors a tile; bulk copies into the
-        // idle ring, eight in flight, 40.6.)
+        // contributors, 12 KB a warp, are in flight at a time, and the loops
+        // over more of either stay rolled.  (Thread = row, six contributors of
+        // eight tokens, took 41.6 us where this takes 35.0, a layer of 50 tokens
+        // with 22 contributors a tile; bulk copies into the idle ring, eight in
+        // flight, 40.6.  Four tokens of six contributors: 13 tokens 29.7 us, not
+        // 30.0, but one token of 128 experts 22.1, not 21.5.)
         auto finish_down = [&](int c_first, int c_last, int slot_first) {
-            constexpr int kTok = NPAD == 64 ? 2 : 4, kCon = NPAD == 16 ? 6 : 12;
+            constexpr int kTok = 2, kCon = 12;
             const int ew = warp - 2;
             uint16_t *const y = p.y + u.j * 128 + 4 * lane;
             const bool y_wide = (reinterpret_cast<uintptr_t>(p.y) & 7u) == 0; // (the entry asks for two bytes)
@@ -736,7 +739,8 @@ fp8bs_status launch_moe_gemm(const MoeLaunch &L, const MoeWorkspace &w, const De
     constexpr bool kUp = PHASE == kMoeUp;
     constexpr int kSmemLimit = 227 * 1024;
     auto kernel = moe_gemm_kernel<NPAD, PHASE>;
-    int stages = (C::kMinBlocks == 2 ? 104 * 1024 : 204 * 1024) / C::kStageBytes;
+    // (two CTAs: the up product's and the down product's together fit an SM)
+    int stages = (C::kMinBlocks == 2 ? (kUp ? 108 : 104) * 1024 : 204 * 1024) / C::kStageBytes;
     stages = stages > C::kMaxStages ? C::kMaxStages : stages;
     const int smem = C::smem_bytes(stages);
     fp8bs_status st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kSmemLimit, dev.device, &attr_done);
