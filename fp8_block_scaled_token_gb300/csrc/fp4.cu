@@ -16,9 +16,10 @@
 // 512-byte atoms of ptx.cuh, four blocks of K to an atom.
 //
 // Each input and output byte moves once.  5,120 x 17,408 bf16: quantising takes
-// 63 us (227 MB; bound by the conversion's integer instructions: the check
-// that keeps codes exact without a division a value is a third of them),
-// reading back to fp32 61 us (406 MB, at the memory's rate).  The activations'
+// 47 us (227 MB, 0.7 of the measured copy bandwidth; MX 35 us), bound by the
+// instructions of the conversion and of the check that keeps codes exact
+// without a division a value; reading back to fp32 61 us (406 MB, at the
+// memory's rate).  The activations'
 // cast is a few microseconds of latency at decode sizes.
 #include <cuda_bf16.h>
 
@@ -30,6 +31,14 @@
 namespace fp8bs {
 
 constexpr int kFp4Chunk = 16; // values a thread converts at a time: one NV block, half an MX block
+// A row's chunks are held in registers between its maximum and the conversion,
+// three (fp32: two) a thread, by as many whole warps as that takes: no warp
+// waits for one that has a chunk more.  5,120 x 17,408, there and back: 108 us;
+// 256 threads of four and a rest read twice 115, four a thread and fewer warps
+// 107 but with spills.  Rows past 384 threads' read the rest twice (4,096 x
+// 34,816: 182 us, 189 with up to 512 threads, of which an SM holds fewer).
+constexpr int kMaxRowThreads = 384;
+template <bool kBf16> constexpr int kRowHold = kBf16 ? 3 : 2;
 
 // Eight fp32 values -> eight E2M1 codes, the first in the lowest four bits.
 // The hardware conversion rounds to nearest even and saturates to +-6.
@@ -46,6 +55,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *v)
         : "=r"(r)
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+
+// One value's code.
+__device__ __forceinline__ uint32_t e2m1_code(float v)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+        "mov.b32 %0, {b, b, b, b};\n\t}"
+        : "=r"(r)
+        : "f"(v), "f"(0.0f));
+    return r & 0xFu;
 }
 
 // Eight codes -> their values.
@@ -105,31 +126,6 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
-// Codes of eight values over the scale d > 0: e2m1 of the correctly rounded
-// quotient.  As in quantize4 (quant_math.cuh): both ends of an interval that
-// holds it are converted, and since the conversion is monotonic equal codes
-// are the quotient's; only where a rounding boundary falls inside is the IEEE
-// division done.
-__device__ __forceinline__ uint32_t nv_codes8(const float *v, float d, float r_lo, float r_hi, bool plain)
-{
-    float q[8];
-    if (plain) {
-        float lo[8], hi[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            mul2(lo[i], lo[i + 1], v[i], v[i + 1], r_lo);
-            mul2(hi[i], hi[i + 1], v[i], v[i + 1], r_hi);
-        }
-        const uint32_t cl = e2m1x8(lo), ch = e2m1x8(hi);
-        if (cl == ch)
-            return cl;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q[i] = __fdiv_rn(v[i], d);
-    return e2m1x8(q);
-}
-
 // E4M3 code of fl32(fl32(amax / 6) / r); inv6 = 1 / (6 r) approximately, or
 // NaN where r is out of plain_range.  (An amax so small that the product is
 // not a normal number is far below the least code either way.)
@@ -158,21 +154,117 @@ template <bool kBf16> __device__ __forceinline__ Raw16<kBf16> load16(const void 
     return r;
 }
 
-template <bool kBf16> __device__ __forceinline__ void values16(const Raw16<kBf16> &r, float (&v)[16])
+// Values 8 h ... 8 h + 7 of the sixteen.
+template <bool kBf16> __device__ __forceinline__ void values8(const Raw16<kBf16> &r, int h, float (&v)[8])
 {
-#pragma unroll
-    for (int i = 0; i < (kBf16 ? 2 : 4); ++i) {
-        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+    if (kBf16) {
+        const uint32_t w[4] = {r.w[h].x, r.w[h].y, r.w[h].z, r.w[h].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (kBf16) {
-                v[8 * i + 2 * q] = bf16_lo(w[q]);
-                v[8 * i + 2 * q + 1] = bf16_hi(w[q]);
-            } else {
-                v[4 * i + q] = __uint_as_float(w[q]);
-            }
+            v[2 * q] = bf16_lo(w[q]);
+            v[2 * q + 1] = bf16_hi(w[q]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 w = r.w[(kBf16 ? 0 : 2 * h) + i];
+            v[4 * i] = __uint_as_float(w.x);
+            v[4 * i + 1] = __uint_as_float(w.y);
+            v[4 * i + 2] = __uint_as_float(w.z);
+            v[4 * i + 3] = __uint_as_float(w.w);
         }
     }
+}
+
+// Word i of the raw bits, i a run-time number (registers have no address: a
+// tree of selections).
+template <int kWords> __device__ __forceinline__ uint32_t pick(const uint32_t (&w)[kWords], int i)
+{
+    uint32_t t[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+        t[k] = w[k];
+#pragma unroll
+    for (int n = kWords / 2; n >= 1; n /= 2)
+#pragma unroll
+        for (int k = 0; k < n; ++k)
+            t[k] = (i & n) ? t[k + n] : t[k];
+    return t[0];
+}
+
+// Value i of the sixteen.
+template <bool kBf16> __device__ __forceinline__ float value_at(const Raw16<kBf16> &r, int i)
+{
+    uint32_t w[kBf16 ? 8 : 16];
+#pragma unroll
+    for (int q = 0; q < (kBf16 ? 2 : 4); ++q) {
+        w[4 * q] = r.w[q].x;
+        w[4 * q + 1] = r.w[q].y;
+        w[4 * q + 2] = r.w[q].z;
+        w[4 * q + 3] = r.w[q].w;
+    }
+    if (kBf16) {
+        const uint32_t two = pick(w, i >> 1);
+        return (i & 1) ? bf16_hi(two) : bf16_lo(two);
+    }
+    return __uint_as_float(pick(w, i));
+}
+
+// Codes of sixteen values over the scale d (0: zero codes): e2m1 of the
+// correctly rounded quotient.  As in quantize4 (quant_math.cuh): both ends of
+// an interval that holds it are converted, and since the conversion is
+// monotonic equal codes are the quotient's.  The IEEE division is left for the
+// values with a rounding boundary inside theirs, one at a time: with bf16
+// values 0.2 % lie exactly on one (value and row maximum have eight bits and
+// the block's scale four, so equality is common), which is in half of a warp's
+// steps (all sixteen divided there: 5,120 x 17,408 to 4 bits and back 138 us,
+// not 115).
+template <bool kBf16> __device__ __forceinline__ uint2 nv_codes16(const Raw16<kBf16> &raw, float d)
+{
+    const float rd = rcp_approx(d);
+    const float r_lo = rd * (1.0f - kQuotientSlack), r_hi = rd * (1.0f + kQuotientSlack);
+    uint32_t codes[2], differ[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[8], q[8];
+        values8<kBf16>(raw, h, v);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+            mul2(q[i], q[i + 1], v[i], v[i + 1], r_lo);
+        codes[h] = e2m1x8(q);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+            mul2(q[i], q[i + 1], v[i], v[i + 1], r_hi);
+        differ[h] = codes[h] ^ e2m1x8(q);
+    }
+    if (!plain_range(d)) {
+        codes[0] = codes[1] = 0u;
+        differ[0] = differ[1] = d == 0.0f ? 0u : 0xFFFFFFFFu;
+    }
+#pragma unroll 1
+    while ((differ[0] | differ[1]) != 0u) {
+        const bool second = differ[0] == 0u;
+        const int shift = (__ffs(static_cast<int>(second ? differ[1] : differ[0])) - 1) & ~3;
+        const float q = __fdiv_rn(value_at<kBf16>(raw, (second ? 8 : 0) + (shift >> 2)), d);
+        const uint32_t keep = ~(0xFu << shift);
+        const uint32_t code = e2m1_code(q) << shift;
+        if (second) {
+            codes[1] = (codes[1] & keep) | code;
+            differ[1] &= keep;
+        } else {
+            codes[0] = (codes[0] & keep) | code;
+            differ[0] &= keep;
+        }
+    }
+    return make_uint2(codes[0], codes[1]);
+}
+
+// The larger magnitude of each half (with the signs' exclusive or).
+__device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // Their largest magnitude (fp32: the bits of non-negative numbers order like
@@ -180,15 +272,9 @@ template <bool kBf16> __device__ __forceinline__ void values16(const Raw16<kBf16
 template <bool kBf16> __device__ __forceinline__ float abs_max16(const Raw16<kBf16> &r)
 {
     if (kBf16) {
-        __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&r.w[0].x));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[q])));
-        }
-        return fmaxf(__low2float(m), __high2float(m));
+        uint32_t m = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(r.w[0].x, r.w[0].y), abs_max_bf16x2(r.w[0].z, r.w[0].w)),
+                                    abs_max_bf16x2(abs_max_bf16x2(r.w[1].x, r.w[1].y), abs_max_bf16x2(r.w[1].z, r.w[1].w)));
+        return fmaxf(fabsf(bf16_lo(m)), fabsf(bf16_hi(m)));
     }
     uint32_t m = 0;
 #pragma unroll
@@ -206,19 +292,10 @@ template <bool kBf16, bool kNv>
 __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, float r, float inv6, int c, bool live,
                                          uint32_t &word)
 {
-    float v[16];
-    values16<kBf16>(raw, v);
-    uint2 codes = make_uint2(0u, 0u);
+    uint2 codes;
     if (kNv) {
         const uint32_t byte = nv_scale_code(amax, r, inv6);
-        if (byte != 0u) {
-            const float d = e4m3_value(byte) * r;
-            const float rd = rcp_approx(d);
-            const float r_lo = rd * (1.0f - kQuotientSlack), r_hi = rd * (1.0f + kQuotientSlack);
-            const bool plain = plain_range(d);
-            codes.x = nv_codes8(v, d, r_lo, r_hi, plain);
-            codes.y = nv_codes8(v + 8, d, r_lo, r_hi, plain);
-        }
+        codes = nv_codes16<kBf16>(raw, byte != 0u ? e4m3_value(byte) * r : 0.0f);
         word = byte << (8 * (c & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 1);
         word |= __shfl_xor_sync(0xffffffffu, word, 2);
@@ -229,11 +306,14 @@ __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, fl
         int e = E == 0 ? (b == 0u ? 0 : -127) : E - 127 - 2;
         e = e < -127 ? -127 : e;
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23); // 2^-e, e <= 125
+        float v[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            values8<kBf16>(raw, h, v[h]);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            v[i] *= inv;
-        codes.x = e2m1x8(v);
-        codes.y = e2m1x8(v + 8);
+            v[i >> 3][i & 7] *= inv;
+        codes = make_uint2(e2m1x8(v[0]), e2m1x8(v[1]));
         word = live ? static_cast<uint32_t>(e + 127) << (8 * ((c >> 1) & 3)) : 0u;
         word |= __shfl_xor_sync(0xffffffffu, word, 2);
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
@@ -249,13 +329,16 @@ __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, fl
 // activations, codes [row][kg * 128].  Atoms [128-row tile][kg * atoms a
 // unit][512] either way; the activations' rows past M are not written (they
 // only ever meet token columns that are not stored).
-template <bool kBf16, bool kNv, bool kTiled, int kRowThreads, int kHold>
-__global__ void __launch_bounds__(kRowThreads)
+// (56 registers: three CTAs of 384 threads an SM, 117 us with two)
+template <bool kBf16, bool kNv, bool kTiled>
+__global__ void __maxnreg__((kBf16 ? 56 : 64))
     fp4_quant_rows_kernel(const void *__restrict__ x, int rows, int K, long long ldx, int kg, uint8_t *__restrict__ xq,
                           uint8_t *__restrict__ sf, float *__restrict__ row_scale, int overlap,
                           unsigned long long *runs)
 {
-    __shared__ float warp_amax[kRowThreads / 32];
+    constexpr int kHold = kRowHold<kBf16>;
+    const int threads = static_cast<int>(blockDim.x);
+    __shared__ float warp_amax[kMaxRowThreads / 32];
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(runs + (kTiled ? FP8BS_RUNS_FP4_QUANT_WEIGHT : FP8BS_RUNS_FP4_QUANT_ACT), 1ull);
     if (!kTiled) {
@@ -277,7 +360,7 @@ __global__ void __launch_bounds__(kRowThreads)
     Raw16<kBf16> held[kHold];
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
-        const int c = static_cast<int>(threadIdx.x) + i * kRowThreads;
+        const int c = static_cast<int>(threadIdx.x) + i * threads;
 #pragma unroll
         for (int q = 0; q < (kBf16 ? 2 : 4); ++q)
             held[i].w[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -295,41 +378,38 @@ __global__ void __launch_bounds__(kRowThreads)
         for (int i = 0; i < kHold; ++i)
             amax = fmaxf(amax, held_amax[i]);
 #pragma unroll 1
-        for (int c = static_cast<int>(threadIdx.x) + kHold * kRowThreads; c < whole; c += kRowThreads)
+        for (int c = static_cast<int>(threadIdx.x) + kHold * threads; c < whole; c += threads)
             amax = fmaxf(amax, abs_max16<kBf16>(load16<kBf16>(src, c * kFp4Chunk)));
         amax = warp_max(amax);
         if ((threadIdx.x & 31) == 0)
             warp_amax[threadIdx.x >> 5] = amax;
         __syncthreads();
-        amax = warp_max(warp_amax[threadIdx.x & (kRowThreads / 32 - 1)]);
+        amax = warp_max(static_cast<int>(threadIdx.x & 31) < threads / 32 ? warp_amax[threadIdx.x & 31] : 0.0f);
         r = nv_row_scale(amax);
         inv6 = plain_range(r) ? rcp_approx(r) * (1.0f / 6.0f) : __int_as_float(0x7fffffff);
     }
     if (threadIdx.x == 0 && real && row_scale != nullptr)
         row_scale[row] = r;
     const int tile = row >> 7, rt = row & 127;
+    constexpr int kPerAtom = kNv ? 4 : 8; // chunks
+    uint8_t *const xq_row = xq + (kTiled ? (static_cast<long long>(tile) * kg * 128 + rt) * 128 : static_cast<long long>(row) * kg * 128);
+    uint8_t *const sf_row = sf + static_cast<long long>(tile) * (chunks / kPerAtom) * 512 + 16 * (rt & 31) + 4 * (rt >> 5);
     // whole warps take part in the shuffles of quant16, also past the last chunk
     auto convert = [&](int c, const Raw16<kBf16> &raw, float amax) {
         uint32_t word;
         const uint2 codes = quant16<kBf16, kNv>(raw, amax, r, inv6, c, c < whole, word);
         if (c < chunks) {
-            const int kb = c >> 4;
-            const long long at = kTiled ? ((static_cast<long long>(tile) * kg + kb) * 128 + rt) * 128 + (c & 15) * 8
-                                        : (static_cast<long long>(row) * kg + kb) * 128 + (c & 15) * 8;
-            *reinterpret_cast<uint2 *>(xq + at) = codes;
-            constexpr int kPerAtom = kNv ? 4 : 8; // chunks
-            if (c % kPerAtom == 0) {
-                const long long atom = static_cast<long long>(tile) * (chunks / kPerAtom) + c / kPerAtom;
-                *reinterpret_cast<uint32_t *>(sf + atom * 512 + 16 * (rt & 31) + 4 * (rt >> 5)) = word;
-            }
+            *reinterpret_cast<uint2 *>(xq_row + static_cast<unsigned>(c >> 4) * (kTiled ? 16384u : 128u) + (c & 15) * 8) = codes;
+            if (c % kPerAtom == 0)
+                *reinterpret_cast<uint32_t *>(sf_row + static_cast<unsigned>(c / kPerAtom) * 512u) = word;
         }
     };
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
-        if (i * kRowThreads + (static_cast<int>(threadIdx.x) & ~31) < chunks)
-            convert(static_cast<int>(threadIdx.x) + i * kRowThreads, held[i], held_amax[i]);
+        if (i * threads + (static_cast<int>(threadIdx.x) & ~31) < chunks)
+            convert(static_cast<int>(threadIdx.x) + i * threads, held[i], held_amax[i]);
 #pragma unroll 1
-    for (int c = static_cast<int>(threadIdx.x) + kHold * kRowThreads; (c & ~31) < chunks; c += kRowThreads) {
+    for (int c = static_cast<int>(threadIdx.x) + kHold * threads; (c & ~31) < chunks; c += threads) {
         Raw16<kBf16> raw = {};
         if (c < whole)
             raw = load16<kBf16>(src, c * kFp4Chunk);
@@ -401,27 +481,25 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Threads that hold a row, in whole warps.
+static int row_threads(int chunks, int hold)
+{
+    const int t = ((chunks + hold - 1) / hold + 31) & ~31;
+    return t < kMaxRowThreads ? t : kMaxRowThreads;
+}
+
 fp8bs_status launch_fp4_quant_weights(const void *w, int wtype, int N, int K, int fmt, uint8_t *wq, uint8_t *sf,
                                       float *rows, cudaStream_t stream, const DeviceInfo &dev)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((N + 127) / 128) * 128u, 1, 1);
     cfg.stream = stream;
-    // Threads a row: 128 hold 8,192 bf16 values, 256 hold 16,384 (quantising
-    // and reading back: 1,000 x 2,080 fp32 in 5.7 us with 128 and 6.8 with
-    // 256, 5,120 x 17,408 bf16 in 130 us with 128 and 123 with 256).
-    const bool wide = K > 8192, nv = fmt == FP8BS_FP4_NV;
-    cfg.blockDim = dim3(wide ? 256 : 128, 1, 1);
-    auto kernel = wtype == FP8BS_BF16
-                      ? (nv ? (wide ? fp4_quant_rows_kernel<true, true, true, 256, 4>
-                                    : fp4_quant_rows_kernel<true, true, true, 128, 4>)
-                            : (wide ? fp4_quant_rows_kernel<true, false, true, 256, 4>
-                                    : fp4_quant_rows_kernel<true, false, true, 128, 4>))
-                      : (nv ? (wide ? fp4_quant_rows_kernel<false, true, true, 256, 2>
-                                    : fp4_quant_rows_kernel<false, true, true, 128, 2>)
-                            : (wide ? fp4_quant_rows_kernel<false, false, true, 256, 2>
-                                    : fp4_quant_rows_kernel<false, false, true, 128, 2>));
-    return launch_status(cudaLaunchKernelEx(&cfg, kernel, w, N, K, static_cast<long long>(K), (K + 255) / 256, wq, sf,
+    const int kg = (K + 255) / 256;
+    const bool bf = wtype == FP8BS_BF16, nv = fmt == FP8BS_FP4_NV;
+    cfg.blockDim = dim3(static_cast<unsigned>(row_threads(kg * 16, bf ? kRowHold<true> : kRowHold<false>)), 1, 1);
+    auto kernel = bf ? (nv ? fp4_quant_rows_kernel<true, true, true> : fp4_quant_rows_kernel<true, false, true>)
+                     : (nv ? fp4_quant_rows_kernel<false, true, true> : fp4_quant_rows_kernel<false, false, true>);
+    return launch_status(cudaLaunchKernelEx(&cfg, kernel, w, N, K, static_cast<long long>(K), kg, wq, sf,
                                             rows, 0, dev.runs));
 }
 
@@ -430,15 +508,15 @@ fp8bs_status launch_fp4_quant_act(const void *x, int M, int K, int ldx, int fmt,
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(M), 1, 1);
-    cfg.blockDim = dim3(512, 1, 1);
+    cfg.blockDim = dim3(kMaxRowThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto kernel = fmt == FP8BS_FP4_NV ? fp4_quant_rows_kernel<true, true, false, 512, 3>
-                                      : fp4_quant_rows_kernel<true, false, false, 512, 3>;
+    auto kernel = fmt == FP8BS_FP4_NV ? fp4_quant_rows_kernel<true, true, false>
+                                      : fp4_quant_rows_kernel<true, false, false>;
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, x, M, K, static_cast<long long>(ldx), (K + 255) / 256, xq, sf,
                                             rows, pdl ? 1 : 0, dev.runs));
 }

@@ -100,6 +100,25 @@ def test_edge_values(fmt):
     _check_packed(*fb.fp4_quant_act(xb.cuda(), fmt), _f32(xb), fmt, False)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(5, 32), (130, 544), (33, 6176), (3, 8192), (2, 34816)])
+def test_ties_between_codes_are_exact(N, K, dtype):
+    """Row maxima of 21 * 2^n make the row scale a power of two, so many
+    quotients of small integers lie exactly between two codes; in rows held
+    whole and in longer ones, with zeros and blocks whose scale byte is 0."""
+    rng = np.random.RandomState(N + K)
+    v = rng.randint(-21, 22, (N, K)) * 2.0 ** rng.randint(-6, 1, (N, K // 16)).repeat(16, axis=1)
+    v[rng.uniform(size=(N, K)) < 0.3] = 0.0
+    v[:, 0] = 21.0
+    v[:, 16:32] *= 2.0 ** -40
+    v *= 2.0 ** rng.randint(-20, 20, (N, 1))
+    w = torch.from_numpy(v.astype(np.float32)).to(dtype)
+    for fmt in FORMATS:
+        _check_packed(*fb.fp4_quant_weights(w.cuda(), fmt), _f32(w), fmt, True)
+        if dtype is torch.bfloat16:
+            _check_packed(*fb.fp4_quant_act(w.cuda(), fmt), _f32(w), fmt, False)
+
+
 def _layer(M, N, K, fmt, seed):
     x = synth.activations(M, K, seed=seed, outlier_p=0.001)
     w = synth.weights(N, K, seed=seed + 1000, outlier_p=0.01)
