@@ -228,7 +228,12 @@ template <int NPAD, int MODE> struct GemmCfg {
     static constexpr bool kProducts = NPAD >= 32 && !kTileAcc;
     static constexpr int kProdPerLane = (kCols + 31) / 32; // token columns per lane
     static constexpr int kProdBytes = kProducts ? kEpiWarps * 2 * kCols * 4 : 0; // per warp, by unit parity
-    static constexpr int kThreads = 32 * (2 + kEpiWarps + kQuantWarps + kSfWarps);
+    // 4-bit: a second producer warp, for the token tiles and their scale atoms.
+    // (A thread takes about 110 cycles to issue a bulk load and a unit has
+    // four, as long as everything else that a unit needs: 34,816 x 5,120 at
+    // M = 512 68.1 us with one producer, 65.8 with two, no less with three.)
+    static constexpr int kTokenWarps = kFp4 ? 1 : 0;
+    static constexpr int kThreads = 32 * (2 + kEpiWarps + kQuantWarps + kSfWarps + kTokenWarps);
     // Registers per thread.  An SM's register file is four 16,384-register
     // banks, one per scheduler, and a CTA's warps are spread over the four:
     // with W resident warps a bank holds ceil(W / 4) of them, so a thread may
@@ -332,7 +337,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
         if (blockIdx.x == 0)
             atomicAdd(p.runs + FP8BS_RUNS_GEMM(MODE, NPAD, GREEDY ? 1 : 0), 1ull); // this instantiation ran
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + C::kTokenWarps); // (every producer arrives with its bytes)
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < C::kAcc; ++a) {
@@ -381,8 +386,8 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
         if (lane == 0) {
             const uint64_t pol_w = l2_policy_evict_first();
             const uint64_t pol_b = l2_policy_evict_last();
-            const uint32_t tx = C::kFp4 ? C::kWBytes + C::kBBytes + p.sf_atoms * 1024 : C::kStageBytes;
             const uint32_t sf_bytes = p.sf_atoms * 512; // 4-bit: scale atoms of one side of a unit
+            const uint32_t tx = C::kFp4 ? C::kWBytes + sf_bytes : C::kStageBytes;
             uint32_t armed_mask = 0, armed_parity = 0;
             const int pre = p.prefetch_before_wait ? (nunits < S ? nunits : S) : 0;
             // Per-unit state (K block, weight tile, first token row) advances
@@ -432,7 +437,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                                  p.sfa + (static_cast<long long>(wt) * kg + kb) * sf_bytes, sf_bytes, &full[i], pol_w);
             }
             grid_dependency_wait();
-            if (MODE != kModeFp8Fused) {
+            if (MODE != kModeFp8Fused && !C::kFp4) {
                 int kb_b = kb0, wt_b = wt_first, trow_b = trow_first;
                 for (int i = 0; i < pre; ++i, step(kb_b, wt_b, trow_b)) {
                     if (i == p.test_skip_unit || !(armed_mask & (1u << i)))
@@ -443,10 +448,6 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         bulk_load_1d(ring + i * C::kStageBytes + C::kWBytes + C::kBBytes + 512,
                                      p.sfb + (static_cast<long long>(trow_b / 128) * kg + kb_b) * 512, 512, &full[i],
                                      pol_b);
-                    if constexpr (C::kFp4)
-                        bulk_load_1d(ring + i * C::kStageBytes + C::kWBytes + C::kBBytes + 2048,
-                                     p.sfb + (static_cast<long long>(trow_b / 128) * kg + kb_b) * sf_bytes, sf_bytes,
-                                     &full[i], pol_b);
                 }
             }
             int s = pre % S;
@@ -467,7 +468,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                     const int wx = p.w_tiled ? 0 : kb * C::kChunkElems;
                     const int wy = p.w_tiled ? (wb * kg + kb) * C::kTileRows : wb * C::kTileRows;
                     tma_load_2d(ring + s * C::kStageBytes, &tm_w, &full[s], wx, wy, pol_w);
-                    if (MODE != kModeFp8Fused)
+                    if (MODE != kModeFp8Fused && !C::kFp4)
                         tma_load_2d(ring + s * C::kStageBytes + C::kWBytes, &tm_b, &full[s], kb * C::kChunkElems,
                                     trow, pol_b);
                     if constexpr (C::kMx) {
@@ -480,8 +481,6 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                         uint8_t *sf = ring + s * C::kStageBytes + C::kWBytes + C::kBBytes;
                         bulk_load_1d(sf, p.sfa + (static_cast<long long>(wt) * kg + kb) * sf_bytes, sf_bytes, &full[s],
                                      pol_w);
-                        bulk_load_1d(sf + 2048, p.sfb + (static_cast<long long>(trow / 128) * kg + kb) * sf_bytes,
-                                     sf_bytes, &full[s], pol_b);
                     }
                 }
                 if (++s == S) {
@@ -510,64 +509,67 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         if constexpr (C::kFp4) {
-            // The whole warp runs the loop and one lane issues: the loop's
-            // values are then uniform, which the tensor instructions' operands
-            // have to be, and the next stage's barrier is looked at before
-            // this stage's MMAs are issued.  A unit's MMAs take a quarter of
-            // the time that a chain of waits, operand moves and issues by a
-            // single thread does.  (sf_ready completes after full: the warps
+            // The whole warp runs the loop and one lane issues, by predicated
+            // instructions: every operand is then uniform, as the tensor
+            // instructions want them, and no branch diverges.  The loop is kept
+            // short (a loop for each format, the waits' polling out of line):
+            // a unit's four MMAs take about 230 cycles, the loop around them
+            // took 700 when its instructions were spread out.  34,816 x 5,120
+            // at M = 512 / 16, 5,120 x 5,120 at M = 8: 63.6 / 22.0 / 10.3 us,
+            // with a branch for the issuing lane and one loop for both formats
+            // 65.8 / 22.3 / 10.8.  (sf_ready completes after full: the warps
             // that store the scale factors wait for it.)
             const bool leader = elect_one();
-            int acc = 0, s = 0, kb = kb0;
-            uint32_t acc_ph = 0, ph = 0;
-            bool ready = false;
-            for (int i = 0; i < nunits; ++i) {
-                const bool fresh = i == 0 || kb == 0;
-                const bool publish = i == nunits - 1 || kb == kg - 1;
-                bool ok = true;
-                if (fresh)
-                    ok = mbar_wait(&tempty[acc], acc_ph ^ 1u, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
-                if (!ready)
-                    ok = ok && mbar_wait(&sf_ready[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
-                if (!__all_sync(0xffffffffu, ok))
-                    break;
-                tc_fence_after_sync();
-                const int s1 = s + 1 == S ? 0 : s + 1;
-                const uint32_t ph1 = s + 1 == S ? ph ^ 1u : ph;
-                ready = __all_sync(0xffffffffu, i + 1 < nunits && mbar_peek(&sf_ready[s1], ph1));
-                if (leader) {
-                    const uint32_t stage = smem_u32(ring) + static_cast<uint32_t>(s * C::kStageBytes);
-                    const uint64_t a_desc = sw128_kmajor_desc(stage);
-                    const uint64_t b_desc = sw128_kmajor_desc(stage + C::kWBytes);
+            const uint32_t lead = leader ? 1u : 0u;
+            const uint32_t a0 = desc_lo(smem_u32(ring)), empty0 = smem_u32(empty);
+            auto issue_all = [&](auto is_nv) {
+                int acc = 0, s = 0, kb = kb0;
+                uint32_t acc_ph = 0, ph = 0;
+                bool ready = false;
+#pragma unroll 1
+                for (int i = 0; i < nunits; ++i) {
+                    const bool fresh = i == 0 || kb == 0;
+                    if (fresh) {
+                        const bool ok =
+                            mbar_wait_far(&tempty[acc], acc_ph ^ 1u, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+                        if (!__all_sync(0xffffffffu, ok))
+                            break;
+                    }
+                    if (!ready) {
+                        const bool ok = mbar_wait_far(&sf_ready[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+                        if (!__all_sync(0xffffffffu, ok))
+                            break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t a_lo = a0 + static_cast<uint32_t>(s * (C::kStageBytes >> 4));
                     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * NPAD);
                     // four MMAs of 64 K, this unit's atoms in its stage's columns
                     const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfCol + s * C::kSfStageCols);
-                    if (p.sf_atoms == 4) {
-#pragma unroll
-                        for (int k = 0; k < C::kMmaSteps; ++k)
-                            mma_nvf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k, idesc_fp4(C::kTileRows, NPAD, 0u, 0u),
-                                     sf + 4 * k, sf + 16 + 4 * k, (k > 0 || !fresh) ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < C::kMmaSteps; ++k)
-                            mma_mxf4(d_tmem, a_desc + 2 * k, b_desc + 2 * k,
-                                     idesc_fp4(C::kTileRows, NPAD, 1u, static_cast<uint32_t>(2 * (k & 1))),
-                                     sf + 4 * (k >> 1), sf + 16 + 4 * (k >> 1), (k > 0 || !fresh) ? 1u : 0u);
+                    if constexpr (decltype(is_nv)::value)
+                        mma_nvf4_unit(lead, d_tmem, a_lo, a_lo + (C::kWBytes >> 4), idesc_fp4(C::kTileRows, NPAD, 0u, 0u),
+                                      sf, sf + 16, fresh ? 0u : 1u, empty0 + 8u * s);
+                    else
+                        mma_mxf4_unit(lead, d_tmem, a_lo, a_lo + (C::kWBytes >> 4), idesc_fp4(C::kTileRows, NPAD, 1u, 0u),
+                                      idesc_fp4(C::kTileRows, NPAD, 1u, 2u), sf, sf + 16, fresh ? 0u : 1u, empty0 + 8u * s);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
                     }
-                    mma_commit(&empty[s]);
-                    if (publish)
-                        mma_commit(&tfull[acc]);
+                    ready = __all_sync(0xffffffffu, i + 1 < nunits && mbar_peek(&sf_ready[s], ph));
+                    if (++kb == kg || i == nunits - 1) {
+                        mma_commit_by(lead, smem_u32(&tfull[acc]));
+                        kb = 0;
+                        if (++acc == C::kAcc) {
+                            acc = 0;
+                            acc_ph ^= 1u;
+                        }
+                    }
                 }
-                __syncwarp();
-                if (publish && ++acc == C::kAcc) {
-                    acc = 0;
-                    acc_ph ^= 1u;
-                }
-                s = s1;
-                ph = ph1;
-                if (++kb == kg)
-                    kb = 0;
-            }
+            };
+            if (p.sf_atoms == 4)
+                issue_all(std::true_type{});
+            else
+                issue_all(std::false_type{});
             if (leader) {
                 mma_commit(mma_done);
                 const uint64_t t0 = globaltimer_ns();
@@ -660,6 +662,63 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
                 }
             }
         }
+    } else if (C::kTokenWarps > 0 && warp == 2 + C::kEpiWarps + C::kSfWarps) {
+        // ------------------------------------------------ TMA producer of the tokens
+        if constexpr (C::kFp4) {
+            if (lane == 0) {
+                const uint64_t pol_b = l2_policy_evict_last();
+                const uint32_t sf_bytes = p.sf_atoms * 512;
+                const int pair_first = static_cast<int>(u0 / kg);
+                int kb = kb0, wt = kOneTT ? pair_first : pair_first % p.ntiles;
+                int trow = kOneTT ? 0 : (pair_first / p.ntiles) * NPAD;
+                uint32_t armed_mask = 0, armed_parity = 0, ph = 0;
+                int s = 0;
+                grid_dependency_wait();
+                for (int i = 0; i < nunits; ++i) {
+                    if (!mbar_wait_far(&empty[s], ph ^ 1u, abort_flag, p.status, kErrTimeoutProducer, p.timeout_ns))
+                        break;
+#ifdef FP8BS_DEBUG
+                    const bool left_out = i == p.test_skip_unit || i == p.test_bad_unit; // (by both producers)
+#else
+                    const bool left_out = i == p.test_skip_unit;
+#endif
+                    if (!left_out &&
+                        FP8BS_CHECK(s < S && kb >= 0 && kb < kg && wt < p.ntiles && trow >= 0 && trow < p.M)) {
+                        mbar_arrive_expect_tx(&full[s], C::kBBytes + sf_bytes);
+                        armed_mask |= 1u << s;
+                        armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
+                        uint8_t *b_tile = ring + s * C::kStageBytes + C::kWBytes;
+                        tma_load_2d(b_tile, &tm_b, &full[s], kb * C::kChunkElems, trow, pol_b);
+                        bulk_load_1d(b_tile + C::kBBytes + 2048,
+                                     p.sfb + (static_cast<long long>(trow / 128) * kg + kb) * sf_bytes, sf_bytes,
+                                     &full[s], pol_b);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (++kb == kg) {
+                        kb = 0;
+                        if (++wt == p.ntiles && !kOneTT) {
+                            wt = 0;
+                            trow += NPAD;
+                        }
+                    }
+                }
+                // as above: nothing may still be landing when the CTA exits
+                for (int q = 0; q < S; ++q) {
+                    if (!(armed_mask & (1u << q)))
+                        continue;
+                    const uint64_t t0 = globaltimer_ns();
+                    while (!mbar_test(&full[q], (armed_parity >> q) & 1u)) {
+                        if (globaltimer_ns() - t0 > p.timeout_ns) {
+                            atomicOr(p.status, kErrTimeoutDrain);
+                            break;
+                        }
+                    }
+                }
+            }
+        }
     } else if (C::kSfWarps > 0 && warp >= 2 + C::kEpiWarps) {
         // ------------------------------------------------ scale factors to tensor memory
         if constexpr (C::kFp4) {
@@ -667,7 +726,7 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
             int s = 0;
             uint32_t ph = 0;
             for (int i = 0; i < nunits; ++i) {
-                const bool ok = mbar_wait(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
+                const bool ok = mbar_wait_far(&full[s], ph, abort_flag, p.status, kErrTimeoutMma, p.timeout_ns);
                 if (!__all_sync(0xffffffffu, ok))
                     break;
                 // line `lane` of the weight atoms, then of the token atoms

@@ -160,6 +160,17 @@ __device__ __forceinline__ bool mbar_peek(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
+// commit of every MMA so far, by the lane whose `lead` is set
+__device__ __forceinline__ void mma_commit_by(uint32_t lead, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
+}
+
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one()
 {
@@ -223,6 +234,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
             }
         }
     }
+}
+
+// The same with the polling out of line, for loops whose instructions have to
+// stay close together: warps of different roles share what a scheduler has
+// fetched.
+static __device__ __noinline__ bool mbar_wait_poll(uint64_t *bar, uint32_t parity, volatile int *abort_flag, unsigned *status,
+                                            uint32_t code, uint64_t timeout_ns)
+{
+    return mbar_wait(bar, parity, abort_flag, status, code, timeout_ns);
+}
+__device__ __forceinline__ bool mbar_wait_far(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                              unsigned *status, uint32_t code, uint64_t timeout_ns)
+{
+    return mbar_test(bar, parity) || mbar_wait_poll(bar, parity, abort_flag, status, code, timeout_ns);
 }
 
 // --------------------------------------------------------------------- TMA
@@ -470,6 +495,10 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr)
     return d;
 }
 
+// The same in two words: the upper one is the same for every tile.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return ((smem_addr & 0x3FFFFu) >> 4) | (1u << 16); }
+
 // Instruction descriptor (kind::f16 / kind::f8f6f4 layout):
 //   bits 4-5  D format (1 = fp32)
 //   bits 7-9  A format, bits 10-12 B format (f8f6f4: 0 = E4M3; f16: 1 = BF16)
@@ -551,27 +580,56 @@ __host__ __device__ constexpr uint32_t idesc_mx_e4m3(int m, int n, uint32_t a_sf
 //     its four bytes per row are the MMA's four factors (scale factor id 0);
 //   scale_vec::2X (one UE8M0 factor per 32 K): an atom covers 128 K, two
 //     MMAs, which take the byte pairs 0-1 and 2-3 (scale factor ids 0, 2).
-__device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+//
+// One unit's four MMAs and the commit of its stage, by the lane whose `lead` is
+// set, as one predicated sequence: the whole warp runs it, so there is no
+// divergent branch and every operand stays in uniform registers.  a_lo, b_lo:
+// desc_lo of the stage's tiles; accumulate: whether the first MMA adds to D.
+#define FP8BS_FP4_MMA(kind, sfa, sfb, idesc, pred)                                                                     \
+    "@e tcgen05.mma.cta_group::1.kind::" kind " [%0], a, b, " idesc ", [" sfa "], [" sfb "], " pred ";\n\t"
+#define FP8BS_FP4_NEXT_K                                                                                               \
+    "add.u32 al, al, 2;\n\tadd.u32 bl, bl, 2;\n\tmov.b64 a, {al, %3};\n\tmov.b64 b, {bl, %3};\n\t"
+#define FP8BS_FP4_BEGIN                                                                                                \
+    "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t.reg .b32 al, bl, fa, fb;\n\t"                                   \
+    "setp.ne.b32 e, %7, 0;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"                                    \
+    "mov.b32 al, %1;\n\tmov.b32 bl, %2;\n\tmov.b32 fa, %4;\n\tmov.b32 fb, %5;\n\t"                                \
+    "mov.b64 a, {al, %3};\n\tmov.b64 b, {bl, %3};\n\t"
+#define FP8BS_FP4_NEXT_SF "add.u32 fa, fa, 4;\n\tadd.u32 fb, fb, 4;\n\t"
+#define FP8BS_FP4_END "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%8];\n\t}"
+
+__device__ __forceinline__ void mma_nvf4_unit(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                              uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                              uint32_t accumulate, uint32_t stage_free)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-        : "memory");
+    asm volatile(FP8BS_FP4_BEGIN
+                 FP8BS_FP4_MMA("mxf4nvf4.block_scale.scale_vec::4X", "fa", "fb", "%9", "p") FP8BS_FP4_NEXT_K FP8BS_FP4_NEXT_SF
+                 FP8BS_FP4_MMA("mxf4nvf4.block_scale.scale_vec::4X", "fa", "fb", "%9", "t") FP8BS_FP4_NEXT_K FP8BS_FP4_NEXT_SF
+                 FP8BS_FP4_MMA("mxf4nvf4.block_scale.scale_vec::4X", "fa", "fb", "%9", "t") FP8BS_FP4_NEXT_K FP8BS_FP4_NEXT_SF
+                 FP8BS_FP4_MMA("mxf4nvf4.block_scale.scale_vec::4X", "fa", "fb", "%9", "t") FP8BS_FP4_END ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(lead),
+                 "r"(stage_free), "r"(idesc)
+                 : "memory");
 }
 
-__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+// idesc, idesc2: scale factor ids 0 and 2 (bytes 0-1 and 2-3 of the atoms' columns).
+__device__ __forceinline__ void mma_mxf4_unit(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                              uint32_t idesc, uint32_t idesc2, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                              uint32_t accumulate, uint32_t stage_free)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-        : "memory");
+    asm volatile(FP8BS_FP4_BEGIN
+                 FP8BS_FP4_MMA("mxf4.block_scale.scale_vec::2X", "fa", "fb", "%9", "p") FP8BS_FP4_NEXT_K
+                 FP8BS_FP4_MMA("mxf4.block_scale.scale_vec::2X", "fa", "fb", "%10", "t") FP8BS_FP4_NEXT_K FP8BS_FP4_NEXT_SF
+                 FP8BS_FP4_MMA("mxf4.block_scale.scale_vec::2X", "fa", "fb", "%9", "t") FP8BS_FP4_NEXT_K
+                 FP8BS_FP4_MMA("mxf4.block_scale.scale_vec::2X", "fa", "fb", "%10", "t") FP8BS_FP4_END ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(lead),
+                 "r"(stage_free), "r"(idesc), "r"(idesc2)
+                 : "memory");
 }
+#undef FP8BS_FP4_MMA
+#undef FP8BS_FP4_NEXT_K
+#undef FP8BS_FP4_BEGIN
+#undef FP8BS_FP4_NEXT_SF
+#undef FP8BS_FP4_END
 
 // Instruction descriptor of kind::mxf4 / kind::mxf4nvf4: as idesc_mx_e4m3,
 // with A and B format 1 (E2M1), scale format 0 = UE4M3, 1 = UE8M0, and bit 31
