@@ -38,11 +38,11 @@
 //               device-scope atomic max, and the last CTA to finish writes
 //               the chosen columns and clears the keys for the next call.
 //   4-bit only: four more warps move each unit's scale factors from the ring
-//               to tensor memory, and the MMA warp runs its loop whole, one
-//               lane issuing; sums stay in tensor memory for a whole segment
-//               and get their row scales at its end.  34,816 x 5,120 at M = 16
-//               22.7 us (100 MB), at M = 512 71 us (2.6 PFLOP/s), bound by a
-//               ring stage's way round (load, scale store, MMA, commit).
+//               to tensor memory, another loads the token tiles, and the MMA
+//               warp runs its loop whole, one lane issuing; sums stay in tensor
+//               memory for a whole segment and get their row scales at its end.
+//               34,816 x 5,120 at M = 16 21.8 us (100 MB), at M = 512 63.6 us
+//               (2.9 PFLOP/s), bound by the issue of its loads and MMAs.
 //   fused only: warps 2-9 first quantise, in the kernel prologue, the token
 //               rows of every K block this CTA will use into an activation
 //               cache in shared memory (E4M3 codes in the swizzled B-operand
