@@ -399,9 +399,11 @@ __global__ void __maxnreg__((kBf16 ? 56 : 64))
         uint32_t word;
         const uint2 codes = quant16<kBf16, kNv>(raw, amax, r, inv6, c, c < whole, word);
         if (c < chunks) {
-            *reinterpret_cast<uint2 *>(xq_row + static_cast<unsigned>(c >> 4) * (kTiled ? 16384u : 128u) + (c & 15) * 8) = codes;
+            // (64-bit offsets: a row of 2^26 values and more has codes past 4 GB, one of 2^29 its scales)
+            *reinterpret_cast<uint2 *>(xq_row + static_cast<unsigned long long>(static_cast<unsigned>(c) >> 4) * (kTiled ? 16384u : 128u) +
+                                       (c & 15) * 8) = codes;
             if (c % kPerAtom == 0)
-                *reinterpret_cast<uint32_t *>(sf_row + static_cast<unsigned>(c / kPerAtom) * 512u) = word;
+                *reinterpret_cast<uint32_t *>(sf_row + static_cast<unsigned long long>(static_cast<unsigned>(c) / kPerAtom) * 512u) = word;
         }
     };
 #pragma unroll

@@ -227,3 +227,40 @@ def test_refusals():
         fb.fp4_gemm_fused(synth.activations(8, 512, seed=1).cuda(), *packed, 256,
                           workspace=fb.make_workspace(1024))
     assert e.value.code == 4
+
+
+def _long_row(K, seed):
+    """One bf16 row of K values, zero but for its first 256 and last 512; the
+    largest lies in both parts, so that either alone has the row's scale."""
+    x = torch.zeros((1, K), dtype=torch.bfloat16, device="cuda")
+    parts = [synth.activations(1, n, seed=seed + n) for n in (256, 512)]
+    for p in parts:
+        p[0, 7] = 64.0
+    x[:, :256], x[:, -512:] = parts[0].cuda(), parts[1].cuda()
+    return x, parts
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_weight_row_whose_codes_pass_32_bit_offsets(fmt):
+    """K = 2^26 + 512: the last K blocks' codes start 4 GB and more after the row's first."""
+    K = (1 << 26) + 512
+    w, parts = _long_row(K, 80)
+    wq, wa, wr = fb.fp4_quant_weights(w, fmt)
+    back = fb.fp4_dequant_weights(wq, wa, wr, 1, K, fmt)
+    for p, got in zip(parts, (back[:, :256], back[:, -512:])):
+        want = ref.values(*ref.quantise(_f32(p), fmt), fmt, np.float32)
+        assert np.array_equal(got.cpu().numpy(), want)
+    assert not back[:, 256:-512].any()
+    per = wa.shape[0] // wq.shape[0]
+    for p, tiles, atoms in ((parts[0], wq[:1], wa[:per]), (parts[1], wq[-2:], wa[-2 * per:])):
+        _check_packed(tiles, atoms, wr, _f32(p), fmt, True)
+
+
+def test_an_activation_row_whose_scales_pass_32_bit_offsets():
+    """K = 2^29 + 512, 16-wide scales: the last atoms lie 4 GB and more after the row's first."""
+    K = (1 << 29) + 512
+    x, parts = _long_row(K, 90)
+    xq, xa, xr = fb.fp4_quant_act(x, fb.FP4_NV)
+    for p, codes, atoms in ((parts[0], xq[:, :128], xa[:4]), (parts[1], xq[:, -256:], xa[-8:])):
+        _check_packed(codes, atoms, xr, _f32(p), fb.FP4_NV, False)
+    assert not xq[:, 128:-256].any()
