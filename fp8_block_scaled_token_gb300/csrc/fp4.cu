@@ -127,8 +127,7 @@ __device__ __forceinline__ float rcp_approx(float x)
 }
 
 // E4M3 code of fl32(fl32(amax / 6) / r); inv6 = 1 / (6 r) approximately, or
-// NaN where r is out of plain_range.  (An amax so small that the product is
-// not a normal number is far below the least code either way.)
+// NaN where nv_inv6 wants the divisions.
 __device__ __forceinline__ uint32_t nv_scale_code(float amax, float r, float inv6)
 {
     const float s = amax * inv6;
@@ -136,6 +135,16 @@ __device__ __forceinline__ uint32_t nv_scale_code(float amax, float r, float inv
     if ((both & 0xFFu) == (both >> 8) && s == s)
         return both & 0xFFu;
     return e4m3x4(__fdiv_rn(__fdiv_rn(amax, 6.0f), r), 0.0f, 0.0f, 0.0f) & 0xFFu;
+}
+
+// 1 / (6 r) approximately for rows where nv_scale_code may use it, else NaN.
+// fl32(amax / 6) is off by more than kQuotientSlack where it is not a normal
+// number.  With r >= 2^-112 such a block's quotient is below 2^-14, far under
+// the least code's boundary of 2^-10, and its code 0 either way; the rows of
+// smaller r (largest value below 5.2e-31) are divided.
+__device__ __forceinline__ float nv_inv6(float r)
+{
+    return r >= 1.92592994e-34f && plain_range(r) ? rcp_approx(r) * (1.0f / 6.0f) : __int_as_float(0x7fffffff);
 }
 
 // Raw bits of sixteen consecutive source values.
@@ -386,7 +395,7 @@ __global__ void __maxnreg__((kBf16 ? 56 : 64))
         __syncthreads();
         amax = warp_max(static_cast<int>(threadIdx.x & 31) < threads / 32 ? warp_amax[threadIdx.x & 31] : 0.0f);
         r = nv_row_scale(amax);
-        inv6 = plain_range(r) ? rcp_approx(r) * (1.0f / 6.0f) : __int_as_float(0x7fffffff);
+        inv6 = nv_inv6(r);
     }
     if (threadIdx.x == 0 && real && row_scale != nullptr)
         row_scale[row] = r;

@@ -264,3 +264,26 @@ def test_an_activation_row_whose_scales_pass_32_bit_offsets():
     for p, codes, atoms in ((parts[0], xq[:, :128], xa[:4]), (parts[1], xq[:, -256:], xa[-8:])):
         _check_packed(codes, atoms, xr, _f32(p), fb.FP4_NV, False)
     assert not xq[:, 128:-256].any()
+
+
+def test_scales_of_blocks_whose_sixth_is_not_a_normal_number():
+    """Rows so small that fl32(amax_16 / 6) is subnormal and its rounding
+    decides the scale byte (the first: 147455 / 6 rounds to 24576 units, the
+    quotient is 1.5 * 2^-9, a tie), and rows on either side of them."""
+    rng = np.random.RandomState(5)
+    rows = []
+    for e in (-126, -125, -120, -114, -113, -112, -111, -108):
+        v = rng.randint(0, 2 ** 18, (4, 512)) * 2.0 ** -149
+        v[0, 17], v[0, 16], v[0, 18:32] = 147455 * 2.0 ** -149, 0, 0
+        v[1] *= 4
+        v[2] *= 2.0 ** (e + 126)
+        v[:, 0] = 2688 * 2.0 ** e
+        rows.append(v * rng.choice([-1, 1], v.shape))
+    v = np.concatenate(rows).astype(np.float32)
+    assert ref.quantise(v[:1], fb.FP4_NV)[1][0, 1] == 2
+    wq, wa, wr = fb.fp4_quant_weights(torch.from_numpy(v).cuda())
+    codes, byte, r = _check_packed(wq, wa, wr, v, fb.FP4_NV, True)
+    back = fb.fp4_dequant_weights(wq, wa, wr, *v.shape)
+    assert np.array_equal(back.cpu().numpy(), ref.values(codes, byte, r, fb.FP4_NV, np.float32))
+    xb = torch.from_numpy(v).to(torch.bfloat16)
+    _check_packed(*fb.fp4_quant_act(xb.cuda()), _f32(xb), fb.FP4_NV, False)
