@@ -10,6 +10,9 @@
 //     e    = floor(log2(amax_32)) - 2, clamped to [-127, 127] (0 for a zero block)
 //     code = e2m1_rn_satfinite(v / 2^e)   (exact scaling)
 // A code's value is fl32(code * d), or code * 2^e.
+// A NaN or an infinity makes its row's r NaN or infinite (NV), or its block's
+// scale byte 255, NaN (MX): every product with it is NaN, whatever the codes,
+// which have no NaN of their own.
 //
 // Two codes to a byte, the lower K in the lower four bits; K is padded with
 // zero codes and zero scales to whole 256-wide blocks.  Scale bytes in the
@@ -268,22 +271,29 @@ template <bool kBf16> __device__ __forceinline__ uint2 nv_codes16(const Raw16<kB
     return make_uint2(codes[0], codes[1]);
 }
 
-// The larger magnitude of each half (with the signs' exclusive or).
+// The larger magnitude of each half (with the signs' exclusive or), NaN where
+// either is NaN.
 __device__ __forceinline__ uint32_t abs_max_bf16x2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Their largest magnitude (fp32: the bits of non-negative numbers order like
-// the values).
+// The larger of two magnitudes, NaN if either is: the bits of non-negative
+// numbers order like the values, and NaN above infinity.
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+// Their largest magnitude, NaN if one is NaN.
 template <bool kBf16> __device__ __forceinline__ float abs_max16(const Raw16<kBf16> &r)
 {
     if (kBf16) {
         uint32_t m = abs_max_bf16x2(abs_max_bf16x2(abs_max_bf16x2(r.w[0].x, r.w[0].y), abs_max_bf16x2(r.w[0].z, r.w[0].w)),
                                     abs_max_bf16x2(abs_max_bf16x2(r.w[1].x, r.w[1].y), abs_max_bf16x2(r.w[1].z, r.w[1].w)));
-        return fmaxf(fabsf(bf16_lo(m)), fabsf(bf16_hi(m)));
+        return __uint_as_float(max((m << 16) & 0x7FFF0000u, m & 0x7FFF0000u));
     }
     uint32_t m = 0;
 #pragma unroll
@@ -309,7 +319,7 @@ __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, fl
         word |= __shfl_xor_sync(0xffffffffu, word, 1);
         word |= __shfl_xor_sync(0xffffffffu, word, 2);
     } else {
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         const uint32_t b = __float_as_uint(amax);
         const int E = static_cast<int>(b >> 23);
         int e = E == 0 ? (b == 0u ? 0 : -127) : E - 127 - 2;
@@ -323,7 +333,8 @@ __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, fl
         for (int i = 0; i < 16; ++i)
             v[i >> 3][i & 7] *= inv;
         codes = make_uint2(e2m1x8(v[0]), e2m1x8(v[1]));
-        word = live ? static_cast<uint32_t>(e + 127) << (8 * ((c >> 1) & 3)) : 0u;
+        const uint32_t byte = E == 255 ? 255u : static_cast<uint32_t>(e + 127); // (NaN or infinite: 255 is NaN)
+        word = live ? byte << (8 * ((c >> 1) & 3)) : 0u;
         word |= __shfl_xor_sync(0xffffffffu, word, 2);
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
     }
@@ -385,10 +396,10 @@ __global__ void __maxnreg__((kBf16 ? 56 : 64))
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < kHold; ++i)
-            amax = fmaxf(amax, held_amax[i]);
+            amax = max_or_nan(amax, held_amax[i]);
 #pragma unroll 1
         for (int c = static_cast<int>(threadIdx.x) + kHold * threads; c < whole; c += threads)
-            amax = fmaxf(amax, abs_max16<kBf16>(load16<kBf16>(src, c * kFp4Chunk)));
+            amax = max_or_nan(amax, abs_max16<kBf16>(load16<kBf16>(src, c * kFp4Chunk)));
         amax = warp_max(amax);
         if ((threadIdx.x & 31) == 0)
             warp_amax[threadIdx.x >> 5] = amax;
@@ -472,7 +483,8 @@ __global__ void __launch_bounds__(256)
         const int k = k0 + t * 32 * kPer;
         if (k >= K)
             continue;
-        const float s = kNv ? e4m3_value(byte[t]) : __uint_as_float(byte[t] == 0u ? 0x400000u : byte[t] << 23);
+        const float s = kNv ? e4m3_value(byte[t])
+                            : __uint_as_float(byte[t] == 0u ? 0x400000u : byte[t] == 255u ? 0x7FFFFFFFu : byte[t] << 23);
         const float d = s * row;
         float v[8];
         e2m1x8_values(cw[t], v);

@@ -399,7 +399,12 @@ FP8BS_API fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8
  *   FP8BS_FP4_MX  every 32 consecutive values share one power of two 2^e:
  *       e    = floor(log2(amax_32)) - 2, clamped to [-127, 127] (0 for zeros)
  *       code = e2m1_rn_satfinite(v / 2^e)   (exact scaling); r = 1
- * Divisions are IEEE fp32.  Inputs must be finite.
+ * Divisions are IEEE fp32.  The codes have no NaN, the scales do: a NaN or an
+ * infinity among the values makes its row's r NaN or infinite (NV), or the
+ * scale byte of its block 255, which is NaN (MX).  Reading back then gives NaN
+ * for that row or block and a product NaN for that token or column, and for
+ * nothing else; the codes (NV: and scale bytes) under such a scale are not
+ * specified.
  *
  * K is a multiple of 32, padded inside the packed operands to kt = ceil(K/256)
  * blocks of 256 with zero codes and zero scale bytes.  Two codes to a byte,

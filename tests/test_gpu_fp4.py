@@ -287,3 +287,54 @@ def test_scales_of_blocks_whose_sixth_is_not_a_normal_number():
     assert np.array_equal(back.cpu().numpy(), ref.values(codes, byte, r, fb.FP4_NV, np.float32))
     xb = torch.from_numpy(v).to(torch.bfloat16)
     _check_packed(*fb.fp4_quant_act(xb.cuda()), _f32(xb), fb.FP4_NV, False)
+
+
+BAD = [float("nan"), -float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("at", [0, 1, 31, 517, 1055, 18500, 20000])   # (rows past 18,432 values are read twice)
+def test_bad_activations_make_their_own_row_nan(fmt, at):
+    M, N, K = 9, 200, 1056 if at < 1056 else 20480
+    x, packed, _, _ = _layer(M, N, K, fmt, seed=31)
+    good = fb.fp4_gemm_fused(x, *packed, N, fmt)
+    bad = x.clone()
+    rows = [1, 3, 6, 8]
+    for m, v in zip(rows, BAD):
+        bad[m, at] = v
+    work = fb.make_workspace(fb.fp4_gemm_workspace_size(M, N, K, fmt))
+    y = fb.fp4_gemm_fused(bad, *packed, N, fmt, workspace=work)
+    assert y[rows].isnan().all()
+    keep = [m for m in range(M) if m not in rows]
+    assert torch.equal(y[keep].view(torch.int16), good[keep].view(torch.int16))
+    y2 = fb.fp4_gemm(*fb.fp4_quant_act(bad, fmt), *packed, N, K, fmt, workspace=work)
+    assert y2[rows].isnan().all() and torch.equal(y2[keep].view(torch.int16), good[keep].view(torch.int16))
+    assert fb.workspace_status(work) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K,at", [(1056, 0), (1056, 1055), (20480, 20001)])
+def test_bad_weights_make_their_own_row_or_block_nan(fmt, dtype, K, at):
+    N = 140
+    w = synth.weights(N, K, seed=41).to(dtype)
+    rows = [0, 5, 128, 139]
+    for n, v in zip(rows, BAD):
+        w[n, at] = v
+    packed = fb.fp4_quant_weights(w.cuda(), fmt)
+    x = synth.activations(3, K, seed=42).cuda()
+    y = fb.fp4_gemm_fused(x, *packed, N, fmt)
+    keep = [n for n in range(N) if n not in rows]
+    assert y[:, rows].isnan().all() and not y[:, keep].isnan().any()
+    for as_type in (torch.float32, torch.bfloat16):
+        back = fb.fp4_dequant_weights(*packed, N, K, fmt, dtype=as_type)
+        nan = torch.zeros((N, K), dtype=torch.bool, device="cuda")
+        if fmt == fb.FP4_NV:
+            nan[rows] = True
+        else:
+            nan[rows, at // 32 * 32:at // 32 * 32 + 32] = True
+        assert torch.equal(back.isnan(), nan)
+    clean = w.clone()
+    clean[rows] = 0
+    want = ref.values(*ref.quantise(_f32(clean), fmt), fmt, np.float32)
+    assert np.array_equal(fb.fp4_dequant_weights(*packed, N, K, fmt).cpu().numpy()[keep], want[keep])
