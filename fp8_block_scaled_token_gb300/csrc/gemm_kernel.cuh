@@ -905,13 +905,39 @@ __global__ void __maxnreg__((GemmCfg<NPAD, MODE>::kMaxRegs))
             // Final values of the tile (weight tile wt, token tile ttile): by TMA
             // from the staging tile where the launch set it up, else per row.
             // Every epilogue warp calls it (it holds named barriers).
-            // 4-bit: the finished sums times their weight row's and token's fp32 scales
+            // 4-bit: the finished sums times their weight row's and token's fp32
+            // scales.  The product of the two scales alone may leave the normal
+            // range where Y does not (two scales of 2^-70, a sum of 2^20), and so
+            // may the sum times either.  So rw = f s1 s2 with f in [0.5, 1) and
+            // powers of two s1, s2 of half its exponent each, and Y = sum s1 (f ra)
+            // s2: a sum (2^-20 to 2^53, or 0) times s1 is normal, f ra is where ra
+            // is, and what leaves the range before the last step, with s2 on the
+            // same side of 1, leaves it in the end as well.  The powers are exact,
+            // so the bits are those of sum (rw ra) wherever rw ra is normal.
             auto apply_rows = [&](int n) {
                 if constexpr (C::kFp4) {
                     const float rw = p.row_w != nullptr && n < p.N ? p.row_w[n] : 1.0f;
+                    const uint32_t bits = __float_as_uint(rw);
+                    const int field = static_cast<int>(bits >> 23 & 0xFFu);
+                    float f = __uint_as_float((bits & 0x807FFFFFu) | 126u << 23);
+                    int e = field - 126;
+                    if (field == 0) // zero or subnormal: 2^64 rw, at most 2^-62
+                        f = rw * 18446744073709551616.0f, e = -64;
+                    if (field == 255)
+                        f = rw, e = 0;
+                    const int e1 = e >> 1;
+                    const float s1 = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+                    const float s2 = __uint_as_float(static_cast<uint32_t>(127 + e - e1) << 23);
 #pragma unroll
-                    for (int m = 0; m < C::kCols; ++m)
-                        acc[m] *= p.row_a != nullptr && m < mcnt ? rw * p.row_a[tok0 + m] : rw;
+                    for (int m = 0; m < C::kCols; m += 2) {
+                        float ra[2], t[2];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            ra[q] = p.row_a != nullptr && m + q < mcnt ? p.row_a[tok0 + m + q] : 1.0f;
+                        mul2(ra[0], ra[1], ra[0], ra[1], f);
+                        mul2(t[0], t[1], acc[m], acc[m + 1], s1);
+                        mul2(acc[m], acc[m + 1], t[0] * ra[0], t[1] * ra[1], s2);
+                    }
                 }
             };
             bool y_pending = false; // warp 2 lane 0: a TMA store may still read the staging tile

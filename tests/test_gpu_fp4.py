@@ -338,3 +338,51 @@ def test_bad_weights_make_their_own_row_or_block_nan(fmt, dtype, K, at):
     clean[rows] = 0
     want = ref.values(*ref.quantise(_f32(clean), fmt), fmt, np.float32)
     assert np.array_equal(fb.fp4_dequant_weights(*packed, N, K, fmt).cpu().numpy()[keep], want[keep])
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 200, 1056), (40, 384, 512), (130, 256, 512)])
+@pytest.mark.parametrize("ew,ex", [(-60, -60), (-70, -45), (-100, 40), (60, -100), (40, 45)])
+def test_row_scales_whose_product_leaves_the_normal_range(M, N, K, ew, ex):
+    """Weights times 2^ew and activations times 2^ex give codes and scales that
+    differ by those powers alone, and Y by 2^(ew + ex): a normal number in all
+    of these, while the product of two row scales, 2^-24 times that, may be none.
+    Tolerance: one bf16 rounding and fp32 sums, 4e-3 of sum |a w|, as above."""
+    x = synth.activations(M, K, seed=M, outlier_p=0.001).float() * 2.0 ** ex
+    w = synth.weights(N, K, seed=N, outlier_p=0.01) * 2.0 ** ew
+    a = ref.values(*ref.quantise(_f32(x), fb.FP4_NV), fb.FP4_NV)
+    b = ref.values(*ref.quantise(_f32(w), fb.FP4_NV), fb.FP4_NV)
+    y = fb.fp4_gemm_fused(x.to(torch.bfloat16).cuda(), *fb.fp4_quant_weights(w.cuda()), N).double().cpu().numpy()
+    assert np.all(np.abs(y - a @ b.T) <= 4e-3 * (np.abs(a) @ np.abs(b).T))
+
+
+def test_row_scales_past_the_largest_number():
+    """r_a r_w overflows; the sum is 0 (no K in common) or small: 0 and a finite Y."""
+    M, N, K = 3, 130, 512
+    x, w = torch.zeros((M, K)), torch.zeros((N, K))
+    x[:, 5], w[:, 300] = 2.0 ** 76, 2.0 ** 76                      # the rows' largest, never multiplied together
+    y = fb.fp4_gemm_fused(x.to(torch.bfloat16).cuda(), *fb.fp4_quant_weights(w.cuda()), N)
+    assert not y.any()
+    x[:, 400], w[:, 400] = 2.0 ** 64, 2.0 ** 62
+    xb = x.to(torch.bfloat16)
+    a = ref.values(*ref.quantise(_f32(xb), fb.FP4_NV), fb.FP4_NV)
+    b = ref.values(*ref.quantise(_f32(w), fb.FP4_NV), fb.FP4_NV)
+    want = a @ b.T
+    assert want.min() > 2.0 ** 125
+    y = fb.fp4_gemm_fused(xb.cuda(), *fb.fp4_quant_weights(w.cuda()), N).double().cpu().numpy()
+    assert np.all(np.abs(y - want) <= 4e-3 * want)
+
+
+def test_given_row_scales_of_any_size():
+    """Scales that the caller gives, zero, subnormal, negative and infinite ones among them."""
+    M, N, K = 6, 128, 256
+    xq, xa, _ = fb.fp4_quant_act(synth.activations(M, K, seed=1).cuda(), fb.FP4_MX)
+    packed = fb.fp4_quant_weights(synth.weights(N, K, seed=2, std=1.0).cuda(), fb.FP4_MX)
+    plain = fb.fp4_gemm(xq, xa, None, *packed[:2], None, N, K, fb.FP4_MX).double().cpu().numpy()
+    ra = np.array([0.0, 2.0 ** -140, -2.0 ** -60, 2.0 ** 100, float("inf"), 1.0], np.float32)
+    rw = np.array([2.0 ** 126, 2.0 ** -70, 2.0 ** 100], np.float32)[np.arange(N) % 3]
+    y = fb.fp4_gemm(xq, xa, torch.from_numpy(ra).cuda(), *packed[:2], torch.from_numpy(rw).cuda(), N, K,
+                    fb.FP4_MX).double().cpu().numpy()
+    want = plain * (ra.astype(np.float64)[:, None] * rw.astype(np.float64)[None])
+    big, small = np.abs(want) > 3.5e38, np.abs(want) < 3.3e38
+    assert np.all(np.isinf(y[big]) & (np.sign(y[big]) == np.sign(want[big])))
+    assert np.all(np.abs(y[small] - want[small]) <= 8e-3 * np.abs(want[small]) + 2.0 ** -133)
