@@ -619,10 +619,17 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
             // s_w * s_a of this unit's tokens, per warp (double-buffered by
             // parity: rewritten only after every lane passed the next __syncwarp)
             float *pr = wprod + (i & 1) * C::kTiles * C::kCols;
+            // down: the tokens that chose this unit's expert.  The others' codes
+            // and scales are 0, but 0 times a weight or a block scale that is not
+            // finite is NaN, and an expert's is to reach no token beside its own.
+            // (A NaN among a row's 128 weights makes all its columns NaN, the
+            // first among them, so the sums are looked through only then:
+            // doing it always took 250 us where 64 tokens take 239.)
+            const unsigned chose = kUp ? 0u : __ballot_sync(0xffffffffu, nx[0].a != 0.0f);
             if (lane < C::kCols) {
 #pragma unroll
                 for (int t = 0; t < C::kTiles; ++t)
-                    pr[t * C::kCols + lane] = nx[0].w[t] * nx[0].a;
+                    pr[t * C::kCols + lane] = kUp || nx[0].a != 0.0f ? nx[0].w[t] * nx[0].a : 0.0f;
             }
             __syncwarp();
             Unit nu = u;
@@ -642,6 +649,10 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
                 uint32_t r[C::kCols];
                 tmem_issue(taddr + t * NPAD, r);
                 tmem_wait(r);
+                if (!kUp && isnan(__uint_as_float(r[0])))
+#pragma unroll
+                    for (int q = 0; q < C::kCols; ++q)
+                        r[q] = chose >> q & 1u ? r[q] : 0u;
 #pragma unroll
                 for (int q = 0; q < C::kCols / 4; ++q) {
                     const float4 sc = reinterpret_cast<const float4 *>(pr + t * C::kCols)[q];

@@ -349,7 +349,8 @@ FP8BS_API fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, c
  *             weight multiplies the scale of h)
  * Only the active experts' weights are read, each byte once.  Bitwise
  * reproducible: no sum's order depends on timing.  A token with NaN or
- * infinite values gives NaN in its own row of y only.
+ * infinite values gives NaN in its own row of y only, and an expert with NaN
+ * codes or scales that are not finite in the rows of the tokens that chose it.
  *
  * x: bf16 [M][ldx], 16-byte aligned, ldx % 8 == 0, ldx >= H.
  * wr: router weights fp32 or bf16 [E][H], 16-byte aligned.

@@ -214,6 +214,32 @@ def test_an_unchosen_experts_overflow_is_not_seen():
     check_y(y[1:], y_ref[1:], bound[1:], "tokens beside an overflow")
 
 
+@pytest.mark.parametrize("where", ["w2", "w13", "s2", "s13"])
+@pytest.mark.parametrize("M", [3, 20, 50])
+def test_an_unchosen_experts_bad_weights_are_not_seen(M, where):
+    """Expert 1 has a NaN code or an infinite or NaN block scale; tokens 0 and M - 1 choose it."""
+    t = Layer(M, 4, 2, 256, 384, seed=M)
+    ids = np.stack([np.full(M, 2), np.arange(M) % 2 * 3], 1).astype(np.int32)
+    ids[[0, M - 1], 1] = 1
+    w = np.random.RandomState(M).uniform(0.2, 1, (M, 2)).astype(np.float32)
+    y_ref, bound = ref.experts(t.x64(), ids, w, t.v13, t.v2)
+    keep = np.arange(1, M - 1)
+    if where == "w2":
+        t.c2[1, :, 130] = 0x7F                                     # a NaN in every row
+    elif where == "w13":
+        t.c13[1, 5:: 384, 7] = 0xFF                                # of one gate and one up row
+    else:
+        s = getattr(t, where)                                      # [128-row tiles of all experts, K blocks]
+        n = s.shape[0] // 4
+        s[n:2 * n] = np.where(np.arange(s.shape[1]) % 2, np.nan, np.inf)
+    work = t.workspace()
+    y = fb.fp8_moe_experts(t.x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), *t.operands(),
+                           experts=4, workspace=work)
+    assert fb.workspace_status(work) == 0
+    check_y(y[1:-1], y_ref[keep], bound[keep], "tokens beside a bad expert")
+    assert y[[0, M - 1]].isnan().all()
+
+
 def test_strides_streams_reruns_and_a_clean_workspace():
     M, E, k, H, I = 11, 20, 4, 640, 256
     t = Layer(M, E, k, H, I, seed=33)
