@@ -349,12 +349,13 @@ __device__ __forceinline__ uint2 quant16(const Raw16<kBf16> &raw, float amax, fl
 // activations, codes [row][kg * 128].  Atoms [128-row tile][kg * atoms a
 // unit][512] either way; the activations' rows past M are not written (they
 // only ever meet token columns that are not stored).
+// (No __restrict__: an activation cast starts while the kernel that writes x may
+// still run, and x must not pass for constant over this kernel's whole life.)
 // (56 registers: three CTAs of 384 threads an SM, 117 us with two)
 template <bool kBf16, bool kNv, bool kTiled>
 __global__ void __maxnreg__((kBf16 ? 56 : 64))
-    fp4_quant_rows_kernel(const void *__restrict__ x, int rows, int K, long long ldx, int kg, uint8_t *__restrict__ xq,
-                          uint8_t *__restrict__ sf, float *__restrict__ row_scale, int overlap,
-                          unsigned long long *runs)
+    fp4_quant_rows_kernel(const void *x, int rows, int K, long long ldx, int kg, uint8_t *xq, uint8_t *sf,
+                          float *row_scale, int overlap, unsigned long long *runs)
 {
     constexpr int kHold = kRowHold<kBf16>;
     const int threads = static_cast<int>(blockDim.x);

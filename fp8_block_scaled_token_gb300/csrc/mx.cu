@@ -107,13 +107,12 @@ __global__ void __launch_bounds__(256) mx_quant_weight_kernel(const void *__rest
 // one atom word they form (word 4 (r % 32) + r / 32), zero for rows >= M; the
 // last slice's CTA also zeroes the words of the rows past every slice (a tile
 // of fewer than 128 tokens has fewer slices).  Codes row-major [M][K]; atoms
-// [token tile][K group].
+// [token tile][K group].  No __restrict__, as in quant_act_kernel.
 constexpr int kMxCastWarps = 4;
 constexpr int kMxSliceRows = 16;                                   // rows per CTA
 constexpr int kMxRowsPerWarp = kMxSliceRows / kMxCastWarps;        // loaded together
 
-__global__ void __maxnreg__(32) mx_quant_act_kernel(const uint16_t *__restrict__ x, int M, int K, int ldx,
-                                                           uint8_t *__restrict__ xq, uint8_t *__restrict__ sf,
+__global__ void __maxnreg__(32) mx_quant_act_kernel(const uint16_t *x, int M, int K, int ldx, uint8_t *xq, uint8_t *sf,
                                                            unsigned long long *runs)
 {
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)

@@ -30,10 +30,11 @@ constexpr int kCastThreads = 128;
 // layout the GEMM reads above 16 tokens) rather than token-major
 // ([M][K/128]); a separate instantiation each, so the token-major one's code
 // is the same as if the other did not exist.
+// No __restrict__: under programmatic dependent launch the kernel that writes x
+// may still run when this one starts, so x must not pass for constant.
 template <bool kKMajor>
-__global__ void __launch_bounds__(kCastThreads) quant_act_kernel(const uint16_t *__restrict__ x, int M, int K, int ldx,
-                                                        uint8_t *__restrict__ xq, float *__restrict__ xs,
-                                                        unsigned long long *runs)
+__global__ void __launch_bounds__(kCastThreads) quant_act_kernel(const uint16_t *x, int M, int K, int ldx,
+                                                        uint8_t *xq, float *xs, unsigned long long *runs)
 {
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(runs + FP8BS_RUNS_QUANT_ACT, 1ull);
