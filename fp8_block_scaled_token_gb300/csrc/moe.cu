@@ -13,6 +13,7 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     const size_t active = static_cast<size_t>(E < M * top_k ? E : M * top_k);
     MoeWorkspace w;
     w.route_off = kMoeRouteOff;
+    w.chosen_off = kMoeRouteOff + (kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32) * 4;
     w.counters_down_off = kCountersOff;
     w.counters_up_off = w.counters_down_off + static_cast<size_t>(H / 128) * 4;
     w.logits_off = kCountersOff + counters_region(static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4);
@@ -34,7 +35,7 @@ namespace {
 // The routing words lie behind the GEMMs' greedy keys and counter (64 64-bit
 // words and one 32-bit word from byte 256), which like them are zero between calls.
 static_assert(kMoeRouteOff >= 256 + 64 * 8 + 4 &&
-                  kMoeRouteOff + (kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32) * 4 <= kCountersOff,
+                  kMoeRouteOff + (kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32 + 1) * 4 <= kCountersOff,
               "routing words");
 static_assert(kMoeMaxTokens / kMoeTokenGroup * (kMoeMaxExperts / 32) * 4 % 256 == 0, "masks");
 

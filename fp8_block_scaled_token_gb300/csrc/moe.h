@@ -21,6 +21,7 @@ constexpr size_t kMoeRouteOff = 832;
 struct MoeWorkspace {
     size_t route_off;         // arrival counters of the kMoeMaxTokens / kMoeTokenGroup groups of tokens, then a
                               // bit mask of the experts (kMoeMaxExperts / 32 words) for a given choice
+    size_t chosen_off;        // 1 from the gate/up product's start to the down product's end: the masks are complete
     size_t logits_off;        // [M][E] router logits
     size_t counters_up_off;   // arrival counters of the (active expert, 128 of I) pairs
     size_t counters_down_off; // arrival counters of the 128-row tiles of H

@@ -53,6 +53,7 @@ struct MoeGemmParams {
     int M, H, I, E;
     int stages;
     const unsigned *masks; // [groups][kMoeMaxExperts / 32] experts that each group of tokens chose
+    unsigned *chosen;      // 1 while the masks are known to be complete: up sets it, down clears it
     int groups;
     const float *wtok;     // [E][NPAD]
     const float *ws;       // weight block scales: s13 [E][2I/128][H/128] or s2 [E][H/128][I/128]
@@ -155,12 +156,21 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
         tmem_relinquish();
     }
     // The list of active experts, ascending, from the masks that the routing
-    // kernel left: the up product's predecessor, which it waits for here, and
-    // the down product's predecessor's, complete because every CTA of the up
-    // product has passed this wait before it lets this grid start.
-    if (kUp)
+    // kernel left: the up product's predecessor, which it waits for here.  The
+    // down product, which is to stream its first weights while the up product
+    // finishes, takes them over from the up product's first CTA: that one has
+    // waited, and publishes so before it lets this grid start (release here,
+    // acquire there).  A CTA that does not find the word set waits for the whole
+    // up product: the last of the down product's CTAs may, after the first has
+    // finished and cleared it.
+    if (kUp) {
         grid_dependency_wait();
+        if (cta == 0 && threadIdx.x == 0)
+            store_release_gpu(p.chosen, 1u);
+    }
     if (warp == 2) {
+        if (!kUp && !__all_sync(0xffffffffu, load_acquire_gpu(p.chosen) != 0u))
+            grid_dependency_wait();
         unsigned word = 0; // lane w: experts 32 w .. 32 w + 31
         if (lane < (p.E + 31) / 32) {
 #pragma unroll
@@ -736,6 +746,8 @@ __global__ void __maxnreg__((MoeCfg<NPAD, PHASE>::kMaxRegs))
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
+    if (!kUp && cta == 0 && threadIdx.x == 0)
+        store_release_gpu(p.chosen, 0u); // (this thread has waited for the up product)
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem_base, C::kTmemCols);
@@ -780,6 +792,7 @@ fp8bs_status launch_moe_gemm(const MoeLaunch &L, const MoeWorkspace &w, const De
     p.E = L.E;
     p.stages = stages;
     p.masks = reinterpret_cast<const unsigned *>(L.workspace + w.masks_off);
+    p.chosen = reinterpret_cast<unsigned *>(L.workspace + w.chosen_off);
     p.groups = L.wr != nullptr ? (L.M + kMoeTokenGroup - 1) / kMoeTokenGroup : 1; // (a given choice: one)
     p.wtok = reinterpret_cast<const float *>(L.workspace + w.wtok_off);
     p.ws = kUp ? L.s13 : L.s2;

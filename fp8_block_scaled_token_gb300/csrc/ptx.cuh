@@ -310,6 +310,19 @@ __device__ __forceinline__ unsigned atomic_add_acq_rel_gpu(unsigned *p, unsigned
     return old;
 }
 
+// Publishes a word with everything that happens-before it, and the read that
+// takes both up.
+__device__ __forceinline__ void store_release_gpu(unsigned *p, unsigned v)
+{
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned load_acquire_gpu(const unsigned *p)
+{
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // ----------------------------------------------- programmatic dependent launch
 __device__ __forceinline__ void grid_dependency_wait()
 {
