@@ -130,6 +130,14 @@ WorkspaceLayout workspace_layout(const GemmShape &sh, int M, int K)
     return w;
 }
 
+fp8bs_status zero_far_counters(void *workspace, size_t bytes, cudaStream_t stream)
+{
+    if (bytes <= kCountersRegion)
+        return FP8BS_OK;
+    return launch_status(cudaMemsetAsync(static_cast<uint8_t *>(workspace) + kCountersOff + kCountersRegion, 0,
+                                         bytes - kCountersRegion, stream));
+}
+
 Fp4Workspace fp4_workspace(const GemmShape &sh, int M, int sf_atoms)
 {
     auto up256 = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -271,6 +279,9 @@ fp8bs_status run_gemm(GemmLaunch &L)
     const size_t need = L.mode == 4 ? fp4_workspace(sh, L.M, L.sf_atoms).total : workspace_layout(sh, L.M, L.K).total;
     if (L.workspace_bytes < need)
         return FP8BS_ERR_WORKSPACE_TOO_SMALL;
+    st = zero_far_counters(L.workspace, static_cast<size_t>(sh.ttiles) * sh.ntiles * 4, L.stream);
+    if (st != FP8BS_OK)
+        return st;
     switch (L.mode) {
     case 0:
         return launch_gemm_fp8(L, dev);

@@ -58,14 +58,17 @@ struct WorkspaceLayout {
 // What has to be zero between calls lies in the same place for every shape and
 // every operator, with no shape's data in it, so that calls of different
 // shapes may share a workspace: up to 16,384 counters (2 million weight rows at
-// one token tile) have a region of that size; a larger shape's region extends
-// over what others use for data, so it needs a workspace of its own.
+// one token tile) have a region of that size.  A larger shape's region extends
+// over what others use for data, and that part is zeroed before its kernels.
 constexpr size_t kCountersOff = 1024;
 constexpr size_t kCountersRegion = 16384 * 4;
 inline size_t counters_region(size_t bytes)
 {
     return bytes <= kCountersRegion ? kCountersRegion : (bytes + 255) / 256 * 256;
 }
+// Enqueues the zeroing of the counters past kCountersRegion, where there are
+// `bytes` of them (nothing for the usual sizes).
+fp8bs_status zero_far_counters(void *workspace, size_t bytes, cudaStream_t stream);
 struct GemmShape;
 WorkspaceLayout workspace_layout(const GemmShape &sh, int M, int K);
 

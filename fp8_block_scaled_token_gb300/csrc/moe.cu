@@ -16,7 +16,8 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     w.chosen_off = kMoeRouteOff + (kMoeMaxTokens / kMoeTokenGroup + kMoeMaxExperts / 32) * 4;
     w.counters_down_off = kCountersOff;
     w.counters_up_off = w.counters_down_off + static_cast<size_t>(H / 128) * 4;
-    w.logits_off = kCountersOff + counters_region(static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4);
+    w.counters_bytes = static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4;
+    w.logits_off = kCountersOff + counters_region(w.counters_bytes);
     w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4);
     w.ids_off = w.masks_off + static_cast<size_t>(kMoeMaxTokens / kMoeTokenGroup) * (kMoeMaxExperts / 32) * 4;
     w.topw_off = w.ids_off + up256(static_cast<size_t>(M) * top_k * 4);
@@ -80,7 +81,9 @@ fp8bs_status run_experts(MoeLaunch &L, size_t workspace_bytes)
         L.ids = reinterpret_cast<int32_t *>(L.workspace + w.ids_off);
     if (L.topw == nullptr)
         L.topw = reinterpret_cast<float *>(L.workspace + w.topw_off);
-    st = launch_moe_route(L, w, dev);
+    st = zero_far_counters(L.workspace, w.counters_bytes, L.stream);
+    if (st == FP8BS_OK)
+        st = launch_moe_route(L, w, dev);
     if (st == FP8BS_OK)
         st = launch_moe_up(L, w, dev);
     if (st == FP8BS_OK)

@@ -25,6 +25,7 @@ struct MoeWorkspace {
     size_t logits_off;        // [M][E] router logits
     size_t counters_up_off;   // arrival counters of the (active expert, 128 of I) pairs
     size_t counters_down_off; // arrival counters of the 128-row tiles of H
+    size_t counters_bytes;    // of both
     size_t masks_off;         // [groups of tokens][kMoeMaxExperts / 32] bit masks of the experts they chose
     size_t ids_off;           // [M][top_k] chosen experts, where the caller keeps none
     size_t topw_off;          // [M][top_k] their weights

@@ -167,9 +167,10 @@ FP8BS_API fp8bs_status fp8_quant_weight_blocks_tiled(const void *w, fp8bs_dtype 
  * first use.  Every call that completes leaves its counter words zero again,
  * and they lie in the same place whatever the shape and the entry point, so one
  * workspace of the largest size serves any number of later calls, of any
- * shapes and of all entry points that take one, and CUDA-graph replays.  (Except
- * a shape with more than 16,384 tiles, ceil(N/128) * token tiles or, for an
- * expert layer, H/128 + active experts * I/128: it needs one of its own.)
+ * shapes and of all entry points that take one, and CUDA-graph replays.  (A
+ * shape with more than 16,384 tiles, ceil(N/128) * token tiles or, for an expert
+ * layer, H/128 + active experts * I/128, zeroes the counters past those before
+ * its kernels, by one cudaMemsetAsync.)
  * Calls that share a workspace must not run concurrently (same stream, or
  * ordered by events).  After FP8BS_ERR_DEVICE_TIMEOUT, zero-fill it again.
  */

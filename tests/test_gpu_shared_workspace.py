@@ -2,6 +2,9 @@
 step's layers share it: what has to be zero between calls (status word, greedy
 keys, routing words, arrival counters) lies where no call keeps its data.
 
+More than 16,384 tiles: the counters past those lie where smaller shapes keep
+data, and the call zeroes them.
+
 The order matters: a call with few tiles first, whose split-K partials are
 written, then one with many, whose counters reach further.
 """
@@ -77,3 +80,59 @@ def test_routing_alone_shares_too():
     wr = synth.weights(100, 512, seed=2, device="cuda")
     _check([(fb.moe_route_workspace_size(20, 100), lambda work: fb.moe_route(x, wr, 4, workspace=work)),
             _fp8(8, 8704, 3, "fp8"), _moe(5, 40, 3, 512, 256, 2)])
+
+
+FAR = 20000 * 128  # rows: 20,000 tiles, two or four K blocks each, so that CTAs share tiles past 16,384
+
+
+def _far(kind):
+    x = synth.activations(8, 512 if kind == "fp4" else 256, seed=5, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    w = torch.randn((FAR, x.shape[1]), generator=g, device="cuda", dtype=torch.bfloat16)
+    if kind == "fp4":
+        q = fb.fp4_quant_weights(w)
+        return fb.fp4_gemm_workspace_size(8, FAR, 512), lambda work, y: fb.fp4_gemm_fused(x, *q, FAR, y=y, workspace=work)
+    if kind == "mx":
+        a, q = fb.fp8_mx_quant_act(x), fb.fp8_mx_quant_weights(w)
+        return fb.fp8_mx_gemm_workspace_size(8, FAR, 256), lambda work, y: fb.fp8_mx_gemm(*a, *q, FAR, y=y, workspace=work)
+    if kind == "bf16":
+        return fb.bf16_gemm_ref_workspace_size(8, FAR, 256), lambda work, y: fb.bf16_gemm_ref(x, w, y=y, workspace=work)
+    q = fb.fp8_quant_weight_blocks(w, tiled=True)
+    return (fb.fp8_blockscaled_gemm_workspace_size(8, FAR, 256),
+            lambda work, y: fb.fp8_blockscaled_gemm_fused(x, *q, y=y, workspace=work, n=FAR))
+
+
+def _check_far(size, call, small):
+    want = call(fb.make_workspace(size), None)
+    work = fb.make_workspace(max(size, small[0]))
+    small_want = [t.clone() for t in small[1](work)]
+    for _ in range(2):
+        work[1024 + 65536:] = 0xA5                                 # what a small shape's data may hold
+        y = torch.full_like(want, float("nan"))
+        call(work, y)
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+        for a, b in zip(small[1](work), small_want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert fb.workspace_status(work) == 0 and not work[:1024 + 65536].any()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "mx", "bf16", "fp4"])
+def test_more_tiles_than_the_shared_counters(kind):
+    size, call = _far(kind)
+    _check_far(size, call, _fp8(8, 1280, 1, "fp8"))
+
+
+def test_more_expert_tiles_than_the_shared_counters():
+    """64 tokens that name every one of 512 experts, 40 tiles of I each."""
+    M, E, k, H, I = 64, 512, 8, 256, 5120
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    x = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    q = []
+    for rows, K in ((E * 2 * I, H), (E * H, I)):
+        q += fb.fp8_quant_weight_blocks(torch.randn((rows, K), generator=g, device="cuda", dtype=torch.bfloat16), tiled=True)
+    ids = torch.randperm(E, generator=g, device="cuda").to(torch.int32).view(M, k)
+    w = torch.rand((M, k), generator=g, device="cuda")
+    _check_far(fb.fp8_moe_workspace_size(M, H, I, E, k),
+               lambda work, y: fb.fp8_moe_experts(x, ids, w, *q, experts=E, y=y, workspace=work), _fp8(8, 1280, 1, "fp8"))
