@@ -21,7 +21,7 @@
 namespace fp8bs {
 namespace {
 
-constexpr size_t kNoallocScratchBytes = 12u << 20; // 12 MiB
+constexpr size_t kNoallocScratchBytes = (12u << 20) + kCountersRegion; // 12 MiB of data behind the counters
 
 __device__ __align__(256) unsigned char g_noalloc_scratch[kNoallocScratchBytes];
 

@@ -265,9 +265,9 @@ FP8BS_API fp8bs_status fp8_blockscaled_gemm_fused_greedy(const void *x, int ldx,
  * that must not allocate, allocator-less embedded runtimes, hooks that run
  * while a framework holds its memory pool).  The pages have no counterpart:
  * this is an interface convenience, not part of the method.
- * The split-K scratch lives in a 12 MiB array inside the library (every GPU
+ * The split-K scratch lives in a 12 MiB + 64 KiB array inside the library (every GPU
  * that loads the library holds it until the process exits); shapes whose
- * workspace (fp8_blockscaled_gemm_workspace_size) exceeds 12 MiB are rejected
+ * workspace (fp8_blockscaled_gemm_workspace_size) exceeds that are rejected
  * with FP8BS_ERR_UNSUPPORTED_SHAPE.  The call allocates nothing.  Its first
  * call on a device looks up the array's device address (cudaGetSymbolAddress),
  * so make that first call before any stream capture.  Each call clears the

@@ -54,6 +54,24 @@ def test_noalloc_matches_workspace_entry_point(M, N, K, tiled):
         check_y(y, ref["y"], ref["bound"], "noalloc call %d" % call)
 
 
+def test_noalloc_serves_shapes_up_to_the_scratch():
+    """The longest K at 64 tokens: 12 MiB of partials and activations beside the 64 KB of counters."""
+    M, N = 64, 128
+    limit = (12 << 20) + 65536
+    K = max(k for k in range(128, 65536, 128) if fb.fp8_blockscaled_gemm_workspace_size(M, N, k) <= limit)
+    assert fb.fp8_blockscaled_gemm_workspace_size(M, N, K) > 12 << 20
+    x = synth.activations(M, K, seed=1, device="cuda")
+    wq, ws = fb.fp8_quant_weight_blocks(synth.weights(N, K, seed=2, device="cuda"))
+    want = fb.fp8_blockscaled_gemm_fused(x, wq, ws)
+    y = torch.full_like(want, float("nan"))
+    for _ in range(2):
+        assert _noalloc(x, wq, ws, y, M, N, K, 0) == 0
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+    x = synth.activations(M, K + 128, seed=1, device="cuda")
+    wq, ws = fb.fp8_quant_weight_blocks(synth.weights(N, K + 128, seed=2, device="cuda"))
+    assert _noalloc(x, wq, ws, y, M, N, K + 128, 0) == SHAPE
+
+
 def test_noalloc_rejects_oversized_shapes():
     # 64 tokens x K = 65,536: the activation area alone (4 MiB) plus the
     # split-K slots need more scratch than the library's 12 MiB; rejected on
