@@ -480,11 +480,23 @@ def fp8_mx_gemm(aq, as_atoms, wq, ws_atoms, n, y=None, workspace=None, flags=0):
 # ------------------------------------------------- expert and 4-bit layers
 # Each tensor is checked and turned into its address in one short call: a
 # decode step makes many of these calls, and between kernel launches every
-# attribute that Python reads costs a tenth of a microsecond or more.
+# attribute that Python reads costs a tenth of a microsecond or more.  So what
+# is no tensor is found out by the attribute it lacks.
+def _tensors(**named):
+    """TypeError for the first argument that is no tensor."""
+    for name, t in named.items():
+        if not isinstance(t, _torch().Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+
+
 def _addr(t, dtype, numel, name):
     """Address of a contiguous CUDA tensor of that type and number of elements."""
-    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == numel:
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _tensors(**{name: t})
     _need(t, dtype, name, t.dim())
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -495,8 +507,12 @@ def _act(x):
     """(M, K, row stride, address) of bf16 activations [M, K]."""
     if _torch_module is None:
         _torch()
-    if x.dtype is not _bf16 or not x.is_cuda or x.dim() != 2:
+    try:
+        if x.dtype is not _bf16 or not x.is_cuda or x.dim() != 2:
+            _need(x, _bf16, "x")
+    except AttributeError:
         _need(x, _bf16, "x")
+        raise
     M, K = x.shape
     ld, unit = x.stride()
     if unit != 1:
@@ -512,8 +528,13 @@ def _matrix(w, name):
     """(rows, K, dtype code, address) of a contiguous fp32 or bf16 matrix."""
     if _torch_module is None:
         _torch()
-    t = w.dtype
+    try:
+        t = w.dtype
+    except AttributeError:
+        _tensors(**{name: w})
+        raise
     if t is not _bf16 and t is not _f32:
+        _tensors(**{name: w})
         raise TypeError("%s must be float32 or bfloat16" % name)
     if not w.is_cuda or w.dim() != 2:
         _need(w, t, name)
@@ -527,17 +548,24 @@ def _out(t, shape, dtype, device, name):
     """(tensor, address) of an output: `t` checked (that shape, contiguous), or a new one."""
     if t is None:
         t = _empty(shape, dtype=dtype, device=device)
-    elif t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        _need(t, dtype, name, len(shape))
-        raise ValueError("%s must be contiguous of shape %s" % (name, shape))
-    return t, t.data_ptr()
+        return t, t.data_ptr()
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return t, t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name, len(shape))
+    raise ValueError("%s must be contiguous of shape %s" % (name, shape))
 
 
 def _work(workspace):
     """(address, bytes) of a workspace."""
-    if workspace.dtype is not _u8 or not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor of bytes (make_workspace)")
-    return workspace.data_ptr(), workspace.numel()
+    try:
+        if workspace.dtype is _u8 and workspace.is_cuda and workspace.is_contiguous():
+            return workspace.data_ptr(), workspace.numel()
+    except AttributeError:
+        pass
+    raise TypeError("workspace must be a contiguous CUDA tensor of bytes (make_workspace)")
 
 
 def moe_route_workspace_size(M, E):
@@ -556,19 +584,22 @@ def _experts(w13, s13, w2, s2, H, E):
     """(I, flag, addresses of w13, s13, w2, s2) of E experts' weights: w13 [E,
     2I, H] and w2 [E, H, I], or both tiled [tiles, 128, 128]."""
     kg = H // 128
-    if E < 1 or s2.dim() != 2 or s13.dim() != 2:
-        raise ValueError("operand shapes do not agree")
-    rows2, rows = s2.shape  # rows: 128-row tiles of I
-    tiles = E * rows * kg
-    if tiles < 1 or rows2 != E * kg or s13.shape != (2 * E * rows, kg):
-        raise ValueError("operand shapes do not agree")
-    I = rows * 128
-    shape13, shape2 = w13.shape, w2.shape
-    if shape13 == (2 * tiles, 128, 128) and shape2 == (tiles, 128, 128):
-        flag = FLAG_WEIGHTS_TILED
-    elif shape13 == (E, 2 * I, H) and shape2 == (E, H, I):
-        flag = 0
-    else:
+    flag = None
+    try:
+        shape13, shape2 = w13.shape, w2.shape
+        if E >= 1 and s2.dim() == 2 and s13.dim() == 2:
+            rows2, rows = s2.shape  # rows: 128-row tiles of I
+            tiles = E * rows * kg
+            if tiles >= 1 and rows2 == E * kg and s13.shape == (2 * E * rows, kg):
+                I = rows * 128
+                if shape13 == (2 * tiles, 128, 128) and shape2 == (tiles, 128, 128):
+                    flag = FLAG_WEIGHTS_TILED
+                elif shape13 == (E, 2 * I, H) and shape2 == (E, H, I):
+                    flag = 0
+    except AttributeError:
+        pass
+    if flag is None:
+        _tensors(w13=w13, s13=s13, w2=w2, s2=s2)
         raise ValueError("operand shapes do not agree")
     return (I, flag, _addr(w13, _u8, 2 * tiles * 16384, "w13"), _addr(s13, _f32, 2 * tiles, "s13"),
             _addr(w2, _u8, tiles * 16384, "w2"), _addr(s2, _f32, tiles, "s2"))
@@ -601,12 +632,19 @@ def fp8_moe_experts(x, ids, weights, w13, s13, w2, s2, experts=None, y=None, wor
     with experts= given; s13, s2 their block scales."""
     M, H, ldx, xp = _act(x)
     if experts is None:
+        _tensors(w13=w13)
         if w13.dim() != 3 or w13.shape[2] != H:
             raise ValueError("w13 is tiled: pass experts= (the number of experts)")
         experts = w13.shape[0]
     E = int(experts)
     I, tf, w13p, s13p, w2p, s2p = _experts(w13, s13, w2, s2, H, E)
-    if ids.dim() != 2 or ids.shape[0] != M or ids.shape != weights.shape:
+    try:
+        bad = ids.dim() != 2 or ids.shape[0] != M or ids.shape != weights.shape
+    except AttributeError:
+        _tensors(ids=ids, weights=weights)
+        raise
+    if bad:
+        _tensors(weights=weights)
         raise ValueError("operand shapes do not agree")
     k = ids.shape[1]
     idp, wp = _addr(ids, _i32, M * k, "ids"), _addr(weights, _f32, M * k, "weights")
@@ -684,6 +722,8 @@ def fp4_dequant_weights(wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, w=None, dtype=No
     N, K = int(n), int(k)
     qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
     if dtype is None:
+        if w is not None:
+            _tensors(w=w)
         dtype = _f32 if w is None else w.dtype
     if dtype is not _f32 and dtype is not _bf16:
         raise TypeError("w must be float32 or bfloat16")
@@ -718,10 +758,16 @@ def fp4_gemm_workspace_size(M, N, K, fmt=FP4_NV):
 def fp4_gemm(aq, as_atoms, a_rows, wq, ws_atoms, w_rows, n, k, fmt=FP4_NV, y=None, workspace=None, flags=0):
     """Y[M, n] bf16 from 4-bit operands (fp4_quant_act / fp4_quant_weights;
     n = the number of weight rows, k = the unpadded K)."""
-    M, N, K = aq.shape[0], int(n), int(k)
+    try:
+        M, N, K = aq.shape[0], int(n), int(k)
+    except AttributeError:
+        _tensors(aq=aq)
+        raise
     kt = (K + 255) // 256
-    qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
+    if _torch_module is None:
+        _torch()
     aqp = _addr(aq, _u8, M * kt * 128, "aq")
+    qp, ap, rp = _fp4_weights(wq, ws_atoms, w_rows, N, K, fmt)
     asp = _addr(as_atoms, _u8, (M + 127) // 128 * kt * _fp4_atoms(fmt) * 512, "as_atoms")
     arp = None if a_rows is None else _addr(a_rows, _f32, M, "a_rows")
     y, yp = _out(y, (M, N), _bf16, aq.device, "y")
