@@ -18,8 +18,10 @@
 // zero codes and zero scales to whole 256-wide blocks.  Scale bytes in the
 // 512-byte atoms of ptx.cuh, four blocks of K to an atom.
 //
-// Each input and output byte moves once.  5,120 x 17,408 bf16: quantising takes
-// 47 us (227 MB, 0.7 of the measured copy bandwidth; MX 35 us), bound by the
+// Each input and output byte moves once, but for NV rows longer than registers
+// hold (18,432 bf16 or 12,288 fp32 values), whose rest is read for the maximum
+// and again for the codes.  5,120 x 17,408 bf16: quantising takes
+// 48 us (227 MB, 0.7 of the measured copy bandwidth; MX 36 us), bound by the
 // instructions of the conversion and of the check that keeps codes exact
 // without a division a value; reading back to fp32 61 us (406 MB, at the
 // memory's rate).  The activations'
@@ -36,7 +38,7 @@ namespace fp8bs {
 constexpr int kFp4Chunk = 16; // values a thread converts at a time: one NV block, half an MX block
 // A row's chunks are held in registers between its maximum and the conversion,
 // three (fp32: two) a thread, by as many whole warps as that takes: no warp
-// waits for one that has a chunk more.  5,120 x 17,408, there and back: 108 us;
+// waits for one that has a chunk more.  5,120 x 17,408, there and back: 110 us;
 // 256 threads of four and a rest read twice 115, four a thread and fewer warps
 // 107 but with spills.  Rows past 384 threads' read the rest twice (4,096 x
 // 34,816: 182 us, 189 with up to 512 threads, of which an SM holds fewer).

@@ -41,7 +41,7 @@
 //               to tensor memory, another loads the token tiles, and the MMA
 //               warp runs its loop whole, one lane issuing; sums stay in tensor
 //               memory for a whole segment and get their row scales at its end.
-//               34,816 x 5,120 at M = 16 21.8 us (100 MB), at M = 512 63.6 us
+//               34,816 x 5,120 at M = 16 21.3 us (100 MB), at M = 512 63.5 us
 //               (2.9 PFLOP/s), bound by the issue of its loads and MMAs.
 //   fused only: warps 2-9 first quantise, in the kernel prologue, the token
 //               rows of every K block this CTA will use into an activation
