@@ -19,6 +19,8 @@ Entry points (same names as the C ABI):
   16-bit output-layer baseline).
 * ``fp8_mx_quant_weights(w)``, ``fp8_mx_quant_act(x)``, ``fp8_mx_gemm(...)``:
   the native block-scaled (MX) variant, one UE8M0 scale per 32 K.
+* ``fp8_rmsnorm_quant_act(x, gamma, eps, residual)``, ``fp8_mx_rmsnorm_quant_act``
+  -> (xq, scales, residual_out, y): residual's addition, RMS norm and 8-bit cast.
 * ``moe_route(x, wr, top_k)`` -> (ids, weights), ``fp8_moe_experts(x, ids,
   weights, w13, s13, w2, s2)`` -> Y and ``fp8_moe_layer(x, wr, top_k, w13, s13,
   w2, s2)`` -> (Y, ids, weights): a mixture-of-experts layer (M up to 64).
@@ -113,6 +115,8 @@ def _load(path):
         "fp8_mx_quant_weights": [vp, i, i, i, vp, vp, vp],
         "fp8_mx_quant_act": [vp, i, i, i, vp, vp, u, vp],
         "fp8_mx_gemm_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "fp8_rmsnorm_quant_act": [vp, i, vp, i, vp, i, vp, i, ctypes.c_float, i, i, vp, vp, vp, u, vp],
+        "fp8_mx_rmsnorm_quant_act": [vp, i, vp, i, vp, i, vp, i, ctypes.c_float, i, i, vp, vp, vp, u, vp],
         "fp8bs_testhook_fp4_stall": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, sz, i, ctypes.c_ulonglong, vp],
         "fp8bs_testhook_moe_stall": [vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, u, i, i,
                                      ctypes.c_ulonglong, vp],
@@ -566,6 +570,90 @@ def _work(workspace):
     except AttributeError:
         pass
     raise TypeError("workspace must be a contiguous CUDA tensor of bytes (make_workspace)")
+
+
+# ---------------------------------------------------------- norm and cast
+def _same_device(x, **named):
+    """ValueError for a tensor that is not on x's device, or an x that is not on
+    the current one (the kernels run there, on its current stream)."""
+    d = x.get_device()
+    if d != _torch_module.cuda.current_device():
+        raise ValueError("the tensors are on device %d, which is not the current one" % d)
+    for name, t in named.items():
+        if t is not None and t.get_device() != d:
+            raise ValueError("%s must be on the device of the first argument" % name)
+
+
+def _rows16(t, shape, name):
+    """(row stride, address) of bf16 rows of that shape with unit stride along K."""
+    _need(t, _bf16, name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+    ld, unit = t.stride()
+    if unit != 1:
+        raise ValueError("%s must have unit stride along K" % name)
+    if shape[0] == 1:
+        ld = shape[1]
+    elif ld > 0x7fffffff:
+        raise ValueError("%s's row stride does not fit in 32 bits" % name)
+    return ld, t.data_ptr()
+
+
+def _vector(v, n, name):
+    """(dtype code, address) of n contiguous fp32 or bf16 values."""
+    _tensors(**{name: v})
+    if v.dtype is not _f32 and v.dtype is not _bf16:
+        raise TypeError("%s must be float32 or bfloat16" % name)
+    return BF16 if v.dtype is _bf16 else F32, _addr(v, v.dtype, n, name)
+
+
+def _rmsnorm(fn, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, scales_dtype, shape, flags):
+    M, K, ldx, xp = _act(x)
+    gt, gp = _vector(gamma, K, "gamma")
+    dev = x.device
+    rp = op = yp = None
+    ldr = ldo = 0
+    if residual is not None:
+        ldr, rp = _rows16(residual, x.shape, "residual")
+        if residual_out is None:
+            residual_out = _empty((M, K), dtype=_bf16, device=dev)
+        ldo, op = _rows16(residual_out, x.shape, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if store_y or y is not None:
+        y, yp = _out(y, (M, K), _bf16, dev, "y")
+    xq, qp = _out(xq, (M, K), _u8, dev, "xq")
+    scales, sp = _out(scales, shape(M, K), scales_dtype, dev, "xs" if scales_dtype is _f32 else "xs_atoms")
+    _same_device(x, gamma=gamma, residual=residual, residual_out=residual_out, y=y, xq=xq, scales=scales)
+    _check(fn, getattr(lib(), fn)(xp, ldx, rp, ldr, op, ldo, gp, gt, eps, M, K, yp, qp, sp, flags, _stream()))
+    return xq, scales, residual_out, y
+
+
+def fp8_rmsnorm_quant_act(x, gamma, eps=1e-6, residual=None, residual_out=None, y=None, store_y=False, xq=None, xs=None,
+                          flags=0):
+    """RMS norm of h = x + residual (bf16 [M, K], row strides may exceed K; h =
+    x without a residual) with weights gamma (fp32 or bf16 [K]), and its E4M3
+    cast: (xq uint8 [M, K], xs fp32 of scales_shape(M, K), residual_out = h bf16
+    [M, K] or None, y = the norm's bf16 values [M, K], None without
+    ``store_y``).  residual_out=residual adds in place."""
+    if _torch_module is None:
+        _torch()
+    return _rmsnorm("fp8_rmsnorm_quant_act", x, gamma, eps, residual, residual_out, y, store_y, xq, xs, _f32, scales_shape,
+                    flags)
+
+
+def _mx_atoms_shape(M, K):
+    return ((M + 127) // 128) * max(K // 128, 0), 512
+
+
+def fp8_mx_rmsnorm_quant_act(x, gamma, eps=1e-6, residual=None, residual_out=None, y=None, store_y=False, xq=None,
+                             xs_atoms=None, flags=0):
+    """The same with the MX cast (M <= 512): (xq, xs_atoms uint8 [ceil(M/128) *
+    K/128, 512], residual_out, y)."""
+    if _torch_module is None:
+        _torch()
+    return _rmsnorm("fp8_mx_rmsnorm_quant_act", x, gamma, eps, residual, residual_out, y, store_y, xq, xs_atoms, _u8,
+                    _mx_atoms_shape, flags)
 
 
 def moe_route_workspace_size(M, E):

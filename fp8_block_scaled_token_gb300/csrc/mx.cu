@@ -20,23 +20,6 @@
 
 namespace fp8bs {
 
-// Shared exponent of one block from its largest magnitude (amax >= 0).
-__device__ __forceinline__ int mx_shared_exponent(float amax)
-{
-    const uint32_t b = __float_as_uint(amax);
-    const int E = static_cast<int>(b >> 23); // biased exponent (sign bit clear)
-    if (E == 0)
-        return b == 0 ? 0 : -127; // zero block; subnormal amax has floor(log2) <= -127
-    const int e = E - 127 - 8;    // E <= 254 for finite input, so e <= 119
-    return e < -127 ? -127 : e;
-}
-
-// 2^-e as a float, exact for e in [-127, 119].
-__device__ __forceinline__ float mx_inv_scale(int e)
-{
-    return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-}
-
 __device__ __forceinline__ int sf_atom_offset(int r, int j)
 {
     return 16 * (r & 31) + 4 * (r >> 5) + j;

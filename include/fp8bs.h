@@ -333,6 +333,45 @@ FP8BS_API fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, c
                                    size_t workspace_bytes, unsigned flags, void *stream);
 
 /*
+ * The norm in front of a quantised layer: the residual's addition, root-mean-
+ * square norm and the 8-bit cast of its result, one kernel.  For every row m of
+ * K values:
+ *   h  = bf16_rn(fl32(x + residual)), stored to residual_out; without a
+ *        residual (both NULL) h = x
+ *   rs = 1 / sqrt(mean(h^2) + eps)      (fp32 sums; no overflow at any finite h)
+ *   u  = fl32(h * gamma)
+ *   y  = bf16_rn(fl32(u * rs)), where y is not NULL
+ * and, of the values u * rs (fp32, not y's bf16),
+ * fp8_rmsnorm_quant_act: one fp32 scale per 128 consecutive values,
+ *     s    = fl32(amax|u| / 448)        (1 where that is 0)
+ *     code = e4m3_rn_satfinite(fl32(u / s))
+ *     xs   = fl32(s * rs)               (1 for a group of zeros)
+ *   laid out as fp8_quant_act writes them: the operands of fp8_blockscaled_gemm.
+ * fp8_mx_rmsnorm_quant_act: codes and scale atoms of fl32(u * rs) by the MX rule
+ *   and in the layout of fp8_mx_quant_act: the operands of fp8_mx_gemm.
+ * A row with a NaN or an infinity gives NaN in its own row of a product with
+ * these operands, and in no other.
+ *
+ * x, residual, residual_out: bf16, M rows of stride ldx, ldr, ldro (>= K, % 8 ==
+ * 0), 16-byte aligned.  residual_out may be the residual itself, with the same
+ * stride (the addition in place); otherwise no output overlaps an input.
+ * gamma: fp32 or bf16 [K], 16-byte aligned.  2^-100 <= eps < infinity.
+ * y: bf16 [M][K], 16-byte aligned, or NULL.  xq: u8 [M][K], 16-byte aligned.
+ * xs: 4-byte aligned, xs_atoms: 16-byte aligned.
+ * M >= 1 (MX: M <= 512), K % 128 == 0, K <= 32,768.
+ * flags: 0 or FP8BS_FLAG_OVERLAP_PREV (programmatic dependent launch; gamma may be
+ * read before the previous kernel completes, everything else after it).
+ */
+FP8BS_API fp8bs_status fp8_rmsnorm_quant_act(const void *x, int ldx, const void *residual, int ldr,
+                                             void *residual_out, int ldro, const void *gamma,
+                                             fp8bs_dtype gamma_type, float eps, int M, int K, void *y,
+                                             uint8_t *xq, float *xs, unsigned flags, void *stream);
+FP8BS_API fp8bs_status fp8_mx_rmsnorm_quant_act(const void *x, int ldx, const void *residual, int ldr,
+                                                void *residual_out, int ldro, const void *gamma,
+                                                fp8bs_dtype gamma_type, float eps, int M, int K, void *y,
+                                                uint8_t *xq, uint8_t *xs_atoms, unsigned flags, void *stream);
+
+/*
  * A mixture-of-experts layer for a few tokens (a decode or speculative-verify
  * batch, M = 1..64), its experts in E4M3 with one fp32 scale per 128x128 block:
  *   l[m,e]  = sum_h x[m,h] * wr[e,h]                       (fp32)

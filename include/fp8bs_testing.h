@@ -42,6 +42,9 @@ extern "C" {
 #define FP8BS_RUNS_MOE_ROUTE 88
 #define FP8BS_RUNS_MOE_PLAN 89
 #define FP8BS_RUNS_MOE_GEMM(phase, npad) (90 + (phase) * 3 + ((npad) == 16 ? 0 : (npad) == 32 ? 1 : 2))
+/* RMS norm with the 8-bit cast (fp32 block scales, MX). */
+#define FP8BS_RUNS_NORM_FP8 96
+#define FP8BS_RUNS_NORM_MX 97
 #define FP8BS_RUNS_SLOTS 128
 
 /*
