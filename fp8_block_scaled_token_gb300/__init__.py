@@ -15,6 +15,8 @@ Entry points (same names as the C ABI):
 * ``fp8_blockscaled_gemm_fused(x, wq, ws)`` -> Y bf16 (cast fused in).
 * ``fp8_blockscaled_gemm_fused_greedy(x, wq, ws)`` -> (token, logit, Y):
   the same plus the greedy next-token choice (M up to 64).
+* ``speculative_verify(logits, sample_u, draft, accept_u)`` -> (tokens,
+  accepted, probs): drafted tokens against the target's logits, and the next one.
 * ``bf16_pack_weights_tiled(w)``, ``bf16_gemm_ref(x, w)`` -> Y bf16 (the
   16-bit output-layer baseline).
 * ``fp8_mx_quant_weights(w)``, ``fp8_mx_quant_act(x)``, ``fp8_mx_gemm(...)``:
@@ -115,6 +117,8 @@ def _load(path):
         "fp8_mx_quant_weights": [vp, i, i, i, vp, vp, vp],
         "fp8_mx_quant_act": [vp, i, i, i, vp, vp, u, vp],
         "fp8_mx_gemm_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "speculative_verify_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "speculative_verify": [vp, i, i, vp, vp, vp, i, vp, vp, vp, i, i, i, vp, vp, vp, vp, sz, u, vp],
         "fp8_rmsnorm_quant_act": [vp, i, vp, i, vp, i, vp, i, ctypes.c_float, i, i, vp, vp, vp, u, vp],
         "fp8_mx_rmsnorm_quant_act": [vp, i, vp, i, vp, i, vp, i, ctypes.c_float, i, i, vp, vp, vp, u, vp],
         "fp8bs_testhook_fp4_stall": [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, sz, i, ctypes.c_ulonglong, vp],
@@ -654,6 +658,78 @@ def fp8_mx_rmsnorm_quant_act(x, gamma, eps=1e-6, residual=None, residual_out=Non
         _torch()
     return _rmsnorm("fp8_mx_rmsnorm_quant_act", x, gamma, eps, residual, residual_out, y, store_y, xq, xs_atoms, _u8,
                     _mx_atoms_shape, flags)
+
+
+# ------------------------------------------------- drafted tokens
+def speculative_verify_workspace_size(B, L, V):
+    n = ctypes.c_size_t(0)
+    _check("speculative_verify_workspace_size", lib().speculative_verify_workspace_size(B, L, V, ctypes.byref(n)))
+    return n.value
+
+
+def _logit_rows(t, rows, V, dtypes, name):
+    """(row stride, address) of rows with unit stride along the vocabulary."""
+    _tensors(**{name: t})
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
+    _need(t, t.dtype, name)
+    if t.shape[1] != V or t.shape[0] != rows:
+        raise ValueError("%s must have shape (%d, %d)" % (name, rows, V))
+    ld, unit = t.stride()
+    if unit != 1 and V > 1:
+        raise ValueError("%s must have unit stride along the vocabulary" % name)
+    if rows <= 1:
+        ld = V
+    elif ld > 0x7fffffff:
+        raise ValueError("%s's row stride does not fit in 32 bits" % name)
+    return ld, t.data_ptr()
+
+
+def speculative_verify(logits, sample_u, draft=None, accept_u=None, draft_probs=None, draft_len=None, temperature=None,
+                       tokens=None, accepted=None, probs=None, workspace=None, flags=0):
+    """Drafted tokens against the target's logits (include/fp8bs.h has the
+    rule): logits bf16 or fp32 [B * (L + 1), V] as the output layer writes them (row
+    stride may exceed V), sample_u fp32 [B], draft int32 [B, L], accept_u fp32 [B,
+    L], draft_probs fp32 [B * L, V] or None (the draft is certain of its tokens),
+    draft_len int32 [B] or None (L each), temperature fp32 [B] or None (1) ->
+    (tokens int32 [B, L + 1]: the accepted ones, the next one, then -1; accepted
+    int32 [B]; probs fp32 [B, L + 1]: the target's probabilities of those tokens).
+    Without a draft one token is drawn from each row."""
+    if _torch_module is None:
+        _torch()
+    _tensors(logits=logits, sample_u=sample_u)
+    B = sample_u.numel()
+    L, dp, ap, qp, np_, tp, ldq = 0, None, None, None, None, None, 0
+    if draft is not None:
+        _need(draft, _i32, "draft")
+        L = draft.shape[1]
+    if L:
+        dp, ap = _addr(draft, _i32, B * L, "draft"), _addr(accept_u, _f32, B * L, "accept_u")
+        if draft_len is not None:
+            np_ = _addr(draft_len, _i32, B, "draft_len")
+    elif draft is None and (accept_u is not None or draft_probs is not None or draft_len is not None):
+        raise ValueError("accept_u, draft_probs and draft_len need a draft")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
+    V = logits.shape[1]
+    ldl, lp = _logit_rows(logits, B * (L + 1), V, (_bf16, _f32), "logits")
+    if draft_probs is not None and L:
+        ldq, qp = _logit_rows(draft_probs, B * L, V, (_f32,), "draft_probs")
+    sp = _addr(sample_u, _f32, B, "sample_u")
+    if temperature is not None:
+        tp = _addr(temperature, _f32, B, "temperature")
+    dev = logits.device
+    tokens, op = _out(tokens, (B, L + 1), _i32, dev, "tokens")
+    accepted, cp = _out(accepted, (B,), _i32, dev, "accepted")
+    probs, pp = _out(probs, (B, L + 1), _f32, dev, "probs")
+    if workspace is None:
+        workspace = make_workspace(speculative_verify_workspace_size(B, L, V), dev)
+    wsp, wsn = _work(workspace)
+    _same_device(logits, sample_u=sample_u, draft=draft, accept_u=accept_u, draft_probs=draft_probs, draft_len=draft_len,
+                 temperature=temperature, tokens=tokens, accepted=accepted, probs=probs, workspace=workspace)
+    _check("speculative_verify", lib().speculative_verify(lp, BF16 if logits.dtype is _bf16 else F32, ldl, dp, np_, qp, ldq,
+                                                          ap, sp, tp, B, L, V, op, cp, pp, wsp, wsn, flags, _stream()))
+    return tokens, accepted, probs
 
 
 def moe_route_workspace_size(M, E):

@@ -260,6 +260,53 @@ FP8BS_API fp8bs_status fp8_blockscaled_gemm_fused_greedy(const void *x, int ldx,
                                                unsigned flags, void *stream);
 
 /*
+ * Verification of drafted tokens against the target model's logits, and the
+ * next token of every sequence, from given random numbers: what follows the
+ * output layer of a speculative-verify batch ("about 8 rows" [P1 "Why this shape
+ * is hard"]).  Sequence b has drafted n = draft_len[b] tokens (0 .. L; L where
+ * draft_len is NULL, other values are clamped), and rows b*(L+1) + j of the
+ * logits, j = 0 .. n, are the target's at those positions.  With
+ *   p_j = softmax(row j / T)             (T = temperature[b], 1 where NULL; T = 0:
+ *         all on the largest logit, the lowest index among equals)
+ *   q_j = draft_probs row b*L + j, or, where that is NULL, all on the drafted token
+ * the drafted token t_j, j = 0, 1, ..., is accepted while
+ *   accept_u[b*L + j] * q_j(t_j) < p_j(t_j)       (a token outside [0, V) is not)
+ * and the next token, at position j = accepted[b], is the lowest index whose
+ * cumulative weight exceeds sample_u[b] times the total, the weights being
+ * max(p_j - q_j, 0) where the draft was rejected (p_j where all of them are 0),
+ * and p_n after n accepted tokens.  L = 0 draws a token from each row.
+ *   tokens[b*(L+1) + j]: the accepted tokens, the next one, then -1
+ *   probs [b*(L+1) + j]: p_j of those tokens, then 0
+ * A row that has a NaN or +infinity or no finite logit, or a T that is neither 0
+ * nor in [2^-20, 2^20], gives token -1 and probability NaN at its position, and
+ * the sequence ends there.  -infinity has probability 0, and so has what lies
+ * more than 64 T below the largest logit.
+ *
+ * Weights are held to 2^-28 of themselves (2^-31 in the mean) and summed as
+ * 64-bit integers: bitwise reproducible, and the choice is that of exact arithmetic
+ * unless a decision lies within 2^-26 of a border.
+ * Rows behind a sequence's first rejected token are read or not, and do not
+ * matter; nor do rows past draft_len.
+ * logits: bf16 or fp32, B*(L+1) rows of stride ldl >= V, aligned to their type
+ * (faster where rows start on 16 bytes).  draft: int32 [B][L], accept_u: fp32
+ * [B][L] in [0, 1), sample_u: fp32 [B] in [0, 1), temperature: fp32 [B] or NULL,
+ * draft_len: int32 [B] or NULL, draft_probs: fp32, B*L rows of stride ldq >= V,
+ * not negative, or NULL; with L = 0 all of draft, draft_len, draft_probs and
+ * accept_u are NULL.  tokens: int32 [B][L+1], accepted: int32 [B], probs: fp32
+ * [B][L+1].  All 4-byte aligned.
+ * B >= 1, 0 <= L <= 31, B * (L + 1) <= 4,096, 1 <= V <= 1,048,576.
+ * workspace: 256-byte aligned, of speculative_verify_workspace_size; the same
+ * contract as the GEMMs' workspace.  flags: 0 or FP8BS_FLAG_OVERLAP_PREV (waits
+ * for the previous kernel before it reads anything).
+ */
+FP8BS_API fp8bs_status speculative_verify_workspace_size(int B, int L, int V, size_t *bytes);
+FP8BS_API fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int ldl, const int32_t *draft,
+                                          const int32_t *draft_len, const float *draft_probs, int ldq,
+                                          const float *accept_u, const float *sample_u, const float *temperature,
+                                          int B, int L, int V, int32_t *tokens, int32_t *accepted, float *probs,
+                                          void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
  * fp8_blockscaled_gemm_fused without a caller-provided workspace, for callers
  * that cannot allocate device memory (code running under a graph capture
  * that must not allocate, allocator-less embedded runtimes, hooks that run
