@@ -45,6 +45,7 @@ FLAG_OVERLAP_PREV = 1
 FLAG_WEIGHTS_TILED = 2
 FLAG_PROLOGUE_CAST = 4
 F32, BF16 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 FP4_NV, FP4_MX = 0, 1  # 4-bit formats: 16-wide E4M3 scales and fp32 row scales; 32-wide powers of two
 
 _lib = None
@@ -129,6 +130,9 @@ def _load(path):
         "fp8_moe_workspace_size": [i, i, i, i, i, ctypes.POINTER(sz)],
         "fp8_moe_experts": [vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, u, vp],
         "fp8_moe_layer": [vp, i, vp, i, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, u, vp],
+        "moe_route_grouped": [vp, i, vp, i, vp, i, i, i, i, i, i, i, i, i, ctypes.c_float, vp, vp, vp, sz, u, vp],
+        "fp8_moe_layer_grouped": [vp, i, vp, i, vp, i, i, i, i, i, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i,
+                                  vp, sz, u, vp],
         "fp4_quant_weights": [vp, i, i, i, i, vp, vp, vp, vp],
         "fp4_dequant_weights": [vp, vp, vp, i, i, i, vp, i, vp],
         "fp4_quant_act": [vp, i, i, i, i, vp, vp, vp, u, vp],
@@ -840,6 +844,59 @@ def fp8_moe_layer(x, wr, top_k, w13, s13, w2, s2, renormalize=True, y=None, ids=
     wsp, wsn = _work(workspace)
     _check("fp8_moe_layer", lib().fp8_moe_layer(xp, ldx, wrp, wt, 1 if renormalize else 0, w13p, s13p, w2p, s2p,
                                                 yp, idp, wp, M, H, I, E, top_k, wsp, wsn, flags | tf, _stream()))
+    return y, ids, weights
+
+
+def _scores(x, wr, bias):
+    """(M, K, row stride, address of x; E, dtype code, address of wr; address of bias)."""
+    M, H, ldx, xp = _act(x)
+    E, Hr, wt, wrp = _matrix(wr, "wr")
+    if H != Hr:
+        raise ValueError("operand shapes do not agree")
+    return M, H, ldx, xp, E, wt, wrp, None if bias is None else _addr(bias, _f32, E, "bias")
+
+
+def moe_route_grouped(x, wr, top_k, bias=None, scoring=SCORE_SIGMOID, groups=1, top_groups=1, group_best=2,
+                      renormalize=True, scale=1.0, ids=None, weights=None, workspace=None, flags=0):
+    """The experts of each token by scores, bias and groups (include/fp8bs.h has
+    the rule): x bf16 [M, H] (row stride may exceed H), wr fp32 or bf16 [E, H], bias
+    fp32 [E] or None -> (ids int32 [M, top_k] by descending score plus bias, weights
+    fp32 [M, top_k]: the scores, over their sum with ``renormalize``, times
+    scale).  Workspace of moe_route_workspace_size."""
+    M, H, ldx, xp, E, wt, wrp, bp = _scores(x, wr, bias)
+    dev = x.device
+    ids, idp = _out(ids, (M, top_k), _i32, dev, "ids")
+    weights, wp = _out(weights, (M, top_k), _f32, dev, "weights")
+    if workspace is None:
+        workspace = make_workspace(moe_route_workspace_size(M, E), dev)
+    wsp, wsn = _work(workspace)
+    _same_device(x, wr=wr, bias=bias, ids=ids, weights=weights, workspace=workspace)
+    _check("moe_route_grouped", lib().moe_route_grouped(xp, ldx, wrp, wt, bp, M, H, E, top_k, scoring, groups, top_groups,
+                                                        group_best, 1 if renormalize else 0, scale, idp, wp, wsp, wsn,
+                                                        flags, _stream()))
+    return ids, weights
+
+
+def fp8_moe_layer_grouped(x, wr, top_k, w13, s13, w2, s2, bias=None, scoring=SCORE_SIGMOID, groups=1, top_groups=1,
+                          group_best=2, renormalize=True, scale=1.0, y=None, ids=None, weights=None, workspace=None,
+                          flags=0):
+    """The whole layer, moe_route_grouped and fp8_moe_experts in three kernels:
+    (y bf16 [M, H], ids int32 [M, top_k], weights fp32 [M, top_k]); w13 and w2 as in
+    fp8_moe_experts, row-major or tiled."""
+    M, H, ldx, xp, E, wt, wrp, bp = _scores(x, wr, bias)
+    I, tf, w13p, s13p, w2p, s2p = _experts(w13, s13, w2, s2, H, E)
+    dev = x.device
+    y, yp = _out(y, (M, H), _bf16, dev, "y")
+    ids, idp = _out(ids, (M, top_k), _i32, dev, "ids")
+    weights, wp = _out(weights, (M, top_k), _f32, dev, "weights")
+    if workspace is None:
+        workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, top_k), dev)
+    wsp, wsn = _work(workspace)
+    _same_device(x, wr=wr, bias=bias, w13=w13, s13=s13, w2=w2, s2=s2, y=y, ids=ids, weights=weights, workspace=workspace)
+    _check("fp8_moe_layer_grouped",
+           lib().fp8_moe_layer_grouped(xp, ldx, wrp, wt, bp, scoring, groups, top_groups, group_best,
+                                       1 if renormalize else 0, scale, w13p, s13p, w2p, s2p, yp, idp, wp, M, H, I, E,
+                                       top_k, wsp, wsn, flags | tf, _stream()))
     return y, ids, weights
 
 

@@ -1,6 +1,8 @@
 // moe.cu -- entry points of the mixture-of-experts layer: argument checks on
 // the host, the workspace's layout, and the three launches (routing or plan,
 // gate/up product, down product).
+#include <cmath>
+
 #include "fp8bs_testing.h"
 #include "moe.h"
 
@@ -18,7 +20,7 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     w.counters_up_off = w.counters_down_off + static_cast<size_t>(H / 128) * 4;
     w.counters_bytes = static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4;
     w.logits_off = kCountersOff + counters_region(w.counters_bytes);
-    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4);
+    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 8);
     w.ids_off = w.masks_off + static_cast<size_t>(kMoeMaxTokens / kMoeTokenGroup) * (kMoeMaxExperts / 32) * 4;
     w.topw_off = w.ids_off + up256(static_cast<size_t>(M) * top_k * 4);
     w.wtok_off = w.topw_off + up256(static_cast<size_t>(M) * top_k * 4);
@@ -91,6 +93,76 @@ fp8bs_status run_experts(MoeLaunch &L, size_t workspace_bytes)
     return st;
 }
 
+// Scores, groups and the router's weights of a grouped choice.
+fp8bs_status set_scores(MoeLaunch &L, const void *wr, fp8bs_dtype wr_type, const float *bias, fp8bs_score scoring,
+                        int groups, int top_groups, int group_best, int renormalize, float scale)
+{
+    if (!wr || (wr_type != FP8BS_F32 && wr_type != FP8BS_BF16) ||
+        (scoring != FP8BS_SCORE_SOFTMAX && scoring != FP8BS_SCORE_SIGMOID) || groups < 1 || top_groups < 1 ||
+        top_groups > groups || group_best < 1 || group_best > 2 || !std::isfinite(scale))
+        return FP8BS_ERR_INVALID_ARG;
+    if (groups > kMoeMaxGroups || L.E % groups != 0 || L.top_k > top_groups * (L.E / groups) ||
+        (top_groups < groups && group_best > L.E / groups))
+        return FP8BS_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(wr, 16) || !aligned(bias, 4))
+        return FP8BS_ERR_MISALIGNED;
+    L.wr = wr;
+    L.wr_type = wr_type;
+    L.renorm = renormalize != 0;
+    L.scores.scored = true;
+    L.scores.sigmoid = scoring == FP8BS_SCORE_SIGMOID;
+    L.scores.bias = bias;
+    L.scores.groups = groups;
+    L.scores.top_groups = top_groups;
+    L.scores.group_best = group_best;
+    L.scores.scale = scale;
+    return FP8BS_OK;
+}
+
+MoeLaunch route_call(const void *x, int ldx, int M, int H, int E, int top_k, int32_t *ids, float *weights,
+                     void *workspace, unsigned flags, void *stream)
+{
+    MoeLaunch L = {};
+    L.M = M;
+    L.H = H;
+    L.E = E;
+    L.top_k = top_k;
+    L.x = x;
+    L.ldx = ldx;
+    L.ids = ids;
+    L.topw = weights;
+    L.workspace = static_cast<uint8_t *>(workspace);
+    L.flags = flags;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return L;
+}
+
+fp8bs_status check_route(const MoeLaunch &L)
+{
+    if (!L.x || !L.ids || !L.topw || !L.workspace)
+        return FP8BS_ERR_INVALID_ARG;
+    fp8bs_status st = check_tokens(L.M, L.H, L.E, L.top_k);
+    if (st != FP8BS_OK)
+        return st;
+    if (L.ldx < L.H || (L.flags & ~FP8BS_FLAG_OVERLAP_PREV) != 0)
+        return FP8BS_ERR_INVALID_ARG;
+    if (!aligned(L.x, 16) || L.ldx % 8 != 0 || !aligned(L.ids, 4) || !aligned(L.topw, 4) || !aligned(L.workspace, 256))
+        return FP8BS_ERR_MISALIGNED;
+    return FP8BS_OK;
+}
+
+fp8bs_status run_route(const MoeLaunch &L, size_t workspace_bytes)
+{
+    DeviceInfo dev;
+    fp8bs_status st = current_device(&dev);
+    if (st != FP8BS_OK)
+        return st;
+    const MoeWorkspace w = moe_workspace(L.M, 128, 128, L.E, 1, dev.sms); // the routing's part depends on M and E alone
+    if (workspace_bytes < w.masks_off)
+        return FP8BS_ERR_WORKSPACE_TOO_SMALL;
+    return launch_moe_route(L, w, dev);
+}
+
 fp8bs_status check_layer(const MoeLaunch &L)
 {
     if (!L.x || !L.w13 || !L.s13 || !L.w2 || !L.s2 || !L.y || !L.workspace)
@@ -131,39 +203,28 @@ fp8bs_status moe_route(const void *x, int ldx, const void *wr, fp8bs_dtype wr_ty
                        int renormalize, int32_t *ids, float *weights, void *workspace, size_t workspace_bytes,
                        unsigned flags, void *stream)
 {
-    if (!x || !wr || !ids || !weights || !workspace || (wr_type != FP8BS_F32 && wr_type != FP8BS_BF16))
+    if (!wr || (wr_type != FP8BS_F32 && wr_type != FP8BS_BF16))
         return FP8BS_ERR_INVALID_ARG;
-    fp8bs_status st = check_tokens(M, H, E, top_k);
-    if (st != FP8BS_OK)
-        return st;
-    if (ldx < H || (flags & ~FP8BS_FLAG_OVERLAP_PREV) != 0)
-        return FP8BS_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(wr, 16) || !aligned(ids, 4) || !aligned(weights, 4) ||
-        !aligned(workspace, 256))
-        return FP8BS_ERR_MISALIGNED;
-    DeviceInfo dev;
-    st = current_device(&dev);
-    if (st != FP8BS_OK)
-        return st;
-    const MoeWorkspace w = moe_workspace(M, 128, 128, E, 1, dev.sms); // the routing's part depends on M and E alone
-    if (workspace_bytes < w.masks_off)
-        return FP8BS_ERR_WORKSPACE_TOO_SMALL;
-    MoeLaunch L = {};
-    L.M = M;
-    L.H = H;
-    L.E = E;
-    L.top_k = top_k;
-    L.x = x;
-    L.ldx = ldx;
+    MoeLaunch L = route_call(x, ldx, M, H, E, top_k, ids, weights, workspace, flags, stream);
     L.wr = wr;
     L.wr_type = wr_type;
     L.renorm = renormalize != 0;
-    L.ids = ids;
-    L.topw = weights;
-    L.workspace = static_cast<uint8_t *>(workspace);
-    L.flags = flags;
-    L.stream = static_cast<cudaStream_t>(stream);
-    return launch_moe_route(L, w, dev);
+    fp8bs_status st = check_route(L);
+    if (st == FP8BS_OK && !aligned(wr, 16))
+        st = FP8BS_ERR_MISALIGNED;
+    return st != FP8BS_OK ? st : run_route(L, workspace_bytes);
+}
+
+fp8bs_status moe_route_grouped(const void *x, int ldx, const void *wr, fp8bs_dtype wr_type, const float *bias, int M,
+                               int H, int E, int top_k, fp8bs_score scoring, int groups, int top_groups,
+                               int group_best, int renormalize, float scale, int32_t *ids, float *weights,
+                               void *workspace, size_t workspace_bytes, unsigned flags, void *stream)
+{
+    MoeLaunch L = route_call(x, ldx, M, H, E, top_k, ids, weights, workspace, flags, stream);
+    fp8bs_status st = check_route(L);
+    if (st == FP8BS_OK)
+        st = set_scores(L, wr, wr_type, bias, scoring, groups, top_groups, group_best, renormalize, scale);
+    return st != FP8BS_OK ? st : run_route(L, workspace_bytes);
 }
 
 fp8bs_status fp8_moe_workspace_size(int M, int H, int I, int E, int top_k, size_t *bytes)
@@ -245,6 +306,38 @@ fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8bs_dtype w
     fp8bs_status st = check_layer(L);
     if (st == FP8BS_OK && !aligned(wr, 16))
         st = FP8BS_ERR_MISALIGNED;
+    return st != FP8BS_OK ? st : run_experts(L, workspace_bytes);
+}
+
+fp8bs_status fp8_moe_layer_grouped(const void *x, int ldx, const void *wr, fp8bs_dtype wr_type, const float *bias,
+                                   fp8bs_score scoring, int groups, int top_groups, int group_best, int renormalize,
+                                   float scale, const uint8_t *w13, const float *s13, const uint8_t *w2,
+                                   const float *s2, void *y, int32_t *ids, float *weights, int M, int H, int I, int E,
+                                   int top_k, void *workspace, size_t workspace_bytes, unsigned flags, void *stream)
+{
+    MoeLaunch L = {};
+    L.M = M;
+    L.H = H;
+    L.I = I;
+    L.E = E;
+    L.top_k = top_k;
+    L.x = x;
+    L.ldx = ldx;
+    L.ids = ids;
+    L.topw = weights;
+    L.test_skip_unit = -1;
+    L.w13 = w13;
+    L.s13 = s13;
+    L.w2 = w2;
+    L.s2 = s2;
+    L.y = y;
+    L.workspace = static_cast<uint8_t *>(workspace);
+    L.flags = flags;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.timeout_ns = kDefaultTimeoutNs;
+    fp8bs_status st = check_layer(L);
+    if (st == FP8BS_OK)
+        st = set_scores(L, wr, wr_type, bias, scoring, groups, top_groups, group_best, renormalize, scale);
     return st != FP8BS_OK ? st : run_experts(L, workspace_bytes);
 }
 

@@ -9,6 +9,7 @@ namespace fp8bs {
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
+constexpr int kMoeMaxGroups = 32;
 constexpr int kMoeTokenGroup = 8; // tokens that one routing CTA multiplies an expert's router row with
 
 inline int moe_token_pad(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
@@ -22,7 +23,7 @@ struct MoeWorkspace {
     size_t route_off;         // arrival counters of the kMoeMaxTokens / kMoeTokenGroup groups of tokens, then a
                               // bit mask of the experts (kMoeMaxExperts / 32 words) for a given choice
     size_t chosen_off;        // 1 from the gate/up product's start to the down product's end: the masks are complete
-    size_t logits_off;        // [M][E] router logits
+    size_t logits_off;        // [M][E] router logits, 8 bytes each (fp32, or pairs under scores)
     size_t counters_up_off;   // arrival counters of the (active expert, 128 of I) pairs
     size_t counters_down_off; // arrival counters of the 128-row tiles of H
     size_t counters_bytes;    // of both
@@ -36,6 +37,15 @@ struct MoeWorkspace {
     size_t total;
 };
 
+// How experts are scored and grouped; scored = false is the plain top_k of the logits.
+struct MoeScores {
+    bool scored = false;
+    bool sigmoid = false;
+    const float *bias = nullptr; // [E], or nullptr
+    int groups = 1, top_groups = 1, group_best = 1;
+    float scale = 1.0f;
+};
+
 struct MoeLaunch {
     int M, H, I, E, top_k;
     const void *x;
@@ -43,6 +53,7 @@ struct MoeLaunch {
     const void *wr;          // router weights [E][H], or nullptr: ids and topw are given
     int wr_type;
     int renorm;
+    MoeScores scores;        // of moe_route_grouped and fp8_moe_layer_grouped
     const uint8_t *w13, *w2; // tiled or row-major E4M3
     const float *s13, *s2;
     int32_t *ids;

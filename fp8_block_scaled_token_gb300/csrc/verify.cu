@@ -15,10 +15,8 @@
 //
 // w(x) = 2^((x - ref) c), c = log2(e) / T as two fp32 numbers.  |ref| is no
 // smaller than |x| for every x that counts, so that t = fl(x - ref) and e = x -
-// (t + ref) are exact (fast two-sum); z = t c + e c in two fp32 numbers; z is cut
-// into n + j/32 + y, |y| <= 2^-6, and 2^z = 2^n T[j] (1 + p(y)) with T[j] = 2^(j/32)
-// in two numbers, a lane's register each (a shuffle is cheaper than the
-// conflicts of a gather from shared memory), p the power series to y^4.
+// (t + ref) are exact (fast two-sum); z = t c + e c in two fp32 numbers, and
+// 2^z as in pair_math.cuh.
 //
 // verify_stats_kernel: a CTA per (row, 8,192 logits), rows in the order of
 // their positions.  Maximum, then the sum of the weights, from registers: one
@@ -32,6 +30,7 @@
 
 #include "fp8bs_testing.h"
 #include "internal.h"
+#include "pair_math.cuh"
 #include "ptx.cuh"
 
 namespace fp8bs {
@@ -77,28 +76,6 @@ struct VerifyParams {
     unsigned long long *runs;
 };
 
-// 2^(j/32): the nearest fp32 number and the rest relative to it.
-__device__ const float2 kPow32[32] = {
-    {0x1.000000p+0f, 0x0.0p+0f},          {0x1.059b0ep+0f, -0x1.947414p-25f},
-    {0x1.0b5586p+0f, 0x1.8d96d4p-25f},    {0x1.11301ep+0f, -0x1.dda2fcp-25f},
-    {0x1.172b84p+0f, -0x1.9c0c22p-27f},   {0x1.1d4874p+0f, -0x1.a2fbb2p-25f},
-    {0x1.2387a6p+0f, 0x1.964904p-25f},    {0x1.29e9e0p+0f, -0x1.2b0dbcp-25f},
-    {0x1.306fe0p+0f, 0x1.125002p-25f},    {0x1.371a74p+0f, -0x1.cde8cep-26f},
-    {0x1.3dea64p+0f, 0x1.370be4p-25f},    {0x1.44e086p+0f, 0x1.336de2p-30f},
-    {0x1.4bfdaep+0f, -0x1.0a3550p-25f},   {0x1.5342b6p+0f, -0x1.c541b4p-26f},
-    {0x1.5ab07ep+0f, -0x1.00d8acp-27f},   {0x1.6247ecp+0f, -0x1.6cb284p-25f},
-    {0x1.6a09e6p+0f, 0x1.26055cp-26f},    {0x1.71f75ep+0f, 0x1.8b2bb8p-26f},
-    {0x1.7a1148p+0f, -0x1.05cb44p-25f},   {0x1.82589ap+0f, -0x1.1c2142p-26f},
-    {0x1.8ace54p+0f, 0x1.67a1cap-28f},    {0x1.93737cp+0f, -0x1.348e56p-25f},
-    {0x1.9c4918p+0f, 0x1.a3b5e4p-28f},    {0x1.a5503cp+0f, -0x1.0b7ec8p-25f},
-    {0x1.ae89fap+0f, -0x1.f9c304p-27f},   {0x1.b7f770p+0f, -0x1.e4c886p-26f},
-    {0x1.c199bep+0f, -0x1.6961b4p-28f},   {0x1.cb720ep+0f, -0x1.b5151ep-28f},
-    {0x1.d5818ep+0f, -0x1.a5217cp-28f},   {0x1.dfc974p+0f, -0x1.ab7132p-26f},
-    {0x1.ea4afap+0f, 0x1.61428ep-28f},    {0x1.f50766p+0f, -0x1.2ad5f8p-27f}};
-
-constexpr float kShift = 393216.0f;       // 1.5 * 2^18: adding it rounds to multiples of 1/32
-constexpr int kShiftBits = 0x48C00000;    // its bits
-
 // Temperature and reference of one row (or chunk), and a lane's table entry.
 struct Scale {
     float ch, cl; // log2(e) / T
@@ -130,19 +107,6 @@ __device__ __forceinline__ void exponent_of(float x, float ref, const Scale &s, 
     const float e = x - (t + ref);
     zh = t * s.ch;
     zl = fmaf(e, s.ch, fmaf(t, s.cl, fmaf(t, s.ch, -zh)));
-}
-
-// 2^(zh + zl) = 2^n th (1 + rest); `entry` is the lane's of kPow32; a whole warp calls it.
-__device__ __forceinline__ int pow_split(float zh, float zl, float2 entry, float &th, float &rest)
-{
-    const float u = zh + kShift;
-    const int bits = __float_as_int(u);
-    const float y = (zh - (u - kShift)) + zl;
-    th = __shfl_sync(0xffffffffu, entry.x, bits & 31);
-    const float tl = __shfl_sync(0xffffffffu, entry.y, bits & 31);
-    constexpr float k1 = 0x1.62e430p-1f, k2 = 0x1.ebfbe0p-3f, k3 = 0x1.c6b08ep-5f, k4 = 0x1.3b2ab6p-7f; // ln(2)^k / k!
-    rest = fmaf(fmaf(fmaf(fmaf(y, k4, k3), y, k2), y, k1), y, tl);
-    return (bits - kShiftBits) >> 5;
 }
 
 // The weight of x relative to 2^exponent as hi + lo (0 below the cutoff); a

@@ -476,6 +476,45 @@ FP8BS_API fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8
                                      void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
 
 /*
+ * The same routing and layer with scores, a bias for balance and groups of
+ * experts:
+ *   s[m,e] = 1 / (1 + exp(-l[m,e])) (sigmoid) or exp(l - l_max) / sum over all E
+ *            experts of exp(l - l_max) (softmax)
+ *   c[m,e] = s + bias[e]              (c = s where bias is NULL)
+ *   the E experts lie in `groups` groups of E / groups consecutive ones; a group's
+ *   score is the sum of its group_best (1 or 2) largest c, and the top_groups
+ *   groups of largest score are open (all of them with top_groups == groups)
+ *   ids[m]  = the top_k experts of largest c in the open groups, in descending
+ *             order
+ *   w[m,j]  = scale * s_j, divided by the sum of the chosen s where renormalize != 0
+ * Ties go to the lowest group and expert; a NaN orders below every number.
+ * Logits and scores are held in two fp32 numbers until the choice is made, so
+ * that it is the one of exact arithmetic unless two c lie within about 2^-24 of
+ * the logits' size of each other.  A bias of -infinity makes an expert the last choice.
+ * bias: fp32 [E] or NULL, 4-byte aligned.  scale: finite.  1 <= top_groups <=
+ * groups <= 32, E % groups == 0, top_k <= top_groups * (E / groups), and, with
+ * top_groups < groups, group_best <= E / groups.  Everything else, workspaces
+ * included, as moe_route and fp8_moe_layer (ids and weights may be NULL for the
+ * layer).
+ */
+typedef enum fp8bs_score {
+    FP8BS_SCORE_SOFTMAX = 0,
+    FP8BS_SCORE_SIGMOID = 1
+} fp8bs_score;
+
+FP8BS_API fp8bs_status moe_route_grouped(const void *x, int ldx, const void *wr, fp8bs_dtype wr_type, const float *bias,
+                                         int M, int H, int E, int top_k, fp8bs_score scoring, int groups,
+                                         int top_groups, int group_best, int renormalize, float scale, int32_t *ids,
+                                         float *weights, void *workspace, size_t workspace_bytes, unsigned flags,
+                                         void *stream);
+FP8BS_API fp8bs_status fp8_moe_layer_grouped(const void *x, int ldx, const void *wr, fp8bs_dtype wr_type,
+                                             const float *bias, fp8bs_score scoring, int groups, int top_groups,
+                                             int group_best, int renormalize, float scale, const uint8_t *w13,
+                                             const float *s13, const uint8_t *w2, const float *s2, void *y,
+                                             int32_t *ids, float *weights, int M, int H, int I, int E, int top_k,
+                                             void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/*
  * Microscaled 4-bit floating point: E2M1 weights and activations (magnitudes
  * 0, 0.5, 1, 1.5, 2, 3, 4, 6) with block scales that the tensor core applies
  * (tcgen05.mma kind::mxf4nvf4 / kind::mxf4, block_scale).  Two formats:

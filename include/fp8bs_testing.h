@@ -48,6 +48,8 @@ extern "C" {
 /* Verification of drafted tokens: the rows' statistics, the choice. */
 #define FP8BS_RUNS_VERIFY_STATS 98
 #define FP8BS_RUNS_VERIFY_CHOOSE 99
+/* Routing by scores, bias and groups. */
+#define FP8BS_RUNS_MOE_ROUTE_GROUPED 100
 #define FP8BS_RUNS_SLOTS 128
 
 /*

@@ -1,5 +1,5 @@
 """The entry points between the layers of a step (norm with the 8-bit cast,
-verification of drafted tokens) on
+verification of drafted tokens, routing with scores and groups) on
 the CPU: declared, and bad arguments rejected on the host before anything would
 reach a GPU.  Nothing here launches a kernel."""
 import ctypes
@@ -10,6 +10,7 @@ import torch
 
 import fp8_block_scaled_token_gb300 as fb
 from tests.test_abi import A1, A16, INVALID, MISALIGNED, NUL, OK, P, S, SHAPE, L, declared_symbols  # noqa: F401
+from tests.route_reference import route
 from tests.verify_reference import verify
 
 A8 = P(0x10008)
@@ -17,7 +18,8 @@ A8 = P(0x10008)
 
 def test_entry_points_are_declared():
     names = declared_symbols()
-    for n in ("fp8_rmsnorm_quant_act", "fp8_mx_rmsnorm_quant_act", "speculative_verify", "speculative_verify_workspace_size"):
+    for n in ("fp8_rmsnorm_quant_act", "fp8_mx_rmsnorm_quant_act", "speculative_verify", "speculative_verify_workspace_size",
+              "moe_route_grouped", "fp8_moe_layer_grouped"):
         assert n in names
 
 
@@ -101,3 +103,44 @@ def test_the_reference_of_the_verification():
     assert run(0, 0.49)[1].tolist() == [1]
     tok, acc = run(1, 0.0, temperature=np.array([0.0]))
     assert acc.tolist() == [0] and tok.tolist() == [[0, -1]]
+
+
+def test_grouped_routing_validation(L):
+    def route(x=A16, ldx=512, wr=A16, wt=1, bias=NUL, M=8, H=512, E=16, k=2, sc=1, G=4, tg=2, best=2, scale=1.0, ids=A16,
+              w=A16, ws=A16, n=1 << 40, flags=0):
+        return L.moe_route_grouped(x, ldx, wr, wt, bias, M, H, E, k, sc, G, tg, best, 1, scale, ids, w, ws, n, flags, S)
+
+    def layer(x=A16, ldx=512, wr=A16, wt=1, bias=NUL, M=8, H=512, E=16, k=2, sc=1, G=4, tg=2, best=2, scale=1.0, ids=A16,
+              w=A16, ws=A16, n=1 << 40, flags=2, w13=A16, s13=A16, w2=A16, s2=A16, y=A16, I=256):
+        return L.fp8_moe_layer_grouped(x, ldx, wr, wt, bias, sc, G, tg, best, 1, scale, w13, s13, w2, s2, y, ids, w, M, H, I,
+                                       E, k, ws, n, flags, S)
+
+    fine = (INVALID, SHAPE, MISALIGNED)
+    for call in (route, layer):
+        assert call() not in fine and call(bias=A16) not in fine and call(G=1, tg=1) not in fine
+        for nul in ("x", "wr", "ws"):
+            assert call(**{nul: NUL}) == INVALID
+        for kw in (dict(wt=2), dict(sc=2), dict(sc=-1), dict(G=0), dict(tg=0), dict(tg=5), dict(best=0), dict(best=3),
+                   dict(scale=float("nan")), dict(scale=float("inf")), dict(M=0), dict(k=0), dict(ldx=256), dict(flags=4)):
+            assert call(**kw) == INVALID, kw
+        for kw in (dict(M=65), dict(E=513, G=1, tg=1), dict(k=17, G=1, tg=1), dict(G=3), dict(k=9), dict(G=16, tg=4),
+                   dict(E=66, G=33), dict(H=576, ldx=576)):
+            assert call(**kw) == SHAPE, kw
+        assert call(G=16, tg=16) not in fine  # every group is open: their scores do not matter
+        assert call(wr=A8) == MISALIGNED and call(bias=A1) == MISALIGNED and call(ws=P(0x10080)) == MISALIGNED
+    assert route(ids=NUL) == INVALID and route(w=NUL) == INVALID and layer(ids=NUL, w=NUL) not in fine
+    assert route(flags=2) == INVALID
+
+
+def test_the_reference_of_the_routing():
+    """Hand-worked: four experts in two groups, scores 1/2, 3/4 | 1/4, 4/5."""
+    l = np.log(np.array([[1.0, 3.0, 1.0 / 3.0, 4.0]]))
+    ids, w, gap = route(l, 2, groups=2, top_groups=1, group_best=2)     # 5/4 against 21/20
+    assert ids.tolist() == [[1, 0]] and np.allclose(w, [[0.6, 0.4]]) and np.isclose(gap, 0.2)
+    assert route(l, 2, groups=2, top_groups=1, group_best=1)[0].tolist() == [[3, 2]]
+    assert route(l, 2, groups=2, top_groups=2)[0].tolist() == [[3, 1]]
+    ids, w, _ = route(l, 2, bias=np.array([0.5, 0.0, 0.0, 0.0]), renorm=False, scale=2.0)
+    assert ids.tolist() == [[0, 3]] and np.allclose(w, [[1.0, 1.6]])
+    ids, w, _ = route(l, 1, sigmoid=False, renorm=False)                # 4 of 1 + 3 + 1/3 + 4
+    assert ids.tolist() == [[3]] and np.allclose(w, [[4.0 / (25.0 / 3.0)]])
+    assert route(np.array([[0.0, 0.0, np.nan, 0.0]]), 4)[0].tolist() == [[0, 1, 3, 2]]
