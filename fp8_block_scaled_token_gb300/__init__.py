@@ -580,60 +580,114 @@ def _work(workspace):
     raise TypeError("workspace must be a contiguous CUDA tensor of bytes (make_workspace)")
 
 
-# ---------------------------------------------------------- norm and cast
-def _same_device(x, **named):
-    """ValueError for a tensor that is not on x's device, or an x that is not on
-    the current one (the kernels run there, on its current stream)."""
-    d = x.get_device()
-    if d != _torch_module.cuda.current_device():
-        raise ValueError("the tensors are on device %d, which is not the current one" % d)
-    for name, t in named.items():
-        if t is not None and t.get_device() != d:
-            raise ValueError("%s must be on the device of the first argument" % name)
+# ----------------------------------- norm and cast, drafted tokens, scored routing
+# As above, one short call a tensor; these also take the device: the kernels run
+# on the current one's current stream, so x has to lie there and the rest with it.
+_device_now = None
 
 
-def _rows16(t, shape, name):
-    """(row stride, address) of bf16 rows of that shape with unit stride along K."""
+def _home(t, name):
+    """The device number of a call's first tensor, which is the current device."""
+    global _device_now
+    if _device_now is None:
+        torch = _torch()
+        torch.cuda.current_device()  # (this initialises CUDA)
+        _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    d = t.get_device()
+    if d != _device_now():
+        raise ValueError("%s is on device %d, which is not the current one" % (name, d))
+    return d
+
+
+def _rows(t, name):
+    """(shape, row stride, address) of a bf16 matrix with unit stride along K."""
+    try:
+        if t.dtype is _bf16 and t.is_cuda:
+            shape = t.shape
+            ld, unit = t.stride()
+            if unit == 1 and 0 <= ld <= 0x7fffffff:
+                return shape, ld if shape[0] != 1 else shape[1], t.data_ptr()
+            if unit == 1 and shape[0] == 1:
+                return shape, shape[1], t.data_ptr()
+    except (AttributeError, ValueError):
+        pass
     _need(t, _bf16, name)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s" % (name, tuple(shape)))
-    ld, unit = t.stride()
-    if unit != 1:
+    if t.stride(1) != 1:
         raise ValueError("%s must have unit stride along K" % name)
-    if shape[0] == 1:
-        ld = shape[1]
-    elif ld > 0x7fffffff:
-        raise ValueError("%s's row stride does not fit in 32 bits" % name)
-    return ld, t.data_ptr()
+    raise ValueError("%s's row stride does not fit in 32 bits" % name)
 
 
-def _vector(v, n, name):
-    """(dtype code, address) of n contiguous fp32 or bf16 values."""
-    _tensors(**{name: v})
-    if v.dtype is not _f32 and v.dtype is not _bf16:
-        raise TypeError("%s must be float32 or bfloat16" % name)
-    return BF16 if v.dtype is _bf16 else F32, _addr(v, v.dtype, n, name)
+def _in(t, dtype, numel, name, d):
+    """Address of a contiguous input of that type and number of elements on device d."""
+    try:
+        if t.dtype is dtype and t.get_device() == d and t.is_contiguous() and t.numel() == numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _addr(t, dtype, numel, name)
+    raise ValueError("%s must be on device %d, as the first argument" % (name, d))
 
 
-def _rmsnorm(fn, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, scales_dtype, shape, flags):
-    M, K, ldx, xp = _act(x)
-    gt, gp = _vector(gamma, K, "gamma")
+def _there(t, name, d):
+    if t.get_device() != d:
+        raise ValueError("%s must be on device %d, as the first argument" % (name, d))
+
+
+def _make(t, shape, dtype, dev, name, d):
+    """(tensor, address) of an output: `t` checked, or a new one."""
+    if t is None:
+        t = _empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    r = _out(t, shape, dtype, dev, name)
+    _there(t, name, d)
+    return r
+
+
+def _rmsnorm(mx, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, flags):
+    if _torch_module is None:
+        _torch()
+    shape, ldx, xp = _rows(x, "x")
+    d = _home(x, "x")
+    M, K = shape
     dev = x.device
+    try:
+        bf = gamma.dtype is _bf16
+    except AttributeError:
+        _tensors(gamma=gamma)
+        raise
+    if not bf and gamma.dtype is not _f32:
+        _tensors(gamma=gamma)
+        raise TypeError("gamma must be float32 or bfloat16")
+    gp = _in(gamma, _bf16 if bf else _f32, K, "gamma", d)
     rp = op = yp = None
     ldr = ldo = 0
     if residual is not None:
-        ldr, rp = _rows16(residual, x.shape, "residual")
+        rshape, ldr, rp = _rows(residual, "residual")
         if residual_out is None:
-            residual_out = _empty((M, K), dtype=_bf16, device=dev)
-        ldo, op = _rows16(residual_out, x.shape, "residual_out")
+            residual_out = _empty(shape, dtype=_bf16, device=dev)
+            ldo, op = K, residual_out.data_ptr()
+        else:
+            oshape, ldo, op = _rows(residual_out, "residual_out")
+            if oshape != shape:
+                raise ValueError("residual_out must have shape %s" % (tuple(shape),))
+            _there(residual_out, "residual_out", d)
+        if rshape != shape:
+            raise ValueError("residual must have shape %s" % (tuple(shape),))
+        _there(residual, "residual", d)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if store_y or y is not None:
-        y, yp = _out(y, (M, K), _bf16, dev, "y")
-    xq, qp = _out(xq, (M, K), _u8, dev, "xq")
-    scales, sp = _out(scales, shape(M, K), scales_dtype, dev, "xs" if scales_dtype is _f32 else "xs_atoms")
-    _same_device(x, gamma=gamma, residual=residual, residual_out=residual_out, y=y, xq=xq, scales=scales)
-    _check(fn, getattr(lib(), fn)(xp, ldx, rp, ldr, op, ldo, gp, gt, eps, M, K, yp, qp, sp, flags, _stream()))
+        y, yp = _make(y, shape, _bf16, dev, "y", d)
+    xq, qp = _make(xq, shape, _u8, dev, "xq", d)
+    if mx:
+        scales, sp = _make(scales, ((M + 127) // 128 * (K // 128), 512), _u8, dev, "xs_atoms", d)
+        call = lib().fp8_mx_rmsnorm_quant_act
+    else:
+        scales, sp = _make(scales, (M, K // 128) if M <= 16 else (K // 128, M), _f32, dev, "xs", d)
+        call = lib().fp8_rmsnorm_quant_act
+    code = call(xp, ldx, rp, ldr, op, ldo, gp, BF16 if bf else F32, eps, M, K, yp, qp, sp, flags, _stream())
+    if code:
+        _check("fp8_mx_rmsnorm_quant_act" if mx else "fp8_rmsnorm_quant_act", code)
     return xq, scales, residual_out, y
 
 
@@ -644,27 +698,16 @@ def fp8_rmsnorm_quant_act(x, gamma, eps=1e-6, residual=None, residual_out=None, 
     cast: (xq uint8 [M, K], xs fp32 of scales_shape(M, K), residual_out = h bf16
     [M, K] or None, y = the norm's bf16 values [M, K], None without
     ``store_y``).  residual_out=residual adds in place."""
-    if _torch_module is None:
-        _torch()
-    return _rmsnorm("fp8_rmsnorm_quant_act", x, gamma, eps, residual, residual_out, y, store_y, xq, xs, _f32, scales_shape,
-                    flags)
-
-
-def _mx_atoms_shape(M, K):
-    return ((M + 127) // 128) * max(K // 128, 0), 512
+    return _rmsnorm(False, x, gamma, eps, residual, residual_out, y, store_y, xq, xs, flags)
 
 
 def fp8_mx_rmsnorm_quant_act(x, gamma, eps=1e-6, residual=None, residual_out=None, y=None, store_y=False, xq=None,
                              xs_atoms=None, flags=0):
     """The same with the MX cast (M <= 512): (xq, xs_atoms uint8 [ceil(M/128) *
     K/128, 512], residual_out, y)."""
-    if _torch_module is None:
-        _torch()
-    return _rmsnorm("fp8_mx_rmsnorm_quant_act", x, gamma, eps, residual, residual_out, y, store_y, xq, xs_atoms, _u8,
-                    _mx_atoms_shape, flags)
+    return _rmsnorm(True, x, gamma, eps, residual, residual_out, y, store_y, xq, xs_atoms, flags)
 
 
-# ------------------------------------------------- drafted tokens
 def speculative_verify_workspace_size(B, L, V):
     n = ctypes.c_size_t(0)
     _check("speculative_verify_workspace_size", lib().speculative_verify_workspace_size(B, L, V, ctypes.byref(n)))
@@ -673,20 +716,25 @@ def speculative_verify_workspace_size(B, L, V):
 
 def _logit_rows(t, rows, V, dtypes, name):
     """(row stride, address) of rows with unit stride along the vocabulary."""
+    try:
+        if t.dtype in dtypes and t.is_cuda and t.shape == (rows, V):
+            ld, unit = t.stride()
+            if unit == 1 or V == 1:
+                if rows <= 1:
+                    return V, t.data_ptr()
+                if V <= ld <= 0x7fffffff:
+                    return ld, t.data_ptr()
+    except AttributeError:
+        pass
     _tensors(**{name: t})
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
     _need(t, t.dtype, name)
-    if t.shape[1] != V or t.shape[0] != rows:
+    if t.shape != (rows, V):
         raise ValueError("%s must have shape (%d, %d)" % (name, rows, V))
-    ld, unit = t.stride()
-    if unit != 1 and V > 1:
+    if t.stride(1) != 1:
         raise ValueError("%s must have unit stride along the vocabulary" % name)
-    if rows <= 1:
-        ld = V
-    elif ld > 0x7fffffff:
-        raise ValueError("%s's row stride does not fit in 32 bits" % name)
-    return ld, t.data_ptr()
+    raise ValueError("%s's rows overlap, or their stride does not fit in 32 bits" % name)
 
 
 def speculative_verify(logits, sample_u, draft=None, accept_u=None, draft_probs=None, draft_len=None, temperature=None,
@@ -701,38 +749,42 @@ def speculative_verify(logits, sample_u, draft=None, accept_u=None, draft_probs=
     Without a draft one token is drawn from each row."""
     if _torch_module is None:
         _torch()
-    _tensors(logits=logits, sample_u=sample_u)
-    B = sample_u.numel()
+    try:
+        B = sample_u.numel()
+        V = logits.shape[-1]
+        d = _home(logits, "logits") if logits.is_cuda else -1
+    except AttributeError:
+        _tensors(logits=logits, sample_u=sample_u)
+        raise
     L, dp, ap, qp, np_, tp, ldq = 0, None, None, None, None, None, 0
     if draft is not None:
         _need(draft, _i32, "draft")
         L = draft.shape[1]
-    if L:
-        dp, ap = _addr(draft, _i32, B * L, "draft"), _addr(accept_u, _f32, B * L, "accept_u")
-        if draft_len is not None:
-            np_ = _addr(draft_len, _i32, B, "draft_len")
-    elif draft is None and (accept_u is not None or draft_probs is not None or draft_len is not None):
+    elif accept_u is not None or draft_probs is not None or draft_len is not None:
         raise ValueError("accept_u, draft_probs and draft_len need a draft")
-    if logits.dim() != 2:
-        raise ValueError("logits must be 2-D")
-    V = logits.shape[1]
     ldl, lp = _logit_rows(logits, B * (L + 1), V, (_bf16, _f32), "logits")
-    if draft_probs is not None and L:
-        ldq, qp = _logit_rows(draft_probs, B * L, V, (_f32,), "draft_probs")
-    sp = _addr(sample_u, _f32, B, "sample_u")
+    if L:
+        dp, ap = _in(draft, _i32, B * L, "draft", d), _in(accept_u, _f32, B * L, "accept_u", d)
+        if draft_len is not None:
+            np_ = _in(draft_len, _i32, B, "draft_len", d)
+        if draft_probs is not None:
+            ldq, qp = _logit_rows(draft_probs, B * L, V, (_f32,), "draft_probs")
+            _there(draft_probs, "draft_probs", d)
+    sp = _in(sample_u, _f32, B, "sample_u", d)
     if temperature is not None:
-        tp = _addr(temperature, _f32, B, "temperature")
+        tp = _in(temperature, _f32, B, "temperature", d)
     dev = logits.device
-    tokens, op = _out(tokens, (B, L + 1), _i32, dev, "tokens")
-    accepted, cp = _out(accepted, (B,), _i32, dev, "accepted")
-    probs, pp = _out(probs, (B, L + 1), _f32, dev, "probs")
+    tokens, op = _make(tokens, (B, L + 1), _i32, dev, "tokens", d)
+    accepted, cp = _make(accepted, (B,), _i32, dev, "accepted", d)
+    probs, pp = _make(probs, (B, L + 1), _f32, dev, "probs", d)
     if workspace is None:
         workspace = make_workspace(speculative_verify_workspace_size(B, L, V), dev)
     wsp, wsn = _work(workspace)
-    _same_device(logits, sample_u=sample_u, draft=draft, accept_u=accept_u, draft_probs=draft_probs, draft_len=draft_len,
-                 temperature=temperature, tokens=tokens, accepted=accepted, probs=probs, workspace=workspace)
-    _check("speculative_verify", lib().speculative_verify(lp, BF16 if logits.dtype is _bf16 else F32, ldl, dp, np_, qp, ldq,
-                                                          ap, sp, tp, B, L, V, op, cp, pp, wsp, wsn, flags, _stream()))
+    _there(workspace, "workspace", d)
+    code = lib().speculative_verify(lp, BF16 if logits.dtype is _bf16 else F32, ldl, dp, np_, qp, ldq, ap, sp, tp, B, L, V, op,
+                                    cp, pp, wsp, wsn, flags, _stream())
+    if code:
+        _check("speculative_verify", code)
     return tokens, accepted, probs
 
 
@@ -848,12 +900,14 @@ def fp8_moe_layer(x, wr, top_k, w13, s13, w2, s2, renormalize=True, y=None, ids=
 
 
 def _scores(x, wr, bias):
-    """(M, K, row stride, address of x; E, dtype code, address of wr; address of bias)."""
+    """(M, K, row stride, address of x; E, dtype code, address of wr; address of bias; device)."""
     M, H, ldx, xp = _act(x)
+    d = _home(x, "x")
     E, Hr, wt, wrp = _matrix(wr, "wr")
     if H != Hr:
         raise ValueError("operand shapes do not agree")
-    return M, H, ldx, xp, E, wt, wrp, None if bias is None else _addr(bias, _f32, E, "bias")
+    _there(wr, "wr", d)
+    return M, H, ldx, xp, E, wt, wrp, None if bias is None else _in(bias, _f32, E, "bias", d), d
 
 
 def moe_route_grouped(x, wr, top_k, bias=None, scoring=SCORE_SIGMOID, groups=1, top_groups=1, group_best=2,
@@ -863,14 +917,14 @@ def moe_route_grouped(x, wr, top_k, bias=None, scoring=SCORE_SIGMOID, groups=1, 
     fp32 [E] or None -> (ids int32 [M, top_k] by descending score plus bias, weights
     fp32 [M, top_k]: the scores, over their sum with ``renormalize``, times
     scale).  Workspace of moe_route_workspace_size."""
-    M, H, ldx, xp, E, wt, wrp, bp = _scores(x, wr, bias)
+    M, H, ldx, xp, E, wt, wrp, bp, d = _scores(x, wr, bias)
     dev = x.device
-    ids, idp = _out(ids, (M, top_k), _i32, dev, "ids")
-    weights, wp = _out(weights, (M, top_k), _f32, dev, "weights")
+    ids, idp = _make(ids, (M, top_k), _i32, dev, "ids", d)
+    weights, wp = _make(weights, (M, top_k), _f32, dev, "weights", d)
     if workspace is None:
         workspace = make_workspace(moe_route_workspace_size(M, E), dev)
     wsp, wsn = _work(workspace)
-    _same_device(x, wr=wr, bias=bias, ids=ids, weights=weights, workspace=workspace)
+    _there(workspace, "workspace", d)
     _check("moe_route_grouped", lib().moe_route_grouped(xp, ldx, wrp, wt, bp, M, H, E, top_k, scoring, groups, top_groups,
                                                         group_best, 1 if renormalize else 0, scale, idp, wp, wsp, wsn,
                                                         flags, _stream()))
@@ -883,16 +937,17 @@ def fp8_moe_layer_grouped(x, wr, top_k, w13, s13, w2, s2, bias=None, scoring=SCO
     """The whole layer, moe_route_grouped and fp8_moe_experts in three kernels:
     (y bf16 [M, H], ids int32 [M, top_k], weights fp32 [M, top_k]); w13 and w2 as in
     fp8_moe_experts, row-major or tiled."""
-    M, H, ldx, xp, E, wt, wrp, bp = _scores(x, wr, bias)
+    M, H, ldx, xp, E, wt, wrp, bp, d = _scores(x, wr, bias)
     I, tf, w13p, s13p, w2p, s2p = _experts(w13, s13, w2, s2, H, E)
     dev = x.device
-    y, yp = _out(y, (M, H), _bf16, dev, "y")
-    ids, idp = _out(ids, (M, top_k), _i32, dev, "ids")
-    weights, wp = _out(weights, (M, top_k), _f32, dev, "weights")
+    y, yp = _make(y, (M, H), _bf16, dev, "y", d)
+    ids, idp = _make(ids, (M, top_k), _i32, dev, "ids", d)
+    weights, wp = _make(weights, (M, top_k), _f32, dev, "weights", d)
     if workspace is None:
         workspace = make_workspace(fp8_moe_workspace_size(M, H, I, E, top_k), dev)
     wsp, wsn = _work(workspace)
-    _same_device(x, wr=wr, bias=bias, w13=w13, s13=s13, w2=w2, s2=s2, y=y, ids=ids, weights=weights, workspace=workspace)
+    for t, name in ((w13, "w13"), (s13, "s13"), (w2, "w2"), (s2, "s2"), (workspace, "workspace")):
+        _there(t, name, d)
     _check("fp8_moe_layer_grouped",
            lib().fp8_moe_layer_grouped(xp, ldx, wrp, wt, bp, scoring, groups, top_groups, group_best,
                                        1 if renormalize else 0, scale, w13p, s13p, w2p, s2p, yp, idp, wp, M, H, I, E,

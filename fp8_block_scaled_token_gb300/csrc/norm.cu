@@ -14,10 +14,14 @@
 // row's sum of squares is still being put together, and rs goes into the scales.
 // The cast takes fp32 values, not y's bf16: one rounding fewer.
 //
-// One CTA per row, eight consecutive values a thread and step, so that a group
-// of 128 is 16 lanes and a 16-byte access per lane is coalesced.  The row stays
-// in registers as bf16 between the sum and what needs it: each input byte is
-// read once and each output byte written once.
+// Eight consecutive values a thread and step, so that a group of 128 is 16 lanes
+// and a 16-byte access per lane is coalesced.  The row stays in registers between
+// the sum and what needs it: each input byte is read once and each output byte
+// written once.  16,384 rows of 5,120 with residual and y: 121 us, 6.2 TB/s (0.93 of
+// the measured copy bandwidth); 512 rows 6.8 us; up to 150 rows 2.3 to 2.7 us, which
+// is latency.  The first form took 258 us, bound by 45 instructions a value; it is
+// 15 with packed fp32, a bf16 addition and a corrected quotient (codes8) in place of
+// converting both ends of an interval.
 #include <cmath>
 
 #include "fp8bs_testing.h"
@@ -28,6 +32,8 @@
 namespace fp8bs {
 
 constexpr int kNormMaxThreads = 1024;
+constexpr int kNormManyThreads = 320; // where several CTAs share an SM
+constexpr int kNormMidThreads = 640;
 constexpr int kNormMaxChunks = 4; // of eight values a thread
 constexpr int kNormMaxK = kNormMaxThreads * kNormMaxChunks * 8;
 
@@ -66,17 +72,53 @@ __device__ __forceinline__ void values8(const uint4 &w, float (&v)[8])
     }
 }
 
-// Eight weights of the norm from element k on.
-template <bool kBf16> __device__ __forceinline__ void gamma8(const void *gamma, int k, float (&g)[8])
-{
-    if (kBf16) {
-        values8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(gamma) + k), g);
-    } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(gamma) + k);
-        const float4 a = p[0], b = p[1];
-        g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
-        g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+// Raw bits of eight weights of the norm, and their values.
+template <bool kBf16> struct Gamma8 {
+    uint4 w[kBf16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *gamma, int k)
+    {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(gamma) + k * (kBf16 ? 2 : 4));
+        w[0] = p[0];
+        if (!kBf16)
+            w[kBf16 ? 0 : 1] = p[1];
     }
+    __device__ __forceinline__ void values(float (&g)[8]) const
+    {
+        if (kBf16) {
+            values8(w[0], g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 a = w[kBf16 ? 0 : i];
+                g[4 * i] = __uint_as_float(a.x);
+                g[4 * i + 1] = __uint_as_float(a.y);
+                g[4 * i + 2] = __uint_as_float(a.z);
+                g[4 * i + 3] = __uint_as_float(a.w);
+            }
+        }
+    }
+};
+
+// d0 = a0 * b0, d1 = a1 * b1 as one packed instruction.
+__device__ __forceinline__ void mul2v(float &d0, float &d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 ra, rb;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 ra, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// bf16_rn(fl32(a + b)) of two values: rounded to bf16 at once, which is the
+// same.  fl32 rounds only where one is below 2^-16 of the other, and such a sum
+// is not near the middle between two bf16 numbers.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ float abs_max8(const float (&v)[8])
@@ -84,40 +126,85 @@ __device__ __forceinline__ float abs_max8(const float (&v)[8])
     return fmaxf(abs_max4(v[0], v[1], v[2], v[3]), abs_max4(v[4], v[5], v[6], v[7]));
 }
 
-// kChunks: steps of blockDim.x * 8 values that cover the row.
-// No __restrict__: x and the residual may still be being written when a kernel
-// launched programmatically starts, and res_out may be the residual itself.
-template <bool kMx, bool kBf16, int kChunks>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(const NormParams p)
+// Between these a quotient by s can be corrected as below without leaving the
+// normal numbers: the remainder of a quotient of 2^-10 is 2^-34 s or more.
+constexpr float kPlainLo = 8.077935669e-28f; // 2^-90
+constexpr float kPlainHi = 1.237940039e+27f; // 2^90
+
+// Codes of eight values over s: e4m3 of the correctly rounded quotients.  With y
+// = fl32(1 / s), q = fl32(v y) and the exact remainder v - q s (one fma), fl32(q +
+// (v - q s) y) is the correctly rounded quotient (Markstein 1990), three packed
+// instructions a pair; quantize4 takes the scales at the ends of the range, NaN and infinity.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s)
+{
+    if (!(s >= kPlainLo && s <= kPlainHi))
+        return make_uint2(quantize4(v[0], v[1], v[2], v[3], s), quantize4(v[4], v[5], v[6], v[7], s));
+    const float y = -__frcp_rn(s); // negative, so that a zero keeps its sign: -0 -> +0, +0, +0 -> -(+0)
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        float r0 = v[i], r1 = v[i + 1];
+        mul2v(q[i], q[i + 1], v[i], v[i + 1], y, y);
+        fma2(r0, r1, q[i], q[i + 1], s, s);
+        fma2(q[i], q[i + 1], r0, r1, y, y);
+    }
+    return make_uint2(e4m3x4(-q[0], -q[1], -q[2], -q[3]), e4m3x4(-q[4], -q[5], -q[6], -q[7]));
+}
+
+// fl32(a / 448), in the same way.
+__device__ __forceinline__ float over_448(float a)
+{
+    if (!(a >= kPlainLo && a <= kPlainHi))
+        return __fdiv_rn(a, kE4M3Max);
+    constexpr float y = 1.0f / 448.0f;
+    const float q = a * y;
+    return fmaf(fmaf(-q, kE4M3Max, a), y, q);
+}
+
+// A CTA: blockDim.y rows of blockDim.x threads; kMost threads at most, kMin CTAs to an SM.
+template <bool kMx, bool kBf16, int kChunks, int kMost, int kMin>
+__global__ void __launch_bounds__(kMost, kMin) rmsnorm_quant_kernel(const NormParams p)
 {
     __shared__ float part[2][32];
-    if (blockIdx.x == 0 && threadIdx.x == 0)
+    if (blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0)
         atomicAdd(p.runs + (kMx ? FP8BS_RUNS_NORM_MX : FP8BS_RUNS_NORM_FP8), 1ull);
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = static_cast<int>(blockDim.x >> 5); // of a row
     const int kg = p.K / 128;
-    if (kMx && static_cast<int>(blockIdx.x) >= p.M) { // one atom's words of the rows past M
+    const int rows = static_cast<int>(blockDim.y);
+    const int ctas = (p.M + rows - 1) / rows;
+    if (kMx && static_cast<int>(blockIdx.x) >= ctas) { // one atom's words of the rows past M
         grid_dependency_wait();
-        const int g = blockIdx.x - p.M, tt = p.M / 128;
+        const int g = blockIdx.x - ctas, tt = p.M / 128;
         uint32_t *const words = reinterpret_cast<uint32_t *>(p.sf + (static_cast<long long>(tt) * kg + g) * 512);
-        for (int r = threadIdx.x; r < 128; r += blockDim.x)
+        for (int r = threadIdx.y * blockDim.x + threadIdx.x; r < 128; r += blockDim.x * blockDim.y)
             if (r >= p.M % 128)
                 words[4 * (r & 31) + (r >> 5)] = 0u;
         return;
     }
-    const int m = blockIdx.x;
+    const int m = static_cast<int>(blockIdx.x) * rows + threadIdx.y;
+    const int K = m < p.M ? p.K : 0; // a row past the last: no loads, no stores
     const int step = static_cast<int>(blockDim.x) * 8;
     const int k0 = static_cast<int>(threadIdx.x) * 8;
+    float *const sum = part[0] + threadIdx.y * warps;
+    Gamma8<kBf16> gamma[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        gamma[c] = {};
+        if (c * step + k0 < K)
+            gamma[c].load(p.gamma, c * step + k0);
+    }
     grid_dependency_wait();
-    uint4 raw[kChunks];
+    uint4 h[kChunks];
     {
         const uint16_t *const xr = p.x + m * p.ldx;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int k = c * step + k0;
-            raw[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (k < p.K)
-                raw[c] = *reinterpret_cast<const uint4 *>(xr + k);
+            h[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (k < K)
+                h[c] = *reinterpret_cast<const uint4 *>(xr + k);
         }
     }
     if (p.res != nullptr) {
@@ -128,77 +215,88 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(const No
         for (int c = 0; c < kChunks; ++c) {
             const int k = c * step + k0;
             add[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (k < p.K)
+            if (k < K)
                 add[c] = *reinterpret_cast<const uint4 *>(rr + k);
         }
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int k = c * step + k0;
-            float a[8], b[8];
-            values8(raw[c], a);
-            values8(add[c], b);
-            raw[c] = make_uint4(bf16x2_rn(a[0] + b[0], a[1] + b[1]), bf16x2_rn(a[2] + b[2], a[3] + b[3]),
-                                bf16x2_rn(a[4] + b[4], a[5] + b[5]), bf16x2_rn(a[6] + b[6], a[7] + b[7]));
-            if (k < p.K)
-                *reinterpret_cast<uint4 *>(ro + k) = raw[c];
+            h[c] = make_uint4(add_bf16x2(h[c].x, add[c].x), add_bf16x2(h[c].y, add[c].y),
+                              add_bf16x2(h[c].z, add[c].z), add_bf16x2(h[c].w, add[c].w));
+            if (k < K)
+                *reinterpret_cast<uint4 *>(ro + k) = h[c];
         }
     }
     // Squares past fp32's range (values above 2^64 / sqrt(K)) are summed again
     // with the row times 2^-80; a row with an infinity or NaN keeps its sum.
-    float pre = 1.0f, rs;
+    float u[kChunks][8];
     float sg[kChunks]; // fp32 scales of this thread's groups, before rs
+    float eps = p.eps, rs;
 #pragma unroll 1
     for (int turn = 0;; ++turn) {
-        float ss = 0.0f;
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int k = c * step + k0;
-            float h[8];
-            values8(raw[c], h);
+            float g[8];
+            values8(h[c], u[c]);
+            gamma[c].values(g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[i] *= pre;
-                ss = fmaf(h[i], h[i], ss);
+            for (int i = 0; i < 8; i += 2) {
+                fma2(s0, s1, u[c][i], u[c][i + 1], u[c][i], u[c][i + 1]);
+                mul2v(u[c][i], u[c][i + 1], u[c][i], u[c][i + 1], g[i], g[i + 1]);
             }
             if (!kMx) {
-                float g[8] = {};
-                if (k < p.K)
-                    gamma8<kBf16>(p.gamma, k, g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    h[i] *= g[i];
-                float am = abs_max8(h);
+                float am = abs_max8(u[c]);
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1)
                     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                float s = __fdiv_rn(am, kE4M3Max);
+                const float s = over_448(am);
                 sg[c] = s;
-                s = s == 0.0f ? 1.0f : s; // zeros, or amax below 448 * 2^-150
-                if (k < p.K)
-                    *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) =
-                        make_uint2(quantize4(h[0], h[1], h[2], h[3], s), quantize4(h[4], h[5], h[6], h[7], s));
+                const uint2 codes = codes8(u[c], s == 0.0f ? 1.0f : s); // 0: zeros, or amax below 448 * 2^-150
+                if (k < K)
+                    *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) = codes;
             }
         }
+        float ss = s0 + s1;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (lane == 0)
-            part[turn][warp] = ss;
+            sum[32 * turn + warp] = ss;
         __syncthreads();
-        ss = lane < static_cast<int>(blockDim.x >> 5) ? part[turn][lane] : 0.0f;
+        ss = lane < warps ? sum[32 * turn + lane] : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rs = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.K)) + p.eps * pre * pre);
-        if (turn == 1 || ss != INFINITY)
+        rs = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.K)) + eps);
+        const bool again = turn == 0 && ss == INFINITY;
+        if (rows == 1 ? !again : !__syncthreads_or(again))
             break;
-        pre = 8.27180613e-25f; // 2^-80
+        const uint16_t *const hr = p.res != nullptr ? p.res_out + m * p.ldo : p.x + m * p.ldx; // what this thread summed
+        if (again)
+            eps = 0.0f; // times 2^-160
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int k = c * step + k0;
+            if (k >= K)
+                continue;
+            h[c] = *reinterpret_cast<const uint4 *>(hr + k);
+            gamma[c].load(p.gamma, k);
+            if (again) {
+                float v[8];
+                values8(h[c], v);
+                constexpr float t = 8.27180613e-25f; // 2^-80
+                h[c] = make_uint4(bf16x2_rn(v[0] * t, v[1] * t), bf16x2_rn(v[2] * t, v[3] * t),
+                                  bf16x2_rn(v[4] * t, v[5] * t), bf16x2_rn(v[6] * t, v[7] * t));
+            }
+        }
     }
     if (!kMx) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int k = c * step + k0;
-            if (k < p.K && (lane & 15) == 0)
+            if (k < K && (lane & 15) == 0)
                 p.xs[p.kmajor ? static_cast<long long>(k >> 7) * p.M + m : static_cast<long long>(m) * kg + (k >> 7)] =
                     sg[c] == 0.0f ? 1.0f : sg[c] * rs;
         }
@@ -208,14 +306,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(const No
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         const int k = c * step + k0;
-        float v[8], g[8] = {};
-        values8(raw[c], v);
-        if (k < p.K)
-            gamma8<kBf16>(p.gamma, k, g);
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = v[i] * pre * g[i] * rs;
-        if (p.y != nullptr && k < p.K)
+        for (int i = 0; i < 8; i += 2)
+            mul2(v[i], v[i + 1], u[c][i], u[c][i + 1], rs);
+        if (p.y != nullptr && k < K)
             *reinterpret_cast<uint4 *>(p.y + static_cast<long long>(m) * p.K + k) =
                 make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
         if (kMx) {
@@ -227,10 +322,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_quant_kernel(const No
             uint32_t byte = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 2) & 3));
             byte |= __shfl_xor_sync(0xffffffffu, byte, 4);
             byte |= __shfl_xor_sync(0xffffffffu, byte, 8);
-            if (k < p.K) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+                mul2(v[i], v[i + 1], v[i], v[i + 1], inv);
+            if (k < K) {
                 *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) =
-                    make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                               e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+                    make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
                 if ((lane & 15) == 0) {
                     const int r = m & 127;
                     reinterpret_cast<uint32_t *>(p.sf + (static_cast<long long>(m >> 7) * kg + (k >> 7)) * 512)
@@ -245,30 +342,44 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <bool kMx, bool kBf16> auto norm_kernel(int chunks)
+// Registers for the values in flight against CTAs to an SM: four CTAs of 320 threads hold two steps (three: 130
+// us for 16,384 rows of 5,120, not 121; five spill, 210), two hold four (three: 63 us for 4,096 of 8,192, not 61).
+template <bool kMx, bool kBf16> auto norm_kernel(int chunks, int threads)
 {
-    return chunks == 1   ? rmsnorm_quant_kernel<kMx, kBf16, 1>
-           : chunks == 2 ? rmsnorm_quant_kernel<kMx, kBf16, 2>
-                         : rmsnorm_quant_kernel<kMx, kBf16, 4>;
+    if (threads <= kNormManyThreads)
+        return chunks == 1   ? rmsnorm_quant_kernel<kMx, kBf16, 1, kNormManyThreads, 4>
+               : chunks == 2 ? rmsnorm_quant_kernel<kMx, kBf16, 2, kNormManyThreads, 4>
+                             : rmsnorm_quant_kernel<kMx, kBf16, 4, kNormManyThreads, 2>;
+    if (chunks == 4 && threads <= kNormMidThreads)
+        return rmsnorm_quant_kernel<kMx, kBf16, 4, kNormMidThreads, 1>;
+    return chunks == 1   ? rmsnorm_quant_kernel<kMx, kBf16, 1, kNormMaxThreads, 1>
+           : chunks == 2 ? rmsnorm_quant_kernel<kMx, kBf16, 2, kNormMaxThreads, 1>
+                         : rmsnorm_quant_kernel<kMx, kBf16, 4, kNormMaxThreads, 1>;
 }
 
-fp8bs_status launch_norm(const NormParams &p, bool mx, bool gamma_bf16, bool pdl, cudaStream_t stream)
+fp8bs_status launch_norm(const NormParams &p, bool mx, bool gamma_bf16, bool pdl, cudaStream_t stream, int sms)
 {
     const int words = p.K / 8;
+    // Up to a row an SM: the whole row's loads in flight at once, in one large CTA (152 rows of 5,120 2.7 us,
+    // 3.3 in small ones).  More: small CTAs, four to an SM (200 rows 3.9 us against 4.1, 16,384 rows 121 against
+    // 225), with several rows each where a row needs few threads (16,384 rows of 256: 9.6 us, 17.5 with one).
+    const int most = p.M <= sms ? kNormMaxThreads : kNormManyThreads;
     int chunks = 1;
-    while (words > chunks * kNormMaxThreads)
+    while (words > chunks * most && chunks < kNormMaxChunks)
         chunks *= 2;
+    const int threads = ((words + chunks - 1) / chunks + 31) / 32 * 32;
+    const int rows = most == kNormMaxThreads ? 1 : most / threads > 1 ? most / threads : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(static_cast<unsigned>(((words + chunks - 1) / chunks + 31) / 32 * 32), 1, 1);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.M + (mx && p.M % 128 != 0 ? p.K / 128 : 0)), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), static_cast<unsigned>(rows), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((p.M + rows - 1) / rows + (mx && p.M % 128 != 0 ? p.K / 128 : 0)), 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    auto kernel = mx ? (gamma_bf16 ? norm_kernel<true, true>(chunks) : norm_kernel<true, false>(chunks))
-                     : (gamma_bf16 ? norm_kernel<false, true>(chunks) : norm_kernel<false, false>(chunks));
+    auto kernel = mx ? (gamma_bf16 ? norm_kernel<true, true>(chunks, threads) : norm_kernel<true, false>(chunks, threads))
+                     : (gamma_bf16 ? norm_kernel<false, true>(chunks, threads) : norm_kernel<false, false>(chunks, threads));
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
@@ -308,7 +419,7 @@ fp8bs_status rmsnorm_quant(const void *x, int ldx, const void *residual, int ldr
     p.kmajor = M > 16;
     p.runs = dev.runs;
     return launch_norm(p, mx, gamma_type == FP8BS_BF16, (flags & FP8BS_FLAG_OVERLAP_PREV) != 0,
-                       static_cast<cudaStream_t>(stream));
+                       static_cast<cudaStream_t>(stream), dev.sms);
 }
 
 } // namespace
