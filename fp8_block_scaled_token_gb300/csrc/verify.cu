@@ -13,19 +13,23 @@
 // chunk, relative to a power of two near its largest) and 2^-41 (a row): integer
 // sums have no order, which makes the result bitwise reproducible.
 //
-// w(x) = 2^((x - ref) c), c = log2(e) / T as two fp32 numbers.  |ref| is no
-// smaller than |x| for every x that counts, so that t = fl(x - ref) and e = x -
-// (t + ref) are exact (fast two-sum); z = t c + e c in two fp32 numbers, and
-// 2^z as in pair_math.cuh.
+// w(x) = 2^((x - ref) c), c = log2(e) / T as two fp32 numbers: z = x c in two
+// numbers, 2^z as in pair_math.cuh, weights relative to a power of two.  ref is 0
+// while the largest logit's z is below 4096 (nothing is subtracted, and sums
+// relative to powers of two add up without another exponential).  Beyond, |ref| is
+// no smaller than |x| for every x that counts, so that t = fl(x - ref) and e = x -
+// (t + ref) are exact (fast two-sum) and z = t c + e c.
 //
-// verify_stats_kernel: a CTA per (row, 8,192 logits), rows in the order of
-// their positions.  Maximum, then the sum of the weights, from registers: one
-// read.  The last CTA of a row puts the chunks together and decides the draft.
-// A row that is not accepted leaves its position in the sequence's word, and
-// CTAs of later positions that start after that have nothing to do.
-// verify_choose_kernel: a CTA per (sequence, chunk).  The chunk that holds the
-// target weight looks for the token; with the draft's probabilities all chunks
-// sum max(p - q, 0) first and the last one looks.  Nothing waits.
+// verify_rows_kernel: a CTA per (row, 8,192 logits), rows in the order of their
+// positions.  Maximum, then the sum of the weights, from registers: one read.
+// The last CTA of a row puts the chunks together and decides the draft.  A row
+// that is not accepted leaves its position in the sequence's word, and CTAs of
+// later positions that start after that have nothing to do.  The last row of a
+// sequence knows where it stops and draws the token: it finds the chunk, the
+// eighth of it that a warp summed, and looks through that.
+// verify_residual_kernel (with the draft's probabilities): a CTA per (sequence,
+// 2,048 logits) of those that stopped at a rejected draft: sums max(p - q, 0); a
+// sequence's last CTA finds the chunk and looks through it.  Nothing waits.
 #include <cmath>
 
 #include "fp8bs_testing.h"
@@ -36,31 +40,37 @@
 namespace fp8bs {
 
 constexpr int kVerifyThreads = 256;
-constexpr int kChunk = 8192;      // logits of a CTA
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyCtas = 4;     // to an SM
+constexpr int kChunk = 8192;       // logits of a CTA
+constexpr int kPart = kChunk / kVerifyWarps; // of a warp
+constexpr int kSlice = 2048;       // logits of a CTA of the residual
 constexpr int kVerifyMaxDraft = 31;
 constexpr int kVerifyMaxRows = 4096;
 constexpr int kVerifyMaxVocab = 1 << 20;
+constexpr int kMaxChunks = kVerifyMaxVocab / kChunk + 1;
 constexpr float kChunkUnits = 281474976710656.0f;  // 2^48
 constexpr float kRowUnits = 2199023255552.0f;      // 2^41: a row's total stays below 2^62
 
 struct ChunkStat {
     float top;       // largest logit; NaN where the chunk holds a NaN or +infinity
     int exponent;    // the sum's unit is 2^(exponent - 48)
-    long long sum;   // after the row is put together: in the row's units; T = 0: the index of `top`
+    long long sum;   // T = 0: the index of `top`
 };
 
-struct RowStat {
+struct alignas(16) RowStat {
     int verdict;     // 1 accepted, 0 not (or no draft at this position), 2 no distribution
     int exponent;    // weights are relative to 2^exponent
     float top;       // largest logit
     int best;        // T = 0: its index
     long long total; // of the weights, in row units
     float prob;      // of the drafted token
-    int pad;
+    int position;    // sequence's stop: where, -1 with nothing left to draw
 };
 
 struct VerifyParams {
-    int B, L, V, chunks;
+    int B, L, V, chunks, slices;
+    unsigned first_wave;                     // CTAs that start at once, before any row can have stopped
     const uint8_t *logits;
     long long ldl; // logits
     const int32_t *draft, *draft_len;
@@ -70,9 +80,12 @@ struct VerifyParams {
     int32_t *tokens, *accepted;
     float *probs;
     unsigned *row_done, *stopped, *seq_done; // zero between calls
-    ChunkStat *chunk;
+    ChunkStat *chunk;                        // [rows][chunks]
+    long long *part;                         // [rows][chunks][warps]: the chunk's sum by warps
+    long long *in_row;                       // [rows][chunks]: the chunk's sum in row units
     RowStat *row;
-    long long *residual; // [B][chunks]
+    RowStat *stop;                           // [B]
+    long long *residual;                     // [B][slices]
     unsigned long long *runs;
 };
 
@@ -95,9 +108,14 @@ __device__ __forceinline__ Scale make_scale(float T)
 // Temperatures that are taken: 0, or those that keep every step in range.
 __device__ __forceinline__ bool good_temperature(float T) { return T == 0.0f || (T >= 9.5367432e-07f && T <= 1048576.0f); }
 
-// The reference for logits up to `top`: no smaller in magnitude than any logit
-// above the cutoff.
-__device__ __forceinline__ float reference(float top, float T) { return top >= 0.0f ? top + 128.0f * T : top - 128.0f * T; }
+// The reference for logits up to `top`: 0, or no smaller in magnitude than any
+// logit above the cutoff.
+__device__ __forceinline__ float reference(float top, const Scale &s)
+{
+    if (fabsf(top) * s.ch <= 4096.0f)
+        return 0.0f;
+    return top >= 0.0f ? top + 128.0f * s.T : top - 128.0f * s.T;
+}
 __device__ __forceinline__ float cutoff(float top, float T) { return top - 64.0f * T; } // weights below 2^-92 count as 0
 
 // z = (x - ref) c for x above the cutoff.
@@ -134,6 +152,13 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ long long warp_sum(long long v)
 {
 #pragma unroll
@@ -142,11 +167,108 @@ __device__ __forceinline__ long long warp_sum(long long v)
     return v;
 }
 
+__device__ __forceinline__ long long warp_scan(long long v) // inclusive
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, v, o);
+        if (static_cast<int>(threadIdx.x & 31) >= o)
+            v += t;
+    }
+    return v;
+}
+
+// Two fp32 numbers as one operand of the packed instructions.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 pmul(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 padd(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 pfma(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Sums of weights relative to 2^exponent, each below 2 and at most 32 of them a
+// thread: `high` holds their multiples of 2^-16 exactly, `low` what is left.
+//
+// Two logits at a time with reference 0, in packed instructions (13 a logit
+// where one at a time, with a reference, takes 27): weight() with n = -z in
+// place of z, which saves the negations.  What lies below the cutoff
+// counts as at it, 2^-92, which leaves no trace in the sums.
+struct WeightSum {
+    f32x2 high, low;
+    f32x2 nch, ch, cl;
+    float cut;
+    uint32_t th; // the lane's table entry with the exponent's and index's offset taken off
+    float tl;
+
+    __device__ __forceinline__ WeightSum(float cut_, int exponent, const Scale &s, float2 entry)
+    {
+        high = low = pack(0.0f, 0.0f);
+        nch = pack(-s.ch, -s.ch);
+        ch = pack(s.ch, s.ch);
+        cl = pack(s.cl, s.cl);
+        cut = cut_;
+        th = __float_as_uint(entry.x) - ((threadIdx.x & 31u) << 18) - (static_cast<uint32_t>(exponent) << 23);
+        tl = entry.y;
+    }
+    __device__ __forceinline__ void add(float x0, float x1)
+    {
+        constexpr float k1 = 0x1.62e430p-1f, k2 = 0x1.ebfbe0p-3f, k3 = 0x1.c6b08ep-5f, k4 = 0x1.3b2ab6p-7f; // ln(2)^k / k!
+        const f32x2 minus = pack(-1.0f, -1.0f), shift = pack(kShift, kShift);
+        const f32x2 x = pack(fmaxf(x0, cut), fmaxf(x1, cut));
+        const f32x2 n = pmul(x, nch);
+        const f32x2 zl = pfma(x, cl, pfma(x, ch, n));
+        const f32x2 u = pfma(n, minus, shift);
+        const f32x2 y = padd(pfma(n, minus, pfma(u, minus, shift)), zl);
+        float u0, u1;
+        unpack(u, u0, u1);
+        const uint32_t b0 = __float_as_uint(u0), b1 = __float_as_uint(u1);
+        const uint32_t t0 = __shfl_sync(0xffffffffu, th, b0), t1 = __shfl_sync(0xffffffffu, th, b1);
+        const f32x2 r = pack(__shfl_sync(0xffffffffu, tl, b0), __shfl_sync(0xffffffffu, tl, b1));
+        const f32x2 p3 = pfma(y, pack(k4, k4), pack(k3, k3));
+        const f32x2 p2 = pfma(p3, y, pack(k2, k2));
+        const f32x2 p1 = pfma(p2, y, pack(k1, k1));
+        const f32x2 rest = pfma(p1, y, r);
+        // the bits of u are kShiftBits + 32 n + j: shifted, n is at the exponent and j at bits 18 to 22
+        const f32x2 hi = pack(__uint_as_float((b0 << 18) + t0), __uint_as_float((b1 << 18) + t1));
+        const f32x2 q = padd(padd(hi, pack(192.0f, 192.0f)), pack(-192.0f, -192.0f));
+        high = padd(high, q);
+        low = pfma(hi, rest, padd(low, pfma(q, minus, hi)));
+    }
+    __device__ __forceinline__ long long units(float u) const
+    {
+        float h0, h1, l0, l1;
+        unpack(high, h0, h1);
+        unpack(low, l0, l1);
+        return fixed(h0, l0, u) + fixed(h1, l1, u);
+    }
+};
+static_assert((static_cast<uint32_t>(kShiftBits) << 18) == 0u, "kShiftBits leaves the shifted word");
+
 // One row's logits, in 16-byte words counted from the aligned address at or
 // before its first.
 template <bool kBf16> struct Row {
     static constexpr int kPer = kBf16 ? 8 : 4;                     // logits of a word
-    static constexpr int kWords = kChunk / kPer / kVerifyThreads;  // words of a thread
+    static constexpr int kWords = kChunk / kPer / kVerifyThreads;  // words of a thread of a chunk
     const uint8_t *words;
     int lead; // logits that the first word has before the row
     int V;
@@ -192,6 +314,15 @@ template <bool kBf16> struct Row {
             return __uint_as_float(a[e & 3]);
         return __uint_as_float((e & 1) ? a[(e >> 1) & 3] & 0xFFFF0000u : a[(e >> 1) & 3] << 16);
     }
+    static __device__ __forceinline__ float largest(const uint4 &w) // of a word; NaN where one is
+    {
+        if (kBf16) {
+            const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(w.x, w.y), max_nan_bf16x2(w.z, w.w));
+            return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        }
+        return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                       max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
     __device__ __forceinline__ float at(int i) const // one logit
     {
         const long long k = static_cast<long long>(i) + lead;
@@ -222,468 +353,621 @@ __device__ __forceinline__ bool behind_a_stop(const VerifyParams &p, int b, int 
     return s != 0u && 64 - static_cast<int>(s) < j;
 }
 
-// The row's chunks put together, and the verdict on its draft; one warp.
+// sum * f, both in units of their own, as units of 2^(-41) of the row: sum is in
+// units of 2^(k - 41), f = th (1 + rest) in [1, 2).
+__device__ __forceinline__ long long rescale(long long sum, float th, float rest, int k)
+{
+    const unsigned long long f = static_cast<unsigned long long>(fixed(th, th * rest, 4611686018427387904.0f)); // 2^62
+    const int shift = -k - 2;
+    if (shift > 63)
+        return 0;
+    const unsigned long long v = __umul64hi(static_cast<unsigned long long>(sum), f);
+    return static_cast<long long>(shift >= 0 ? v >> shift : v << -shift);
+}
+
+// The factor that takes sums of a chunk (largest logit ctop, exponent cexp) to
+// row units, as th, rest and k of rescale; false where the chunk is below the
+// row's cutoff.  A whole warp calls it.
+__device__ __forceinline__ bool to_row(float ctop, int cexp, float ref, float cut, int exponent, const Scale &s,
+                                       float2 entry, float &th, float &rest, int &k)
+{
+    const bool live = ctop >= cut;
+    // the chunk's reference seen from the row's, by a two-sum without conditions
+    const float cref = live ? reference(ctop, s) : ref;
+    const float d = cref - ref, bb = d - cref;
+    const float e = (cref - (d - bb)) + (-ref - bb);
+    const float zh = d * s.ch;
+    const float zl = fmaf(e, s.ch, fmaf(d, s.cl, fmaf(d, s.ch, -zh)));
+    k = pow_split(zh, zl, entry, th, rest) + cexp - exponent + 41 - 48;
+    return live;
+}
+
+// a b < c, of numbers that are not negative.
+__device__ __forceinline__ bool less(Pair a, Pair b, Pair c)
+{
+    const float p = a.hi * b.hi;
+    const float e = fmaf(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi);
+    return (p - c.hi) + (e - c.lo) < 0.0f;
+}
+
+__device__ __forceinline__ Pair pair_of(long long v) // to 48 bits
+{
+    const float hi = __ll2float_rn(v);
+    return {hi, __ll2float_rn(v - __float2ll_rn(hi))};
+}
+
+// What a CTA of verify_rows_kernel shares.
+struct RowShared {
+    float top[kVerifyWarps];
+    long long part[kVerifyWarps];  // this chunk's sums by warps
+    long long in_row[kMaxChunks];  // this row's chunks
+    RowStat row;                   // this row, then the one that the sequence stops at
+    long long scan[kVerifyWarps];
+    long long target;
+    int skip, last_chunk, last_row, draw_now, without, chunk, part_of, found, end;
+};
+
+// The row's chunks put together, and the verdict on its draft; one warp of the
+// CTA that summed chunk c as `mine`.
 template <bool kBf16>
-__device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, int len, const Row<kBf16> &x)
+__device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, int len, const Row<kBf16> &x, int c,
+                                           const ChunkStat &mine, RowShared &sh)
 {
     const int lane = threadIdx.x & 31;
     const long long row = static_cast<long long>(b) * (p.L + 1) + j;
-    ChunkStat *const st = p.chunk + row * p.chunks;
+    const ChunkStat *const st = p.chunk + row * p.chunks;
     const float T = temperature(p, b);
     const float2 entry = kPow32[lane];
+    const long long d = static_cast<long long>(b) * p.L + j;
+    const int t = j < len ? p.draft[d] : -1;
+    const bool inside = t >= 0 && t < p.V;
+    const float xt = inside ? x.at(t) : 0.0f;
+    const float qt = j >= len || !inside ? 0.0f : p.q == nullptr ? 1.0f : p.q[d * p.ldq + t];
+    const float ut = j < len ? p.accept_u[d] : 0.0f;
     float top = -INFINITY;
-    for (int c = lane; c < p.chunks; c += 32)
-        top = max_nan(top, __ldcg(&st[c].top));
+    for (int i = lane; i < p.chunks; i += 32)
+        top = max_nan(top, i == c ? mine.top : __ldcg(&st[i].top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     RowStat r = {};
     r.top = top;
+    r.position = j;
     if (!(top > -INFINITY && top < INFINITY) || !good_temperature(T)) {
         r.verdict = 2;
+    } else if (T == 0.0f) {
+        int best = 0x7fffffff;
+        for (int i = lane; i < p.chunks; i += 32)
+            if ((i == c ? mine.top : __ldcg(&st[i].top)) == top)
+                best = min(best, static_cast<int>(i == c ? mine.sum : __ldcg(&st[i].sum)));
+        r.best = __reduce_min_sync(0xffffffffu, best);
+        r.prob = t == r.best ? 1.0f : 0.0f;
+        r.verdict = inside && ut * qt < r.prob ? 1 : 0;
     } else {
-        const int t = j < len ? p.draft[static_cast<long long>(b) * p.L + j] : -1;
-        const bool inside = t >= 0 && t < p.V;
-        double wt = 0.0, total = 1.0; // the drafted token's weight and that of all
-        if (T == 0.0f) {
-            int best = 0x7fffffff;
-            for (int c = lane; c < p.chunks; c += 32)
-                if (__ldcg(&st[c].top) == top)
-                    best = min(best, static_cast<int>(__ldcg(&st[c].sum)));
-            best = __reduce_min_sync(0xffffffffu, best);
-            r.best = best;
-            wt = t == best ? 1.0 : 0.0;
-        } else {
-            const Scale s = make_scale(T);
-            const float ref = reference(top, T), cut = cutoff(top, T);
-            float zh, zl, th, rest;
-            exponent_of(top, ref, s, zh, zl);
-            r.exponent = pow_split(zh, zl, entry, th, rest);
-            long long sum = 0;
-            for (int c0 = 0; c0 < p.chunks; c0 += 32) {
-                const int c = c0 + lane;
-                const float ctop = c < p.chunks ? __ldcg(&st[c].top) : -INFINITY;
-                const bool live = ctop >= cut;
-                // the chunk's reference seen from the row's, by a two-sum without conditions
-                const float cref = live ? reference(ctop, T) : ref;
-                const float d = cref - ref, bb = d - cref;
-                const float e = (cref - (d - bb)) + (-ref - bb);
-                zh = d * s.ch;
-                zl = fmaf(e, s.ch, fmaf(d, s.cl, fmaf(d, s.ch, -zh)));
-                const int n = pow_split(zh, zl, entry, th, rest);
-                long long g = 0;
-                if (live) {
-                    const int k = __ldcg(&st[c].exponent) + n - r.exponent + 41 - 48;
-                    const double f = (static_cast<double>(th) + static_cast<double>(th * rest)) *
-                                     static_cast<double>(__ldcg(&st[c].sum));
-                    g = k < -200 ? 0 : __double2ll_rn(f * __hiloint2double((1023 + k) << 20, 0));
-                }
-                if (c < p.chunks) {
-                    __stcg(&st[c].sum, g);
-                    sum += g;
-                }
-            }
-            r.total = warp_sum(sum);
-            total = static_cast<double>(r.total);
-            if (inside) {
-                float hi, lo;
-                weight(x.at(t), top, ref, cut, r.exponent, s, entry, hi, lo);
-                wt = (static_cast<double>(hi) + static_cast<double>(lo)) * static_cast<double>(kRowUnits);
+        const Scale s = make_scale(T);
+        const float ref = reference(top, s), cut = cutoff(top, T);
+        float zh, zl, th, rest;
+        exponent_of(top, ref, s, zh, zl);
+        r.exponent = pow_split(zh, zl, entry, th, rest);
+        long long sum = 0;
+        for (int i0 = 0; i0 < p.chunks; i0 += 32) {
+            const int i = i0 + lane;
+            const bool there = i < p.chunks;
+            const float ctop = !there ? -INFINITY : i == c ? mine.top : __ldcg(&st[i].top);
+            const int cexp = !there ? 0 : i == c ? mine.exponent : __ldcg(&st[i].exponent);
+            const long long csum = !there ? 0 : i == c ? mine.sum : __ldcg(&st[i].sum);
+            int k;
+            const bool live = to_row(ctop, cexp, ref, cut, r.exponent, s, entry, th, rest, k);
+            const long long g = live ? rescale(csum, th, rest, k) : 0;
+            if (there) {
+                __stcg(p.in_row + row * p.chunks + i, g);
+                sh.in_row[i] = g;
+                sum += g;
             }
         }
+        r.total = warp_sum(sum);
         if (j < len) {
-            const long long d = static_cast<long long>(b) * p.L + j;
-            const double q = p.q == nullptr ? 1.0 : inside ? static_cast<double>(p.q[d * p.ldq + t]) : 0.0;
-            r.prob = static_cast<float>(wt / total);
-            r.verdict = inside && static_cast<double>(p.accept_u[d]) * q * total < wt ? 1 : 0;
+            float hi, lo;
+            weight(inside ? xt : -INFINITY, top, ref, cut, r.exponent, s, entry, hi, lo);
+            const Pair w = {hi * kRowUnits, lo * kRowUnits}, total = pair_of(r.total);
+            const float uq = ut * qt;
+            r.verdict = inside && less({uq, fmaf(ut, qt, -uq)}, total, w) ? 1 : 0;
+            r.prob = divide(fast_two_sum(w.hi, w.lo), total).hi;
         }
     }
     if (lane == 0) {
         p.row[row] = r;
+        sh.row = r;
         if (r.verdict != 1)
             atomicMax(p.stopped + b, static_cast<unsigned>(64 - j));
     }
 }
 
-template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(const VerifyParams p)
-{
-    using R = Row<kBf16>;
-    __shared__ float wtop[kVerifyThreads / 32];
-    __shared__ long long wsum[kVerifyThreads / 32];
-    __shared__ int skip, finish;
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        atomicAdd(p.runs + FP8BS_RUNS_VERIFY_STATS, 1ull);
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = static_cast<int>(blockIdx.x % p.chunks);
-    const int rank = static_cast<int>(blockIdx.x / p.chunks);
-    const int j = rank / p.B, b = rank % p.B;
-    const int len = drafted(p, b);
-    if (j > len)
-        return;
-    if (threadIdx.x == 0)
-        skip = behind_a_stop(p, b, j) ? 1 : 0;
-    __syncthreads();
-    const long long row = static_cast<long long>(b) * (p.L + 1) + j;
-    const R x(p, row);
-    if (skip == 0) {
-        const int w0 = c * (kChunk / R::kPer) + static_cast<int>(threadIdx.x);
-        uint4 raw[R::kWords];
-#pragma unroll
-        for (int s = 0; s < R::kWords; ++s)
-            raw[s] = x.load(w0 + s * kVerifyThreads);
-        const float T = temperature(p, b);
-        const float2 entry = kPow32[lane];
-        float top = -INFINITY;
-#pragma unroll
-        for (int s = 0; s < R::kWords; ++s)
-#pragma unroll
-            for (int e = 0; e < R::kPer; ++e)
-                top = max_nan(top, R::value(raw[s], e));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0)
-            wtop[warp] = top;
-        __syncthreads();
-        top = wtop[0];
-#pragma unroll
-        for (int i = 1; i < kVerifyThreads / 32; ++i)
-            top = max_nan(top, wtop[i]);
-        ChunkStat out = {top, 0, 0};
-        long long sum = 0;
-        if (top > -INFINITY && top < INFINITY && good_temperature(T)) {
-            if (T == 0.0f) {
-                sum = 0x7fffffff;
-#pragma unroll
-                for (int s = R::kWords - 1; s >= 0; --s)
-#pragma unroll
-                    for (int e = R::kPer - 1; e >= 0; --e)
-                        if (R::value(raw[s], e) == top)
-                            sum = x.index(w0 + s * kVerifyThreads) + e;
-                sum = __reduce_min_sync(0xffffffffu, static_cast<int>(sum));
-            } else {
-                const Scale sc = make_scale(T);
-                const float ref = reference(top, T), cut = cutoff(top, T);
-                float zh, zl, th, rest;
-                exponent_of(top, ref, sc, zh, zl);
-                out.exponent = pow_split(zh, zl, entry, th, rest);
-                // Weights below 2, at most 32 of them: `high` holds their multiples of 2^-16 exactly,
-                // `low` what is left.
-                float high = 0.0f, low = 0.0f;
-#pragma unroll
-                for (int s = 0; s < R::kWords; ++s)
-#pragma unroll
-                    for (int e = 0; e < R::kPer; ++e) {
-                        float hi, lo;
-                        weight(R::value(raw[s], e), top, ref, cut, out.exponent, sc, entry, hi, lo);
-                        const float q = (hi + 192.0f) - 192.0f;
-                        high += q;
-                        low += hi - q;
-                        low += lo;
-                    }
-                sum = warp_sum(fixed(high, low, kChunkUnits));
-            }
-        }
-        if (lane == 0)
-            wsum[warp] = sum;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            out.sum = wsum[0];
-            for (int i = 1; i < kVerifyThreads / 32; ++i)
-                out.sum = T == 0.0f ? min(out.sum, wsum[i]) : out.sum + wsum[i];
-            ChunkStat *const to = p.chunk + row * p.chunks + c;
-            __stcg(&to->top, out.top);
-            __stcg(&to->exponent, out.exponent);
-            __stcg(&to->sum, out.sum);
-        }
-    }
-    if (threadIdx.x == 0) {
-        const unsigned before = atomic_add_acq_rel_gpu(p.row_done + row, 1u);
-        finish = 0;
-        if (before == static_cast<unsigned>(p.chunks - 1)) {
-            p.row_done[row] = 0u;
-            finish = behind_a_stop(p, b, j) ? 0 : 1; // where a chunk was left out, this sees why
-        }
-    }
-    __syncthreads();
-    if (finish != 0 && warp == 0) {
-        __threadfence();
-        finish_row<kBf16>(p, b, j, len, x);
-    }
-}
-
-// What a drawn token's weight is.
-enum VerifyMode { kFromTarget, kWithoutDraft, kResidual };
-
-template <bool kBf16> struct Picker {
-    const VerifyParams &p;
-    Row<kBf16> x;
-    Scale s;
-    float top, ref, cut;
-    int exponent;
-    float2 entry;
-    VerifyMode mode;
-    int except;     // kWithoutDraft
-    const float *q; // kResidual
-    float Wh, Wl;   // the row's total, relative to 2^exponent
-
-    // Weight in row units of logit i with value v (whole warps call it).
-    __device__ __forceinline__ long long units(float v, int i)
-    {
-        float hi, lo;
-        weight(v, top, ref, cut, exponent, s, entry, hi, lo);
-        if (mode == kResidual) {
-            const float qi = i >= 0 && i < p.V ? q[i] : 0.0f;
-            const float ph = qi * Wh;
-            const float pl = fmaf(qi, Wl, fmaf(qi, Wh, -ph));
-            const float d = hi - ph, bb = d - hi;
-            const float e = (hi - (d - bb)) + (-ph - bb);
-            lo = (lo - pl) + e;
-            hi = d;
-            if (!(hi + lo > 0.0f))
-                hi = lo = 0.0f;
-        } else if (mode == kWithoutDraft && i == except) {
-            hi = lo = 0.0f;
-        }
-        return fixed(hi, lo, kRowUnits);
-    }
-};
-
-// The first logit of chunk c whose cumulative weight passes `target`; the last
-// one with a weight where rounding leaves none, -1 where none has any.  All
-// threads call it and get the answer.
-template <bool kBf16>
-__device__ __forceinline__ int look(Picker<kBf16> &k, int c, long long target, long long *wsum, int *found)
-{
-    using R = Row<kBf16>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int w0 = c * (kChunk / R::kPer) + static_cast<int>(threadIdx.x) * R::kWords;
-    if (threadIdx.x < 2)
-        found[threadIdx.x] = threadIdx.x == 0 ? 0x7fffffff : -1;
-    long long mine = 0;
-    int last = -1;
-#pragma unroll 1
-    for (int s = 0; s < R::kWords; ++s) {
-        const uint4 w = k.x.load(w0 + s);
-#pragma unroll
-        for (int e = 0; e < R::kPer; ++e) {
-            const int i = k.x.index(w0 + s) + e;
-            const long long g = k.units(R::value(w, e), i);
-            mine += g;
-            if (g > 0)
-                last = i;
-        }
-    }
-    long long upto = mine; // inclusive over the warp
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o)
-            upto += v;
-    }
-    __syncthreads(); // wsum and found are free, and found is set
-    if (lane == 31)
-        wsum[warp] = upto;
-    if (last >= 0)
-        atomicMax(found + 1, last);
-    __syncthreads();
-    for (int i = 0; i < warp; ++i)
-        upto += wsum[i];
-    const bool here = upto - mine <= target && target < upto;
-    if (__any_sync(0xffffffffu, here)) {
-        long long at = upto - mine;
-        bool done = !here;
-#pragma unroll 1
-        for (int s = 0; s < R::kWords; ++s) {
-            const uint4 w = k.x.load(w0 + s);
-#pragma unroll
-            for (int e = 0; e < R::kPer; ++e) {
-                const int i = k.x.index(w0 + s) + e;
-                at += k.units(R::value(w, e), i);
-                if (!done && at > target) {
-                    found[0] = i;
-                    done = true;
-                }
-            }
-        }
-    }
-    __syncthreads();
-    const int at = found[0] != 0x7fffffff ? found[0] : found[1];
-    __syncthreads();
-    return at;
-}
-
-// Chunk of the target weight sample_u * (sum of `sum(c)`) and what lies before it;
-// one warp.  Returns -1 where the sum is not positive.
+// Position of the target weight u * (sum of `sum(i)`, i < n) and what is left of it
+// there; one warp.  Returns -1 where the sum is not positive.
 template <class Sum>
-__device__ __forceinline__ int target_chunk(int chunks, float u, Sum sum, long long &target)
+__device__ __forceinline__ int find_target(int n, float u, Sum sum, long long &target)
 {
     const int lane = threadIdx.x & 31;
     long long total = 0;
-    for (int c = lane; c < chunks; c += 32)
-        total += sum(c);
+    for (int i = lane; i < n; i += 32)
+        total += sum(i);
     total = warp_sum(total);
     if (total <= 0)
         return -1;
     target = __double2ll_rz(static_cast<double>(u) * static_cast<double>(total));
     target = target < 0 ? 0 : target >= total ? total - 1 : target;
     long long before = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 32) {
-        const long long g = c0 + lane < chunks ? sum(c0 + lane) : 0;
-        long long upto = g;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o)
-                upto += v;
-        }
-        upto += before;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const long long g = i0 + lane < n ? sum(i0 + lane) : 0;
+        const long long upto = warp_scan(g) + before;
         const unsigned past = __ballot_sync(0xffffffffu, upto > target);
         if (past != 0u) {
             const int l = __ffs(static_cast<int>(past)) - 1;
             target -= __shfl_sync(0xffffffffu, upto - g, l);
-            return c0 + l;
+            return i0 + l;
         }
         before = __shfl_sync(0xffffffffu, upto, 31);
     }
     return -1;
 }
 
-template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_choose_kernel(const VerifyParams p)
+// A row's weights in row units.
+template <bool kBf16> struct Weights {
+    Row<kBf16> x;
+    Scale s;
+    float top, ref, cut;
+    int exponent;
+    float2 entry;
+
+    __device__ __forceinline__ Weights(const VerifyParams &p, long long row, const RowStat &r, float T)
+        : x(p, row), s(make_scale(T)), top(r.top), ref(reference(r.top, s)), cut(cutoff(r.top, T)), exponent(r.exponent),
+          entry(kPow32[threadIdx.x & 31])
+    {
+    }
+    __device__ __forceinline__ void pair(float v, float &hi, float &lo) const // whole warps
+    {
+        weight(v, top, ref, cut, exponent, s, entry, hi, lo);
+    }
+    __device__ __forceinline__ float probability(int i, long long total) const // one warp
+    {
+        float hi, lo;
+        pair(x.at(i), hi, lo);
+        return divide(fast_two_sum(hi * kRowUnits, lo * kRowUnits), pair_of(total)).hi;
+    }
+};
+
+// The first of a thread block's weights g (kN a thread, in order, of the logits
+// from i0 on) whose cumulative sum passes `target`; the last one with a weight where
+// rounding leaves none, -1 where none has any.  All threads call it; `found` and
+// `end` are the answer's places.
+template <int kN>
+__device__ __forceinline__ int look(const long long (&g)[kN], int i0, long long target, long long *scan, int &found, int &end)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        found = 0x7fffffff;
+        end = -1;
+    }
+    long long mine = 0;
+    int last = -1;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+        mine += g[e];
+        if (g[e] > 0)
+            last = i0 + e;
+    }
+    long long upto = warp_scan(mine);
+    if (lane == 31)
+        scan[warp] = upto;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i)
+        upto += scan[i];
+    if (upto - mine <= target && target < upto) {
+        long long at = upto - mine;
+#pragma unroll
+        for (int e = kN - 1; e >= 0; --e) { // from behind: the first that passes is written last
+            long long before = at;
+#pragma unroll
+            for (int i = 0; i < e; ++i)
+                before += g[i];
+            if (before + g[e] > target)
+                found = i0 + e;
+        }
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0 && last >= 0)
+        atomicMax(&end, last);
+    __syncthreads();
+    return found != 0x7fffffff ? found : end;
+}
+
+// Draws the token of row `r` (of sequence b, at r.position) from its own weights,
+// without that of logit `except` where it is in the row.  The whole CTA calls it;
+// `own`: the chunk sums lie in sh.in_row, and chunk own_chunk's in sh.part.
+template <bool kBf16>
+__device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat &r, float T, int except, bool own,
+                                     int own_chunk, RowShared &sh)
 {
     using R = Row<kBf16>;
-    __shared__ long long wsum[kVerifyThreads / 32];
-    __shared__ long long starget;
-    __shared__ int found[2], schunk, sn, last_one, swhole;
-    __shared__ RowStat sr;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(b) * (p.L + 1) + r.position;
+    const Weights<kBf16> w(p, row, r, T);
+    if (warp == 0) {
+        const float u = p.sample_u[b];
+        const long long *const in_row = p.in_row + row * p.chunks;
+        const bool with = except >= 0 && except < p.V;
+        float hi = 0.0f, lo = 0.0f;
+        w.pair(with ? w.x.at(except) : -INFINITY, hi, lo);
+        const long long less_by = fixed(hi, lo, kRowUnits);
+        const int home = with ? (except + w.x.lead) / kChunk : -1;
+        auto sum = [&](int i) { return own ? sh.in_row[i] : __ldcg(in_row + i); };
+        long long target = 0;
+        int c = -1;
+        if (with)
+            c = find_target(p.chunks, u, [&](int i) {
+                const long long g = sum(i);
+                return i != home ? g : g > less_by ? g - less_by : 0;
+            }, target);
+        const bool all = c < 0; // nothing is left beside it: from everything
+        if (all)
+            c = find_target(p.chunks, u, sum, target);
+        c = c < 0 ? 0 : c; // (a row's total is positive)
+        // the part of the chunk: its warps' sums in row units
+        const ChunkStat *const st = p.chunk + row * p.chunks + c;
+        float th, rest;
+        int k;
+        const bool live = to_row(__ldcg(&st->top), __ldcg(&st->exponent), w.ref, w.cut, w.exponent, w.s, w.entry, th, rest, k);
+        long long g = 0;
+        if (lane < kVerifyWarps && live)
+            g = rescale(own && c == own_chunk ? sh.part[lane] : __ldcg(p.part + (row * p.chunks + c) * kVerifyWarps + lane), th,
+                        rest, k);
+        if (!all && c == home && lane == (except + w.x.lead) % kChunk / kPart)
+            g = g > less_by ? g - less_by : 0;
+        const long long upto = warp_scan(g);
+        const unsigned past = __ballot_sync(0xffffffffu, upto > target), some = __ballot_sync(0xffffffffu, g > 0);
+        const int l = past != 0u ? __ffs(static_cast<int>(past)) - 1 : some != 0u ? 31 - __clz(some) : 0;
+        target -= __shfl_sync(0xffffffffu, upto - g, l); // past the last part: found by its end
+        if (lane == 0) {
+            sh.chunk = c;
+            sh.part_of = l;
+            sh.target = target;
+            sh.without = all ? -1 : except;
+        }
+    }
+    __syncthreads();
+    // kPart logits: a word a thread, as far as they go
+    constexpr int kWords = kPart / R::kPer;
+    static_assert(kWords <= kVerifyThreads, "a word a thread");
+    const int word = sh.chunk * (kChunk / R::kPer) + sh.part_of * kWords + static_cast<int>(threadIdx.x);
+    const int i0 = w.x.index(word);
+    const long long target = sh.target;
+    const int without = sh.without;
+    long long g[R::kPer];
+    if (warp * 32 < kWords) {
+        const uint4 v = w.x.load(word);
+#pragma unroll
+        for (int e = 0; e < R::kPer; ++e) {
+            float hi, lo;
+            w.pair(R::value(v, e), hi, lo);
+            g[e] = i0 + e == without ? 0 : fixed(hi, lo, kRowUnits);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < R::kPer; ++e)
+            g[e] = 0;
+    }
+    const int token = look(g, i0, target, sh.scan, sh.found, sh.end);
+    if (warp == 0) {
+        const float prob = token >= 0 ? w.probability(token, r.total) : NAN;
+        if (lane == 0) {
+            p.tokens[row] = token;
+            p.probs[row] = prob;
+        }
+    }
+}
+
+// A CTA per (position, sequence, chunk), in that order.
+template <bool kBf16>
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kernel(const VerifyParams p)
+{
+    using R = Row<kBf16>;
+    __shared__ RowShared sh;
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        atomicAdd(p.runs + FP8BS_RUNS_VERIFY_CHOOSE, 1ull);
+        atomicAdd(p.runs + FP8BS_RUNS_VERIFY_ROWS, 1ull);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float2 entry = kPow32[lane];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = static_cast<int>(blockIdx.x % p.chunks), b = static_cast<int>(blockIdx.x / p.chunks);
+    const int c = static_cast<int>(blockIdx.x % p.chunks);
+    const int rank = static_cast<int>(blockIdx.x / p.chunks);
+    const int j = rank / p.B, b = rank % p.B;
     const int len = drafted(p, b);
+    if (j > len)
+        return;
+    bool skip = false;
+    if (blockIdx.x >= p.first_wave && j > 0) {
+        if (threadIdx.x == 0)
+            sh.skip = behind_a_stop(p, b, j) ? 1 : 0;
+        __syncthreads();
+        skip = sh.skip != 0;
+    }
+    const long long row = static_cast<long long>(b) * (p.L + 1) + j;
+    const R x(p, row);
+    const float T = temperature(p, b);
+    ChunkStat out = {NAN, 0, 0};
+    if (!skip) {
+        const int w0 = c * (kChunk / R::kPer) + warp * (kPart / R::kPer) + lane;
+        uint4 raw[R::kWords];
+#pragma unroll
+        for (int s = 0; s < R::kWords; ++s)
+            raw[s] = x.load(w0 + s * 32);
+        float top = R::largest(raw[0]);
+#pragma unroll
+        for (int s = 1; s < R::kWords; ++s)
+            top = max_nan(top, R::largest(raw[s]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0)
+            sh.top[warp] = top;
+        __syncthreads();
+        top = sh.top[0];
+#pragma unroll
+        for (int i = 1; i < kVerifyWarps; ++i)
+            top = max_nan(top, sh.top[i]);
+        out.top = top;
+        long long sum = 0;
+        if (top > -INFINITY && top < INFINITY && good_temperature(T)) {
+            if (T == 0.0f) {
+                int first = 0x7fffffff;
+#pragma unroll
+                for (int s = R::kWords - 1; s >= 0; --s)
+#pragma unroll
+                    for (int e = R::kPer - 1; e >= 0; --e)
+                        if (R::value(raw[s], e) == top)
+                            first = x.index(w0 + s * 32) + e;
+                sum = __reduce_min_sync(0xffffffffu, first);
+            } else {
+                const Scale sc = make_scale(T);
+                const float ref = reference(top, sc), cut = cutoff(top, T);
+                float zh, zl, th, rest;
+                exponent_of(top, ref, sc, zh, zl);
+                out.exponent = pow_split(zh, zl, entry, th, rest);
+                WeightSum sums(cut, out.exponent, sc, entry);
+                if (ref == 0.0f) {
+#pragma unroll
+                    for (int s = 0; s < R::kWords; ++s)
+#pragma unroll
+                        for (int e = 0; e < R::kPer; e += 2)
+                            sums.add(R::value(raw[s], e), R::value(raw[s], e + 1));
+                } else {
+                    float high = 0.0f, low = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < R::kWords; ++s)
+#pragma unroll 1
+                        for (int e = 0; e < R::kPer; ++e) {
+                            const uint32_t a = (kBf16 ? e >> 1 : e) == 0 ? raw[s].x : (kBf16 ? e >> 1 : e) == 1 ? raw[s].y
+                                               : (kBf16 ? e >> 1 : e) == 2 ? raw[s].z : raw[s].w;
+                            const float v = __uint_as_float(!kBf16 ? a : (e & 1) ? a & 0xFFFF0000u : a << 16);
+                            float hi, lo;
+                            weight(v, top, ref, cut, out.exponent, sc, entry, hi, lo);
+                            const float q = (hi + 192.0f) - 192.0f;
+                            high += q;
+                            low += hi - q;
+                            low += lo;
+                        }
+                    sums.high = pack(high, 0.0f);
+                    sums.low = pack(low, 0.0f);
+                }
+                sum = warp_sum(sums.units(kChunkUnits));
+            }
+        }
+        if (lane == 0) {
+            sh.part[warp] = sum;
+            __stcg(p.part + (row * p.chunks + c) * kVerifyWarps + warp, sum);
+        }
+    }
+    __syncthreads();
+    if (!skip) {
+        out.sum = sh.part[0];
+#pragma unroll
+        for (int i = 1; i < kVerifyWarps; ++i)
+            out.sum = T == 0.0f ? min(out.sum, sh.part[i]) : out.sum + sh.part[i];
+    }
+    if (threadIdx.x == 0) {
+        sh.last_chunk = 1;
+        if (p.chunks > 1) {
+            if (!skip) {
+                ChunkStat *const to = p.chunk + row * p.chunks + c;
+                __stcg(&to->top, out.top);
+                __stcg(&to->exponent, out.exponent);
+                __stcg(&to->sum, out.sum);
+            }
+            sh.last_chunk = atomic_add_acq_rel_gpu(p.row_done + row, 1u) == static_cast<unsigned>(p.chunks - 1);
+            if (sh.last_chunk != 0)
+                p.row_done[row] = 0u;
+        } else if (!skip) {
+            ChunkStat *const to = p.chunk + row;
+            __stcg(&to->top, out.top);
+            __stcg(&to->exponent, out.exponent);
+        }
+        // where a chunk was left out, this sees why
+        sh.skip = sh.last_chunk != 0 && j > 0 && behind_a_stop(p, b, j) ? 1 : 0;
+    }
+    __syncthreads();
+    if (sh.last_chunk == 0)
+        return;
+    __threadfence();
+    const bool finish = sh.skip == 0;
+    if (warp == 0) {
+        if (finish)
+            finish_row<kBf16>(p, b, j, len, x, c, out, sh);
+        __syncwarp();
+        if (lane == 0) {
+            sh.last_row = 1;
+            if (len > 0) {
+                sh.last_row = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(len);
+                if (sh.last_row != 0)
+                    p.seq_done[b] = 0u;
+            }
+        }
+    }
+    __syncthreads();
+    if (sh.last_row == 0)
+        return;
+    // the sequence's last row: where it stops, and its token
+    __threadfence();
     const long long row0 = static_cast<long long>(b) * (p.L + 1);
     if (warp == 0) {
         // the first position that was not accepted (position len never is); rows behind it may be old
-        const int v = lane <= len ? __ldcg(&p.row[row0 + lane].verdict) : 0;
+        const int v = lane > len ? 0 : finish && lane == j ? sh.row.verdict : __ldcg(&p.row[row0 + lane].verdict);
         const int n = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, v != 1))) - 1;
-        if (c == 0) {
-            if (lane < n) {
-                p.tokens[row0 + lane] = p.draft[static_cast<long long>(b) * p.L + lane];
-                p.probs[row0 + lane] = __ldcg(&p.row[row0 + lane].prob);
-            } else if (lane > n && lane <= p.L) {
-                p.tokens[row0 + lane] = -1;
-                p.probs[row0 + lane] = 0.0f;
-            }
-            if (lane == 0) {
-                p.accepted[b] = n;
-                p.stopped[b] = 0u;
-            }
+        if (lane < n) {
+            p.tokens[row0 + lane] = p.draft[static_cast<long long>(b) * p.L + lane];
+            p.probs[row0 + lane] = finish && lane == j ? sh.row.prob : __ldcg(&p.row[row0 + lane].prob);
+        } else if (lane > n && lane <= p.L) {
+            p.tokens[row0 + lane] = -1;
+            p.probs[row0 + lane] = 0.0f;
         }
+        __syncwarp();
         if (lane == 0) {
-            sn = n;
-            sr = p.row[row0 + n];
+            p.accepted[b] = n;
+            p.stopped[b] = 0u;
+            if (!(finish && n == j)) {
+                const uint4 *const from = reinterpret_cast<const uint4 *>(p.row + row0 + n);
+                uint4 *const to = reinterpret_cast<uint4 *>(&sh.row);
+                to[0] = __ldcg(from);
+                to[1] = __ldcg(from + 1);
+            }
+            const bool done = sh.row.verdict == 2 || T == 0.0f; // no distribution, or no choice
+            const bool later = !done && p.q != nullptr && n < len;
+            if (done) {
+                p.tokens[row0 + n] = sh.row.verdict == 2 ? -1 : sh.row.best;
+                p.probs[row0 + n] = sh.row.verdict == 2 ? NAN : 1.0f;
+            }
+            if (p.q != nullptr) {
+                RowStat s = sh.row;
+                s.position = later ? n : -1;
+                p.stop[b] = s;
+            }
+            sh.draw_now = !done && !later;
         }
     }
     __syncthreads();
-    const int n = sn;
+    if (sh.draw_now == 0)
+        return;
+    const RowStat r = sh.row;
+    const int except = r.position < len ? p.draft[static_cast<long long>(b) * p.L + r.position] : -1;
+    draw<kBf16>(p, b, r, T, except, finish && r.position == j, c, sh);
+}
+
+// A CTA per (sequence, slice of kSlice logits): the weights max(p - q, 0) where a
+// draft was rejected.
+template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_residual_kernel(const VerifyParams p)
+{
+    using R = Row<kBf16>;
+    constexpr int kN = kSlice / kVerifyThreads; // logits of a thread, one after the other
+    __shared__ RowShared sh;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        atomicAdd(p.runs + FP8BS_RUNS_VERIFY_RESIDUAL, 1ull);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = static_cast<int>(blockIdx.x / p.slices), c = static_cast<int>(blockIdx.x % p.slices);
+    const uint4 *const from = reinterpret_cast<const uint4 *>(p.stop + b);
+    RowStat r;
+    reinterpret_cast<uint4 *>(&r)[0] = __ldcg(from);
+    reinterpret_cast<uint4 *>(&r)[1] = __ldcg(from + 1);
+    if (r.position < 0)
+        return;
     const float T = temperature(p, b);
-    if (sr.verdict == 2 || T == 0.0f) {
-        if (c == 0 && threadIdx.x == 0) {
-            p.tokens[row0 + n] = sr.verdict == 2 ? -1 : sr.best;
-            p.probs[row0 + n] = sr.verdict == 2 ? NAN : 1.0f;
-        }
-        return;
-    }
-    const ChunkStat *const st = p.chunk + (row0 + n) * p.chunks;
-    const float u = p.sample_u[b];
-    Picker<kBf16> k = {p, R(p, row0 + n), make_scale(T), sr.top, reference(sr.top, T), cutoff(sr.top, T), sr.exponent,
-                       kPow32[lane], kFromTarget, -1, nullptr, 0.0f, 0.0f};
-    if (n < len) {
-        const int t = p.draft[static_cast<long long>(b) * p.L + n];
-        if (p.q != nullptr) {
-            k.mode = kResidual;
-            k.q = p.q + (static_cast<long long>(b) * p.L + n) * p.ldq;
-            const double W = static_cast<double>(sr.total) * (1.0 / static_cast<double>(kRowUnits));
-            k.Wh = static_cast<float>(W);
-            k.Wl = static_cast<float>(W - static_cast<double>(k.Wh));
-        } else if (t >= 0 && t < p.V) {
-            k.mode = kWithoutDraft;
-            k.except = t;
-        }
-    }
-    bool mine = false; // this CTA looks for the token
-    if (k.mode == kResidual) {
-        const int w0 = c * (kChunk / R::kPer) + static_cast<int>(threadIdx.x);
-        long long sum = 0;
-#pragma unroll 1
-        for (int s = 0; s < R::kWords; ++s) {
-            const uint4 w = k.x.load(w0 + s * kVerifyThreads);
+    const Weights<kBf16> w(p, static_cast<long long>(b) * (p.L + 1) + r.position, r, T);
+    const float *const q = p.q + (static_cast<long long>(b) * p.L + r.position) * p.ldq;
+    Pair W = pair_of(r.total);
+    W.hi *= 1.0f / kRowUnits;
+    W.lo *= 1.0f / kRowUnits;
+    // this thread's weights in slice i
+    auto weights = [&](int i, long long(&g)[kN]) {
+        const int word = (i * kSlice + static_cast<int>(threadIdx.x) * kN) / R::kPer;
+        const int i0 = w.x.index(word);
+        uint4 v[kN / R::kPer];
+        float qi[kN];
 #pragma unroll
-            for (int e = 0; e < R::kPer; ++e)
-                sum += k.units(R::value(w, e), k.x.index(w0 + s * kVerifyThreads) + e);
+        for (int s = 0; s < kN / R::kPer; ++s)
+            v[s] = w.x.load(word + s);
+        if (i0 >= 0 && i0 + kN <= p.V && (reinterpret_cast<uintptr_t>(q + i0) & 15) == 0) {
+#pragma unroll
+            for (int e = 0; e < kN; e += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(q + i0 + e);
+                qi[e] = f.x;
+                qi[e + 1] = f.y;
+                qi[e + 2] = f.z;
+                qi[e + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e)
+                qi[e] = i0 + e >= 0 && i0 + e < p.V ? q[i0 + e] : 0.0f;
         }
-        sum = warp_sum(sum);
-        if (lane == 0)
-            wsum[warp] = sum;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int i = 1; i < kVerifyThreads / 32; ++i)
-                sum += wsum[i];
-            __stcg(p.residual + static_cast<long long>(b) * p.chunks + c, sum);
-            const unsigned before = atomic_add_acq_rel_gpu(p.seq_done + b, 1u);
-            last_one = before == static_cast<unsigned>(p.chunks - 1);
-            if (last_one)
-                p.seq_done[b] = 0u;
-        }
-        __syncthreads();
-        if (!last_one)
-            return;
-        __threadfence();
-        mine = true;
-    }
-    if (warp == 0) {
-        long long target = 0;
-        int at = -1;
-        if (k.mode == kResidual)
-            at = target_chunk(p.chunks, u, [&](int i) { return __ldcg(p.residual + static_cast<long long>(b) * p.chunks + i); },
-                              target);
-        else if (k.mode == kWithoutDraft) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
             float hi, lo;
-            weight(k.x.at(k.except), k.top, k.ref, k.cut, k.exponent, k.s, k.entry, hi, lo);
-            const long long w = fixed(hi, lo, kRowUnits);
-            const int home = (k.except + k.x.lead) / kChunk;
-            at = target_chunk(p.chunks, u, [&](int i) {
-                const long long g = __ldcg(&st[i].sum);
-                return i != home ? g : g > w ? g - w : 0;
-            }, target);
+            w.pair(R::value(v[e / R::kPer], e % R::kPer), hi, lo);
+            // hi + lo - q W as a pair; 0 where that is not positive, or q is NaN
+            const float ph = qi[e] * W.hi;
+            const float pl = fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -ph));
+            const float d = hi - ph, bb = d - hi;
+            lo = (lo - pl) + ((hi - (d - bb)) + (-ph - bb));
+            g[e] = d + lo > 0.0f ? fixed(d, lo, kRowUnits) : 0;
         }
-        const bool whole = at < 0; // nothing left beside the draft: the target's own distribution
-        if (whole)
-            at = target_chunk(p.chunks, u, [&](int i) { return __ldcg(&st[i].sum); }, target);
+        return i0;
+    };
+    long long g[kN];
+    weights(c, g);
+    long long sum = 0;
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+        sum += g[e];
+    sum = warp_sum(sum);
+    if (lane == 0)
+        sh.part[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kVerifyWarps; ++i)
+            sum += sh.part[i];
+        __stcg(p.residual + static_cast<long long>(b) * p.slices + c, sum);
+        sh.last_chunk = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(p.slices - 1);
+        if (sh.last_chunk != 0)
+            p.seq_done[b] = 0u;
+    }
+    __syncthreads();
+    if (sh.last_chunk == 0)
+        return;
+    __threadfence();
+    if (warp == 0) {
+        const long long *const sums = p.residual + static_cast<long long>(b) * p.slices;
+        long long target = 0;
+        const int at = find_target(p.slices, p.sample_u[b], [&](int i) { return __ldcg(sums + i); }, target);
         if (lane == 0) {
-            schunk = at;
-            starget = target;
-            swhole = whole;
+            sh.chunk = at;
+            sh.target = target;
         }
     }
     __syncthreads();
-    if (swhole)
-        k.mode = kFromTarget;
-    if (!mine && schunk != c)
+    if (sh.chunk < 0) { // p nowhere above q: from p
+        draw<kBf16>(p, b, r, T, -1, false, -1, sh);
         return;
-    const int token = look<kBf16>(k, schunk, starget, wsum, found);
+    }
+    const long long target = sh.target;
+    const int i0 = weights(sh.chunk, g);
+    const int token = look(g, i0, target, sh.scan, sh.found, sh.end);
     if (warp == 0) {
-        float hi, lo;
-        weight(token >= 0 ? k.x.at(token) : k.top, k.top, k.ref, k.cut, k.exponent, k.s, k.entry, hi, lo);
+        const float prob = token >= 0 ? w.probability(token, r.total) : NAN;
         if (lane == 0) {
-            p.tokens[row0 + n] = token;
-            p.probs[row0 + n] = token < 0 ? NAN
-                                          : static_cast<float>((static_cast<double>(hi) + static_cast<double>(lo)) *
-                                                               static_cast<double>(kRowUnits) / static_cast<double>(sr.total));
+            const long long to = static_cast<long long>(b) * (p.L + 1) + r.position;
+            p.tokens[to] = token;
+            p.probs[to] = prob;
         }
     }
 }
@@ -693,8 +977,8 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct VerifyWorkspace {
-    size_t counters_bytes, chunk_off, row_off, residual_off, total;
-    int chunks;
+    size_t counters_bytes, chunk_off, part_off, in_row_off, row_off, stop_off, residual_off, total;
+    int chunks, slices;
 };
 
 VerifyWorkspace verify_workspace(int B, int L, int V)
@@ -703,14 +987,19 @@ VerifyWorkspace verify_workspace(int B, int L, int V)
     const size_t rows = static_cast<size_t>(B) * (L + 1);
     VerifyWorkspace w;
     w.chunks = (V + 7 + kChunk - 1) / kChunk; // a row may start up to seven logits into its first word
+    w.slices = (V + 7 + kSlice - 1) / kSlice;
     w.counters_bytes = (rows + 2 * static_cast<size_t>(B)) * 4;
     w.chunk_off = kCountersOff + counters_region(w.counters_bytes);
-    w.row_off = w.chunk_off + up256(rows * w.chunks * sizeof(ChunkStat));
-    w.residual_off = w.row_off + up256(rows * sizeof(RowStat));
-    w.total = w.residual_off + up256(static_cast<size_t>(B) * w.chunks * 8);
+    w.part_off = w.chunk_off + up256(rows * w.chunks * sizeof(ChunkStat));
+    w.in_row_off = w.part_off + up256(rows * w.chunks * kVerifyWarps * 8);
+    w.row_off = w.in_row_off + up256(rows * w.chunks * 8);
+    w.stop_off = w.row_off + up256(rows * sizeof(RowStat));
+    w.residual_off = w.stop_off + up256(static_cast<size_t>(B) * sizeof(RowStat));
+    w.total = w.residual_off + up256(static_cast<size_t>(B) * w.slices * 8);
     return w;
 }
 static_assert((kVerifyMaxRows + 2 * kVerifyMaxRows) * 4 <= kCountersRegion, "every size's counters lie in the shared region");
+static_assert(kMaxChunks * kChunk >= kVerifyMaxVocab + 7, "chunks of a row");
 static_assert(sizeof(ChunkStat) == 16 && sizeof(RowStat) == 32, "workspace layout");
 
 fp8bs_status check_verify(int B, int L, int V)
@@ -774,6 +1063,8 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.L = L;
     p.V = V;
     p.chunks = w.chunks;
+    p.slices = w.slices;
+    p.first_wave = static_cast<unsigned>(dev.sms * kVerifyCtas);
     p.logits = static_cast<const uint8_t *>(logits);
     p.ldl = ldl;
     p.draft = draft;
@@ -790,7 +1081,10 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.stopped = p.row_done + static_cast<size_t>(B) * (L + 1);
     p.seq_done = p.stopped + B;
     p.chunk = reinterpret_cast<ChunkStat *>(ws + w.chunk_off);
+    p.part = reinterpret_cast<long long *>(ws + w.part_off);
+    p.in_row = reinterpret_cast<long long *>(ws + w.in_row_off);
     p.row = reinterpret_cast<RowStat *>(ws + w.row_off);
+    p.stop = reinterpret_cast<RowStat *>(ws + w.stop_off);
     p.residual = reinterpret_cast<long long *>(ws + w.residual_off);
     p.runs = dev.runs;
     cudaLaunchAttribute attr[1];
@@ -803,12 +1097,12 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     cfg.attrs = attr;
     cfg.numAttrs = (flags & FP8BS_FLAG_OVERLAP_PREV) ? 1 : 0;
     const bool bf = logits_type == FP8BS_BF16;
-    st = launch_status(cudaLaunchKernelEx(&cfg, bf ? verify_stats_kernel<true> : verify_stats_kernel<false>, p));
-    if (st != FP8BS_OK)
+    st = launch_status(cudaLaunchKernelEx(&cfg, bf ? verify_rows_kernel<true> : verify_rows_kernel<false>, p));
+    if (st != FP8BS_OK || !draft_probs)
         return st;
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(B) * w.chunks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(B) * w.slices), 1, 1);
     cfg.numAttrs = 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, bf ? verify_choose_kernel<true> : verify_choose_kernel<false>, p));
+    return launch_status(cudaLaunchKernelEx(&cfg, bf ? verify_residual_kernel<true> : verify_residual_kernel<false>, p));
 }
 
 } // extern "C"

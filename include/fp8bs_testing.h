@@ -45,9 +45,9 @@ extern "C" {
 /* RMS norm with the 8-bit cast (fp32 block scales, MX). */
 #define FP8BS_RUNS_NORM_FP8 96
 #define FP8BS_RUNS_NORM_MX 97
-/* Verification of drafted tokens: the rows' statistics, the choice. */
-#define FP8BS_RUNS_VERIFY_STATS 98
-#define FP8BS_RUNS_VERIFY_CHOOSE 99
+/* Verification of drafted tokens: the rows, the choice where a draft with probabilities was rejected. */
+#define FP8BS_RUNS_VERIFY_ROWS 98
+#define FP8BS_RUNS_VERIFY_RESIDUAL 99
 /* Routing by scores, bias and groups. */
 #define FP8BS_RUNS_MOE_ROUTE_GROUPED 100
 #define FP8BS_RUNS_SLOTS 128
