@@ -35,6 +35,9 @@ static __device__ const float2 kPow32[32] = {
 constexpr float kShift = 393216.0f;       // 1.5 * 2^18: adding it rounds to multiples of 1/32
 constexpr int kShiftBits = 0x48C00000;    // its bits
 
+// n of pow_split.
+__device__ __forceinline__ int pow_exponent(float zh) { return (__float_as_int(zh + kShift) - kShiftBits) >> 5; }
+
 // 2^(zh + zl) = 2^n th (1 + rest); `entry` is the lane's of kPow32; a whole warp calls it.
 __device__ __forceinline__ int pow_split(float zh, float zl, float2 entry, float &th, float &rest)
 {

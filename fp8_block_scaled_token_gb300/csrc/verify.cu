@@ -10,7 +10,7 @@
 // The choice is a whole number that a cumulative sum over up to a million
 // entries decides, so the weights are held to 2^-28 of themselves, 2^-31 in the
 // mean (two fp32 numbers), and summed as 64-bit integers in units of 2^-48 (a
-// chunk, relative to a power of two near its largest) and 2^-41 (a row): integer
+// part of a row, relative to a power of two near its largest) and 2^-41 (a row): integer
 // sums have no order, which makes the result bitwise reproducible.
 //
 // w(x) = 2^((x - ref) c), c = log2(e) / T as two fp32 numbers: z = x c in two
@@ -20,13 +20,13 @@
 // no smaller than |x| for every x that counts, so that t = fl(x - ref) and e = x -
 // (t + ref) are exact (fast two-sum) and z = t c + e c.
 //
-// verify_rows_kernel: a CTA per (row, 8,192 logits), rows in the order of their
-// positions.  Maximum, then the sum of the weights, from registers: one read.
-// The last CTA of a row puts the chunks together and decides the draft.  A row
-// that is not accepted leaves its position in the sequence's word, and CTAs of
-// later positions that start after that have nothing to do.  The last row of a
-// sequence knows where it stops and draws the token: it finds the chunk, the
-// eighth of it that a warp summed, and looks through that.
+// verify_rows_kernel: a warp per part of 1,024 logits of a row, rows in the order
+// of their positions.  Maximum, then the sum of the weights, from registers: one
+// read, and nothing that another warp has to wait for.  The last CTA of a row puts
+// the parts together and decides the draft.  A row that is not accepted leaves its
+// position in the sequence's word, and CTAs of later positions that start after
+// that have nothing to do.  The last row of a sequence knows where it stops and
+// draws the token: it finds the part and looks through it.
 // verify_residual_kernel (with the draft's probabilities): a CTA per (sequence,
 // 2,048 logits) of those that stopped at a rejected draft: sums max(p - q, 0); a
 // sequence's last CTA finds the chunk and looks through it.  Nothing waits.
@@ -41,19 +41,22 @@ namespace fp8bs {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyCtas = 4;     // to an SM
-constexpr int kChunk = 8192;       // logits of a CTA
-constexpr int kPart = kChunk / kVerifyWarps; // of a warp
-constexpr int kSlice = 2048;       // logits of a CTA of the residual
+#ifndef VCTAS
+#define VCTAS 5
+#endif
+constexpr int kVerifyCtas = VCTAS;  // to an SM
+constexpr int kPart = 1024;         // logits that a warp sums
+constexpr int kMostParts = 4;       // of a warp, one after the other
+constexpr int kSlice = 2048;        // logits of a CTA of the residual
 constexpr int kVerifyMaxDraft = 31;
 constexpr int kVerifyMaxRows = 4096;
 constexpr int kVerifyMaxVocab = 1 << 20;
-constexpr int kMaxChunks = kVerifyMaxVocab / kChunk + 1;
-constexpr float kChunkUnits = 281474976710656.0f;  // 2^48
-constexpr float kRowUnits = 2199023255552.0f;      // 2^41: a row's total stays below 2^62
+constexpr int kMaxParts = kVerifyMaxVocab / kPart + 1;
+constexpr float kPartUnits = 281474976710656.0f;  // 2^48
+constexpr float kRowUnits = 2199023255552.0f;     // 2^41: a row's total stays below 2^62
 
-struct ChunkStat {
-    float top;       // largest logit; NaN where the chunk holds a NaN or +infinity
+struct alignas(16) PartStat {
+    float top;       // largest logit; NaN where the part holds a NaN or +infinity
     int exponent;    // the sum's unit is 2^(exponent - 48)
     long long sum;   // T = 0: the index of `top`
 };
@@ -69,7 +72,9 @@ struct alignas(16) RowStat {
 };
 
 struct VerifyParams {
-    int B, L, V, chunks, slices;
+    int B, L, V;
+    int parts, chunks, slices;               // of a row: a CTA's parts are a chunk
+    int parts_each;                          // of a warp
     unsigned first_wave;                     // CTAs that start at once, before any row can have stopped
     const uint8_t *logits;
     long long ldl; // logits
@@ -80,16 +85,15 @@ struct VerifyParams {
     int32_t *tokens, *accepted;
     float *probs;
     unsigned *row_done, *stopped, *seq_done; // zero between calls
-    ChunkStat *chunk;                        // [rows][chunks]
-    long long *part;                         // [rows][chunks][warps]: the chunk's sum by warps
-    long long *in_row;                       // [rows][chunks]: the chunk's sum in row units
+    PartStat *part;                          // [rows][parts]
+    long long *in_row;                       // [rows][parts]: the part's sum in row units
     RowStat *row;
     RowStat *stop;                           // [B]
     long long *residual;                     // [B][slices]
     unsigned long long *runs;
 };
 
-// Temperature and reference of one row (or chunk), and a lane's table entry.
+// Temperature and reference of one row (or part), and a lane's table entry.
 struct Scale {
     float ch, cl; // log2(e) / T
     float T;
@@ -206,16 +210,33 @@ __device__ __forceinline__ f32x2 pfma(f32x2 a, f32x2 b, f32x2 c)
     return r;
 }
 
+__device__ __forceinline__ f32x2 psub(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A thread's sum of weights: `high` in multiples of 2^-16 below 64, `low` below 1.
+__device__ __forceinline__ long long sum_units(float high, float low0, float low1)
+{
+    // in units of 2^-48, by 32-bit conversions: low's multiples of 2^-30, then the rest
+    const float a = rintf(low0 * 1073741824.0f), b = rintf(low1 * 1073741824.0f);
+    const float c = fmaf(a, -9.31322575e-10f, low0), d = fmaf(b, -9.31322575e-10f, low1);
+    const int mid = __float2int_rn(a) + __float2int_rn(b);
+    const int rest = __float2int_rn(c * kPartUnits) + __float2int_rn(d * kPartUnits);
+    return (static_cast<long long>(__float2int_rn(high * 65536.0f)) << 32) + static_cast<long long>(mid) * 262144 + rest;
+}
+
 // Sums of weights relative to 2^exponent, each below 2 and at most 32 of them a
 // thread: `high` holds their multiples of 2^-16 exactly, `low` what is left.
 //
-// Two logits at a time with reference 0, in packed instructions (13 a logit
-// where one at a time, with a reference, takes 27): weight() with n = -z in
-// place of z, which saves the negations.  What lies below the cutoff
-// counts as at it, 2^-92, which leaves no trace in the sums.
+// Two logits at a time with reference 0, in packed instructions (half of what
+// weight() takes for each).  What lies below the cutoff counts as at it, 2^-92, which
+// leaves no trace in the sums.
 struct WeightSum {
     f32x2 high, low;
-    f32x2 nch, ch, cl;
+    f32x2 ch, nch, ncl;
     float cut;
     uint32_t th; // the lane's table entry with the exponent's and index's offset taken off
     float tl;
@@ -223,9 +244,9 @@ struct WeightSum {
     __device__ __forceinline__ WeightSum(float cut_, int exponent, const Scale &s, float2 entry)
     {
         high = low = pack(0.0f, 0.0f);
-        nch = pack(-s.ch, -s.ch);
         ch = pack(s.ch, s.ch);
-        cl = pack(s.cl, s.cl);
+        nch = pack(-s.ch, -s.ch);
+        ncl = pack(-s.cl, -s.cl);
         cut = cut_;
         th = __float_as_uint(entry.x) - ((threadIdx.x & 31u) << 18) - (static_cast<uint32_t>(exponent) << 23);
         tl = entry.y;
@@ -233,12 +254,11 @@ struct WeightSum {
     __device__ __forceinline__ void add(float x0, float x1)
     {
         constexpr float k1 = 0x1.62e430p-1f, k2 = 0x1.ebfbe0p-3f, k3 = 0x1.c6b08ep-5f, k4 = 0x1.3b2ab6p-7f; // ln(2)^k / k!
-        const f32x2 minus = pack(-1.0f, -1.0f), shift = pack(kShift, kShift);
+        const f32x2 shift = pack(kShift, kShift), top = pack(192.0f, 192.0f);
         const f32x2 x = pack(fmaxf(x0, cut), fmaxf(x1, cut));
-        const f32x2 n = pmul(x, nch);
-        const f32x2 zl = pfma(x, cl, pfma(x, ch, n));
-        const f32x2 u = pfma(n, minus, shift);
-        const f32x2 y = padd(pfma(n, minus, pfma(u, minus, shift)), zl);
+        const f32x2 z = pmul(x, ch);
+        const f32x2 u = padd(z, shift);
+        const f32x2 y = psub(psub(z, psub(u, shift)), pfma(x, ncl, pfma(x, nch, z))); // z - round(z), less z's own error
         float u0, u1;
         unpack(u, u0, u1);
         const uint32_t b0 = __float_as_uint(u0), b1 = __float_as_uint(u1);
@@ -250,16 +270,16 @@ struct WeightSum {
         const f32x2 rest = pfma(p1, y, r);
         // the bits of u are kShiftBits + 32 n + j: shifted, n is at the exponent and j at bits 18 to 22
         const f32x2 hi = pack(__uint_as_float((b0 << 18) + t0), __uint_as_float((b1 << 18) + t1));
-        const f32x2 q = padd(padd(hi, pack(192.0f, 192.0f)), pack(-192.0f, -192.0f));
+        const f32x2 q = psub(padd(hi, top), top);
         high = padd(high, q);
-        low = pfma(hi, rest, padd(low, pfma(q, minus, hi)));
+        low = pfma(hi, rest, padd(low, psub(hi, q)));
     }
-    __device__ __forceinline__ long long units(float u) const
+    __device__ __forceinline__ long long units() const
     {
         float h0, h1, l0, l1;
         unpack(high, h0, h1);
         unpack(low, l0, l1);
-        return fixed(h0, l0, u) + fixed(h1, l1, u);
+        return sum_units(h0 + h1, l0, l1);
     }
 };
 static_assert((static_cast<uint32_t>(kShiftBits) << 18) == 0u, "kShiftBits leaves the shifted word");
@@ -268,7 +288,7 @@ static_assert((static_cast<uint32_t>(kShiftBits) << 18) == 0u, "kShiftBits leave
 // before its first.
 template <bool kBf16> struct Row {
     static constexpr int kPer = kBf16 ? 8 : 4;                     // logits of a word
-    static constexpr int kWords = kChunk / kPer / kVerifyThreads;  // words of a thread of a chunk
+    static constexpr int kWords = kPart / kPer / 32;               // words of a lane of a part
     const uint8_t *words;
     int lead; // logits that the first word has before the row
     int V;
@@ -282,6 +302,10 @@ template <bool kBf16> struct Row {
         V = p.V;
     }
     __device__ __forceinline__ int index(int word) const { return word * kPer - lead; } // of its first logit
+    __device__ __forceinline__ uint4 whole(int word) const // all of whose logits are in the row
+    {
+        return *reinterpret_cast<const uint4 *>(words + static_cast<long long>(word) * 16);
+    }
     // A word; -infinity for what is not in the row (whose memory is not read).
     __device__ __forceinline__ uint4 load(int word) const
     {
@@ -365,14 +389,14 @@ __device__ __forceinline__ long long rescale(long long sum, float th, float rest
     return static_cast<long long>(shift >= 0 ? v >> shift : v << -shift);
 }
 
-// The factor that takes sums of a chunk (largest logit ctop, exponent cexp) to
-// row units, as th, rest and k of rescale; false where the chunk is below the
+// The factor that takes sums of a part (largest logit ctop, exponent cexp) to
+// row units, as th, rest and k of rescale; false where the part is below the
 // row's cutoff.  A whole warp calls it.
 __device__ __forceinline__ bool to_row(float ctop, int cexp, float ref, float cut, int exponent, const Scale &s,
                                        float2 entry, float &th, float &rest, int &k)
 {
     const bool live = ctop >= cut;
-    // the chunk's reference seen from the row's, by a two-sum without conditions
+    // the part's reference seen from the row's, by a two-sum without conditions
     const float cref = live ? reference(ctop, s) : ref;
     const float d = cref - ref, bb = d - cref;
     const float e = (cref - (d - bb)) + (-ref - bb);
@@ -396,40 +420,45 @@ __device__ __forceinline__ Pair pair_of(long long v) // to 48 bits
     return {hi, __ll2float_rn(v - __float2ll_rn(hi))};
 }
 
-// What a CTA of verify_rows_kernel shares.
+// What a CTA shares.
 struct RowShared {
     float top[kVerifyWarps];
-    long long part[kVerifyWarps];  // this chunk's sums by warps
-    long long in_row[kMaxChunks];  // this row's chunks
+    int best[kVerifyWarps];
+    long long sum[kVerifyWarps];
+    long long in_row[kMaxParts];   // this row's parts
     RowStat row;                   // this row, then the one that the sequence stops at
-    long long scan[kVerifyWarps];
     long long target;
-    int skip, last_chunk, last_row, draw_now, without, chunk, part_of, found, end;
+    int skip, last_chunk, last_row, draw_now, without, part, found, end;
 };
 
-// The row's chunks put together, and the verdict on its draft; one warp of the
-// CTA that summed chunk c as `mine`.
+// The row's parts put together, and the verdict on its draft; the whole CTA.
 template <bool kBf16>
-__device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, int len, const Row<kBf16> &x, int c,
-                                           const ChunkStat &mine, RowShared &sh)
+__device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, int len, const Row<kBf16> &x, RowShared &sh)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = static_cast<long long>(b) * (p.L + 1) + j;
-    const ChunkStat *const st = p.chunk + row * p.chunks;
+    const PartStat *const st = p.part + row * p.parts;
     const float T = temperature(p, b);
     const float2 entry = kPow32[lane];
     const long long d = static_cast<long long>(b) * p.L + j;
     const int t = j < len ? p.draft[d] : -1;
     const bool inside = t >= 0 && t < p.V;
-    const float xt = inside ? x.at(t) : 0.0f;
+    const float xt = inside ? x.at(t) : -INFINITY;
     const float qt = j >= len || !inside ? 0.0f : p.q == nullptr ? 1.0f : p.q[d * p.ldq + t];
     const float ut = j < len ? p.accept_u[d] : 0.0f;
     float top = -INFINITY;
-    for (int i = lane; i < p.chunks; i += 32)
-        top = max_nan(top, i == c ? mine.top : __ldcg(&st[i].top));
+    for (int i = threadIdx.x; i < p.parts; i += kVerifyThreads)
+        top = max_nan(top, __ldcg(&st[i].top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0)
+        sh.top[warp] = top;
+    __syncthreads();
+    top = sh.top[0];
+#pragma unroll
+    for (int i = 1; i < kVerifyWarps; ++i)
+        top = max_nan(top, sh.top[i]);
     RowStat r = {};
     r.top = top;
     r.position = j;
@@ -437,10 +466,17 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
         r.verdict = 2;
     } else if (T == 0.0f) {
         int best = 0x7fffffff;
-        for (int i = lane; i < p.chunks; i += 32)
-            if ((i == c ? mine.top : __ldcg(&st[i].top)) == top)
-                best = min(best, static_cast<int>(i == c ? mine.sum : __ldcg(&st[i].sum)));
-        r.best = __reduce_min_sync(0xffffffffu, best);
+        for (int i = threadIdx.x; i < p.parts; i += kVerifyThreads)
+            if (__ldcg(&st[i].top) == top)
+                best = min(best, static_cast<int>(__ldcg(&st[i].sum)));
+        best = __reduce_min_sync(0xffffffffu, best);
+        if (lane == 0)
+            sh.best[warp] = best;
+        __syncthreads();
+        r.best = sh.best[0];
+#pragma unroll
+        for (int i = 1; i < kVerifyWarps; ++i)
+            r.best = min(r.best, sh.best[i]);
         r.prob = t == r.best ? 1.0f : 0.0f;
         r.verdict = inside && ut * qt < r.prob ? 1 : 0;
     } else {
@@ -448,34 +484,44 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
         const float ref = reference(top, s), cut = cutoff(top, T);
         float zh, zl, th, rest;
         exponent_of(top, ref, s, zh, zl);
-        r.exponent = pow_split(zh, zl, entry, th, rest);
+        r.exponent = pow_exponent(zh);
         long long sum = 0;
-        for (int i0 = 0; i0 < p.chunks; i0 += 32) {
-            const int i = i0 + lane;
-            const bool there = i < p.chunks;
-            const float ctop = !there ? -INFINITY : i == c ? mine.top : __ldcg(&st[i].top);
-            const int cexp = !there ? 0 : i == c ? mine.exponent : __ldcg(&st[i].exponent);
-            const long long csum = !there ? 0 : i == c ? mine.sum : __ldcg(&st[i].sum);
+#pragma unroll 1
+        for (int i0 = 0; i0 < p.parts; i0 += kVerifyThreads) {
+            const int i = i0 + static_cast<int>(threadIdx.x);
+            PartStat v = {-INFINITY, 0, 0};
+            if (i < p.parts) {
+                const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(st + i));
+                v.top = __uint_as_float(w.x);
+                v.exponent = static_cast<int>(w.y);
+                v.sum = static_cast<long long>(static_cast<unsigned long long>(w.w) << 32 | w.z);
+            }
             int k;
-            const bool live = to_row(ctop, cexp, ref, cut, r.exponent, s, entry, th, rest, k);
-            const long long g = live ? rescale(csum, th, rest, k) : 0;
-            if (there) {
-                __stcg(p.in_row + row * p.chunks + i, g);
+            const bool live = to_row(v.top, v.exponent, ref, cut, r.exponent, s, entry, th, rest, k);
+            const long long g = live ? rescale(v.sum, th, rest, k) : 0;
+            if (i < p.parts) {
+                __stcg(p.in_row + row * p.parts + i, g);
                 sh.in_row[i] = g;
                 sum += g;
             }
         }
-        r.total = warp_sum(sum);
+        sum = warp_sum(sum);
+        if (lane == 0)
+            sh.sum[warp] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kVerifyWarps; ++i)
+            r.total += sh.sum[i];
         if (j < len) {
             float hi, lo;
-            weight(inside ? xt : -INFINITY, top, ref, cut, r.exponent, s, entry, hi, lo);
+            weight(xt, top, ref, cut, r.exponent, s, entry, hi, lo);
             const Pair w = {hi * kRowUnits, lo * kRowUnits}, total = pair_of(r.total);
             const float uq = ut * qt;
             r.verdict = inside && less({uq, fmaf(ut, qt, -uq)}, total, w) ? 1 : 0;
             r.prob = divide(fast_two_sum(w.hi, w.lo), total).hi;
         }
     }
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
         p.row[row] = r;
         sh.row = r;
         if (r.verdict != 1)
@@ -529,25 +575,25 @@ template <bool kBf16> struct Weights {
     {
         weight(v, top, ref, cut, exponent, s, entry, hi, lo);
     }
-    __device__ __forceinline__ float probability(int i, long long total) const // one warp
-    {
-        float hi, lo;
-        pair(x.at(i), hi, lo);
-        return divide(fast_two_sum(hi * kRowUnits, lo * kRowUnits), pair_of(total)).hi;
-    }
 };
 
-// The first of a thread block's weights g (kN a thread, in order, of the logits
-// from i0 on) whose cumulative sum passes `target`; the last one with a weight where
-// rounding leaves none, -1 where none has any.  All threads call it; `found` and
-// `end` are the answer's places.
+__device__ __forceinline__ float probability(float hi, float lo, long long total)
+{
+    return divide(fast_two_sum(hi * kRowUnits, lo * kRowUnits), pair_of(total)).hi;
+}
+
+// Where the cumulative sum of a CTA's weights passes `target`: g, kN a thread, of the
+// logits from i0 on, in order; the last one with a weight where rounding leaves none.
+// The thread that has it writes it and its probability (weights hi + lo of the row,
+// whose total is r.total); with no weight at all, -1 and NaN.  All threads call it.
 template <int kN>
-__device__ __forceinline__ int look(const long long (&g)[kN], int i0, long long target, long long *scan, int &found, int &end)
+__device__ __forceinline__ void look(const VerifyParams &p, long long to, const RowStat &r, const long long (&g)[kN],
+                                     const float (&hi)[kN], const float (&lo)[kN], int i0, long long target, RowShared &sh)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        found = 0x7fffffff;
-        end = -1;
+        sh.found = 0x7fffffff;
+        sh.end = -1;
     }
     long long mine = 0;
     int last = -1;
@@ -559,35 +605,44 @@ __device__ __forceinline__ int look(const long long (&g)[kN], int i0, long long 
     }
     long long upto = warp_scan(mine);
     if (lane == 31)
-        scan[warp] = upto;
+        sh.sum[warp] = upto;
     __syncthreads();
     for (int i = 0; i < warp; ++i)
-        upto += scan[i];
+        upto += sh.sum[i];
     if (upto - mine <= target && target < upto) {
-        long long at = upto - mine;
+        long long at = upto;
 #pragma unroll
         for (int e = kN - 1; e >= 0; --e) { // from behind: the first that passes is written last
-            long long before = at;
-#pragma unroll
-            for (int i = 0; i < e; ++i)
-                before += g[i];
-            if (before + g[e] > target)
-                found = i0 + e;
+            if (at > target)
+                sh.found = i0 + e;
+            at -= g[e];
         }
     }
     last = __reduce_max_sync(0xffffffffu, last);
     if (lane == 0 && last >= 0)
-        atomicMax(&end, last);
+        atomicMax(&sh.end, last);
     __syncthreads();
-    return found != 0x7fffffff ? found : end;
+    const int token = sh.found != 0x7fffffff ? sh.found : sh.end;
+    if (token >= i0 && token < i0 + kN) {
+        float h = hi[0], l = lo[0];
+#pragma unroll
+        for (int e = 1; e < kN; ++e) {
+            h = token == i0 + e ? hi[e] : h;
+            l = token == i0 + e ? lo[e] : l;
+        }
+        p.tokens[to] = token;
+        p.probs[to] = probability(h, l, r.total);
+    } else if (token < 0 && threadIdx.x == 0) {
+        p.tokens[to] = -1;
+        p.probs[to] = NAN;
+    }
 }
 
 // Draws the token of row `r` (of sequence b, at r.position) from its own weights,
 // without that of logit `except` where it is in the row.  The whole CTA calls it;
-// `own`: the chunk sums lie in sh.in_row, and chunk own_chunk's in sh.part.
+// `own`: the parts' sums lie in sh.in_row.
 template <bool kBf16>
-__device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat &r, float T, int except, bool own,
-                                     int own_chunk, RowShared &sh)
+__device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat &r, float T, int except, bool own, RowShared &sh)
 {
     using R = Row<kBf16>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,42 +650,25 @@ __device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat
     const Weights<kBf16> w(p, row, r, T);
     if (warp == 0) {
         const float u = p.sample_u[b];
-        const long long *const in_row = p.in_row + row * p.chunks;
+        const long long *const in_row = p.in_row + row * p.parts;
         const bool with = except >= 0 && except < p.V;
         float hi = 0.0f, lo = 0.0f;
         w.pair(with ? w.x.at(except) : -INFINITY, hi, lo);
         const long long less_by = fixed(hi, lo, kRowUnits);
-        const int home = with ? (except + w.x.lead) / kChunk : -1;
+        const int home = with ? (except + w.x.lead) / kPart : -1;
         auto sum = [&](int i) { return own ? sh.in_row[i] : __ldcg(in_row + i); };
         long long target = 0;
         int c = -1;
         if (with)
-            c = find_target(p.chunks, u, [&](int i) {
+            c = find_target(p.parts, u, [&](int i) {
                 const long long g = sum(i);
                 return i != home ? g : g > less_by ? g - less_by : 0;
             }, target);
         const bool all = c < 0; // nothing is left beside it: from everything
         if (all)
-            c = find_target(p.chunks, u, sum, target);
-        c = c < 0 ? 0 : c; // (a row's total is positive)
-        // the part of the chunk: its warps' sums in row units
-        const ChunkStat *const st = p.chunk + row * p.chunks + c;
-        float th, rest;
-        int k;
-        const bool live = to_row(__ldcg(&st->top), __ldcg(&st->exponent), w.ref, w.cut, w.exponent, w.s, w.entry, th, rest, k);
-        long long g = 0;
-        if (lane < kVerifyWarps && live)
-            g = rescale(own && c == own_chunk ? sh.part[lane] : __ldcg(p.part + (row * p.chunks + c) * kVerifyWarps + lane), th,
-                        rest, k);
-        if (!all && c == home && lane == (except + w.x.lead) % kChunk / kPart)
-            g = g > less_by ? g - less_by : 0;
-        const long long upto = warp_scan(g);
-        const unsigned past = __ballot_sync(0xffffffffu, upto > target), some = __ballot_sync(0xffffffffu, g > 0);
-        const int l = past != 0u ? __ffs(static_cast<int>(past)) - 1 : some != 0u ? 31 - __clz(some) : 0;
-        target -= __shfl_sync(0xffffffffu, upto - g, l); // past the last part: found by its end
+            c = find_target(p.parts, u, sum, target);
         if (lane == 0) {
-            sh.chunk = c;
-            sh.part_of = l;
+            sh.part = c < 0 ? 0 : c; // (a row's total is positive)
             sh.target = target;
             sh.without = all ? -1 : except;
         }
@@ -639,32 +677,27 @@ __device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat
     // kPart logits: a word a thread, as far as they go
     constexpr int kWords = kPart / R::kPer;
     static_assert(kWords <= kVerifyThreads, "a word a thread");
-    const int word = sh.chunk * (kChunk / R::kPer) + sh.part_of * kWords + static_cast<int>(threadIdx.x);
+    const int word = sh.part * kWords + static_cast<int>(threadIdx.x);
     const int i0 = w.x.index(word);
     const long long target = sh.target;
     const int without = sh.without;
     long long g[R::kPer];
+    float hi[R::kPer], lo[R::kPer];
     if (warp * 32 < kWords) {
         const uint4 v = w.x.load(word);
 #pragma unroll
         for (int e = 0; e < R::kPer; ++e) {
-            float hi, lo;
-            w.pair(R::value(v, e), hi, lo);
-            g[e] = i0 + e == without ? 0 : fixed(hi, lo, kRowUnits);
+            w.pair(R::value(v, e), hi[e], lo[e]);
+            g[e] = i0 + e == without ? 0 : fixed(hi[e], lo[e], kRowUnits);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < R::kPer; ++e)
+        for (int e = 0; e < R::kPer; ++e) {
             g[e] = 0;
-    }
-    const int token = look(g, i0, target, sh.scan, sh.found, sh.end);
-    if (warp == 0) {
-        const float prob = token >= 0 ? w.probability(token, r.total) : NAN;
-        if (lane == 0) {
-            p.tokens[row] = token;
-            p.probs[row] = prob;
+            hi[e] = lo[e] = 0.0f;
         }
     }
+    look(p, row, r, g, hi, lo, i0, target, sh);
 }
 
 // A CTA per (position, sequence, chunk), in that order.
@@ -681,7 +714,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
     grid_dependency_wait();
     const int c = static_cast<int>(blockIdx.x % p.chunks);
     const int rank = static_cast<int>(blockIdx.x / p.chunks);
-    const int j = rank / p.B, b = rank % p.B;
+    const int j = rank / p.B, b = rank - j * p.B;
     const int len = drafted(p, b);
     if (j > len)
         return;
@@ -695,104 +728,92 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
     const long long row = static_cast<long long>(b) * (p.L + 1) + j;
     const R x(p, row);
     const float T = temperature(p, b);
-    ChunkStat out = {NAN, 0, 0};
     if (!skip) {
-        const int w0 = c * (kChunk / R::kPer) + warp * (kPart / R::kPer) + lane;
-        uint4 raw[R::kWords];
+        const bool drawing = good_temperature(T) && T != 0.0f;
+        const Scale sc = make_scale(drawing ? T : 1.0f);
+        int part = (c * kVerifyWarps + warp) * p.parts_each;
+        const int end = min(part + p.parts_each, p.parts);
+#pragma unroll 1
+        for (; part < end; ++part) {
+            const int w0 = part * (kPart / R::kPer) + lane;
+            uint4 raw[R::kWords];
+            const int first = x.index(part * (kPart / R::kPer));
+            if (first >= 0 && first + kPart <= p.V) {
 #pragma unroll
-        for (int s = 0; s < R::kWords; ++s)
-            raw[s] = x.load(w0 + s * 32);
-        float top = R::largest(raw[0]);
+                for (int s = 0; s < R::kWords; ++s)
+                    raw[s] = x.whole(w0 + s * 32);
+            } else {
 #pragma unroll
-        for (int s = 1; s < R::kWords; ++s)
-            top = max_nan(top, R::largest(raw[s]));
+                for (int s = 0; s < R::kWords; ++s)
+                    raw[s] = x.load(w0 + s * 32);
+            }
+            float top = R::largest(raw[0]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0)
-            sh.top[warp] = top;
-        __syncthreads();
-        top = sh.top[0];
+            for (int s = 1; s < R::kWords; ++s)
+                top = max_nan(top, R::largest(raw[s]));
 #pragma unroll
-        for (int i = 1; i < kVerifyWarps; ++i)
-            top = max_nan(top, sh.top[i]);
-        out.top = top;
-        long long sum = 0;
-        if (top > -INFINITY && top < INFINITY && good_temperature(T)) {
-            if (T == 0.0f) {
-                int first = 0x7fffffff;
+            for (int o = 16; o > 0; o >>= 1)
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+            PartStat out = {top, 0, 0};
+            if (!(top > -INFINITY && top < INFINITY)) {
+                // no sum
+            } else if (!drawing) {
+                int best = 0x7fffffff;
 #pragma unroll
                 for (int s = R::kWords - 1; s >= 0; --s)
 #pragma unroll
                     for (int e = R::kPer - 1; e >= 0; --e)
                         if (R::value(raw[s], e) == top)
-                            first = x.index(w0 + s * 32) + e;
-                sum = __reduce_min_sync(0xffffffffu, first);
+                            best = x.index(w0 + s * 32) + e;
+                out.sum = __reduce_min_sync(0xffffffffu, best);
             } else {
-                const Scale sc = make_scale(T);
                 const float ref = reference(top, sc), cut = cutoff(top, T);
-                float zh, zl, th, rest;
+                float zh, zl;
                 exponent_of(top, ref, sc, zh, zl);
-                out.exponent = pow_split(zh, zl, entry, th, rest);
-                WeightSum sums(cut, out.exponent, sc, entry);
+                out.exponent = pow_exponent(zh);
+                long long sum;
                 if (ref == 0.0f) {
+                    WeightSum sums(cut, out.exponent, sc, entry);
 #pragma unroll
                     for (int s = 0; s < R::kWords; ++s)
 #pragma unroll
                         for (int e = 0; e < R::kPer; e += 2)
                             sums.add(R::value(raw[s], e), R::value(raw[s], e + 1));
+                    sum = sums.units();
                 } else {
-                    float high = 0.0f, low = 0.0f;
+                    sum = 0;
 #pragma unroll
-                    for (int s = 0; s < R::kWords; ++s)
+                    for (int s = 0; s < R::kWords; ++s) {
 #pragma unroll 1
                         for (int e = 0; e < R::kPer; ++e) {
-                            const uint32_t a = (kBf16 ? e >> 1 : e) == 0 ? raw[s].x : (kBf16 ? e >> 1 : e) == 1 ? raw[s].y
-                                               : (kBf16 ? e >> 1 : e) == 2 ? raw[s].z : raw[s].w;
-                            const float v = __uint_as_float(!kBf16 ? a : (e & 1) ? a & 0xFFFF0000u : a << 16);
+                            const int i = kBf16 ? e >> 1 : e;
+                            const uint32_t a = i == 0 ? raw[s].x : i == 1 ? raw[s].y : i == 2 ? raw[s].z : raw[s].w;
                             float hi, lo;
-                            weight(v, top, ref, cut, out.exponent, sc, entry, hi, lo);
-                            const float q = (hi + 192.0f) - 192.0f;
-                            high += q;
-                            low += hi - q;
-                            low += lo;
+                            weight(__uint_as_float(!kBf16 ? a : (e & 1) ? a & 0xFFFF0000u : a << 16), top, ref, cut,
+                                   out.exponent, sc, entry, hi, lo);
+                            sum += fixed(hi, lo, kPartUnits);
                         }
-                    sums.high = pack(high, 0.0f);
-                    sums.low = pack(low, 0.0f);
+                    }
                 }
-                sum = warp_sum(sums.units(kChunkUnits));
+                out.sum = warp_sum(sum);
             }
-        }
-        if (lane == 0) {
-            sh.part[warp] = sum;
-            __stcg(p.part + (row * p.chunks + c) * kVerifyWarps + warp, sum);
+            if (lane == 0) {
+                const unsigned long long v = static_cast<unsigned long long>(out.sum);
+                __stcg(reinterpret_cast<uint4 *>(p.part + row * p.parts + part),
+                       make_uint4(__float_as_uint(out.top), static_cast<uint32_t>(out.exponent), static_cast<uint32_t>(v),
+                                  static_cast<uint32_t>(v >> 32)));
+            }
         }
     }
     __syncthreads();
-    if (!skip) {
-        out.sum = sh.part[0];
-#pragma unroll
-        for (int i = 1; i < kVerifyWarps; ++i)
-            out.sum = T == 0.0f ? min(out.sum, sh.part[i]) : out.sum + sh.part[i];
-    }
     if (threadIdx.x == 0) {
         sh.last_chunk = 1;
         if (p.chunks > 1) {
-            if (!skip) {
-                ChunkStat *const to = p.chunk + row * p.chunks + c;
-                __stcg(&to->top, out.top);
-                __stcg(&to->exponent, out.exponent);
-                __stcg(&to->sum, out.sum);
-            }
             sh.last_chunk = atomic_add_acq_rel_gpu(p.row_done + row, 1u) == static_cast<unsigned>(p.chunks - 1);
             if (sh.last_chunk != 0)
                 p.row_done[row] = 0u;
-        } else if (!skip) {
-            ChunkStat *const to = p.chunk + row;
-            __stcg(&to->top, out.top);
-            __stcg(&to->exponent, out.exponent);
         }
-        // where a chunk was left out, this sees why
+        // where a part was left out, this sees why
         sh.skip = sh.last_chunk != 0 && j > 0 && behind_a_stop(p, b, j) ? 1 : 0;
     }
     __syncthreads();
@@ -800,17 +821,15 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
         return;
     __threadfence();
     const bool finish = sh.skip == 0;
-    if (warp == 0) {
-        if (finish)
-            finish_row<kBf16>(p, b, j, len, x, c, out, sh);
-        __syncwarp();
-        if (lane == 0) {
-            sh.last_row = 1;
-            if (len > 0) {
-                sh.last_row = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(len);
-                if (sh.last_row != 0)
-                    p.seq_done[b] = 0u;
-            }
+    if (finish)
+        finish_row<kBf16>(p, b, j, len, x, sh);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sh.last_row = 1;
+        if (len > 0) {
+            sh.last_row = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(len);
+            if (sh.last_row != 0)
+                p.seq_done[b] = 0u;
         }
     }
     __syncthreads();
@@ -859,7 +878,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
         return;
     const RowStat r = sh.row;
     const int except = r.position < len ? p.draft[static_cast<long long>(b) * p.L + r.position] : -1;
-    draw<kBf16>(p, b, r, T, except, finish && r.position == j, c, sh);
+    draw<kBf16>(p, b, r, T, except, finish && r.position == j, sh);
 }
 
 // A CTA per (sequence, slice of kSlice logits): the weights max(p - q, 0) where a
@@ -887,8 +906,8 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
     Pair W = pair_of(r.total);
     W.hi *= 1.0f / kRowUnits;
     W.lo *= 1.0f / kRowUnits;
-    // this thread's weights in slice i
-    auto weights = [&](int i, long long(&g)[kN]) {
+    // this thread's weights in slice i, and the target's alone
+    auto weights = [&](int i, long long(&g)[kN], float(&ph)[kN], float(&pl)[kN]) {
         const int word = (i * kSlice + static_cast<int>(threadIdx.x) * kN) / R::kPer;
         const int i0 = w.x.index(word);
         uint4 v[kN / R::kPer];
@@ -912,30 +931,30 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
         }
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-            float hi, lo;
-            w.pair(R::value(v[e / R::kPer], e % R::kPer), hi, lo);
-            // hi + lo - q W as a pair; 0 where that is not positive, or q is NaN
-            const float ph = qi[e] * W.hi;
-            const float pl = fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -ph));
-            const float d = hi - ph, bb = d - hi;
-            lo = (lo - pl) + ((hi - (d - bb)) + (-ph - bb));
+            w.pair(R::value(v[e / R::kPer], e % R::kPer), ph[e], pl[e]);
+            // p - q W as a pair; 0 where that is not positive, or q is NaN
+            const float bh = qi[e] * W.hi;
+            const float bl = fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -bh));
+            const float d = ph[e] - bh, bb = d - ph[e];
+            const float lo = (pl[e] - bl) + ((ph[e] - (d - bb)) + (-bh - bb));
             g[e] = d + lo > 0.0f ? fixed(d, lo, kRowUnits) : 0;
         }
         return i0;
     };
     long long g[kN];
-    weights(c, g);
+    float hi[kN], lo[kN];
+    weights(c, g, hi, lo);
     long long sum = 0;
 #pragma unroll
     for (int e = 0; e < kN; ++e)
         sum += g[e];
     sum = warp_sum(sum);
     if (lane == 0)
-        sh.part[warp] = sum;
+        sh.sum[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < kVerifyWarps; ++i)
-            sum += sh.part[i];
+            sum += sh.sum[i];
         __stcg(p.residual + static_cast<long long>(b) * p.slices + c, sum);
         sh.last_chunk = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(p.slices - 1);
         if (sh.last_chunk != 0)
@@ -950,26 +969,18 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
         long long target = 0;
         const int at = find_target(p.slices, p.sample_u[b], [&](int i) { return __ldcg(sums + i); }, target);
         if (lane == 0) {
-            sh.chunk = at;
+            sh.part = at;
             sh.target = target;
         }
     }
     __syncthreads();
-    if (sh.chunk < 0) { // p nowhere above q: from p
-        draw<kBf16>(p, b, r, T, -1, false, -1, sh);
+    if (sh.part < 0) { // p nowhere above q: from p
+        draw<kBf16>(p, b, r, T, -1, false, sh);
         return;
     }
     const long long target = sh.target;
-    const int i0 = weights(sh.chunk, g);
-    const int token = look(g, i0, target, sh.scan, sh.found, sh.end);
-    if (warp == 0) {
-        const float prob = token >= 0 ? w.probability(token, r.total) : NAN;
-        if (lane == 0) {
-            const long long to = static_cast<long long>(b) * (p.L + 1) + r.position;
-            p.tokens[to] = token;
-            p.probs[to] = prob;
-        }
-    }
+    const int i0 = weights(sh.part, g, hi, lo);
+    look(p, static_cast<long long>(b) * (p.L + 1) + r.position, r, g, hi, lo, i0, target, sh);
 }
 
 namespace {
@@ -977,8 +988,8 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct VerifyWorkspace {
-    size_t counters_bytes, chunk_off, part_off, in_row_off, row_off, stop_off, residual_off, total;
-    int chunks, slices;
+    size_t counters_bytes, part_off, in_row_off, row_off, stop_off, residual_off, total;
+    int parts, slices;
 };
 
 VerifyWorkspace verify_workspace(int B, int L, int V)
@@ -986,21 +997,20 @@ VerifyWorkspace verify_workspace(int B, int L, int V)
     auto up256 = [](size_t b) { return (b + 255) / 256 * 256; };
     const size_t rows = static_cast<size_t>(B) * (L + 1);
     VerifyWorkspace w;
-    w.chunks = (V + 7 + kChunk - 1) / kChunk; // a row may start up to seven logits into its first word
+    w.parts = (V + 7 + kPart - 1) / kPart; // a row may start up to seven logits into its first word
     w.slices = (V + 7 + kSlice - 1) / kSlice;
     w.counters_bytes = (rows + 2 * static_cast<size_t>(B)) * 4;
-    w.chunk_off = kCountersOff + counters_region(w.counters_bytes);
-    w.part_off = w.chunk_off + up256(rows * w.chunks * sizeof(ChunkStat));
-    w.in_row_off = w.part_off + up256(rows * w.chunks * kVerifyWarps * 8);
-    w.row_off = w.in_row_off + up256(rows * w.chunks * 8);
+    w.part_off = kCountersOff + counters_region(w.counters_bytes);
+    w.in_row_off = w.part_off + up256(rows * w.parts * sizeof(PartStat));
+    w.row_off = w.in_row_off + up256(rows * w.parts * 8);
     w.stop_off = w.row_off + up256(rows * sizeof(RowStat));
     w.residual_off = w.stop_off + up256(static_cast<size_t>(B) * sizeof(RowStat));
     w.total = w.residual_off + up256(static_cast<size_t>(B) * w.slices * 8);
     return w;
 }
 static_assert((kVerifyMaxRows + 2 * kVerifyMaxRows) * 4 <= kCountersRegion, "every size's counters lie in the shared region");
-static_assert(kMaxChunks * kChunk >= kVerifyMaxVocab + 7, "chunks of a row");
-static_assert(sizeof(ChunkStat) == 16 && sizeof(RowStat) == 32, "workspace layout");
+static_assert(kMaxParts * kPart >= kVerifyMaxVocab + 7, "parts of a row");
+static_assert(sizeof(PartStat) == 16 && sizeof(RowStat) == 32, "workspace layout");
 
 fp8bs_status check_verify(int B, int L, int V)
 {
@@ -1062,7 +1072,17 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.B = B;
     p.L = L;
     p.V = V;
-    p.chunks = w.chunks;
+    // parts of a warp: more than one where the GPU is filled three times over all the same
+    const long long rows = static_cast<long long>(B) * (L + 1);
+    p.parts = w.parts;
+    p.parts_each = 1;
+#ifdef VEACH
+    p.parts_each = VEACH;
+#else
+    while (p.parts_each < kMostParts && rows * w.parts >= 2ll * p.parts_each * 3 * kVerifyWarps * kVerifyCtas * dev.sms)
+        p.parts_each *= 2;
+#endif
+    p.chunks = (w.parts + p.parts_each * kVerifyWarps - 1) / (p.parts_each * kVerifyWarps);
     p.slices = w.slices;
     p.first_wave = static_cast<unsigned>(dev.sms * kVerifyCtas);
     p.logits = static_cast<const uint8_t *>(logits);
@@ -1080,8 +1100,7 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.row_done = reinterpret_cast<unsigned *>(ws + kCountersOff);
     p.stopped = p.row_done + static_cast<size_t>(B) * (L + 1);
     p.seq_done = p.stopped + B;
-    p.chunk = reinterpret_cast<ChunkStat *>(ws + w.chunk_off);
-    p.part = reinterpret_cast<long long *>(ws + w.part_off);
+    p.part = reinterpret_cast<PartStat *>(ws + w.part_off);
     p.in_row = reinterpret_cast<long long *>(ws + w.in_row_off);
     p.row = reinterpret_cast<RowStat *>(ws + w.row_off);
     p.stop = reinterpret_cast<RowStat *>(ws + w.stop_off);
@@ -1092,7 +1111,7 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kVerifyThreads, 1, 1);
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(B) * (L + 1) * w.chunks), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * p.chunks), 1, 1);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = (flags & FP8BS_FLAG_OVERLAP_PREV) ? 1 : 0;
