@@ -131,15 +131,36 @@ __device__ __forceinline__ void exponent_of(float x, float ref, const Scale &s, 
     zl = fmaf(e, s.ch, fmaf(t, s.cl, fmaf(t, s.ch, -zh)));
 }
 
+// The same with reference 0 and x at the cutoff at least, in fewer operations: the
+// rounding to n + j/32 and the rest straight from the product, which an fma holds
+// exactly; p the cubic nearest to the power series on |y| <= 2^-6 (2^-33).
+constexpr float kPow1 = 0x1.62e430p-1f, kPow2 = 0x1.ebfd1cp-3f, kPow3 = 0x1.c6b168p-5f;
+__device__ __forceinline__ int pow_direct(float x, const Scale &s, float2 entry, float &th, float &rest)
+{
+    const float u = fmaf(x, s.ch, kShift);
+    const int bits = __float_as_int(u);
+    const float y = fmaf(x, s.cl, fmaf(x, s.ch, kShift - u));
+    th = __shfl_sync(0xffffffffu, entry.x, bits & 31);
+    const float tl = __shfl_sync(0xffffffffu, entry.y, bits & 31);
+    rest = fmaf(fmaf(fmaf(y, kPow3, kPow2), y, kPow1), y, tl);
+    return (bits - kShiftBits) >> 5;
+}
+
 // The weight of x relative to 2^exponent as hi + lo (0 below the cutoff); a
 // whole warp calls it.
 __device__ __forceinline__ void weight(float x, float top, float ref, float cut, int exponent, const Scale &s,
                                        float2 entry, float &hi, float &lo)
 {
     const bool live = x >= cut;
-    float zh, zl, th, rest;
-    exponent_of(live ? x : top, ref, s, zh, zl);
-    const int n = pow_split(zh, zl, entry, th, rest);
+    float th, rest;
+    int n;
+    if (ref == 0.0f) {
+        n = pow_direct(live ? x : top, s, entry, th, rest);
+    } else {
+        float zh, zl;
+        exponent_of(live ? x : top, ref, s, zh, zl);
+        n = pow_split(zh, zl, entry, th, rest);
+    }
     hi = live ? __uint_as_float(__float_as_uint(th) + (static_cast<uint32_t>(n - exponent) << 23)) : 0.0f;
     lo = hi * rest;
 }
@@ -147,6 +168,18 @@ __device__ __forceinline__ void weight(float x, float top, float ref, float cut,
 __device__ __forceinline__ long long fixed(float hi, float lo, float units)
 {
     return __float2ll_rn(hi * units) + __float2ll_rn(lo * units);
+}
+
+// The same for hi and lo between -4 and 4 and row units, without the conversions to 64
+// bits, which go through the 64-bit pipe: adding 12 leaves a number's multiples of
+// 2^-20 in the sum's low bits, adding 1.5 * 2^-18 those of 2^-41 of what is left.
+__device__ __forceinline__ long long row_units(float hi, float lo)
+{
+    const float a = hi + 12.0f, b = lo + 12.0f;
+    const float c = ((hi - (a - 12.0f)) + (lo - (b - 12.0f))) + 5.72204590e-06f;
+    constexpr int kA = 0x41400000, kC = 0x36C00000; // the bits of 12 and of 1.5 * 2^-18
+    const int whole = (__float_as_int(a) - kA) + (__float_as_int(b) - kA);
+    return static_cast<long long>(whole) * 2097152 + (__float_as_int(c) - kC);
 }
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -236,7 +269,7 @@ __device__ __forceinline__ long long sum_units(float high, float low0, float low
 // leaves no trace in the sums.
 struct WeightSum {
     f32x2 high, low;
-    f32x2 ch, nch, ncl;
+    f32x2 ch, cl;
     float cut;
     uint32_t th; // the lane's table entry with the exponent's and index's offset taken off
     float tl;
@@ -245,29 +278,23 @@ struct WeightSum {
     {
         high = low = pack(0.0f, 0.0f);
         ch = pack(s.ch, s.ch);
-        nch = pack(-s.ch, -s.ch);
-        ncl = pack(-s.cl, -s.cl);
+        cl = pack(s.cl, s.cl);
         cut = cut_;
         th = __float_as_uint(entry.x) - ((threadIdx.x & 31u) << 18) - (static_cast<uint32_t>(exponent) << 23);
         tl = entry.y;
     }
     __device__ __forceinline__ void add(float x0, float x1)
     {
-        constexpr float k1 = 0x1.62e430p-1f, k2 = 0x1.ebfbe0p-3f, k3 = 0x1.c6b08ep-5f, k4 = 0x1.3b2ab6p-7f; // ln(2)^k / k!
         const f32x2 shift = pack(kShift, kShift), top = pack(192.0f, 192.0f);
         const f32x2 x = pack(fmaxf(x0, cut), fmaxf(x1, cut));
-        const f32x2 z = pmul(x, ch);
-        const f32x2 u = padd(z, shift);
-        const f32x2 y = psub(psub(z, psub(u, shift)), pfma(x, ncl, pfma(x, nch, z))); // z - round(z), less z's own error
+        const f32x2 u = pfma(x, ch, shift);
+        const f32x2 y = pfma(x, cl, pfma(x, ch, psub(shift, u)));
         float u0, u1;
         unpack(u, u0, u1);
         const uint32_t b0 = __float_as_uint(u0), b1 = __float_as_uint(u1);
         const uint32_t t0 = __shfl_sync(0xffffffffu, th, b0), t1 = __shfl_sync(0xffffffffu, th, b1);
         const f32x2 r = pack(__shfl_sync(0xffffffffu, tl, b0), __shfl_sync(0xffffffffu, tl, b1));
-        const f32x2 p3 = pfma(y, pack(k4, k4), pack(k3, k3));
-        const f32x2 p2 = pfma(p3, y, pack(k2, k2));
-        const f32x2 p1 = pfma(p2, y, pack(k1, k1));
-        const f32x2 rest = pfma(p1, y, r);
+        const f32x2 rest = pfma(pfma(pfma(y, pack(kPow3, kPow3), pack(kPow2, kPow2)), y, pack(kPow1, kPow1)), y, r);
         // the bits of u are kShiftBits + 32 n + j: shifted, n is at the exponent and j at bits 18 to 22
         const f32x2 hi = pack(__uint_as_float((b0 << 18) + t0), __uint_as_float((b1 << 18) + t1));
         const f32x2 q = psub(padd(hi, top), top);
@@ -428,8 +455,15 @@ struct RowShared {
     long long in_row[kMaxParts];   // this row's parts
     RowStat row;                   // this row, then the one that the sequence stops at
     long long target;
-    int skip, last_chunk, last_row, draw_now, without, part, found, end;
+    int skip, last_chunk, last_row, draw_now, part, found, end;
 };
+
+__device__ __forceinline__ PartStat load_stat(const PartStat *st)
+{
+    const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(st));
+    return {__uint_as_float(w.x), static_cast<int>(w.y),
+            static_cast<long long>(static_cast<unsigned long long>(w.w) << 32 | w.z)};
+}
 
 // The row's parts put together, and the verdict on its draft; the whole CTA.
 template <bool kBf16>
@@ -446,8 +480,9 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
     const float xt = inside ? x.at(t) : -INFINITY;
     const float qt = j >= len || !inside ? 0.0f : p.q == nullptr ? 1.0f : p.q[d * p.ldq + t];
     const float ut = j < len ? p.accept_u[d] : 0.0f;
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < p.parts; i += kVerifyThreads)
+    const PartStat first = static_cast<int>(threadIdx.x) < p.parts ? load_stat(st + threadIdx.x) : PartStat{-INFINITY, 0, 0};
+    float top = first.top;
+    for (int i = threadIdx.x + kVerifyThreads; i < p.parts; i += kVerifyThreads)
         top = max_nan(top, __ldcg(&st[i].top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -489,13 +524,7 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
 #pragma unroll 1
         for (int i0 = 0; i0 < p.parts; i0 += kVerifyThreads) {
             const int i = i0 + static_cast<int>(threadIdx.x);
-            PartStat v = {-INFINITY, 0, 0};
-            if (i < p.parts) {
-                const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(st + i));
-                v.top = __uint_as_float(w.x);
-                v.exponent = static_cast<int>(w.y);
-                v.sum = static_cast<long long>(static_cast<unsigned long long>(w.w) << 32 | w.z);
-            }
+            const PartStat v = i0 == 0 ? first : i < p.parts ? load_stat(st + i) : PartStat{-INFINITY, 0, 0};
             int k;
             const bool live = to_row(v.top, v.exponent, ref, cut, r.exponent, s, entry, th, rest, k);
             const long long g = live ? rescale(v.sum, th, rest, k) : 0;
@@ -530,32 +559,44 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
 }
 
 // Position of the target weight u * (sum of `sum(i)`, i < n) and what is left of it
-// there; one warp.  Returns -1 where the sum is not positive.
-template <class Sum>
-__device__ __forceinline__ int find_target(int n, float u, Sum sum, long long &target)
+// there, to sh.part and sh.target; -1 where the sum is not positive.  The whole CTA
+// calls it, a thread for n / 256 positions in a row.
+template <class Sum> __device__ __forceinline__ void find_target(int n, float u, Sum sum, RowShared &sh)
 {
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int each = (n + kVerifyThreads - 1) / kVerifyThreads;
+    const int first = static_cast<int>(threadIdx.x) * each;
+    long long mine = 0;
+    for (int i = first; i < first + each && i < n; ++i)
+        mine += sum(i);
+    long long upto = warp_scan(mine);
+    if (lane == 31)
+        sh.sum[warp] = upto;
+    if (threadIdx.x == 0)
+        sh.part = -1;
+    __syncthreads();
     long long total = 0;
-    for (int i = lane; i < n; i += 32)
-        total += sum(i);
-    total = warp_sum(total);
-    if (total <= 0)
-        return -1;
-    target = __double2ll_rz(static_cast<double>(u) * static_cast<double>(total));
-    target = target < 0 ? 0 : target >= total ? total - 1 : target;
-    long long before = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const long long g = i0 + lane < n ? sum(i0 + lane) : 0;
-        const long long upto = warp_scan(g) + before;
-        const unsigned past = __ballot_sync(0xffffffffu, upto > target);
-        if (past != 0u) {
-            const int l = __ffs(static_cast<int>(past)) - 1;
-            target -= __shfl_sync(0xffffffffu, upto - g, l);
-            return i0 + l;
-        }
-        before = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+    for (int i = 0; i < kVerifyWarps; ++i) {
+        upto += i < warp ? sh.sum[i] : 0;
+        total += sh.sum[i];
     }
-    return -1;
+    if (total > 0) {
+        long long target = __double2ll_rz(static_cast<double>(u) * static_cast<double>(total));
+        target = target < 0 ? 0 : target >= total ? total - 1 : target;
+        long long at = upto - mine;
+        if (at <= target && target < upto)
+            for (int i = first;; ++i) {
+                const long long g = sum(i);
+                if (target < at + g) {
+                    sh.part = i;
+                    sh.target = target - at;
+                    break;
+                }
+                at += g;
+            }
+    }
+    __syncthreads();
 }
 
 // A row's weights in row units.
@@ -645,42 +686,36 @@ template <bool kBf16>
 __device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat &r, float T, int except, bool own, RowShared &sh)
 {
     using R = Row<kBf16>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const long long row = static_cast<long long>(b) * (p.L + 1) + r.position;
     const Weights<kBf16> w(p, row, r, T);
-    if (warp == 0) {
-        const float u = p.sample_u[b];
-        const long long *const in_row = p.in_row + row * p.parts;
-        const bool with = except >= 0 && except < p.V;
-        float hi = 0.0f, lo = 0.0f;
-        w.pair(with ? w.x.at(except) : -INFINITY, hi, lo);
-        const long long less_by = fixed(hi, lo, kRowUnits);
-        const int home = with ? (except + w.x.lead) / kPart : -1;
-        auto sum = [&](int i) { return own ? sh.in_row[i] : __ldcg(in_row + i); };
-        long long target = 0;
-        int c = -1;
-        if (with)
-            c = find_target(p.parts, u, [&](int i) {
-                const long long g = sum(i);
-                return i != home ? g : g > less_by ? g - less_by : 0;
-            }, target);
-        const bool all = c < 0; // nothing is left beside it: from everything
-        if (all)
-            c = find_target(p.parts, u, sum, target);
-        if (lane == 0) {
-            sh.part = c < 0 ? 0 : c; // (a row's total is positive)
-            sh.target = target;
-            sh.without = all ? -1 : except;
-        }
+    const float u = p.sample_u[b];
+    const long long *const in_row = p.in_row + row * p.parts;
+    auto sum = [&](int i) { return own ? sh.in_row[i] : __ldcg(in_row + i); };
+    int without = -1;
+    if (except >= 0 && except < p.V) {
+        float h, l;
+        w.pair(w.x.at(except), h, l);
+        const long long less_by = row_units(h, l);
+        const int home = (except + w.x.lead) / kPart;
+        find_target(p.parts, u, [&](int i) {
+            const long long g = sum(i);
+            return i != home ? g : g > less_by ? g - less_by : 0;
+        }, sh);
+        without = except;
     }
-    __syncthreads();
+    if (without < 0 || sh.part < 0) { // (or nothing is left beside it)
+        __syncthreads();
+        find_target(p.parts, u, sum, sh);
+        without = -1;
+    }
+    const int part = sh.part < 0 ? 0 : sh.part; // (a row's total is positive)
+    const long long target = sh.target;
     // kPart logits: a word a thread, as far as they go
     constexpr int kWords = kPart / R::kPer;
     static_assert(kWords <= kVerifyThreads, "a word a thread");
-    const int word = sh.part * kWords + static_cast<int>(threadIdx.x);
+    const int word = part * kWords + static_cast<int>(threadIdx.x);
     const int i0 = w.x.index(word);
-    const long long target = sh.target;
-    const int without = sh.without;
     long long g[R::kPer];
     float hi[R::kPer], lo[R::kPer];
     if (warp * 32 < kWords) {
@@ -688,7 +723,7 @@ __device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat
 #pragma unroll
         for (int e = 0; e < R::kPer; ++e) {
             w.pair(R::value(v, e), hi[e], lo[e]);
-            g[e] = i0 + e == without ? 0 : fixed(hi[e], lo[e], kRowUnits);
+            g[e] = i0 + e == without ? 0 : row_units(hi[e], lo[e]);
         }
     } else {
 #pragma unroll
@@ -937,7 +972,7 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
             const float bl = fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -bh));
             const float d = ph[e] - bh, bb = d - ph[e];
             const float lo = (pl[e] - bl) + ((ph[e] - (d - bb)) + (-bh - bb));
-            g[e] = d + lo > 0.0f ? fixed(d, lo, kRowUnits) : 0;
+            g[e] = d + lo > 0.0f ? row_units(d, lo) : 0;
         }
         return i0;
     };
@@ -964,17 +999,10 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
     if (sh.last_chunk == 0)
         return;
     __threadfence();
-    if (warp == 0) {
-        const long long *const sums = p.residual + static_cast<long long>(b) * p.slices;
-        long long target = 0;
-        const int at = find_target(p.slices, p.sample_u[b], [&](int i) { return __ldcg(sums + i); }, target);
-        if (lane == 0) {
-            sh.part = at;
-            sh.target = target;
-        }
-    }
-    __syncthreads();
+    const long long *const sums = p.residual + static_cast<long long>(b) * p.slices;
+    find_target(p.slices, p.sample_u[b], [&](int i) { return __ldcg(sums + i); }, sh);
     if (sh.part < 0) { // p nowhere above q: from p
+        __syncthreads();
         draw<kBf16>(p, b, r, T, -1, false, sh);
         return;
     }
