@@ -20,7 +20,7 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     w.counters_up_off = w.counters_down_off + static_cast<size_t>(H / 128) * 4;
     w.counters_bytes = static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4;
     w.logits_off = kCountersOff + counters_region(w.counters_bytes);
-    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 8);
+    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4 * kMoeMaxSplits);
     w.ids_off = w.masks_off + static_cast<size_t>(kMoeMaxTokens / kMoeTokenGroup) * (kMoeMaxExperts / 32) * 4;
     w.topw_off = w.ids_off + up256(static_cast<size_t>(M) * top_k * 4);
     w.wtok_off = w.topw_off + up256(static_cast<size_t>(M) * top_k * 4);

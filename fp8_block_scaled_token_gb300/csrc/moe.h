@@ -1,5 +1,5 @@
 // moe.h -- host-side plumbing of the mixture-of-experts layer (moe.cu,
-// moe_route.cu, moe_up.cu, moe_down.cu); not part of the public ABI.
+// moe_route.cu, moe_scored.cu, moe_up.cu, moe_down.cu); not part of the public ABI.
 #pragma once
 
 #include "internal.h"
@@ -10,6 +10,7 @@ constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxGroups = 32;
+constexpr int kMoeMaxSplits = 4; // of H in the router's product under scores
 constexpr int kMoeTokenGroup = 8; // tokens that one routing CTA multiplies an expert's router row with
 
 inline int moe_token_pad(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
@@ -23,7 +24,7 @@ struct MoeWorkspace {
     size_t route_off;         // arrival counters of the kMoeMaxTokens / kMoeTokenGroup groups of tokens, then a
                               // bit mask of the experts (kMoeMaxExperts / 32 words) for a given choice
     size_t chosen_off;        // 1 from the gate/up product's start to the down product's end: the masks are complete
-    size_t logits_off;        // [M][E] router logits, 8 bytes each (fp32, or pairs under scores)
+    size_t logits_off;        // [M][E] router logits; under scores [splits of H][M][E] partial sums
     size_t counters_up_off;   // arrival counters of the (active expert, 128 of I) pairs
     size_t counters_down_off; // arrival counters of the 128-row tiles of H
     size_t counters_bytes;    // of both
@@ -68,6 +69,7 @@ struct MoeLaunch {
 };
 
 MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms);
+fp8bs_status launch_moe_scored(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);
 fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);
 fp8bs_status launch_moe_up(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);
 fp8bs_status launch_moe_down(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);

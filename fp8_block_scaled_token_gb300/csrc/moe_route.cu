@@ -9,13 +9,6 @@
 //   w[m, j] = exp(l_j - l_max) / sum exp(l - l_max), the sum over the chosen
 //             experts (renormalised) or over all of them
 //
-// or, with scores and groups (choose_scored):
-//
-//   s = sigmoid(l) or softmax(l) over all experts,  c = s + bias
-//   groups of E / groups consecutive experts, the top_groups of largest sum of
-//   their one or two largest c; ids[m] = the top_k experts of largest c in those
-//   w = s of the chosen, over their sum where renormalised, times scale
-//
 // Grid: one CTA per (one or four experts, group of 8 tokens), then the CTAs of
 // the cast, a warp per (token, 128 of H).  The last CTA of a token group chooses for its
 // eight tokens and leaves a bit mask of the experts they chose; arrivals are
@@ -23,49 +16,13 @@
 // loads are issued for all eight tokens at once, and the choice keeps its
 // loops rolled (unrolled code run once costs more in instruction fetches than
 // it saves).
-#include <cmath>
 #include <cuda_bf16.h>
 
-#include "fp8bs_testing.h"
-#include "moe.h"
-#include "pair_math.cuh"
-#include "ptx.cuh"
-#include "quant_math.cuh"
+#include "moe_route.cuh"
 
 namespace fp8bs {
 
-constexpr int kRouteThreads = 256;
 constexpr int kRouteWide = 1024; // at most, for long rows
-constexpr int kTG = kMoeTokenGroup;
-static_assert(kRouteThreads / 32 == kTG, "one warp chooses for each token of a group");
-
-struct RouteParams {
-    int M, H, E, top_k, npad;
-    const uint16_t *x;
-    int ldx;
-    const void *wr;
-    int renorm;
-    int32_t *ids;
-    float *topw;
-    float *logits;
-    float *wtok;
-    unsigned *group_done; // arrival counters; moe_plan_kernel: [0], and its bit mask after the counters
-    unsigned *masks;      // [groups][kMoeMaxExperts / 32] chosen experts
-    uint8_t *xq;
-    float *xs;
-    unsigned long long *runs;
-    MoeScores sc;
-};
-
-// Order-preserving key of a logit: larger value, larger key; NaN is 0, below
-// every number.
-__device__ __forceinline__ uint32_t route_key(float v)
-{
-    const uint32_t b = __float_as_uint(v);
-    if (v != v)
-        return 0u;
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
 
 // One warp: the choice for token m.  Its E logits are in `l` (shared memory);
 // kInRegs (E <= 128): each lane keeps the keys of its experts lane, lane + 32,
@@ -146,207 +103,6 @@ __device__ __forceinline__ void choose(const RouteParams &p, int m, const float 
     }
 }
 
-// Whether the order of the scores plus bias is that of the logits, so that no
-// score is needed for the choice (and none loses digits next to 1 or to 0).
-__host__ __device__ __forceinline__ bool by_logit(const MoeScores &sc)
-{
-    return sc.bias == nullptr && (sc.top_groups == sc.groups || sc.group_best == 1);
-}
-
-__device__ __forceinline__ bool greater(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
-
-// One warp: the choice for token m by scores, bias and groups.  `c` and `l`
-// (shared memory): E pairs and E numbers of this warp.  Logits and scores are
-// pairs (pair_math.cuh): the sum of 5,120 products is a few 2^-25 off, where
-// fp32's own step at a logit of 3 is 2^-22 and a score next to 1 has lost
-// the difference of two logits; what is left decides.  A NaN orders below every number.
-__device__ __forceinline__ void choose_scored(const RouteParams &p, int m, float2 *c, float *l, unsigned *mask)
-{
-    const int lane = threadIdx.x & 31;
-    const MoeScores &sc = p.sc;
-    const float2 *const logits = reinterpret_cast<const float2 *>(p.logits) + static_cast<long long>(m) * p.E;
-    const float2 entry = kPow32[lane];
-    const bool plain = by_logit(sc);
-    float lmax = -INFINITY;
-#pragma unroll 4
-    for (int e = lane; e < p.E; e += 32) {
-        const float2 v = __ldcg(logits + e);
-        c[e] = v;
-        l[e] = v.x;
-        lmax = fmaxf(lmax, v.x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
-    if (!plain) {
-        Pair all = {1.0f, 0.0f};
-        if (!sc.sigmoid) {
-            all.hi = 0.0f;
-#pragma unroll 1
-            for (int e0 = 0; e0 < p.E; e0 += 32) {
-                const int e = e0 + lane;
-                const float2 v = e < p.E ? c[e] : make_float2(-INFINITY, 0.0f);
-                const Pair d = two_sum(v.x, -lmax);
-                const Pair a = exp_pair(fast_two_sum(d.hi, d.lo + v.y), entry);
-                all = add(all, a);
-                if (e < p.E)
-                    c[e] = make_float2(a.hi, a.lo);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                all = add(all, {__shfl_xor_sync(0xffffffffu, all.hi, o), __shfl_xor_sync(0xffffffffu, all.lo, o)});
-        }
-#pragma unroll 1
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            const float2 v = e < p.E ? c[e] : make_float2(0.0f, 0.0f);
-            Pair s = {v.x, v.y};
-            if (sc.sigmoid) { // through exp(-|l|), which cannot overflow
-                const bool neg = v.x < 0.0f;
-                const Pair a = exp_pair({neg ? v.x : -v.x, neg ? v.y : -v.y}, entry);
-                s = divide(neg ? a : Pair{1.0f, 0.0f}, add({1.0f, 0.0f}, a));
-            } else {
-                s = divide(s, all);
-            }
-            if (e < p.E) {
-                if (sc.bias != nullptr)
-                    s = add(s, {__ldg(sc.bias + e), 0.0f});
-                c[e] = make_float2(s.hi, s.lo);
-            }
-        }
-    }
-    __syncwarp();
-    const int per = p.E / sc.groups;
-    unsigned open = 0xffffffffu; // bit g * q: group g may be chosen from
-    int q = 1;                   // lanes of a group
-    if (sc.top_groups < sc.groups) {
-        while (2 * q * sc.groups <= 32)
-            q *= 2;
-        const int g = lane / q;
-        Pair b1 = {-INFINITY, 0.0f}, b2 = b1;
-        if (g < sc.groups) {
-#pragma unroll 1
-            for (int e = lane % q; e < per; e += q) {
-                const float2 v = c[g * per + e];
-                const Pair t = {v.x, v.y};
-                if (greater(t, b1)) {
-                    b2 = b1;
-                    b1 = t;
-                } else if (greater(t, b2)) {
-                    b2 = t;
-                }
-            }
-        }
-#pragma unroll 1
-        for (int o = q / 2; o > 0; o /= 2) {
-            const Pair o1 = {__shfl_xor_sync(0xffffffffu, b1.hi, o), __shfl_xor_sync(0xffffffffu, b1.lo, o)};
-            const Pair o2 = {__shfl_xor_sync(0xffffffffu, b2.hi, o), __shfl_xor_sync(0xffffffffu, b2.lo, o)};
-            const bool other = greater(o1, b1);
-            const Pair low = other ? b1 : o1; // the lesser of the two largest
-            b2 = greater(b2, o2) ? b2 : o2;
-            b2 = greater(low, b2) ? low : b2;
-            b1 = other ? o1 : b1;
-        }
-        const Pair score = sc.group_best == 2 ? add(b1, b2) : b1;
-        int rank = 0;
-#pragma unroll 1
-        for (int i = 0; i < sc.groups; ++i) {
-            const Pair t = {__shfl_sync(0xffffffffu, score.hi, i * q), __shfl_sync(0xffffffffu, score.lo, i * q)};
-            rank += greater(t, score) || (i < g && !greater(score, t)) ? 1 : 0;
-        }
-        open = __ballot_sync(0xffffffffu, g < sc.groups && rank < sc.top_groups);
-    }
-    unsigned taken = 0; // bit i: expert 32 i + lane
-    if (sc.top_groups < sc.groups) {
-#pragma unroll 1
-        for (int i = 0; 32 * i + lane < p.E; ++i)
-            if (!(open >> ((32 * i + lane) / per * q) & 1u))
-                taken |= 1u << i;
-    }
-    uint32_t kh = 0, kl = 0;
-    int mine = 0x7fffffff;
-    auto look = [&]() { // this lane's best that is not taken yet, ties to the lowest
-        kh = kl = 0;
-        mine = 0x7fffffff;
-#pragma unroll 1
-        for (int i = 0; 32 * i + lane < p.E; ++i) {
-            const float2 v = c[32 * i + lane];
-            const uint32_t h = route_key(v.x), w = route_key(v.y);
-            if (!(taken >> i & 1u) && (mine == 0x7fffffff || h > kh || (h == kh && w > kl))) {
-                kh = h;
-                kl = w;
-                mine = 32 * i + lane;
-            }
-        }
-    };
-    look();
-    int mine_e = 0;
-#pragma unroll 1
-    for (int j = 0; j < p.top_k; ++j) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, kh);
-        const uint32_t low = __reduce_max_sync(0xffffffffu, kh == top ? kl : 0u);
-        const int best = static_cast<int>(
-            __reduce_min_sync(0xffffffffu, kh == top && kl == low ? static_cast<uint32_t>(mine) : 0x7fffffffu));
-        if (lane == j)
-            mine_e = best;
-        if (lane == (best & 31)) {
-            taken |= 1u << (best >> 5);
-            look();
-        }
-    }
-    const bool chosen = lane < p.top_k;
-    const float lm = l[mine_e];
-    float top = chosen ? lm : -INFINITY;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float w;
-    if (sc.sigmoid) { // renormalised: over exp of the largest logit where all are negative, so that not all of them vanish
-        const float t = p.renorm ? fminf(top, 0.0f) : 0.0f;
-        w = lm >= 0.0f ? __fdiv_rn(1.0f, 1.0f + expf(-lm)) : __fdiv_rn(expf(lm - t), 1.0f + expf(lm));
-    } else {
-        w = expf(lm - (p.renorm ? top : lmax));
-    }
-    if (p.renorm || !sc.sigmoid) {
-        float sum = chosen ? w : 0.0f;
-        if (!p.renorm) {
-            sum = 0.0f;
-#pragma unroll 1
-            for (int e = lane; e < p.E; e += 32)
-                sum += expf(l[e] - lmax);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        w = __fdiv_rn(w, sum);
-    }
-    w *= sc.scale;
-    if (chosen) {
-        p.ids[static_cast<long long>(m) * p.top_k + lane] = mine_e;
-        p.topw[static_cast<long long>(m) * p.top_k + lane] = w;
-        if (p.wtok != nullptr) {
-            p.wtok[static_cast<long long>(mine_e) * p.npad + m] = w;
-            atomicOr(mask + (mine_e >> 5), 1u << (mine_e & 31));
-        }
-    }
-}
-
-// One warp: one (token, 128 of H) group of the cast; scales [H/128][M].
-__device__ __forceinline__ void cast_group(const RouteParams &p, long long group)
-{
-    const int lane = threadIdx.x & 31;
-    const int kg = p.H / 128;
-    if (group >= static_cast<long long>(p.M) * kg)
-        return;
-    const int m = static_cast<int>(group % p.M), g = static_cast<int>(group / p.M);
-    const uint2 raw = *reinterpret_cast<const uint2 *>(p.x + static_cast<long long>(m) * p.ldx + g * 128 + lane * 4);
-    uint32_t codes;
-    const float s = quant_group_warp(raw, codes);
-    *reinterpret_cast<uint32_t *>(p.xq + static_cast<long long>(m) * p.H + g * 128 + lane * 4) = codes;
-    if (lane == 0)
-        p.xs[g * p.M + m] = s;
-}
-
 // kEx experts a CTA: one where the CTAs then fill the GPU at most twice (each
 // reads its tokens' rows of x from L2: 42 MB at 64 tokens, 64 experts and H =
 // 5,120), four otherwise.
@@ -354,17 +110,15 @@ __device__ __forceinline__ void cast_group(const RouteParams &p, long long group
 // H above 4,096, where a thread for every eight values of H puts the whole
 // row's loads in flight at once (M = 8, 64 experts, H = 5,120: the layer 91.8
 // -> 90.9 us; at H = 2,048 the smaller register budget costs 0.2 us).
-// kScored: choose_scored, with the logits as pairs and its shared memory behind the launch.
-template <bool kBf16, int kEx, int kMost, bool kScored>
+template <bool kBf16, int kEx, int kMost>
 __global__ void __launch_bounds__(kMost) moe_route_kernel(const RouteParams p)
 {
     __shared__ float part[kMost / 32][kEx * kTG];
     __shared__ unsigned arrived;
     __shared__ unsigned smask[kMoeMaxExperts / 32];
-    __shared__ float logit[kScored ? 1 : kTG][kScored ? 1 : kMoeMaxExperts];
-    extern __shared__ float2 scored[]; // kScored: a warp's E pairs, all warps', then E numbers each
+    __shared__ float logit[kTG][kMoeMaxExperts];
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        atomicAdd(p.runs + (kScored ? FP8BS_RUNS_MOE_ROUTE_GROUPED : FP8BS_RUNS_MOE_ROUTE), 1ull);
+        atomicAdd(p.runs + FP8BS_RUNS_MOE_ROUTE, 1ull);
     grid_launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -455,21 +209,10 @@ __global__ void __launch_bounds__(kMost) moe_route_kernel(const RouteParams p)
     if (threadIdx.x < kEx * kTG) {
         const int t = threadIdx.x % kTG, e = e0 + threadIdx.x / kTG;
         if (t < nt && e < p.E) {
-            if (kScored) {
-                Pair s = {part[0][threadIdx.x], 0.0f};
-                for (int i = 1; i < warps; ++i) {
-                    const Pair a = two_sum(s.hi, part[i][threadIdx.x]);
-                    s = {a.hi, s.lo + a.lo};
-                }
-                s = fast_two_sum(s.hi, s.lo);
-                __stcg(reinterpret_cast<float2 *>(p.logits) + static_cast<long long>(t0 + t) * p.E + e,
-                       make_float2(s.hi, s.lo));
-            } else {
-                float s = part[0][threadIdx.x];
-                for (int i = 1; i < warps; ++i)
-                    s += part[i][threadIdx.x];
-                __stcg(p.logits + static_cast<long long>(t0 + t) * p.E + e, s);
-            }
+            float s = part[0][threadIdx.x];
+            for (int i = 1; i < warps; ++i)
+                s += part[i][threadIdx.x];
+            __stcg(p.logits + static_cast<long long>(t0 + t) * p.E + e, s);
             if (p.wtok != nullptr)
                 __stcg(p.wtok + static_cast<long long>(e) * p.npad + t0 + t, 0.0f);
         }
@@ -483,10 +226,7 @@ __global__ void __launch_bounds__(kMost) moe_route_kernel(const RouteParams p)
     if (arrived != static_cast<unsigned>(per_group - 1))
         return;
     __threadfence(); // the other CTAs' logits and zeroed weights, for every thread of this one
-    if (kScored) {
-        if (warp < nt)
-            choose_scored(p, t0 + warp, scored + warp * p.E, reinterpret_cast<float *>(scored + kTG * p.E) + warp * p.E, smask);
-    } else if (warp < nt) {
+    if (warp < nt) {
         float *const l = logit[warp];
         for (int i = lane; i < p.E; i += 32)
             l[i] = __ldcg(p.logits + static_cast<long long>(t0 + warp) * p.E + i);
@@ -549,14 +289,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_plan_kernel(const RoutePara
         p.group_done[0] = 0u;
 }
 
-template <bool kScored> static auto route_kernel(bool bf, bool four, bool wide)
-{
-    return four   ? (bf ? moe_route_kernel<true, 4, kRouteThreads, kScored> : moe_route_kernel<false, 4, kRouteThreads, kScored>)
-           : wide ? (bf ? moe_route_kernel<true, 1, kRouteWide, kScored> : moe_route_kernel<false, 1, kRouteWide, kScored>)
-                  : (bf ? moe_route_kernel<true, 1, kRouteThreads, kScored> : moe_route_kernel<false, 1, kRouteThreads, kScored>);
-}
-
-fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev)
+RouteParams route_params(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev)
 {
     RouteParams p = {};
     p.M = L.M;
@@ -578,7 +311,15 @@ fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const D
     p.xq = L.workspace + w.xq_off;
     p.xs = reinterpret_cast<float *>(L.workspace + w.xs_off);
     p.runs = dev.runs;
-    p.sc = L.scores;
+    return p;
+}
+
+fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev)
+{
+    if (L.scores.scored)
+        return launch_moe_scored(L, w, dev);
+    const RouteParams p = route_params(L, w, dev);
+    const bool layer = L.w13 != nullptr;
     const int groups = (L.M + kTG - 1) / kTG;
     const bool four = L.E * groups > 2 * dev.sms; // experts a CTA
     const bool wide = L.wr != nullptr && !four && L.H > 4096;
@@ -595,16 +336,11 @@ fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const D
     cfg.attrs = attr;
     cfg.numAttrs = (L.flags & FP8BS_FLAG_OVERLAP_PREV) ? 1 : 0;
     const bool bf = L.wr_type == FP8BS_BF16;
-    if (L.wr == nullptr)
-        return launch_status(cudaLaunchKernelEx(&cfg, moe_plan_kernel, p));
-    if (!L.scores.scored)
-        return launch_status(cudaLaunchKernelEx(&cfg, route_kernel<false>(bf, four, wide), p));
-    cfg.dynamicSmemBytes = static_cast<size_t>(kTG) * L.E * 12;
-    static unsigned long long done[6];
-    const auto kernel = route_kernel<true>(bf, four, wide);
-    const fp8bs_status st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kTG * kMoeMaxExperts * 12, dev.device,
-                                             done + (bf ? 3 : 0) + (four ? 2 : wide ? 1 : 0));
-    return st != FP8BS_OK ? st : launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
+    auto kernel = L.wr == nullptr ? moe_plan_kernel
+                  : four ? (bf ? moe_route_kernel<true, 4, kRouteThreads> : moe_route_kernel<false, 4, kRouteThreads>)
+                  : wide ? (bf ? moe_route_kernel<true, 1, kRouteWide> : moe_route_kernel<false, 1, kRouteWide>)
+                         : (bf ? moe_route_kernel<true, 1, kRouteThreads> : moe_route_kernel<false, 1, kRouteThreads>);
+    return launch_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 } // namespace fp8bs

@@ -1,0 +1,480 @@
+// moe_scored.cu -- the first kernel of an expert layer whose experts are chosen by
+// scores, bias and groups: router product, choice, weights, the sets of experts,
+// and the E4M3 cast of the activations beside it (as moe_route.cu).
+//
+//   l[m, e] = sum_h x[m, h] * wr[e, h]
+//   s = sigmoid(l) or softmax(l) over all experts,  c = s + bias
+//   groups of E / groups consecutive experts, the top_groups of largest sum of
+//   their one or two largest c; ids[m] = the top_k experts of largest c in those
+//   w = s of the chosen, over their sum where renormalised, times scale
+//
+// Logits and scores are pairs of fp32 numbers (pair_math.cuh) from the warps'
+// partial sums on: a sum of 5,120 products is then a few 2^-25 off, where fp32's own
+// step at a logit of 3 is 2^-22 and a score next to 1 has lost the difference of two
+// logits.  What is left decides.
+//
+// Product: a warp holds 256 of H of eight tokens in registers and runs through up
+// to eight experts' rows; the eight sums are put together over the lanes by halving
+// (nine shuffles for eight sums).  x is read once for those experts, H is split over
+// the warps of a CTA and up to four CTAs, whose partial sums the chooser adds in
+// order.  The last CTA of a token group chooses for its eight tokens, a warp each;
+// arrivals are counted, nobody waits.  A few microseconds of latency, not
+// bandwidth, and much of it the fetching of instructions that run once: loops stay
+// rolled (the choice unrolled into registers, 74 KB of code, took 19 us in all for 8
+// tokens of 256 experts, where its instructions alone would take 1.5).
+#include <cmath>
+
+#include "moe_route.cuh"
+#include "pair_math.cuh"
+
+namespace fp8bs {
+
+struct ScoredParams {
+    RouteParams r;
+    MoeScores sc;
+    int hw, splits, loops; // warps that share H in a CTA, CTAs that do, 256-wide units of a warp
+    int ex, sets;          // experts of a warp (2, 4 or 8), CTAs over the experts
+};
+
+// Whether the order of the scores plus bias is that of the logits, so that no
+// score is needed for the choice (and none loses digits next to 1 or to 0).
+__device__ __forceinline__ bool by_logit(const MoeScores &sc)
+{
+    return sc.bias == nullptr && (sc.top_groups == sc.groups || sc.group_best == 1);
+}
+
+__device__ __forceinline__ bool greater(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / b for 1 <= b <= 2^10.
+__device__ __forceinline__ Pair inverse(Pair b)
+{
+    const float q = rcp_approx(b.hi);
+    return fast_two_sum(q, q * (fmaf(-q, b.hi, 1.0f) - q * b.lo));
+}
+
+__device__ __forceinline__ Pair times(Pair a, Pair b)
+{
+    const float p = a.hi * b.hi;
+    return fast_two_sum(p, fmaf(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+
+// One warp: the choice for token m.  `c` and `l`: E pairs and E numbers of this
+// warp in shared memory, expert 32 i + lane the lane's own.  A NaN orders below
+// every number.  `mask`: the token group's bit mask of experts (shared).
+__device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, float2 *c, float *l, unsigned *mask)
+{
+    const RouteParams &p = q.r;
+    const MoeScores &sc = q.sc;
+    const int lane = threadIdx.x & 31;
+    const float2 entry = kPow32[lane];
+    float lmax = -INFINITY;
+#pragma unroll 1
+    for (int e0 = lane; e0 < p.E; e0 += 128) {
+        float part[4][kMoeMaxSplits];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < kMoeMaxSplits; ++s)
+                part[i][s] = s < q.splits && e0 + 32 * i < p.E
+                                 ? __ldcg(p.logits + (static_cast<long long>(s) * p.M + m) * p.E + e0 + 32 * i) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Pair s = {part[i][0], 0.0f};
+#pragma unroll
+            for (int k = 1; k < kMoeMaxSplits; ++k) {
+                const Pair a = two_sum(s.hi, part[i][k]);
+                s = {a.hi, s.lo + a.lo};
+            }
+            s = fast_two_sum(s.hi, s.lo);
+            if (e0 + 32 * i < p.E) {
+                c[e0 + 32 * i] = make_float2(s.hi, s.lo);
+                l[e0 + 32 * i] = s.hi;
+                lmax = fmaxf(lmax, s.hi);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
+    if (!by_logit(sc)) {
+        Pair all = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int e0 = lane; e0 - lane < p.E; e0 += 64) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = e0 + 32 * i;
+                const float2 v = e < p.E ? c[e] : make_float2(0.0f, 0.0f);
+                Pair s;
+                if (sc.sigmoid) { // through exp(-|l|), which cannot overflow
+                    const bool neg = v.x < 0.0f;
+                    const Pair a = exp_pair({neg ? v.x : -v.x, neg ? v.y : -v.y}, entry);
+                    const Pair r = inverse(add({1.0f, 0.0f}, a));
+                    s = neg ? times(a, r) : r;
+                    if (sc.bias != nullptr && e < p.E)
+                        s = add(s, {__ldg(sc.bias + e), 0.0f});
+                } else {
+                    const Pair d = two_sum(v.x, -lmax);
+                    s = exp_pair(fast_two_sum(d.hi, d.lo + v.y), entry);
+                    if (e < p.E)
+                        all = add(all, s);
+                }
+                if (e < p.E)
+                    c[e] = make_float2(s.hi, s.lo);
+            }
+        }
+        if (!sc.sigmoid) {
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1)
+                all = add(all, {__shfl_xor_sync(0xffffffffu, all.hi, o), __shfl_xor_sync(0xffffffffu, all.lo, o)});
+            const Pair r = inverse(all);
+#pragma unroll 2
+            for (int e = lane; e < p.E; e += 32) {
+                const float2 v = c[e];
+                Pair s = times({v.x, v.y}, r);
+                if (sc.bias != nullptr)
+                    s = add(s, {__ldg(sc.bias + e), 0.0f});
+                c[e] = make_float2(s.hi, s.lo);
+            }
+        }
+    }
+    __syncwarp();
+    unsigned taken = 0; // bit i: expert 32 i + lane cannot be chosen (any more)
+    if (sc.top_groups < sc.groups) {
+        const int per = p.E / sc.groups;
+        int w = 1; // lanes of a group
+        while (2 * w * sc.groups <= 32)
+            w *= 2;
+        const int g = lane / w;
+        Pair b1 = {-INFINITY, 0.0f}, b2 = b1; // its two largest
+        if (g < sc.groups) {
+#pragma unroll 4
+            for (int e = lane % w; e < per; e += w) {
+                const float2 v = c[g * per + e];
+                const Pair t = {v.x, v.y};
+                const bool first = greater(t, b1);
+                const Pair low = first ? b1 : t;
+                b1 = first ? t : b1;
+                b2 = greater(low, b2) ? low : b2;
+            }
+        }
+#pragma unroll 1
+        for (int o = w / 2; o > 0; o /= 2) {
+            const Pair o1 = {__shfl_xor_sync(0xffffffffu, b1.hi, o), __shfl_xor_sync(0xffffffffu, b1.lo, o)};
+            const Pair o2 = {__shfl_xor_sync(0xffffffffu, b2.hi, o), __shfl_xor_sync(0xffffffffu, b2.lo, o)};
+            const bool other = greater(o1, b1);
+            const Pair low = other ? b1 : o1; // the lesser of the two largest
+            b2 = greater(b2, o2) ? b2 : o2;
+            b2 = greater(low, b2) ? low : b2;
+            b1 = other ? o1 : b1;
+        }
+        const Pair score = sc.group_best == 2 ? add(b1, b2) : b1;
+        int rank = 0;
+#pragma unroll 2
+        for (int i = 0; i < sc.groups; ++i) {
+            const Pair t = {__shfl_sync(0xffffffffu, score.hi, i * w), __shfl_sync(0xffffffffu, score.lo, i * w)};
+            rank += greater(t, score) || (i < g && !greater(score, t)) ? 1 : 0;
+        }
+        const unsigned open = __ballot_sync(0xffffffffu, g < sc.groups && rank < sc.top_groups);
+        const unsigned inv = (1u << 20) / per + 1; // e / per = e * inv >> 20 for e < 512, per <= 512
+#pragma unroll 2
+        for (int i = 0; 32 * i + lane < p.E; ++i)
+            if (!(open >> ((((32 * i + lane) * inv) >> 20) * w & 31) & 1u))
+                taken |= 1u << i;
+    }
+    // A lane's two best that are not taken, ties to the lowest; it looks again
+    // only after both are.
+    uint32_t h1, l1, h2, l2;
+    int e1, e2;
+    auto look = [&]() {
+        h1 = l1 = h2 = l2 = 0;
+        e1 = e2 = 0x7fffffff;
+#pragma unroll 2
+        for (int i = 0; 32 * i + lane < p.E; ++i) {
+            const float2 v = c[32 * i + lane];
+            const uint32_t h = route_key(v.x), w = route_key(v.y);
+            const bool is = (taken >> i & 1u) == 0u;
+            const bool first = is && (e1 == 0x7fffffff || h > h1 || (h == h1 && w > l1));
+            const bool second = is && !first && (e2 == 0x7fffffff || h > h2 || (h == h2 && w > l2));
+            h2 = first ? h1 : second ? h : h2;
+            l2 = first ? l1 : second ? w : l2;
+            e2 = first ? e1 : second ? 32 * i + lane : e2;
+            h1 = first ? h : h1;
+            l1 = first ? w : l1;
+            e1 = first ? 32 * i + lane : e1;
+        }
+    };
+    look();
+    int mine_e = 0;
+#pragma unroll 1
+    for (int j = 0; j < p.top_k; ++j) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, h1);
+        unsigned at = __ballot_sync(0xffffffffu, e1 != 0x7fffffff && h1 == top);
+        if ((at & (at - 1)) != 0u) { // equal high parts: the low parts, then the lowest expert
+            const bool in = (at >> lane & 1u) != 0u;
+            const uint32_t low = __reduce_max_sync(0xffffffffu, in ? l1 : 0u);
+            const uint32_t e = __reduce_min_sync(0xffffffffu, in && l1 == low ? static_cast<uint32_t>(e1) : 0x7fffffffu);
+            at = 1u << (e & 31);
+        }
+        const int from = __ffs(static_cast<int>(at)) - 1;
+        const int e = __shfl_sync(0xffffffffu, e1, from);
+        mine_e = lane == j ? e : mine_e;
+        if (lane == from) {
+            taken |= 1u << (e >> 5);
+            if (e2 != 0x7fffffff) {
+                h1 = h2;
+                l1 = l2;
+                e1 = e2;
+                h2 = 0;
+                e2 = 0x7fffffff;
+            } else {
+                look();
+            }
+        }
+    }
+    const bool chosen = lane < p.top_k;
+    const float lm = l[mine_e];
+    float top = chosen ? lm : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // sigmoid, renormalised: over exp of the largest logit where all are negative, so that not all of them vanish
+    const float shift = !sc.sigmoid ? (p.renorm ? top : lmax) : p.renorm ? fminf(top, 0.0f) : 0.0f;
+    const float ex = expf(sc.sigmoid && lm >= 0.0f ? -lm : lm - shift);
+    float w = ex;
+    if (sc.sigmoid)
+        w = __fdiv_rn(lm >= 0.0f ? 1.0f : ex, 1.0f + (lm >= 0.0f ? ex : expf(lm)));
+    if (p.renorm || !sc.sigmoid) {
+        float sum = chosen ? w : 0.0f;
+        if (!p.renorm) {
+            sum = 0.0f;
+#pragma unroll 2
+            for (int e = lane; e < p.E; e += 32)
+                sum += expf(l[e] - lmax);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        w = __fdiv_rn(w, sum);
+    }
+    w *= sc.scale;
+    if (chosen) {
+        p.ids[static_cast<long long>(m) * p.top_k + lane] = mine_e;
+        p.topw[static_cast<long long>(m) * p.top_k + lane] = w;
+        if (p.wtok != nullptr) {
+            p.wtok[static_cast<long long>(mine_e) * p.npad + m] = w;
+            atomicOr(mask + (mine_e >> 5), 1u << (mine_e & 31));
+        }
+    }
+}
+
+// The sums over the warp of eight values a lane: on return the first is that of
+// value 4 b4 + 2 b3 + b2 of the lane's number's bits.
+__device__ __forceinline__ float sums_of_8(float (&v)[8])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16, n = 4; n >= 1; o /= 2, n /= 2) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n];
+            v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// Raw bits of eight router weights of a lane.
+template <bool kBf16> struct Weights8 {
+    uint4 w[kBf16 ? 1 : 2];
+    __device__ __forceinline__ void load(const RouteParams &p, int e, int h, bool there)
+    {
+#pragma unroll
+        for (int i = 0; i < (kBf16 ? 1 : 2); ++i)
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (there) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.wr) +
+                                                               (static_cast<long long>(e) * p.H + h) * (kBf16 ? 2 : 4));
+            w[0] = src[0];
+            if (!kBf16)
+                w[kBf16 ? 0 : 1] = src[1];
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < (kBf16 ? 1 : 2); ++i) {
+            const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (kBf16) {
+                    v[2 * k] = bf16_lo(a[k]);
+                    v[2 * k + 1] = bf16_hi(a[k]);
+                } else {
+                    v[4 * i + k] = __uint_as_float(a[k]);
+                }
+            }
+        }
+    }
+};
+
+constexpr int kMostEx = 8; // experts of a warp
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kRouteThreads, 2) moe_scored_kernel(const __grid_constant__ ScoredParams q)
+{
+    __shared__ float part[kTG][kMostEx][kTG]; // [warp][expert][token]
+    __shared__ unsigned arrived;
+    __shared__ unsigned smask[kMoeMaxExperts / 32];
+    extern __shared__ float2 scratch[]; // a warp's E pairs, all warps', then E numbers each
+    const RouteParams &p = q.r;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        atomicAdd(p.runs + FP8BS_RUNS_MOE_SCORED, 1ull);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int groups = (p.M + kTG - 1) / kTG;
+    const int per_group = q.sets * q.splits; // CTAs
+    const int routing = per_group * groups;
+    if (static_cast<int>(blockIdx.x) >= routing) {
+        cast_group(p, static_cast<long long>(blockIdx.x - routing) * (kRouteThreads / 32) + warp);
+        return;
+    }
+    const int tg = blockIdx.x / per_group, in = blockIdx.x - tg * per_group;
+    const int set = in / q.splits, split = in - set * q.splits;
+    const int share = warp / q.hw; // of the CTA's experts
+    const int t0 = tg * kTG;
+    const int nt = p.M - t0 < kTG ? p.M - t0 : kTG;
+    const int e0 = (set * (kRouteThreads / 32 / q.hw) + share) * q.ex; // this warp's experts
+    const uint16_t *const x0 = p.x + static_cast<long long>(t0) * p.ldx;
+#pragma unroll 1
+    for (int n = 0; n < q.loops; ++n) {
+        const int h = ((n * q.splits + split) * q.hw + warp - share * q.hw) * 256 + lane * 8;
+        const bool in_row = h < p.H;
+        uint4 xr[kTG];
+#pragma unroll
+        for (int t = 0; t < kTG; ++t) {
+            xr[t] = make_uint4(0u, 0u, 0u, 0u);
+            if (in_row && t < nt)
+                xr[t] = *reinterpret_cast<const uint4 *>(x0 + static_cast<long long>(t) * p.ldx + h);
+        }
+        Weights8<kBf16> next[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            next[i].load(p, e0 + i, h, in_row && e0 + i < p.E);
+        float x[kTG][8];
+#pragma unroll
+        for (int t = 0; t < kTG; ++t) {
+            const uint32_t a[4] = {xr[t].x, xr[t].y, xr[t].z, xr[t].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[t][2 * i] = bf16_lo(a[i]);
+                x[t][2 * i + 1] = bf16_hi(a[i]);
+            }
+        }
+#pragma unroll 1
+        for (int k = 0; k < q.ex; k += 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float w[8], v[kTG];
+                next[i].values(w);
+                const int e = e0 + k + 2 + i;
+                next[i].load(p, e, h, in_row && k + 2 < q.ex && e < p.E);
+#pragma unroll
+                for (int t = 0; t < kTG; ++t) {
+                    float a = 0.0f, b = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        fma2(a, b, x[t][j], x[t][j + 1], w[j], w[j + 1]);
+                    v[t] = a + b;
+                }
+                const float sum = sums_of_8(v);
+                float *const to = &part[warp][k + i][lane >> 2];
+                if ((lane & 3) == 0)
+                    *to = n == 0 ? sum : *to + sum;
+            }
+        }
+    }
+    __syncthreads();
+    // the warps that share H, in order; a thread per (share of the experts, expert, token)
+    const int shares = kRouteThreads / 32 / q.hw;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < shares * q.ex * kTG; i += kRouteThreads) {
+        const int t = i % kTG, s = i / (kTG * q.ex), k = i / kTG - s * q.ex;
+        const int e = (set * shares + s) * q.ex + k;
+        if (t < nt && e < p.E) {
+            Pair a = {part[s * q.hw][k][t], 0.0f};
+            for (int j = 1; j < q.hw; ++j) {
+                const Pair b = two_sum(a.hi, part[s * q.hw + j][k][t]);
+                a = {b.hi, a.lo + b.lo};
+            }
+            __stcg(p.logits + (static_cast<long long>(split) * p.M + t0 + t) * p.E + e, a.hi + a.lo);
+            if (p.wtok != nullptr && split == 0)
+                __stcg(p.wtok + static_cast<long long>(e) * p.npad + t0 + t, 0.0f);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        arrived = atomic_add_acq_rel_gpu(p.group_done + tg, 1u);
+    if (threadIdx.x < kMoeMaxExperts / 32)
+        smask[threadIdx.x] = 0u;
+    __syncthreads();
+    if (arrived != static_cast<unsigned>(per_group - 1))
+        return;
+    __threadfence(); // the other CTAs' sums and zeroed weights, for every thread of this one
+    if (warp < nt)
+        choose_scored(q, t0 + warp, scratch + warp * p.E, reinterpret_cast<float *>(scratch + kTG * p.E) + warp * p.E, smask);
+    if (threadIdx.x == 0)
+        p.group_done[tg] = 0u;
+    __syncthreads();
+    if (p.wtok != nullptr && threadIdx.x < kMoeMaxExperts / 32)
+        p.masks[tg * (kMoeMaxExperts / 32) + threadIdx.x] = smask[threadIdx.x];
+}
+
+fp8bs_status launch_moe_scored(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev)
+{
+    ScoredParams q = {};
+    q.r = route_params(L, w, dev);
+    q.sc = L.scores;
+    constexpr int kWarps = kRouteThreads / 32;
+    const int units = (L.H + 255) / 256;
+    q.hw = 1;
+    while (q.hw < kWarps && q.hw < units)
+        q.hw *= 2;
+    q.splits = (units + q.hw - 1) / q.hw < kMoeMaxSplits ? (units + q.hw - 1) / q.hw : kMoeMaxSplits;
+    q.loops = (units + q.hw * q.splits - 1) / (q.hw * q.splits);
+    const int groups = (L.M + kTG - 1) / kTG;
+    // experts of a warp: as many as leave a CTA for every SM
+    auto sets = [&](int k) { return (L.E + k * (kWarps / q.hw) - 1) / (k * (kWarps / q.hw)); };
+    q.ex = kMostEx;
+    while (q.ex > 2 && sets(q.ex) * q.splits * groups < dev.sms)
+        q.ex /= 2;
+    q.sets = sets(q.ex);
+    const long long cast = L.w13 != nullptr ? (static_cast<long long>(L.M) * (L.H / 128) + kWarps - 1) / kWarps : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cast + static_cast<long long>(q.sets) * q.splits * groups), 1, 1);
+    cfg.blockDim = dim3(kRouteThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(kTG) * L.E * 12;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (L.flags & FP8BS_FLAG_OVERLAP_PREV) ? 1 : 0;
+    const bool bf = L.wr_type == FP8BS_BF16;
+    auto kernel = bf ? moe_scored_kernel<true> : moe_scored_kernel<false>;
+    static unsigned long long done[2];
+    const fp8bs_status st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kTG * kMoeMaxExperts * 12, dev.device,
+                                             done + (bf ? 1 : 0));
+    return st != FP8BS_OK ? st : launch_status(cudaLaunchKernelEx(&cfg, kernel, q));
+}
+
+} // namespace fp8bs

@@ -49,7 +49,7 @@ extern "C" {
 #define FP8BS_RUNS_VERIFY_ROWS 98
 #define FP8BS_RUNS_VERIFY_RESIDUAL 99
 /* Routing by scores, bias and groups. */
-#define FP8BS_RUNS_MOE_ROUTE_GROUPED 100
+#define FP8BS_RUNS_MOE_SCORED 100
 #define FP8BS_RUNS_SLOTS 128
 
 /*

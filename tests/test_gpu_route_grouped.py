@@ -20,7 +20,7 @@ from tests.test_gpu_moe import Layer, runs_moe_gemm
 
 pytestmark = pytest.mark.gpu
 
-RUNS_ROUTE_GROUPED, RUNS_MOE_PLAN = 100, 89
+RUNS_MOE_SCORED, RUNS_MOE_PLAN = 100, 89
 GAP, W_TOL = 4e-6, 5e-6
 
 
@@ -65,7 +65,7 @@ def test_matches_64_bits(M, E, k, H, G, tg, best):
         x, wr, b = _inputs(M, E, H, bias, dtype, seed=SEEDS.get((M, E, n), 10 * M + E + n))
         with Ran() as r:
             got = _call(x, wr, k, b, **kw)
-        assert r.launched() == {RUNS_ROUTE_GROUPED: 1}
+        assert r.launched() == {RUNS_MOE_SCORED: 1}
         _check(got, _logits(x, wr), k, b, **kw)
 
 
@@ -164,7 +164,7 @@ def test_the_layer_is_the_choice_and_the_experts(M, E, k, H, I, G, tg, tiled):
     ops, work = t.operands(tiled), t.workspace()
     with Ran() as r:
         y, ids, w = fb.fp8_moe_layer_grouped(t.x.cuda(), t.wr.cuda(), k, *ops, workspace=work, **kw)
-    assert r.launched() == {RUNS_ROUTE_GROUPED: 1, runs_moe_gemm(0, M): 1, runs_moe_gemm(1, M): 1}
+    assert r.launched() == {RUNS_MOE_SCORED: 1, runs_moe_gemm(0, M): 1, runs_moe_gemm(1, M): 1}
     ids2, w2 = fb.moe_route_grouped(t.x.cuda(), t.wr.cuda(), k, workspace=work, **kw)
     assert torch.equal(ids, ids2) and torch.equal(w, w2)
     y2 = fb.fp8_moe_experts(t.x.cuda(), ids, w, *ops, experts=E, workspace=work)
