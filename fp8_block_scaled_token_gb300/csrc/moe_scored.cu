@@ -65,155 +65,163 @@ __device__ __forceinline__ Pair times(Pair a, Pair b)
     return fast_two_sum(p, fmaf(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
 }
 
-// One warp: the choice for token m.  `c` and `l`: E pairs and E numbers of this
-// warp in shared memory, expert 32 i + lane the lane's own.  A NaN orders below
-// every number.  `mask`: the token group's bit mask of experts (shared).
-__device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, float2 *c, float *l, unsigned *mask)
+// Four bytes from global to shared memory, and the wait for this thread's.
+__device__ __forceinline__ void copy_async_4(float *to, const float *from)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// One warp: the choice for token m.  `a`: kMoeMaxSplits planes of E numbers of this
+// warp in shared memory, first the partial sums of the logits, then the high and low
+// parts of the scores and the logits; expert 32 i + lane is the lane's own.  A NaN
+// orders below every number.  `mask`: the token group's bit mask of experts (shared).
+__device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, float *a, unsigned *mask)
 {
     const RouteParams &p = q.r;
     const MoeScores &sc = q.sc;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, E = p.E;
     const float2 entry = kPow32[lane];
+    float *const hi = a, *const lo = a + E, *const l = a + 2 * E;
+#pragma unroll 1
+    for (int s = 0; s < q.splits; ++s) {
+        const float *const from = p.logits + (static_cast<long long>(s) * p.M + m) * E;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32)
+            copy_async_4(a + s * E + e, from + e);
+    }
+    copy_async_wait();
     float lmax = -INFINITY;
 #pragma unroll 1
-    for (int e0 = lane; e0 < p.E; e0 += 128) {
-        float part[4][kMoeMaxSplits];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int s = 0; s < kMoeMaxSplits; ++s)
-                part[i][s] = s < q.splits && e0 + 32 * i < p.E
-                                 ? __ldcg(p.logits + (static_cast<long long>(s) * p.M + m) * p.E + e0 + 32 * i) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            Pair s = {part[i][0], 0.0f};
-#pragma unroll
-            for (int k = 1; k < kMoeMaxSplits; ++k) {
-                const Pair a = two_sum(s.hi, part[i][k]);
-                s = {a.hi, s.lo + a.lo};
-            }
-            s = fast_two_sum(s.hi, s.lo);
-            if (e0 + 32 * i < p.E) {
-                c[e0 + 32 * i] = make_float2(s.hi, s.lo);
-                l[e0 + 32 * i] = s.hi;
-                lmax = fmaxf(lmax, s.hi);
-            }
+    for (int e = lane; e < E; e += 32) { // its own copies: no other lane's
+        Pair s = {a[e], 0.0f};
+#pragma unroll 1
+        for (int k = 1; k < q.splits; ++k) {
+            const Pair t = two_sum(s.hi, a[k * E + e]);
+            s = {t.hi, s.lo + t.lo};
         }
+        s = fast_two_sum(s.hi, s.lo);
+        hi[e] = s.hi;
+        lo[e] = s.lo;
+        l[e] = s.hi;
+        lmax = fmaxf(lmax, s.hi);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
     if (!by_logit(sc)) {
-        Pair all = {0.0f, 0.0f};
+        // Sigmoid through exp(-|l|), which cannot overflow; softmax in a second round, when its sum is known.
+        Pair all = {0.0f, 0.0f}, inv = {1.0f, 0.0f};
 #pragma unroll 1
-        for (int e0 = lane; e0 - lane < p.E; e0 += 64) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int e = e0 + 32 * i;
-                const float2 v = e < p.E ? c[e] : make_float2(0.0f, 0.0f);
-                Pair s;
-                if (sc.sigmoid) { // through exp(-|l|), which cannot overflow
-                    const bool neg = v.x < 0.0f;
-                    const Pair a = exp_pair({neg ? v.x : -v.x, neg ? v.y : -v.y}, entry);
-                    const Pair r = inverse(add({1.0f, 0.0f}, a));
-                    s = neg ? times(a, r) : r;
-                    if (sc.bias != nullptr && e < p.E)
-                        s = add(s, {__ldg(sc.bias + e), 0.0f});
-                } else {
-                    const Pair d = two_sum(v.x, -lmax);
-                    s = exp_pair(fast_two_sum(d.hi, d.lo + v.y), entry);
-                    if (e < p.E)
-                        all = add(all, s);
+        for (int round = 0; round < (sc.sigmoid ? 1 : 2); ++round) {
+#pragma unroll 1
+            for (int e0 = 0; e0 < E; e0 += 32) {
+                const int e = e0 + lane < E ? e0 + lane : E - 1;
+                const Pair v = {hi[e], lo[e]};
+                const bool neg = v.hi < 0.0f;
+                Pair s = v;
+                if (round == 0) {
+                    Pair d = {neg ? v.hi : -v.hi, neg ? v.lo : -v.lo};
+                    if (!sc.sigmoid) {
+                        d = two_sum(v.hi, -lmax);
+                        d = fast_two_sum(d.hi, d.lo + v.lo);
+                    }
+                    s = exp_pair(d, entry);
                 }
-                if (e < p.E)
-                    c[e] = make_float2(s.hi, s.lo);
+                if (sc.sigmoid)
+                    inv = inverse(add({1.0f, 0.0f}, s));
+                else if (round == 0 && e0 + lane < E)
+                    all = add(all, s);
+                if (sc.sigmoid || round == 1) {
+                    s = sc.sigmoid && !neg ? inv : times(s, inv);
+                    if (sc.bias != nullptr)
+                        s = add(s, {__ldg(sc.bias + e), 0.0f});
+                }
+                __syncwarp(); // (lanes past E re-read the last expert's)
+                if (e0 + lane < E) {
+                    hi[e] = s.hi;
+                    lo[e] = s.lo;
+                }
             }
-        }
-        if (!sc.sigmoid) {
+            if (!sc.sigmoid && round == 0) {
 #pragma unroll 1
-            for (int o = 16; o > 0; o >>= 1)
-                all = add(all, {__shfl_xor_sync(0xffffffffu, all.hi, o), __shfl_xor_sync(0xffffffffu, all.lo, o)});
-            const Pair r = inverse(all);
-#pragma unroll 2
-            for (int e = lane; e < p.E; e += 32) {
-                const float2 v = c[e];
-                Pair s = times({v.x, v.y}, r);
-                if (sc.bias != nullptr)
-                    s = add(s, {__ldg(sc.bias + e), 0.0f});
-                c[e] = make_float2(s.hi, s.lo);
+                for (int o = 16; o > 0; o >>= 1)
+                    all = add(all, {__shfl_xor_sync(0xffffffffu, all.hi, o), __shfl_xor_sync(0xffffffffu, all.lo, o)});
+                inv = inverse(all);
             }
         }
     }
     __syncwarp();
     unsigned taken = 0; // bit i: expert 32 i + lane cannot be chosen (any more)
     if (sc.top_groups < sc.groups) {
-        const int per = p.E / sc.groups;
+        const int per = E / sc.groups;
         int w = 1; // lanes of a group
         while (2 * w * sc.groups <= 32)
             w *= 2;
         const int g = lane / w;
         Pair b1 = {-INFINITY, 0.0f}, b2 = b1; // its two largest
-        if (g < sc.groups) {
-#pragma unroll 4
-            for (int e = lane % w; e < per; e += w) {
-                const float2 v = c[g * per + e];
-                const Pair t = {v.x, v.y};
-                const bool first = greater(t, b1);
-                const Pair low = first ? b1 : t;
-                b1 = first ? t : b1;
-                b2 = greater(low, b2) ? low : b2;
-            }
-        }
+        // over the lane's share of the group, then over the lanes of the group: the other lane's two
 #pragma unroll 1
-        for (int o = w / 2; o > 0; o /= 2) {
-            const Pair o1 = {__shfl_xor_sync(0xffffffffu, b1.hi, o), __shfl_xor_sync(0xffffffffu, b1.lo, o)};
-            const Pair o2 = {__shfl_xor_sync(0xffffffffu, b2.hi, o), __shfl_xor_sync(0xffffffffu, b2.lo, o)};
-            const bool other = greater(o1, b1);
-            const Pair low = other ? b1 : o1; // the lesser of the two largest
-            b2 = greater(b2, o2) ? b2 : o2;
+        for (int e = lane % w, o = w / 2;;) {
+            const bool scan = e < per && g < sc.groups;
+            if (!__any_sync(0xffffffffu, scan) && o == 0)
+                break;
+            Pair t = {-INFINITY, 0.0f}, t2 = t;
+            if (__any_sync(0xffffffffu, scan)) {
+                if (scan)
+                    t = {hi[g * per + e], lo[g * per + e]};
+                e += w;
+            } else {
+                t = {__shfl_xor_sync(0xffffffffu, b1.hi, o), __shfl_xor_sync(0xffffffffu, b1.lo, o)};
+                t2 = {__shfl_xor_sync(0xffffffffu, b2.hi, o), __shfl_xor_sync(0xffffffffu, b2.lo, o)};
+                o /= 2;
+            }
+            const bool first = greater(t, b1);
+            const Pair low = first ? b1 : t; // the lesser of the two largest
+            b1 = first ? t : b1;
+            b2 = greater(b2, t2) ? b2 : t2;
             b2 = greater(low, b2) ? low : b2;
-            b1 = other ? o1 : b1;
         }
         const Pair score = sc.group_best == 2 ? add(b1, b2) : b1;
         int rank = 0;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < sc.groups; ++i) {
             const Pair t = {__shfl_sync(0xffffffffu, score.hi, i * w), __shfl_sync(0xffffffffu, score.lo, i * w)};
             rank += greater(t, score) || (i < g && !greater(score, t)) ? 1 : 0;
         }
         const unsigned open = __ballot_sync(0xffffffffu, g < sc.groups && rank < sc.top_groups);
-        const unsigned inv = (1u << 20) / per + 1; // e / per = e * inv >> 20 for e < 512, per <= 512
-#pragma unroll 2
-        for (int i = 0; 32 * i + lane < p.E; ++i)
-            if (!(open >> ((((32 * i + lane) * inv) >> 20) * w & 31) & 1u))
+        const unsigned over = (1u << 20) / per + 1; // e / per = e * over >> 20 for e < 512, per <= 512
+#pragma unroll 1
+        for (int i = 0; 32 * i + lane < E; ++i)
+            if (!(open >> ((((32 * i + lane) * over) >> 20) * w & 31) & 1u))
                 taken |= 1u << i;
     }
     // A lane's two best that are not taken, ties to the lowest; it looks again
     // only after both are.
-    uint32_t h1, l1, h2, l2;
-    int e1, e2;
-    auto look = [&]() {
-        h1 = l1 = h2 = l2 = 0;
-        e1 = e2 = 0x7fffffff;
-#pragma unroll 2
-        for (int i = 0; 32 * i + lane < p.E; ++i) {
-            const float2 v = c[32 * i + lane];
-            const uint32_t h = route_key(v.x), w = route_key(v.y);
-            const bool is = (taken >> i & 1u) == 0u;
-            const bool first = is && (e1 == 0x7fffffff || h > h1 || (h == h1 && w > l1));
-            const bool second = is && !first && (e2 == 0x7fffffff || h > h2 || (h == h2 && w > l2));
-            h2 = first ? h1 : second ? h : h2;
-            l2 = first ? l1 : second ? w : l2;
-            e2 = first ? e1 : second ? 32 * i + lane : e2;
-            h1 = first ? h : h1;
-            l1 = first ? w : l1;
-            e1 = first ? 32 * i + lane : e1;
-        }
-    };
-    look();
+    uint32_t h1 = 0, l1 = 0, h2 = 0, l2 = 0;
+    int e1 = 0x7fffffff, e2 = 0x7fffffff;
+    bool look = true;
     int mine_e = 0;
 #pragma unroll 1
     for (int j = 0; j < p.top_k; ++j) {
+        if (look) {
+            h1 = l1 = h2 = l2 = 0;
+            e1 = e2 = 0x7fffffff;
+#pragma unroll 1
+            for (int i = 0; 32 * i + lane < E; ++i) {
+                const uint32_t h = route_key(hi[32 * i + lane]), w = route_key(lo[32 * i + lane]);
+                const bool is = (taken >> i & 1u) == 0u;
+                const bool first = is && (e1 == 0x7fffffff || h > h1 || (h == h1 && w > l1));
+                const bool second = is && !first && (e2 == 0x7fffffff || h > h2 || (h == h2 && w > l2));
+                h2 = first ? h1 : second ? h : h2;
+                l2 = first ? l1 : second ? w : l2;
+                e2 = first ? e1 : second ? 32 * i + lane : e2;
+                h1 = first ? h : h1;
+                l1 = first ? w : l1;
+                e1 = first ? 32 * i + lane : e1;
+            }
+            look = false;
+        }
         const uint32_t top = __reduce_max_sync(0xffffffffu, h1);
         unsigned at = __ballot_sync(0xffffffffu, e1 != 0x7fffffff && h1 == top);
         if ((at & (at - 1)) != 0u) { // equal high parts: the low parts, then the lowest expert
@@ -227,15 +235,12 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
         mine_e = lane == j ? e : mine_e;
         if (lane == from) {
             taken |= 1u << (e >> 5);
-            if (e2 != 0x7fffffff) {
-                h1 = h2;
-                l1 = l2;
-                e1 = e2;
-                h2 = 0;
-                e2 = 0x7fffffff;
-            } else {
-                look();
-            }
+            look = e2 == 0x7fffffff;
+            h1 = h2;
+            l1 = l2;
+            e1 = e2;
+            h2 = 0;
+            e2 = 0x7fffffff;
         }
     }
     const bool chosen = lane < p.top_k;
@@ -245,17 +250,17 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // sigmoid, renormalised: over exp of the largest logit where all are negative, so that not all of them vanish
+    const bool neg = !(lm >= 0.0f);
     const float shift = !sc.sigmoid ? (p.renorm ? top : lmax) : p.renorm ? fminf(top, 0.0f) : 0.0f;
-    const float ex = expf(sc.sigmoid && lm >= 0.0f ? -lm : lm - shift);
-    float w = ex;
+    float w = expf(sc.sigmoid && !neg ? -lm : lm - shift);
     if (sc.sigmoid)
-        w = __fdiv_rn(lm >= 0.0f ? 1.0f : ex, 1.0f + (lm >= 0.0f ? ex : expf(lm)));
+        w = __fdiv_rn(neg ? w : 1.0f, 1.0f + (neg ? expf(lm) : w));
     if (p.renorm || !sc.sigmoid) {
         float sum = chosen ? w : 0.0f;
         if (!p.renorm) {
             sum = 0.0f;
-#pragma unroll 2
-            for (int e = lane; e < p.E; e += 32)
+#pragma unroll 1
+            for (int e = lane; e < E; e += 32)
                 sum += expf(l[e] - lmax);
         }
 #pragma unroll
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) moe_scored_kernel(const __gr
     __shared__ float part[kTG][kMostEx][kTG]; // [warp][expert][token]
     __shared__ unsigned arrived;
     __shared__ unsigned smask[kMoeMaxExperts / 32];
-    extern __shared__ float2 scratch[]; // a warp's E pairs, all warps', then E numbers each
+    extern __shared__ float scratch[]; // kMoeMaxSplits planes of E numbers a warp
     const RouteParams &p = q.r;
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(p.runs + FP8BS_RUNS_MOE_SCORED, 1ull);
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) moe_scored_kernel(const __gr
         return;
     __threadfence(); // the other CTAs' sums and zeroed weights, for every thread of this one
     if (warp < nt)
-        choose_scored(q, t0 + warp, scratch + warp * p.E, reinterpret_cast<float *>(scratch + kTG * p.E) + warp * p.E, smask);
+        choose_scored(q, t0 + warp, scratch + warp * kMoeMaxSplits * p.E, smask);
     if (threadIdx.x == 0)
         p.group_done[tg] = 0u;
     __syncthreads();
@@ -446,23 +451,33 @@ fp8bs_status launch_moe_scored(const MoeLaunch &L, const MoeWorkspace &w, const 
     q.sc = L.scores;
     constexpr int kWarps = kRouteThreads / 32;
     const int units = (L.H + 255) / 256;
-    q.hw = 1;
-    while (q.hw < kWarps && q.hw < units)
-        q.hw *= 2;
-    q.splits = (units + q.hw - 1) / q.hw < kMoeMaxSplits ? (units + q.hw - 1) / q.hw : kMoeMaxSplits;
-    q.loops = (units + q.hw * q.splits - 1) / (q.hw * q.splits);
     const int groups = (L.M + kTG - 1) / kTG;
-    // experts of a warp: as many as leave a CTA for every SM
-    auto sets = [&](int k) { return (L.E + k * (kWarps / q.hw) - 1) / (k * (kWarps / q.hw)); };
-    q.ex = kMostEx;
-    while (q.ex > 2 && sets(q.ex) * q.splits * groups < dev.sms)
-        q.ex /= 2;
-    q.sets = sets(q.ex);
+    // Warps that share H, CTAs that do, experts of a warp: the least of a wave's fixed time (about 2 us: launch, first
+    // loads, arrival) and a unit's (0.8 us and 0.2 for each expert), in fifths of a microsecond, two CTAs an SM.
+    long long best = 0;
+    for (int hw = kWarps; hw >= 1; hw /= 2)
+        for (int splits = 1; splits <= kMoeMaxSplits; ++splits)
+            for (int ex = kMostEx; ex >= 2; ex /= 2) {
+                const int loops = (units + hw * splits - 1) / (hw * splits);
+                if ((splits > 1 && units <= hw * (splits - 1)) || (hw > 1 && units <= hw / 2))
+                    continue; // a CTA or half of the warps would have nothing to do
+                const long long sets = (L.E + ex * (kWarps / hw) - 1) / (ex * (kWarps / hw));
+                const long long waves = (sets * splits * groups + 2 * dev.sms - 1) / (2 * dev.sms);
+                const long long cost = waves * (10 + static_cast<long long>(loops) * (4 + ex));
+                if (best == 0 || cost < best) {
+                    best = cost;
+                    q.hw = hw;
+                    q.splits = splits;
+                    q.ex = ex;
+                    q.loops = loops;
+                    q.sets = static_cast<int>(sets);
+                }
+            }
     const long long cast = L.w13 != nullptr ? (static_cast<long long>(L.M) * (L.H / 128) + kWarps - 1) / kWarps : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cast + static_cast<long long>(q.sets) * q.splits * groups), 1, 1);
     cfg.blockDim = dim3(kRouteThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(kTG) * L.E * 12;
+    cfg.dynamicSmemBytes = static_cast<size_t>(kTG) * L.E * kMoeMaxSplits * 4;
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -472,7 +487,7 @@ fp8bs_status launch_moe_scored(const MoeLaunch &L, const MoeWorkspace &w, const 
     const bool bf = L.wr_type == FP8BS_BF16;
     auto kernel = bf ? moe_scored_kernel<true> : moe_scored_kernel<false>;
     static unsigned long long done[2];
-    const fp8bs_status st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kTG * kMoeMaxExperts * 12, dev.device,
+    const fp8bs_status st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kTG * kMoeMaxExperts * kMoeMaxSplits * 4, dev.device,
                                              done + (bf ? 1 : 0));
     return st != FP8BS_OK ? st : launch_status(cudaLaunchKernelEx(&cfg, kernel, q));
 }
