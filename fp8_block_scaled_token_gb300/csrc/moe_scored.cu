@@ -43,8 +43,6 @@ __device__ __forceinline__ bool by_logit(const MoeScores &sc)
     return sc.bias == nullptr && (sc.top_groups == sc.groups || sc.group_best == 1);
 }
 
-__device__ __forceinline__ bool greater(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
-
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float r;
@@ -72,10 +70,26 @@ __device__ __forceinline__ void copy_async_4(float *to, const float *from)
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// A score as one number whose order is the scores': the high part's key, 27 bits of
+// the low part's (so 43 bits or more of the value) and 31 - i, which puts lower experts
+// of a lane first.  Never 0; NaN is below every number.
+using Key = unsigned long long;
+__device__ __forceinline__ Key score_key(Pair s, int i)
+{
+    return static_cast<Key>(route_key(s.hi)) << 32 | (route_key(s.lo) & ~31u) | static_cast<uint32_t>(31 - i);
+}
+__device__ __forceinline__ float key_value(uint32_t k) // of route_key
+{
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
+__device__ __forceinline__ Key lesser(Key a, Key b) { return a > b ? b : a; }
+
 // One warp: the choice for token m.  `a`: kMoeMaxSplits planes of E numbers of this
-// warp in shared memory, first the partial sums of the logits, then the high and low
-// parts of the scores and the logits; expert 32 i + lane is the lane's own.  A NaN
-// orders below every number.  `mask`: the token group's bit mask of experts (shared).
+// warp in shared memory, first the partial sums of the logits, then the scores' high
+// and low parts (or their keys) and the logits; expert 32 i + lane is the lane's own.
+// `mask`: the token group's bit mask of experts (shared).  Four experts of a lane at
+// a time: one alone is a chain of 120 dependent instructions.
 __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, float *a, unsigned *mask)
 {
     const RouteParams &p = q.r;
@@ -83,64 +97,91 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
     const int lane = threadIdx.x & 31, E = p.E;
     const float2 entry = kPow32[lane];
     float *const hi = a, *const lo = a + E, *const l = a + 2 * E;
+    uint32_t *const key_hi = reinterpret_cast<uint32_t *>(hi), *const key_lo = reinterpret_cast<uint32_t *>(lo);
+    const bool plain = by_logit(sc);
 #pragma unroll 1
     for (int s = 0; s < q.splits; ++s) {
         const float *const from = p.logits + (static_cast<long long>(s) * p.M + m) * E;
-#pragma unroll 1
+#pragma unroll 4
         for (int e = lane; e < E; e += 32)
             copy_async_4(a + s * E + e, from + e);
     }
     copy_async_wait();
     float lmax = -INFINITY;
 #pragma unroll 1
-    for (int e = lane; e < E; e += 32) { // its own copies: no other lane's
-        Pair s = {a[e], 0.0f};
-#pragma unroll 1
-        for (int k = 1; k < q.splits; ++k) {
-            const Pair t = two_sum(s.hi, a[k * E + e]);
-            s = {t.hi, s.lo + t.lo};
+    for (int e0 = lane; e0 < E; e0 += 128) { // its own copies: no other lane's
+        float part[4][kMoeMaxSplits];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < kMoeMaxSplits; ++k)
+                part[i][k] = k < q.splits && e0 + 32 * i < E ? a[k * E + e0 + 32 * i] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = e0 + 32 * i;
+            Pair s = {part[i][0], 0.0f};
+#pragma unroll
+            for (int k = 1; k < kMoeMaxSplits; ++k) {
+                const Pair t = two_sum(s.hi, part[i][k]);
+                s = {t.hi, s.lo + t.lo};
+            }
+            s = fast_two_sum(s.hi, s.lo);
+            if (e < E) {
+                l[e] = s.hi;
+                lmax = fmaxf(lmax, s.hi);
+                const Key key = score_key(s, e >> 5);
+                key_hi[e] = plain ? static_cast<uint32_t>(key >> 32) : __float_as_uint(s.hi);
+                key_lo[e] = plain ? static_cast<uint32_t>(key) : __float_as_uint(s.lo);
+            }
         }
-        s = fast_two_sum(s.hi, s.lo);
-        hi[e] = s.hi;
-        lo[e] = s.lo;
-        l[e] = s.hi;
-        lmax = fmaxf(lmax, s.hi);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
-    if (!by_logit(sc)) {
+    if (!plain) {
         // Sigmoid through exp(-|l|), which cannot overflow; softmax in a second round, when its sum is known.
         Pair all = {0.0f, 0.0f}, inv = {1.0f, 0.0f};
 #pragma unroll 1
         for (int round = 0; round < (sc.sigmoid ? 1 : 2); ++round) {
 #pragma unroll 1
-            for (int e0 = 0; e0 < E; e0 += 32) {
-                const int e = e0 + lane < E ? e0 + lane : E - 1;
-                const Pair v = {hi[e], lo[e]};
-                const bool neg = v.hi < 0.0f;
-                Pair s = v;
+            for (int e0 = 0; e0 < E; e0 += 128) {
+                Pair s[4];
+                bool neg[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = e0 + 32 * i + lane;
+                    s[i] = e < E ? Pair{hi[e], lo[e]} : Pair{0.0f, 0.0f};
+                    neg[i] = s[i].hi < 0.0f;
+                }
                 if (round == 0) {
-                    Pair d = {neg ? v.hi : -v.hi, neg ? v.lo : -v.lo};
-                    if (!sc.sigmoid) {
-                        d = two_sum(v.hi, -lmax);
-                        d = fast_two_sum(d.hi, d.lo + v.lo);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        Pair d = {neg[i] ? s[i].hi : -s[i].hi, neg[i] ? s[i].lo : -s[i].lo};
+                        if (!sc.sigmoid) {
+                            d = two_sum(s[i].hi, -lmax);
+                            d = fast_two_sum(d.hi, d.lo + s[i].lo);
+                        }
+                        s[i] = exp_pair(d, entry);
                     }
-                    s = exp_pair(d, entry);
                 }
-                if (sc.sigmoid)
-                    inv = inverse(add({1.0f, 0.0f}, s));
-                else if (round == 0 && e0 + lane < E)
-                    all = add(all, s);
-                if (sc.sigmoid || round == 1) {
-                    s = sc.sigmoid && !neg ? inv : times(s, inv);
-                    if (sc.bias != nullptr)
-                        s = add(s, {__ldg(sc.bias + e), 0.0f});
-                }
-                __syncwarp(); // (lanes past E re-read the last expert's)
-                if (e0 + lane < E) {
-                    hi[e] = s.hi;
-                    lo[e] = s.lo;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = e0 + 32 * i + lane;
+                    if (sc.sigmoid)
+                        inv = inverse(add({1.0f, 0.0f}, s[i]));
+                    else if (round == 0 && e < E)
+                        all = add(all, s[i]);
+                    if (sc.sigmoid || round == 1) {
+                        s[i] = sc.sigmoid && !neg[i] ? inv : times(s[i], inv);
+                        if (sc.bias != nullptr && e < E)
+                            s[i] = add(s[i], {__ldg(sc.bias + e), 0.0f});
+                    }
+                    if (e < E) {
+                        const Key key = score_key(s[i], e >> 5);
+                        const bool done = sc.sigmoid || round == 1;
+                        key_hi[e] = done ? static_cast<uint32_t>(key >> 32) : __float_as_uint(s[i].hi);
+                        key_lo[e] = done ? static_cast<uint32_t>(key) : __float_as_uint(s[i].lo);
+                    }
                 }
             }
             if (!sc.sigmoid && round == 0) {
@@ -152,6 +193,7 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
         }
     }
     __syncwarp();
+    auto key_of = [&](int e) { return static_cast<Key>(key_hi[e]) << 32 | key_lo[e]; };
     unsigned taken = 0; // bit i: expert 32 i + lane cannot be chosen (any more)
     if (sc.top_groups < sc.groups) {
         const int per = E / sc.groups;
@@ -159,88 +201,71 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
         while (2 * w * sc.groups <= 32)
             w *= 2;
         const int g = lane / w;
-        Pair b1 = {-INFINITY, 0.0f}, b2 = b1; // its two largest
-        // over the lane's share of the group, then over the lanes of the group: the other lane's two
-#pragma unroll 1
-        for (int e = lane % w, o = w / 2;;) {
-            const bool scan = e < per && g < sc.groups;
-            if (!__any_sync(0xffffffffu, scan) && o == 0)
-                break;
-            Pair t = {-INFINITY, 0.0f}, t2 = t;
-            if (__any_sync(0xffffffffu, scan)) {
-                if (scan)
-                    t = {hi[g * per + e], lo[g * per + e]};
-                e += w;
-            } else {
-                t = {__shfl_xor_sync(0xffffffffu, b1.hi, o), __shfl_xor_sync(0xffffffffu, b1.lo, o)};
-                t2 = {__shfl_xor_sync(0xffffffffu, b2.hi, o), __shfl_xor_sync(0xffffffffu, b2.lo, o)};
-                o /= 2;
+        Key b1 = 0, b2 = 0; // the group's two largest
+        if (g < sc.groups) {
+#pragma unroll 4
+            for (int e = lane % w; e < per; e += w) {
+                const Key t = key_of(g * per + e);
+                b2 = larger(b2, lesser(b1, t));
+                b1 = larger(b1, t);
             }
-            const bool first = greater(t, b1);
-            const Pair low = first ? b1 : t; // the lesser of the two largest
-            b1 = first ? t : b1;
-            b2 = greater(b2, t2) ? b2 : t2;
-            b2 = greater(low, b2) ? low : b2;
         }
-        const Pair score = sc.group_best == 2 ? add(b1, b2) : b1;
-        int rank = 0;
 #pragma unroll 1
+        for (int o = w / 2; o > 0; o /= 2) {
+            const Key o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+            b2 = larger(larger(b2, o2), lesser(b1, o1));
+            b1 = larger(b1, o1);
+        }
+        Pair score = {key_value(static_cast<uint32_t>(b1 >> 32)), key_value(static_cast<uint32_t>(b1) & ~31u)};
+        if (sc.group_best == 2)
+            score = add(score, {key_value(static_cast<uint32_t>(b2 >> 32)), key_value(static_cast<uint32_t>(b2) & ~31u)});
+        const Key mine = score_key(score, 31);
+        int rank = 0;
+#pragma unroll 4
         for (int i = 0; i < sc.groups; ++i) {
-            const Pair t = {__shfl_sync(0xffffffffu, score.hi, i * w), __shfl_sync(0xffffffffu, score.lo, i * w)};
-            rank += greater(t, score) || (i < g && !greater(score, t)) ? 1 : 0;
+            const Key t = __shfl_sync(0xffffffffu, mine, i * w);
+            rank += t > mine || (t == mine && i < g) ? 1 : 0;
         }
         const unsigned open = __ballot_sync(0xffffffffu, g < sc.groups && rank < sc.top_groups);
         const unsigned over = (1u << 20) / per + 1; // e / per = e * over >> 20 for e < 512, per <= 512
-#pragma unroll 1
+#pragma unroll 4
         for (int i = 0; 32 * i + lane < E; ++i)
-            if (!(open >> ((((32 * i + lane) * over) >> 20) * w & 31) & 1u))
-                taken |= 1u << i;
+            taken |= (open >> ((((32 * i + lane) * over) >> 20) * w & 31) & 1u) == 0u ? 1u << i : 0u;
     }
-    // A lane's two best that are not taken, ties to the lowest; it looks again
-    // only after both are.
-    uint32_t h1 = 0, l1 = 0, h2 = 0, l2 = 0;
-    int e1 = 0x7fffffff, e2 = 0x7fffffff;
+    // A lane's three best that are not taken, 0 for none; it looks again only
+    // after all of them are.
+    Key b1 = 0, b2 = 0, b3 = 0;
     bool look = true;
     int mine_e = 0;
 #pragma unroll 1
     for (int j = 0; j < p.top_k; ++j) {
         if (look) {
-            h1 = l1 = h2 = l2 = 0;
-            e1 = e2 = 0x7fffffff;
-#pragma unroll 1
+#pragma unroll 4
             for (int i = 0; 32 * i + lane < E; ++i) {
-                const uint32_t h = route_key(hi[32 * i + lane]), w = route_key(lo[32 * i + lane]);
-                const bool is = (taken >> i & 1u) == 0u;
-                const bool first = is && (e1 == 0x7fffffff || h > h1 || (h == h1 && w > l1));
-                const bool second = is && !first && (e2 == 0x7fffffff || h > h2 || (h == h2 && w > l2));
-                h2 = first ? h1 : second ? h : h2;
-                l2 = first ? l1 : second ? w : l2;
-                e2 = first ? e1 : second ? 32 * i + lane : e2;
-                h1 = first ? h : h1;
-                l1 = first ? w : l1;
-                e1 = first ? 32 * i + lane : e1;
+                Key t = (taken >> i & 1u) == 0u ? key_of(32 * i + lane) : 0;
+                Key u = lesser(b1, t);
+                b1 = larger(b1, t);
+                b3 = larger(b3, lesser(b2, u));
+                b2 = larger(b2, u);
             }
             look = false;
         }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, h1);
-        unsigned at = __ballot_sync(0xffffffffu, e1 != 0x7fffffff && h1 == top);
-        if ((at & (at - 1)) != 0u) { // equal high parts: the low parts, then the lowest expert
+        const uint32_t top = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(b1 >> 32));
+        unsigned at = __ballot_sync(0xffffffffu, b1 != 0 && static_cast<uint32_t>(b1 >> 32) == top);
+        if ((at & (at - 1)) != 0u) { // equal high parts: the rest; equal there too: the lowest lane
             const bool in = (at >> lane & 1u) != 0u;
-            const uint32_t low = __reduce_max_sync(0xffffffffu, in ? l1 : 0u);
-            const uint32_t e = __reduce_min_sync(0xffffffffu, in && l1 == low ? static_cast<uint32_t>(e1) : 0x7fffffffu);
-            at = 1u << (e & 31);
+            const uint32_t rest = __reduce_max_sync(0xffffffffu, in ? static_cast<uint32_t>(b1) : 0u);
+            at = __ballot_sync(0xffffffffu, in && static_cast<uint32_t>(b1) == rest);
         }
         const int from = __ffs(static_cast<int>(at)) - 1;
-        const int e = __shfl_sync(0xffffffffu, e1, from);
-        mine_e = lane == j ? e : mine_e;
+        const int i = 31 - static_cast<int>(__shfl_sync(0xffffffffu, static_cast<uint32_t>(b1), from) & 31u);
+        mine_e = lane == j ? 32 * i + from : mine_e;
         if (lane == from) {
-            taken |= 1u << (e >> 5);
-            look = e2 == 0x7fffffff;
-            h1 = h2;
-            l1 = l2;
-            e1 = e2;
-            h2 = 0;
-            e2 = 0x7fffffff;
+            taken |= 1u << i;
+            b1 = b2;
+            b2 = b3;
+            b3 = 0;
+            look = b1 == 0;
         }
     }
     const bool chosen = lane < p.top_k;
@@ -259,7 +284,7 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
         float sum = chosen ? w : 0.0f;
         if (!p.renorm) {
             sum = 0.0f;
-#pragma unroll 1
+#pragma unroll 4
             for (int e = lane; e < E; e += 32)
                 sum += expf(l[e] - lmax);
         }
