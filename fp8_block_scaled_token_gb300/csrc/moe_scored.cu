@@ -50,23 +50,60 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
-// 1 / b for 1 <= b <= 2^10.
-__device__ __forceinline__ Pair inverse(Pair b)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    const float q = rcp_approx(b.hi);
-    return fast_two_sum(q, q * (fmaf(-q, b.hi, 1.0f) - q * b.lo));
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// a + b, the error in `lo` besides what is there.
+__device__ __forceinline__ float sum_into(float a, float b, float &lo)
+{
+    const float s = a + b, t = s - a;
+    lo += (a - (s - t)) + (b - t);
+    return s;
+}
+
+// exp(x + xl) for x <= 0, that of -80 below it, as hi + lo (pow_split's steps with the
+// product held by an fma); a whole warp calls it, `entry` the lane's of kPow32.
+__device__ __forceinline__ Pair exp_of(float x, float xl, float2 entry)
+{
+    constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f; // log2(e)
+    constexpr float k1 = 0x1.62e430p-1f, k2 = 0x1.ebfd1cp-3f, k3 = 0x1.c6b168p-5f; // nearest cubic to 2^y - 1 over y, |y| <= 2^-6
+    x = max_nan(x, -80.0f);
+    const float u = fmaf(x, kHi, kShift);
+    const uint32_t bits = __float_as_uint(u);
+    const float y = fmaf(xl, kHi, fmaf(x, kLo, fmaf(x, kHi, kShift - u)));
+    const float th = __shfl_sync(0xffffffffu, entry.x, bits & 31u), tl = __shfl_sync(0xffffffffu, entry.y, bits & 31u);
+    const float rest = fmaf(fmaf(fmaf(y, k3, k2), y, k1), y, tl);
+    const float hi = __uint_as_float(__float_as_uint(th) + ((bits - static_cast<uint32_t>(kShiftBits)) >> 5 << 23));
+    return {hi, hi * rest};
+}
+
+// 1 / (1 + a) for 0 <= a <= 2^10.
+__device__ __forceinline__ Pair inverse_of_1_plus(Pair a)
+{
+    const float d = 1.0f + a.hi;
+    const float dl = (a.hi >= 1.0f ? 1.0f - (d - a.hi) : a.hi - (d - 1.0f)) + a.lo;
+    const float q = rcp_approx(d);
+    return {q, q * (fmaf(-q, d, 1.0f) - q * dl)};
 }
 
 __device__ __forceinline__ Pair times(Pair a, Pair b)
 {
     const float p = a.hi * b.hi;
-    return fast_two_sum(p, fmaf(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+    return {p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi)};
 }
 
-// Four bytes from global to shared memory, and the wait for this thread's.
+// Bytes from global to shared memory, and the wait for this thread's.
 __device__ __forceinline__ void copy_async_4(float *to, const float *from)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_16(float *to, const float *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -74,9 +111,17 @@ __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_
 // the low part's (so 43 bits or more of the value) and 31 - i, which puts lower experts
 // of a lane first.  Never 0; NaN is below every number.
 using Key = unsigned long long;
-__device__ __forceinline__ Key score_key(Pair s, int i)
+__device__ __forceinline__ uint32_t bits_key(float v) // route_key of a number
 {
-    return static_cast<Key>(route_key(s.hi)) << 32 | (route_key(s.lo) & ~31u) | static_cast<uint32_t>(31 - i);
+    const uint32_t b = __float_as_uint(v);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ void store_key(Pair s, int i, uint32_t *hi, uint32_t *lo)
+{
+    const float t = s.hi + s.lo;
+    const float rest = s.lo - (t - s.hi);
+    *hi = t != t ? 0u : bits_key(t);
+    *lo = (bits_key(fabsf(t) < INFINITY ? rest : 0.0f) & ~31u) | static_cast<uint32_t>(31 - i);
 }
 __device__ __forceinline__ float key_value(uint32_t k) // of route_key
 {
@@ -102,93 +147,110 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
 #pragma unroll 1
     for (int s = 0; s < q.splits; ++s) {
         const float *const from = p.logits + (static_cast<long long>(s) * p.M + m) * E;
-#pragma unroll 4
-        for (int e = lane; e < E; e += 32)
-            copy_async_4(a + s * E + e, from + e);
+        if (E % 4 == 0) {
+#pragma unroll 1
+            for (int e = 4 * lane; e < E; e += 128)
+                copy_async_16(a + s * E + e, from + e);
+        } else {
+#pragma unroll 1
+            for (int e = lane; e < E; e += 32)
+                copy_async_4(a + s * E + e, from + e);
+        }
     }
     copy_async_wait();
+    __syncwarp();
     float lmax = -INFINITY;
 #pragma unroll 1
-    for (int e0 = lane; e0 < E; e0 += 128) { // its own copies: no other lane's
-        float part[4][kMoeMaxSplits];
+    for (int e0 = lane; e0 < E; e0 += 128) {
+        Pair s[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
+            s[i] = {e0 + 32 * i < E ? a[e0 + 32 * i] : 0.0f, 0.0f};
+#pragma unroll 1
+        for (int k = 1; k < q.splits; ++k)
 #pragma unroll
-            for (int k = 0; k < kMoeMaxSplits; ++k)
-                part[i][k] = k < q.splits && e0 + 32 * i < E ? a[k * E + e0 + 32 * i] : 0.0f;
+            for (int i = 0; i < 4; ++i)
+                s[i].hi = sum_into(s[i].hi, e0 + 32 * i < E ? a[k * E + e0 + 32 * i] : 0.0f, s[i].lo);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = e0 + 32 * i;
-            Pair s = {part[i][0], 0.0f};
-#pragma unroll
-            for (int k = 1; k < kMoeMaxSplits; ++k) {
-                const Pair t = two_sum(s.hi, part[i][k]);
-                s = {t.hi, s.lo + t.lo};
-            }
-            s = fast_two_sum(s.hi, s.lo);
             if (e < E) {
-                l[e] = s.hi;
-                lmax = fmaxf(lmax, s.hi);
-                const Key key = score_key(s, e >> 5);
-                key_hi[e] = plain ? static_cast<uint32_t>(key >> 32) : __float_as_uint(s.hi);
-                key_lo[e] = plain ? static_cast<uint32_t>(key) : __float_as_uint(s.lo);
+                const bool finite = fabsf(s[i].hi) < INFINITY;
+                const float t = finite ? s[i].hi + s[i].lo : s[i].hi;
+                l[e] = t;
+                lmax = fmaxf(lmax, t);
+                if (plain) {
+                    store_key({t, finite ? s[i].lo - (t - s[i].hi) : 0.0f}, e >> 5, key_hi + e, key_lo + e);
+                } else {
+                    hi[e] = t;
+                    lo[e] = finite ? s[i].lo - (t - s[i].hi) : 0.0f;
+                }
             }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
-    if (!plain) {
-        // Sigmoid through exp(-|l|), which cannot overflow; softmax in a second round, when its sum is known.
-        Pair all = {0.0f, 0.0f}, inv = {1.0f, 0.0f};
+    // Softmax: exp(l - lmax) and its sum; then (sigmoid: at once) the scores.  Sigmoid goes
+    // through exp(-|l|), which cannot overflow.
+    Pair inv = {1.0f, 0.0f};
+    if (!plain && !sc.sigmoid) {
+        Pair all = {0.0f, 0.0f};
 #pragma unroll 1
-        for (int round = 0; round < (sc.sigmoid ? 1 : 2); ++round) {
-#pragma unroll 1
-            for (int e0 = 0; e0 < E; e0 += 128) {
-                Pair s[4];
-                bool neg[4];
+        for (int e0 = 0; e0 < E; e0 += 64) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = e0 + 32 * i + lane;
-                    s[i] = e < E ? Pair{hi[e], lo[e]} : Pair{0.0f, 0.0f};
-                    neg[i] = s[i].hi < 0.0f;
-                }
-                if (round == 0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        Pair d = {neg[i] ? s[i].hi : -s[i].hi, neg[i] ? s[i].lo : -s[i].lo};
-                        if (!sc.sigmoid) {
-                            d = two_sum(s[i].hi, -lmax);
-                            d = fast_two_sum(d.hi, d.lo + s[i].lo);
-                        }
-                        s[i] = exp_pair(d, entry);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = e0 + 32 * i + lane;
-                    if (sc.sigmoid)
-                        inv = inverse(add({1.0f, 0.0f}, s[i]));
-                    else if (round == 0 && e < E)
-                        all = add(all, s[i]);
-                    if (sc.sigmoid || round == 1) {
-                        s[i] = sc.sigmoid && !neg[i] ? inv : times(s[i], inv);
-                        if (sc.bias != nullptr && e < E)
-                            s[i] = add(s[i], {__ldg(sc.bias + e), 0.0f});
-                    }
-                    if (e < E) {
-                        const Key key = score_key(s[i], e >> 5);
-                        const bool done = sc.sigmoid || round == 1;
-                        key_hi[e] = done ? static_cast<uint32_t>(key >> 32) : __float_as_uint(s[i].hi);
-                        key_lo[e] = done ? static_cast<uint32_t>(key) : __float_as_uint(s[i].lo);
-                    }
+            for (int i = 0; i < 2; ++i) {
+                const int e = e0 + 32 * i + lane;
+                const bool there = e < E;
+                float dl = there ? lo[e] : 0.0f;
+                const float d = sum_into(there ? hi[e] : lmax, -lmax, dl);
+                const Pair s = exp_of(d, fabsf(d) < INFINITY ? dl : 0.0f, entry);
+                if (there) {
+                    all.hi = sum_into(all.hi, s.hi, all.lo);
+                    all.lo += s.lo;
+                    hi[e] = s.hi;
+                    lo[e] = s.lo;
                 }
             }
-            if (!sc.sigmoid && round == 0) {
+        }
 #pragma unroll 1
-                for (int o = 16; o > 0; o >>= 1)
-                    all = add(all, {__shfl_xor_sync(0xffffffffu, all.hi, o), __shfl_xor_sync(0xffffffffu, all.lo, o)});
-                inv = inverse(all);
+        for (int o = 16; o > 0; o >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, all.hi, o), w = __shfl_xor_sync(0xffffffffu, all.lo, o);
+            all.lo += w;
+            all.hi = sum_into(all.hi, h, all.lo);
+        }
+        inv = inverse_of_1_plus({all.hi - 1.0f, all.lo}); // (the sum is 1 or more, so nothing is lost)
+    }
+    if (!plain) {
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += 128) {
+            Pair s[4];
+            float b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + 32 * i + lane;
+                s[i] = e < E ? Pair{hi[e], lo[e]} : Pair{0.0f, 0.0f};
+                b[i] = sc.bias != nullptr && e < E ? __ldg(sc.bias + e) : 0.0f;
+            }
+            if (sc.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool neg = s[i].hi < 0.0f;
+                    const Pair x = exp_of(neg ? s[i].hi : -s[i].hi, neg ? s[i].lo : -s[i].lo, entry);
+                    const Pair r = inverse_of_1_plus(x), t = times(x, r);
+                    s[i] = {neg ? t.hi : r.hi, neg ? t.lo : r.lo};
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[i] = times(s[i], inv);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + 32 * i + lane;
+                s[i].hi = sum_into(s[i].hi, b[i], s[i].lo);
+                if (e < E)
+                    store_key({s[i].hi, fabsf(s[i].hi) < INFINITY ? s[i].lo : 0.0f}, e >> 5, key_hi + e, key_lo + e);
             }
         }
     }
@@ -219,7 +281,9 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
         Pair score = {key_value(static_cast<uint32_t>(b1 >> 32)), key_value(static_cast<uint32_t>(b1) & ~31u)};
         if (sc.group_best == 2)
             score = add(score, {key_value(static_cast<uint32_t>(b2 >> 32)), key_value(static_cast<uint32_t>(b2) & ~31u)});
-        const Key mine = score_key(score, 31);
+        uint32_t mine_hi, mine_lo;
+        store_key(score, 31, &mine_hi, &mine_lo);
+        const Key mine = static_cast<Key>(mine_hi) << 32 | mine_lo;
         int rank = 0;
 #pragma unroll 4
         for (int i = 0; i < sc.groups; ++i) {
