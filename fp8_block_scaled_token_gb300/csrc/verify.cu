@@ -41,10 +41,7 @@ namespace fp8bs {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-#ifndef VCTAS
-#define VCTAS 5
-#endif
-constexpr int kVerifyCtas = VCTAS;  // to an SM
+constexpr int kVerifyCtas = 5;      // to an SM (4: 64 rows of 248,320 at once 21.4 us, not 21.0)
 constexpr int kPart = 1024;         // logits that a warp sums
 constexpr int kMostParts = 4;       // of a warp, one after the other
 constexpr int kSlice = 2048;        // logits of a CTA of the residual
@@ -69,6 +66,8 @@ struct alignas(16) RowStat {
     long long total; // of the weights, in row units
     float prob;      // of the drafted token
     int position;    // sequence's stop: where, -1 with nothing left to draw
+    Pair sum;        // the total as two numbers
+    int pad[2];
 };
 
 struct VerifyParams {
@@ -146,6 +145,15 @@ __device__ __forceinline__ int pow_direct(float x, const Scale &s, float2 entry,
     return (bits - kShiftBits) >> 5;
 }
 
+// th, rest and the bits of n of pow_split for x - ref.
+__device__ __forceinline__ float4 pow_far(float x, float ref, float ch, float cl, float2 entry)
+{
+    float zh, zl, th, rest;
+    exponent_of(x, ref, {ch, cl, 0.0f}, zh, zl);
+    const int n = pow_split(zh, zl, entry, th, rest);
+    return make_float4(th, rest, __int_as_float(n), 0.0f);
+}
+
 // The weight of x relative to 2^exponent as hi + lo (0 below the cutoff); a
 // whole warp calls it.
 __device__ __forceinline__ void weight(float x, float top, float ref, float cut, int exponent, const Scale &s,
@@ -157,9 +165,10 @@ __device__ __forceinline__ void weight(float x, float top, float ref, float cut,
     if (ref == 0.0f) {
         n = pow_direct(live ? x : top, s, entry, th, rest);
     } else {
-        float zh, zl;
-        exponent_of(live ? x : top, ref, s, zh, zl);
-        n = pow_split(zh, zl, entry, th, rest);
+        const float4 r = pow_far(live ? x : top, ref, s.ch, s.cl, entry);
+        th = r.x;
+        rest = r.y;
+        n = __float_as_int(r.z);
     }
     hi = live ? __uint_as_float(__float_as_uint(th) + (static_cast<uint32_t>(n - exponent) << 23)) : 0.0f;
     lo = hi * rest;
@@ -180,6 +189,18 @@ __device__ __forceinline__ long long row_units(float hi, float lo)
     constexpr int kA = 0x41400000, kC = 0x36C00000; // the bits of 12 and of 1.5 * 2^-18
     const int whole = (__float_as_int(a) - kA) + (__float_as_int(b) - kA);
     return static_cast<long long>(whole) * 2097152 + (__float_as_int(c) - kC);
+}
+
+// row_units of (hi + lo) - (bh + bl), 0 where that is not positive or b is not below
+// 4: the whole multiples of 2^-20 of hi and bh apart, their rests with lo - bl.
+__device__ __forceinline__ long long difference_units(float hi, float lo, float bh, float bl)
+{
+    const float a = hi + 12.0f, b = bh + 12.0f, t = lo - bl, d = t + 12.0f;
+    const float c = ((hi - (a - 12.0f)) - (bh - (b - 12.0f))) + (t - (d - 12.0f)) + 5.72204590e-06f;
+    constexpr int kA = 0x41400000, kC = 0x36C00000;
+    const int whole = (__float_as_int(a) - __float_as_int(b)) + (__float_as_int(d) - kA);
+    const long long g = static_cast<long long>(whole) * 2097152 + (__float_as_int(c) - kC);
+    return bh < 4.0f && g > 0 ? g : 0;
 }
 
 __device__ __forceinline__ float max_nan(float a, float b)
@@ -311,6 +332,26 @@ struct WeightSum {
 };
 static_assert((static_cast<uint32_t>(kShiftBits) << 18) == 0u, "kShiftBits leaves the shifted word");
 
+// The word at `at` whose first logit has index i: -infinity for what is not in the
+// row of V, whose memory is not read.  Out of line: a row's first and last word.
+template <bool kBf16> __device__ __noinline__ uint4 edge_word(const uint8_t *at, int i, int V)
+{
+    constexpr int kPer = kBf16 ? 8 : 4, kBits = 128 / kPer;
+    unsigned long long w0 = kBf16 ? 0xFF80FF80FF80FF80ull : 0xFF800000FF800000ull, w1 = w0;
+#pragma unroll 1
+    for (int e = 0; e < kPer; ++e)
+        if (i + e >= 0 && i + e < V) {
+            // the bits in which it differs from -infinity
+            const uint32_t b = kBf16 ? *reinterpret_cast<const uint16_t *>(at + e * 2) ^ 0xFF80u
+                                     : *reinterpret_cast<const uint32_t *>(at + e * 4) ^ 0xFF800000u;
+            const unsigned long long v = static_cast<unsigned long long>(b) << (e * kBits & 63);
+            w0 ^= e < kPer / 2 ? v : 0ull;
+            w1 ^= e < kPer / 2 ? 0ull : v;
+        }
+    return make_uint4(static_cast<uint32_t>(w0), static_cast<uint32_t>(w0 >> 32), static_cast<uint32_t>(w1),
+                      static_cast<uint32_t>(w1 >> 32));
+}
+
 // One row's logits, in 16-byte words counted from the aligned address at or
 // before its first.
 template <bool kBf16> struct Row {
@@ -337,27 +378,9 @@ template <bool kBf16> struct Row {
     __device__ __forceinline__ uint4 load(int word) const
     {
         const int i = index(word);
-        if (i >= 0 && i + kPer <= V)
-            return *reinterpret_cast<const uint4 *>(words + static_cast<long long>(word) * 16);
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = kBf16 ? 0xFF80FF80u : 0xFF800000u;
-        if (i + kPer > 0 && i < V) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                if (i + e < 0 || i + e >= V)
-                    continue;
-                if (kBf16) {
-                    const uint32_t h = *reinterpret_cast<const uint16_t *>(words + static_cast<long long>(word) * 16 + e * 2);
-                    w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xFFFFu) | (h << 16) : (w[e >> 1] & 0xFFFF0000u) | h;
-                } else {
-                    w[e & 3] = *reinterpret_cast<const uint32_t *>(words + static_cast<long long>(word) * 16 + e * 4);
-                }
-            }
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return i >= 0 && i + kPer <= V ? whole(word) : edge(word);
     }
+    __device__ __forceinline__ uint4 edge(int word) const { return edge_word<kBf16>(words + static_cast<long long>(word) * 16, index(word), V); }
     static __device__ __forceinline__ float value(const uint4 &w, int e)
     {
         const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -408,7 +431,10 @@ __device__ __forceinline__ bool behind_a_stop(const VerifyParams &p, int b, int 
 // units of 2^(k - 41), f = th (1 + rest) in [1, 2).
 __device__ __forceinline__ long long rescale(long long sum, float th, float rest, int k)
 {
-    const unsigned long long f = static_cast<unsigned long long>(fixed(th, th * rest, 4611686018427387904.0f)); // 2^62
+    // f in units of 2^-62: th's 24 bits as they are, th * rest (below 2^-5) in units of 2^-36
+    const unsigned long long f = (static_cast<unsigned long long>((__float_as_uint(th) & 0x7FFFFFu) | 0x800000u) << 39) +
+                                 (static_cast<unsigned long long>(__float2uint_rn(fmaxf(th * rest, 0.0f) * 68719476736.0f)) << 26) -
+                                 (static_cast<unsigned long long>(__float2uint_rn(fmaxf(-th * rest, 0.0f) * 68719476736.0f)) << 26);
     const int shift = -k - 2;
     if (shift > 63)
         return 0;
@@ -482,6 +508,7 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
     const float ut = j < len ? p.accept_u[d] : 0.0f;
     const PartStat first = static_cast<int>(threadIdx.x) < p.parts ? load_stat(st + threadIdx.x) : PartStat{-INFINITY, 0, 0};
     float top = first.top;
+#pragma unroll 1
     for (int i = threadIdx.x + kVerifyThreads; i < p.parts; i += kVerifyThreads)
         top = max_nan(top, __ldcg(&st[i].top));
 #pragma unroll
@@ -501,6 +528,7 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
         r.verdict = 2;
     } else if (T == 0.0f) {
         int best = 0x7fffffff;
+#pragma unroll 1
         for (int i = threadIdx.x; i < p.parts; i += kVerifyThreads)
             if (__ldcg(&st[i].top) == top)
                 best = min(best, static_cast<int>(__ldcg(&st[i].sum)));
@@ -541,13 +569,14 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
 #pragma unroll
         for (int i = 0; i < kVerifyWarps; ++i)
             r.total += sh.sum[i];
+        r.sum = pair_of(r.total);
         if (j < len) {
             float hi, lo;
             weight(xt, top, ref, cut, r.exponent, s, entry, hi, lo);
-            const Pair w = {hi * kRowUnits, lo * kRowUnits}, total = pair_of(r.total);
+            const Pair w = {hi * kRowUnits, lo * kRowUnits};
             const float uq = ut * qt;
-            r.verdict = inside && less({uq, fmaf(ut, qt, -uq)}, total, w) ? 1 : 0;
-            r.prob = divide(fast_two_sum(w.hi, w.lo), total).hi;
+            r.verdict = inside && less({uq, fmaf(ut, qt, -uq)}, r.sum, w) ? 1 : 0;
+            r.prob = divide(fast_two_sum(w.hi, w.lo), r.sum).hi;
         }
     }
     if (threadIdx.x == 0) {
@@ -556,6 +585,27 @@ __device__ __forceinline__ void finish_row(const VerifyParams &p, int b, int j, 
         if (r.verdict != 1)
             atomicMax(p.stopped + b, static_cast<unsigned>(64 - j));
     }
+}
+
+__device__ __forceinline__ float probability(float hi, float lo, Pair total)
+{
+    return divide(fast_two_sum(hi * kRowUnits, lo * kRowUnits), total).hi;
+}
+
+// floor(u * total), at most total - 1; 0 where u is NaN or not positive.
+__device__ __forceinline__ long long target_of(float u, long long total)
+{
+    if (!(u > 0.0f))
+        return 0;
+    if (u >= 1.0f)
+        return total - 1;
+    const uint32_t b = __float_as_uint(u);
+    const unsigned long long m = (b >> 23) == 0u ? b : (b & 0x7FFFFFu) | 0x800000u; // u = m 2^-shift
+    const int shift = 150 - static_cast<int>((b >> 23) == 0u ? 1u : b >> 23);         // 24 or more
+    const unsigned long long t = static_cast<unsigned long long>(total);
+    const unsigned long long lo = t * m, hi = __umul64hi(t, m);
+    const unsigned long long v = shift < 64 ? lo >> shift | hi << (64 - shift) : shift < 128 ? hi >> (shift - 64) : 0ull;
+    return static_cast<long long>(v);
 }
 
 // Position of the target weight u * (sum of `sum(i)`, i < n) and what is left of it
@@ -567,6 +617,7 @@ template <class Sum> __device__ __forceinline__ void find_target(int n, float u,
     const int each = (n + kVerifyThreads - 1) / kVerifyThreads;
     const int first = static_cast<int>(threadIdx.x) * each;
     long long mine = 0;
+#pragma unroll 1
     for (int i = first; i < first + each && i < n; ++i)
         mine += sum(i);
     long long upto = warp_scan(mine);
@@ -582,10 +633,10 @@ template <class Sum> __device__ __forceinline__ void find_target(int n, float u,
         total += sh.sum[i];
     }
     if (total > 0) {
-        long long target = __double2ll_rz(static_cast<double>(u) * static_cast<double>(total));
-        target = target < 0 ? 0 : target >= total ? total - 1 : target;
+        const long long target = target_of(u, total);
         long long at = upto - mine;
-        if (at <= target && target < upto)
+        if (at <= target && target < upto) {
+#pragma unroll 1
             for (int i = first;; ++i) {
                 const long long g = sum(i);
                 if (target < at + g) {
@@ -595,6 +646,7 @@ template <class Sum> __device__ __forceinline__ void find_target(int n, float u,
                 }
                 at += g;
             }
+        }
     }
     __syncthreads();
 }
@@ -617,11 +669,6 @@ template <bool kBf16> struct Weights {
         weight(v, top, ref, cut, exponent, s, entry, hi, lo);
     }
 };
-
-__device__ __forceinline__ float probability(float hi, float lo, long long total)
-{
-    return divide(fast_two_sum(hi * kRowUnits, lo * kRowUnits), pair_of(total)).hi;
-}
 
 // Where the cumulative sum of a CTA's weights passes `target`: g, kN a thread, of the
 // logits from i0 on, in order; the last one with a weight where rounding leaves none.
@@ -648,8 +695,9 @@ __device__ __forceinline__ void look(const VerifyParams &p, long long to, const 
     if (lane == 31)
         sh.sum[warp] = upto;
     __syncthreads();
-    for (int i = 0; i < warp; ++i)
-        upto += sh.sum[i];
+#pragma unroll
+    for (int i = 0; i < kVerifyWarps; ++i)
+        upto += i < warp ? sh.sum[i] : 0;
     if (upto - mine <= target && target < upto) {
         long long at = upto;
 #pragma unroll
@@ -672,7 +720,7 @@ __device__ __forceinline__ void look(const VerifyParams &p, long long to, const 
             l = token == i0 + e ? lo[e] : l;
         }
         p.tokens[to] = token;
-        p.probs[to] = probability(h, l, r.total);
+        p.probs[to] = probability(h, l, r.sum);
     } else if (token < 0 && threadIdx.x == 0) {
         p.tokens[to] = -1;
         p.probs[to] = NAN;
@@ -683,54 +731,45 @@ __device__ __forceinline__ void look(const VerifyParams &p, long long to, const 
 // without that of logit `except` where it is in the row.  The whole CTA calls it;
 // `own`: the parts' sums lie in sh.in_row.
 template <bool kBf16>
-__device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat &r, float T, int except, bool own, RowShared &sh)
+__device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat &r, float T, float u, int except, bool own,
+                                     RowShared &sh)
 {
-    using R = Row<kBf16>;
-    const int warp = threadIdx.x >> 5;
     const long long row = static_cast<long long>(b) * (p.L + 1) + r.position;
     const Weights<kBf16> w(p, row, r, T);
-    const float u = p.sample_u[b];
     const long long *const in_row = p.in_row + row * p.parts;
     auto sum = [&](int i) { return own ? sh.in_row[i] : __ldcg(in_row + i); };
-    int without = -1;
-    if (except >= 0 && except < p.V) {
+    int without = except >= 0 && except < p.V ? except : -1, home = -1;
+    long long less_by = 0;
+    if (without >= 0) {
         float h, l;
-        w.pair(w.x.at(except), h, l);
-        const long long less_by = row_units(h, l);
-        const int home = (except + w.x.lead) / kPart;
+        w.pair(w.x.at(without), h, l);
+        less_by = row_units(h, l);
+        home = (without + w.x.lead) / kPart;
+    }
+#pragma unroll 1
+    for (;;) { // the second time from everything, where nothing is left beside it
         find_target(p.parts, u, [&](int i) {
             const long long g = sum(i);
             return i != home ? g : g > less_by ? g - less_by : 0;
         }, sh);
-        without = except;
-    }
-    if (without < 0 || sh.part < 0) { // (or nothing is left beside it)
+        if (sh.part >= 0 || without < 0)
+            break;
         __syncthreads();
-        find_target(p.parts, u, sum, sh);
-        without = -1;
+        without = home = -1;
     }
     const int part = sh.part < 0 ? 0 : sh.part; // (a row's total is positive)
     const long long target = sh.target;
-    // kPart logits: a word a thread, as far as they go
-    constexpr int kWords = kPart / R::kPer;
-    static_assert(kWords <= kVerifyThreads, "a word a thread");
-    const int word = part * kWords + static_cast<int>(threadIdx.x);
-    const int i0 = w.x.index(word);
-    long long g[R::kPer];
-    float hi[R::kPer], lo[R::kPer];
-    if (warp * 32 < kWords) {
-        const uint4 v = w.x.load(word);
+    constexpr int kN = kPart / kVerifyThreads; // logits of a thread
+    const int i0 = part * kPart - w.x.lead + static_cast<int>(threadIdx.x) * kN;
+    float v[kN], hi[kN], lo[kN];
+    long long g[kN];
 #pragma unroll
-        for (int e = 0; e < R::kPer; ++e) {
-            w.pair(R::value(v, e), hi[e], lo[e]);
-            g[e] = i0 + e == without ? 0 : row_units(hi[e], lo[e]);
-        }
-    } else {
+    for (int e = 0; e < kN; ++e)
+        v[e] = i0 + e >= 0 && i0 + e < p.V ? w.x.at(i0 + e) : -INFINITY;
 #pragma unroll
-        for (int e = 0; e < R::kPer; ++e) {
-            g[e] = 0;
-            hi[e] = lo[e] = 0.0f;
-        }
+    for (int e = 0; e < kN; ++e) {
+        w.pair(v[e], hi[e], lo[e]);
+        g[e] = i0 + e == without ? 0 : row_units(hi[e], lo[e]);
     }
     look(p, row, r, g, hi, lo, i0, target, sh);
 }
@@ -780,7 +819,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
             } else {
 #pragma unroll
                 for (int s = 0; s < R::kWords; ++s)
-                    raw[s] = x.load(w0 + s * 32);
+                    raw[s] = x.edge(w0 + s * 32);
             }
             float top = R::largest(raw[0]);
 #pragma unroll
@@ -817,17 +856,12 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
                     sum = sums.units();
                 } else {
                     sum = 0;
-#pragma unroll
-                    for (int s = 0; s < R::kWords; ++s) {
 #pragma unroll 1
-                        for (int e = 0; e < R::kPer; ++e) {
-                            const int i = kBf16 ? e >> 1 : e;
-                            const uint32_t a = i == 0 ? raw[s].x : i == 1 ? raw[s].y : i == 2 ? raw[s].z : raw[s].w;
-                            float hi, lo;
-                            weight(__uint_as_float(!kBf16 ? a : (e & 1) ? a & 0xFFFF0000u : a << 16), top, ref, cut,
-                                   out.exponent, sc, entry, hi, lo);
-                            sum += fixed(hi, lo, kPartUnits);
-                        }
+                    for (int i = 0; i < kPart / 32; ++i) {
+                        const int at = first + i * 32 + lane;
+                        float hi, lo;
+                        weight(at >= 0 && at < p.V ? x.at(at) : -INFINITY, top, ref, cut, out.exponent, sc, entry, hi, lo);
+                        sum += fixed(hi, lo, kPartUnits);
                     }
                 }
                 out.sum = warp_sum(sum);
@@ -852,26 +886,25 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
         sh.skip = sh.last_chunk != 0 && j > 0 && behind_a_stop(p, b, j) ? 1 : 0;
     }
     __syncthreads();
+    // (the arrival of thread 0 acquires the others' writes, and the barrier passes that on)
     if (sh.last_chunk == 0)
         return;
-    __threadfence();
     const bool finish = sh.skip == 0;
+    const float u = p.sample_u[b];
     if (finish)
         finish_row<kBf16>(p, b, j, len, x, sh);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        sh.last_row = 1;
-        if (len > 0) {
+    if (len > 0) {
+        if (threadIdx.x == 0) {
             sh.last_row = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(len);
             if (sh.last_row != 0)
                 p.seq_done[b] = 0u;
         }
+        __syncthreads();
+        if (sh.last_row == 0)
+            return;
     }
-    __syncthreads();
-    if (sh.last_row == 0)
-        return;
     // the sequence's last row: where it stops, and its token
-    __threadfence();
     const long long row0 = static_cast<long long>(b) * (p.L + 1);
     if (warp == 0) {
         // the first position that was not accepted (position len never is); rows behind it may be old
@@ -891,8 +924,9 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
             if (!(finish && n == j)) {
                 const uint4 *const from = reinterpret_cast<const uint4 *>(p.row + row0 + n);
                 uint4 *const to = reinterpret_cast<uint4 *>(&sh.row);
-                to[0] = __ldcg(from);
-                to[1] = __ldcg(from + 1);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    to[i] = __ldcg(from + i);
             }
             const bool done = sh.row.verdict == 2 || T == 0.0f; // no distribution, or no choice
             const bool later = !done && p.q != nullptr && n < len;
@@ -913,12 +947,12 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
         return;
     const RowStat r = sh.row;
     const int except = r.position < len ? p.draft[static_cast<long long>(b) * p.L + r.position] : -1;
-    draw<kBf16>(p, b, r, T, except, finish && r.position == j, sh);
+    draw<kBf16>(p, b, r, T, u, except, finish && r.position == j, sh);
 }
 
 // A CTA per (sequence, slice of kSlice logits): the weights max(p - q, 0) where a
 // draft was rejected.
-template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_residual_kernel(const VerifyParams p)
+template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_residual_kernel(const VerifyParams p)
 {
     using R = Row<kBf16>;
     constexpr int kN = kSlice / kVerifyThreads; // logits of a thread, one after the other
@@ -929,18 +963,17 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = static_cast<int>(blockIdx.x / p.slices), c = static_cast<int>(blockIdx.x % p.slices);
+    const float T = temperature(p, b), u = p.sample_u[b];
     const uint4 *const from = reinterpret_cast<const uint4 *>(p.stop + b);
     RowStat r;
-    reinterpret_cast<uint4 *>(&r)[0] = __ldcg(from);
-    reinterpret_cast<uint4 *>(&r)[1] = __ldcg(from + 1);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        reinterpret_cast<uint4 *>(&r)[i] = __ldcg(from + i);
     if (r.position < 0)
         return;
-    const float T = temperature(p, b);
     const Weights<kBf16> w(p, static_cast<long long>(b) * (p.L + 1) + r.position, r, T);
     const float *const q = p.q + (static_cast<long long>(b) * p.L + r.position) * p.ldq;
-    Pair W = pair_of(r.total);
-    W.hi *= 1.0f / kRowUnits;
-    W.lo *= 1.0f / kRowUnits;
+    const Pair W = {r.sum.hi * (1.0f / kRowUnits), r.sum.lo * (1.0f / kRowUnits)};
     // this thread's weights in slice i, and the target's alone
     auto weights = [&](int i, long long(&g)[kN], float(&ph)[kN], float(&pl)[kN]) {
         const int word = (i * kSlice + static_cast<int>(threadIdx.x) * kN) / R::kPer;
@@ -967,12 +1000,7 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
             w.pair(R::value(v[e / R::kPer], e % R::kPer), ph[e], pl[e]);
-            // p - q W as a pair; 0 where that is not positive, or q is NaN
-            const float bh = qi[e] * W.hi;
-            const float bl = fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -bh));
-            const float d = ph[e] - bh, bb = d - ph[e];
-            const float lo = (pl[e] - bl) + ((ph[e] - (d - bb)) + (-bh - bb));
-            g[e] = d + lo > 0.0f ? row_units(d, lo) : 0;
+            g[e] = difference_units(ph[e], pl[e], qi[e] * W.hi, fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -(qi[e] * W.hi))));
         }
         return i0;
     };
@@ -988,6 +1016,7 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
         sh.sum[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
+#pragma unroll
         for (int i = 1; i < kVerifyWarps; ++i)
             sum += sh.sum[i];
         __stcg(p.residual + static_cast<long long>(b) * p.slices + c, sum);
@@ -998,12 +1027,11 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads) verify_r
     __syncthreads();
     if (sh.last_chunk == 0)
         return;
-    __threadfence();
     const long long *const sums = p.residual + static_cast<long long>(b) * p.slices;
-    find_target(p.slices, p.sample_u[b], [&](int i) { return __ldcg(sums + i); }, sh);
+    find_target(p.slices, u, [&](int i) { return __ldcg(sums + i); }, sh);
     if (sh.part < 0) { // p nowhere above q: from p
         __syncthreads();
-        draw<kBf16>(p, b, r, T, -1, false, sh);
+        draw<kBf16>(p, b, r, T, u, -1, false, sh);
         return;
     }
     const long long target = sh.target;
@@ -1038,7 +1066,7 @@ VerifyWorkspace verify_workspace(int B, int L, int V)
 }
 static_assert((kVerifyMaxRows + 2 * kVerifyMaxRows) * 4 <= kCountersRegion, "every size's counters lie in the shared region");
 static_assert(kMaxParts * kPart >= kVerifyMaxVocab + 7, "parts of a row");
-static_assert(sizeof(PartStat) == 16 && sizeof(RowStat) == 32, "workspace layout");
+static_assert(sizeof(PartStat) == 16 && sizeof(RowStat) == 48, "workspace layout");
 
 fp8bs_status check_verify(int B, int L, int V)
 {
@@ -1100,16 +1128,13 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.B = B;
     p.L = L;
     p.V = V;
-    // parts of a warp: more than one where the GPU is filled three times over all the same
+    // parts of a warp: more than one where the GPU is filled three times over all the same (512 rows of 248,320 in
+    // 131 us, 137 with one; two, for 5 rows, 18 us instead of 17)
     const long long rows = static_cast<long long>(B) * (L + 1);
     p.parts = w.parts;
     p.parts_each = 1;
-#ifdef VEACH
-    p.parts_each = VEACH;
-#else
     while (p.parts_each < kMostParts && rows * w.parts >= 2ll * p.parts_each * 3 * kVerifyWarps * kVerifyCtas * dev.sms)
         p.parts_each *= 2;
-#endif
     p.chunks = (w.parts + p.parts_each * kVerifyWarps - 1) / (p.parts_each * kVerifyWarps);
     p.slices = w.slices;
     p.first_wave = static_cast<unsigned>(dev.sms * kVerifyCtas);
