@@ -586,13 +586,18 @@ def _work(workspace):
 _device_now = None
 
 
+def _first_use():
+    """torch, and how to ask for the current device."""
+    global _device_now
+    torch = _torch()
+    torch.cuda.is_available() and torch.cuda.current_device()  # (this initialises CUDA)
+    _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _home(t, name):
     """The device number of a call's first tensor, which is the current device."""
-    global _device_now
     if _device_now is None:
-        torch = _torch()
-        torch.cuda.current_device()  # (this initialises CUDA)
-        _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _first_use()
     d = t.get_device()
     if d != _device_now():
         raise ValueError("%s is on device %d, which is not the current one" % (name, d))
@@ -644,10 +649,12 @@ def _make(t, shape, dtype, dev, name, d):
 
 
 def _rmsnorm(mx, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, flags):
-    if _torch_module is None:
-        _torch()
+    if _device_now is None:
+        _first_use()
     shape, ldx, xp = _rows(x, "x")
-    d = _home(x, "x")
+    d = x.get_device()
+    if d != _device_now():
+        raise ValueError("x is on device %d, which is not the current one" % d)
     M, K = shape
     dev = x.device
     try:
@@ -663,6 +670,10 @@ def _rmsnorm(mx, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, 
     ldr = ldo = 0
     if residual is not None:
         rshape, ldr, rp = _rows(residual, "residual")
+        if rshape != shape:
+            raise ValueError("residual must have shape %s" % (tuple(shape),))
+        if residual.get_device() != d:
+            _there(residual, "residual", d)
         if residual_out is None:
             residual_out = _empty(shape, dtype=_bf16, device=dev)
             ldo, op = K, residual_out.data_ptr()
@@ -671,21 +682,22 @@ def _rmsnorm(mx, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, 
             if oshape != shape:
                 raise ValueError("residual_out must have shape %s" % (tuple(shape),))
             _there(residual_out, "residual_out", d)
-        if rshape != shape:
-            raise ValueError("residual must have shape %s" % (tuple(shape),))
-        _there(residual, "residual", d)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if store_y or y is not None:
         y, yp = _make(y, shape, _bf16, dev, "y", d)
-    xq, qp = _make(xq, shape, _u8, dev, "xq", d)
+    if xq is None:
+        xq = _empty(shape, dtype=_u8, device=dev)
+        qp = xq.data_ptr()
+    else:
+        xq, qp = _make(xq, shape, _u8, dev, "xq", d)
     if mx:
         scales, sp = _make(scales, ((M + 127) // 128 * (K // 128), 512), _u8, dev, "xs_atoms", d)
         call = lib().fp8_mx_rmsnorm_quant_act
     else:
         scales, sp = _make(scales, (M, K // 128) if M <= 16 else (K // 128, M), _f32, dev, "xs", d)
         call = lib().fp8_rmsnorm_quant_act
-    code = call(xp, ldx, rp, ldr, op, ldo, gp, BF16 if bf else F32, eps, M, K, yp, qp, sp, flags, _stream())
+    code = call(xp, ldx, rp, ldr, op, ldo, gp, 1 if bf else 0, eps, M, K, yp, qp, sp, flags, _stream())
     if code:
         _check("fp8_mx_rmsnorm_quant_act" if mx else "fp8_rmsnorm_quant_act", code)
     return xq, scales, residual_out, y

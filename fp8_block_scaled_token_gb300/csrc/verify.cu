@@ -671,13 +671,15 @@ template <bool kBf16> struct Weights {
 };
 
 // Where the cumulative sum of a CTA's weights passes `target`: g, kN a thread, of the
-// logits from i0 on, in order; the last one with a weight where rounding leaves none.
-// The thread that has it writes it and its probability (weights hi + lo of the row,
-// whose total is r.total); with no weight at all, -1 and NaN.  All threads call it.
+// logits from i0 on, in order.  Where rounding leaves none (sums were taken in finer
+// units), the last one with a weight, of those with one unit or more if there are
+// any.  The thread that has it writes it and its probability (weights hi + lo, whose
+// total is r.sum).  All threads call it; false where no logit has a weight.
 template <int kN>
-__device__ __forceinline__ void look(const VerifyParams &p, long long to, const RowStat &r, const long long (&g)[kN],
+__device__ __forceinline__ bool look(const VerifyParams &p, long long to, const RowStat &r, const long long (&g)[kN],
                                      const float (&hi)[kN], const float (&lo)[kN], int i0, long long target, RowShared &sh)
 {
+    constexpr int kWhole = 2 * kVerifyMaxVocab; // above every index
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         sh.found = 0x7fffffff;
@@ -689,6 +691,8 @@ __device__ __forceinline__ void look(const VerifyParams &p, long long to, const 
     for (int e = 0; e < kN; ++e) {
         mine += g[e];
         if (g[e] > 0)
+            last = i0 + e + kWhole;
+        else if (hi[e] > 0.0f && last < kWhole)
             last = i0 + e;
     }
     long long upto = warp_scan(mine);
@@ -711,7 +715,7 @@ __device__ __forceinline__ void look(const VerifyParams &p, long long to, const 
     if (lane == 0 && last >= 0)
         atomicMax(&sh.end, last);
     __syncthreads();
-    const int token = sh.found != 0x7fffffff ? sh.found : sh.end;
+    const int token = sh.found != 0x7fffffff ? sh.found : sh.end >= kWhole ? sh.end - kWhole : sh.end;
     if (token >= i0 && token < i0 + kN) {
         float h = hi[0], l = lo[0];
 #pragma unroll
@@ -721,10 +725,8 @@ __device__ __forceinline__ void look(const VerifyParams &p, long long to, const 
         }
         p.tokens[to] = token;
         p.probs[to] = probability(h, l, r.sum);
-    } else if (token < 0 && threadIdx.x == 0) {
-        p.tokens[to] = -1;
-        p.probs[to] = NAN;
     }
+    return token >= 0;
 }
 
 // Draws the token of row `r` (of sequence b, at r.position) from its own weights,
@@ -752,26 +754,27 @@ __device__ __forceinline__ void draw(const VerifyParams &p, int b, const RowStat
             const long long g = sum(i);
             return i != home ? g : g > less_by ? g - less_by : 0;
         }, sh);
-        if (sh.part >= 0 || without < 0)
-            break;
+        const int part = sh.part;
+        if (part >= 0 || without < 0) {
+            constexpr int kN = kPart / kVerifyThreads; // logits of a thread
+            const long long target = sh.target;
+            const int i0 = (part < 0 ? 0 : part) * kPart - w.x.lead + static_cast<int>(threadIdx.x) * kN; // (a row's total is positive)
+            float v[kN], hi[kN], lo[kN];
+            long long g[kN];
+#pragma unroll
+            for (int e = 0; e < kN; ++e)
+                v[e] = i0 + e >= 0 && i0 + e < p.V && i0 + e != without ? w.x.at(i0 + e) : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                w.pair(v[e], hi[e], lo[e]);
+                g[e] = row_units(hi[e], lo[e]);
+            }
+            if (look(p, row, r, g, hi, lo, i0, target, sh) || without < 0)
+                break;
+        }
         __syncthreads();
         without = home = -1;
     }
-    const int part = sh.part < 0 ? 0 : sh.part; // (a row's total is positive)
-    const long long target = sh.target;
-    constexpr int kN = kPart / kVerifyThreads; // logits of a thread
-    const int i0 = part * kPart - w.x.lead + static_cast<int>(threadIdx.x) * kN;
-    float v[kN], hi[kN], lo[kN];
-    long long g[kN];
-#pragma unroll
-    for (int e = 0; e < kN; ++e)
-        v[e] = i0 + e >= 0 && i0 + e < p.V ? w.x.at(i0 + e) : -INFINITY;
-#pragma unroll
-    for (int e = 0; e < kN; ++e) {
-        w.pair(v[e], hi[e], lo[e]);
-        g[e] = i0 + e == without ? 0 : row_units(hi[e], lo[e]);
-    }
-    look(p, row, r, g, hi, lo, i0, target, sh);
 }
 
 // A CTA per (position, sequence, chunk), in that order.

@@ -184,6 +184,27 @@ def test_the_same_probabilities_accept_and_draw_from_the_target():
     assert got[1].tolist() == [1] and got[0].tolist() == [[1, 0]]
 
 
+def test_a_rejected_draft_that_has_all_the_weight_but_traces():
+    """p of the draft is 1 but for 2^-23, spread so thin that no other token has a
+    unit (2^-41) of weight; rejected (by a number just below 1), another token has to
+    come, with its probability; with a number above 1 and nothing left at all, the
+    draft itself."""
+    V = 600_000
+    x = torch.full((2, V), -np.log(V * 2.0 ** 23), dtype=torch.float32)
+    x[:, 77_777] = 0.0
+    draft = torch.full((1, 1), 77_777, dtype=torch.int32)
+    for u in (0.1, 0.7, float(np.nextafter(np.float32(1), np.float32(0)))):
+        tok, acc, p = fb.speculative_verify(x.cuda(), torch.tensor([u]).cuda(), draft.cuda(), torch.tensor([[1 - 2.0 ** -24]]).cuda())
+        assert acc.tolist() == [0] and 0 <= tok[0, 0] < V and tok[0, 0] != 77_777 and tok[0, 1] == -1
+        assert abs(tok[0, 0].item() - u * V) < 1100  # in the right part of the row
+        assert abs(p[0, 0].item() * V * 2.0 ** 23 - 1) < 1e-5
+    x[:, :77_777] = x[:, 77_778:] = -float("inf")
+    tok, acc, p = fb.speculative_verify(x.cuda(), torch.tensor([0.4]).cuda(), draft.cuda(), torch.tensor([[2.0]]).cuda())
+    assert acc.tolist() == [0] and tok.tolist() == [[77_777, -1]] and p.tolist() == [[1.0, 0.0]]
+    tok = fb.speculative_verify(x[:1].cuda(), torch.tensor([5.0]).cuda())[0]
+    assert tok.tolist() == [[77_777]]
+
+
 def test_drafted_tokens_outside_the_vocabulary_are_rejected():
     for q in (True, False):
         t = Batch(4, 2, 500, torch.bfloat16, q, seed=6)
