@@ -651,29 +651,37 @@ def _make(t, shape, dtype, dev, name, d):
 def _rmsnorm(mx, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, flags):
     if _device_now is None:
         _first_use()
-    shape, ldx, xp = _rows(x, "x")
-    d = x.get_device()
-    if d != _device_now():
-        raise ValueError("x is on device %d, which is not the current one" % d)
-    M, K = shape
-    dev = x.device
-    try:
+    bf = False
+    try:  # the usual call, in as few reads as it takes; anything else is looked at one by one
+        shape = x.shape
+        M, K = shape
+        ldx, unit = x.stride()
+        d = x.get_device()
         bf = gamma.dtype is _bf16
-    except AttributeError:
+        usual = (x.dtype is _bf16 and unit == 1 and ldx <= 0x7fffffff and d >= 0 and d == _device_now() and
+                 (bf or gamma.dtype is _f32) and gamma.get_device() == d and gamma.is_contiguous() and gamma.numel() == K)
+    except (AttributeError, ValueError):
+        usual = False
+    if usual:
+        xp, gp = x.data_ptr(), gamma.data_ptr()
+        if M == 1:
+            ldx = K
+    else:
+        shape, ldx, xp = _rows(x, "x")
+        M, K = shape
+        d = _home(x, "x")
         _tensors(gamma=gamma)
-        raise
-    if not bf and gamma.dtype is not _f32:
-        _tensors(gamma=gamma)
-        raise TypeError("gamma must be float32 or bfloat16")
-    gp = _in(gamma, _bf16 if bf else _f32, K, "gamma", d)
+        if not bf and gamma.dtype is not _f32:
+            raise TypeError("gamma must be float32 or bfloat16")
+        gp = _in(gamma, _bf16 if bf else _f32, K, "gamma", d)
+    dev = x.device
     rp = op = yp = None
     ldr = ldo = 0
     if residual is not None:
         rshape, ldr, rp = _rows(residual, "residual")
         if rshape != shape:
             raise ValueError("residual must have shape %s" % (tuple(shape),))
-        if residual.get_device() != d:
-            _there(residual, "residual", d)
+        _there(residual, "residual", d)
         if residual_out is None:
             residual_out = _empty(shape, dtype=_bf16, device=dev)
             ldo, op = K, residual_out.data_ptr()
@@ -692,11 +700,14 @@ def _rmsnorm(mx, x, gamma, eps, residual, residual_out, y, store_y, xq, scales, 
     else:
         xq, qp = _make(xq, shape, _u8, dev, "xq", d)
     if mx:
-        scales, sp = _make(scales, ((M + 127) // 128 * (K // 128), 512), _u8, dev, "xs_atoms", d)
-        call = lib().fp8_mx_rmsnorm_quant_act
+        sshape, sdtype, call = ((M + 127) // 128 * (K // 128), 512), _u8, lib().fp8_mx_rmsnorm_quant_act
     else:
-        scales, sp = _make(scales, (M, K // 128) if M <= 16 else (K // 128, M), _f32, dev, "xs", d)
-        call = lib().fp8_rmsnorm_quant_act
+        sshape, sdtype, call = (M, K // 128) if M <= 16 else (K // 128, M), _f32, lib().fp8_rmsnorm_quant_act
+    if scales is None:
+        scales = _empty(sshape, dtype=sdtype, device=dev)
+        sp = scales.data_ptr()
+    else:
+        scales, sp = _make(scales, sshape, sdtype, dev, "xs_atoms" if mx else "xs", d)
     code = call(xp, ldx, rp, ldr, op, ldo, gp, 1 if bf else 0, eps, M, K, yp, qp, sp, flags, _stream())
     if code:
         _check("fp8_mx_rmsnorm_quant_act" if mx else "fp8_rmsnorm_quant_act", code)
