@@ -27,9 +27,9 @@
 // position in the sequence's word, and CTAs of later positions that start after
 // that have nothing to do.  The last row of a sequence knows where it stops and
 // draws the token: it finds the part and looks through it.
-// verify_residual_kernel (with the draft's probabilities): a CTA per (sequence,
-// 2,048 logits) of those that stopped at a rejected draft: sums max(p - q, 0); a
-// sequence's last CTA finds the chunk and looks through it.  Nothing waits.
+// verify_residual_kernel (with the draft's probabilities): for the sequences that
+// stopped at a rejected draft, a warp sums max(p - q, 0) over 256 logits at a time;
+// a sequence's last CTA finds the 256 and looks through them.  Nothing waits.
 #include <cmath>
 
 #include "fp8bs_testing.h"
@@ -44,7 +44,7 @@ constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCtas = 5;      // to an SM (4: 64 rows of 248,320 at once 21.4 us, not 21.0)
 constexpr int kPart = 1024;         // logits that a warp sums
 constexpr int kMostParts = 4;       // of a warp, one after the other
-constexpr int kSlice = 2048;        // logits of a CTA of the residual
+constexpr int kBit = 256;           // logits that a warp sums for the residual
 constexpr int kVerifyMaxDraft = 31;
 constexpr int kVerifyMaxRows = 4096;
 constexpr int kVerifyMaxVocab = 1 << 20;
@@ -72,8 +72,9 @@ struct alignas(16) RowStat {
 
 struct VerifyParams {
     int B, L, V;
-    int parts, chunks, slices;               // of a row: a CTA's parts are a chunk
+    int parts, chunks;                       // of a row: a CTA's parts are a chunk
     int parts_each;                          // of a warp
+    int bits, runs_each, bit_ctas;           // the residual's: of a row, of a warp, CTAs of a row
     unsigned first_wave;                     // CTAs that start at once, before any row can have stopped
     const uint8_t *logits;
     long long ldl; // logits
@@ -88,7 +89,7 @@ struct VerifyParams {
     long long *in_row;                       // [rows][parts]: the part's sum in row units
     RowStat *row;
     RowStat *stop;                           // [B]
-    long long *residual;                     // [B][slices]
+    long long *residual;                     // [B][bits]
     unsigned long long *runs;
 };
 
@@ -618,8 +619,13 @@ template <class Sum> __device__ __forceinline__ void find_target(int n, float u,
     const int first = static_cast<int>(threadIdx.x) * each;
     long long mine = 0;
 #pragma unroll 1
-    for (int i = first; i < first + each && i < n; ++i)
-        mine += sum(i);
+    for (int i = first; i < first + each && i < n; i += 4) {
+        long long g[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            g[k] = i + k < first + each && i + k < n ? sum(i + k) : 0;
+        mine += (g[0] + g[1]) + (g[2] + g[3]);
+    }
     long long upto = warp_scan(mine);
     if (lane == 31)
         sh.sum[warp] = upto;
@@ -637,14 +643,19 @@ template <class Sum> __device__ __forceinline__ void find_target(int n, float u,
         long long at = upto - mine;
         if (at <= target && target < upto) {
 #pragma unroll 1
-            for (int i = first;; ++i) {
-                const long long g = sum(i);
-                if (target < at + g) {
-                    sh.part = i;
-                    sh.target = target - at;
-                    break;
+            for (int i = first; i < first + each && i < n; i += 4) {
+                long long g[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    g[k] = i + k < first + each && i + k < n ? sum(i + k) : 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (at <= target && target < at + g[k]) {
+                        sh.part = i + k;
+                        sh.target = target - at;
+                    }
+                    at += g[k];
                 }
-                at += g;
             }
         }
     }
@@ -953,19 +964,19 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_rows_kerne
     draw<kBf16>(p, b, r, T, u, except, finish && r.position == j, sh);
 }
 
-// A CTA per (sequence, slice of kSlice logits): the weights max(p - q, 0) where a
-// draft was rejected.
+// A CTA per (sequence, runs_each times kBit logits a warp): the weights max(p - q, 0)
+// where a draft was rejected.
 template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads, kVerifyCtas) verify_residual_kernel(const VerifyParams p)
 {
     using R = Row<kBf16>;
-    constexpr int kN = kSlice / kVerifyThreads; // logits of a thread, one after the other
+    constexpr int kN = kBit / 32; // logits of a lane, one after the other
     __shared__ RowShared sh;
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(p.runs + FP8BS_RUNS_VERIFY_RESIDUAL, 1ull);
     grid_launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = static_cast<int>(blockIdx.x / p.slices), c = static_cast<int>(blockIdx.x % p.slices);
+    const int b = static_cast<int>(blockIdx.x / p.bit_ctas), c = static_cast<int>(blockIdx.x % p.bit_ctas);
     const float T = temperature(p, b), u = p.sample_u[b];
     const uint4 *const from = reinterpret_cast<const uint4 *>(p.stop + b);
     RowStat r;
@@ -977,9 +988,17 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads, kVerifyC
     const Weights<kBf16> w(p, static_cast<long long>(b) * (p.L + 1) + r.position, r, T);
     const float *const q = p.q + (static_cast<long long>(b) * p.L + r.position) * p.ldq;
     const Pair W = {r.sum.hi * (1.0f / kRowUnits), r.sum.lo * (1.0f / kRowUnits)};
-    // this thread's weights in slice i, and the target's alone
-    auto weights = [&](int i, long long(&g)[kN], float(&ph)[kN], float(&pl)[kN]) {
-        const int word = (i * kSlice + static_cast<int>(threadIdx.x) * kN) / R::kPer;
+    auto residual = [&](float hi, float lo, float qi) {
+        const float bh = qi * W.hi;
+        return difference_units(hi, lo, bh, fmaf(qi, W.lo, fmaf(qi, W.hi, -bh)));
+    };
+    long long *const sums = p.residual + static_cast<long long>(b) * p.bits;
+#pragma unroll 1
+    for (int n = 0; n < p.runs_each; ++n) {
+        const int bit = (c * p.runs_each + n) * kVerifyWarps + warp;
+        if (bit >= p.bits)
+            break;
+        const int word = (bit * kBit + lane * kN) / R::kPer;
         const int i0 = w.x.index(word);
         uint4 v[kN / R::kPer];
         float qi[kN];
@@ -1000,46 +1019,41 @@ template <bool kBf16> __global__ void __launch_bounds__(kVerifyThreads, kVerifyC
             for (int e = 0; e < kN; ++e)
                 qi[e] = i0 + e >= 0 && i0 + e < p.V ? q[i0 + e] : 0.0f;
         }
+        long long sum = 0;
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-            w.pair(R::value(v[e / R::kPer], e % R::kPer), ph[e], pl[e]);
-            g[e] = difference_units(ph[e], pl[e], qi[e] * W.hi, fmaf(qi[e], W.lo, fmaf(qi[e], W.hi, -(qi[e] * W.hi))));
+            float hi, lo;
+            w.pair(R::value(v[e / R::kPer], e % R::kPer), hi, lo);
+            sum += residual(hi, lo, qi[e]);
         }
-        return i0;
-    };
-    long long g[kN];
-    float hi[kN], lo[kN];
-    weights(c, g, hi, lo);
-    long long sum = 0;
-#pragma unroll
-    for (int e = 0; e < kN; ++e)
-        sum += g[e];
-    sum = warp_sum(sum);
-    if (lane == 0)
-        sh.sum[warp] = sum;
+        sum = warp_sum(sum);
+        if (lane == 0)
+            __stcg(sums + bit, sum);
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 1; i < kVerifyWarps; ++i)
-            sum += sh.sum[i];
-        __stcg(p.residual + static_cast<long long>(b) * p.slices + c, sum);
-        sh.last_chunk = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(p.slices - 1);
+        sh.last_chunk = atomic_add_acq_rel_gpu(p.seq_done + b, 1u) == static_cast<unsigned>(p.bit_ctas - 1);
         if (sh.last_chunk != 0)
             p.seq_done[b] = 0u;
     }
     __syncthreads();
     if (sh.last_chunk == 0)
         return;
-    const long long *const sums = p.residual + static_cast<long long>(b) * p.slices;
-    find_target(p.slices, u, [&](int i) { return __ldcg(sums + i); }, sh);
-    if (sh.part < 0) { // p nowhere above q: from p
+    find_target(p.bits, u, [&](int i) { return __ldcg(sums + i); }, sh);
+    const int bit = sh.part;
+    const long long target = sh.target;
+    if (bit < 0) { // p nowhere above q: from p
         __syncthreads();
         draw<kBf16>(p, b, r, T, u, -1, false, sh);
         return;
     }
-    const long long target = sh.target;
-    const int i0 = weights(sh.part, g, hi, lo);
-    look(p, static_cast<long long>(b) * (p.L + 1) + r.position, r, g, hi, lo, i0, target, sh);
+    static_assert(kBit == kVerifyThreads, "a logit a thread");
+    const int i = bit * kBit - w.x.lead + static_cast<int>(threadIdx.x);
+    const bool inside = i >= 0 && i < p.V;
+    float hi[1], lo[1];
+    w.pair(inside ? w.x.at(i) : -INFINITY, hi[0], lo[0]);
+    const long long g[1] = {residual(hi[0], lo[0], inside ? q[i] : 0.0f)};
+    look(p, static_cast<long long>(b) * (p.L + 1) + r.position, r, g, hi, lo, i, target, sh);
 }
 
 namespace {
@@ -1048,7 +1062,7 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 struct VerifyWorkspace {
     size_t counters_bytes, part_off, in_row_off, row_off, stop_off, residual_off, total;
-    int parts, slices;
+    int parts, bits;
 };
 
 VerifyWorkspace verify_workspace(int B, int L, int V)
@@ -1057,14 +1071,14 @@ VerifyWorkspace verify_workspace(int B, int L, int V)
     const size_t rows = static_cast<size_t>(B) * (L + 1);
     VerifyWorkspace w;
     w.parts = (V + 7 + kPart - 1) / kPart; // a row may start up to seven logits into its first word
-    w.slices = (V + 7 + kSlice - 1) / kSlice;
+    w.bits = (V + 7 + kBit - 1) / kBit;
     w.counters_bytes = (rows + 2 * static_cast<size_t>(B)) * 4;
     w.part_off = kCountersOff + counters_region(w.counters_bytes);
     w.in_row_off = w.part_off + up256(rows * w.parts * sizeof(PartStat));
     w.row_off = w.in_row_off + up256(rows * w.parts * 8);
     w.stop_off = w.row_off + up256(rows * sizeof(RowStat));
     w.residual_off = w.stop_off + up256(static_cast<size_t>(B) * sizeof(RowStat));
-    w.total = w.residual_off + up256(static_cast<size_t>(B) * w.slices * 8);
+    w.total = w.residual_off + up256(static_cast<size_t>(B) * w.bits * 8);
     return w;
 }
 static_assert((kVerifyMaxRows + 2 * kVerifyMaxRows) * 4 <= kCountersRegion, "every size's counters lie in the shared region");
@@ -1138,8 +1152,15 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.parts_each = 1;
     while (p.parts_each < kMostParts && rows * w.parts >= 2ll * p.parts_each * 3 * kVerifyWarps * kVerifyCtas * dev.sms)
         p.parts_each *= 2;
+    // the same for the residual, where a CTA's first loads and its arrival are most of its time (512 rows: 131 us with one
+    // run each, 118 with two, 116 with four; 64 rows 32, 33, 35)
+    p.bits = w.bits;
+    p.runs_each = 1;
+    const int runs = (w.bits + kVerifyWarps - 1) / kVerifyWarps;
+    while (p.runs_each < kMostParts && static_cast<long long>(B) * runs >= 2ll * p.runs_each * kVerifyCtas * dev.sms)
+        p.runs_each *= 2;
+    p.bit_ctas = (runs + p.runs_each - 1) / p.runs_each;
     p.chunks = (w.parts + p.parts_each * kVerifyWarps - 1) / (p.parts_each * kVerifyWarps);
-    p.slices = w.slices;
     p.first_wave = static_cast<unsigned>(dev.sms * kVerifyCtas);
     p.logits = static_cast<const uint8_t *>(logits);
     p.ldl = ldl;
@@ -1175,7 +1196,7 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     st = launch_status(cudaLaunchKernelEx(&cfg, bf ? verify_rows_kernel<true> : verify_rows_kernel<false>, p));
     if (st != FP8BS_OK || !draft_probs)
         return st;
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(B) * w.slices), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(B) * p.bit_ctas), 1, 1);
     cfg.numAttrs = 1;
     return launch_status(cudaLaunchKernelEx(&cfg, bf ? verify_residual_kernel<true> : verify_residual_kernel<false>, p));
 }
