@@ -18,12 +18,10 @@
 // and a 16-byte access per lane is coalesced.  The row stays in registers between
 // the sum and what needs it: each input byte is read once and each output byte
 // written once.  16,384 rows of 5,120 with residual and y: 121 us, 6.2 TB/s (0.93 of
-// the measured copy bandwidth); 512 rows 6.8 us; up to 150 rows 2.3 to 2.7 us, which
-// is latency.  The first form took 258 us, bound by 45 instructions a value; it is
+// the measured copy bandwidth); 512 rows 5.6 us; up to 150 rows 2.1 to 2.7 us, which
+// is latency.  The first form took 255 us, bound by 45 instructions a value; it is
 // 15 with packed fp32, a bf16 addition and a corrected quotient (codes8) in place of
 // converting both ends of an interval.
-#include <cmath>
-
 #include "fp8bs_testing.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -274,8 +272,9 @@ __global__ void __launch_bounds__(kMost, kMin) rmsnorm_quant_kernel(const NormPa
         if (rows == 1 ? !again : !__syncthreads_or(again))
             break;
         const uint16_t *const hr = p.res != nullptr ? p.res_out + m * p.ldo : p.x + m * p.ldx; // what this thread summed
+        constexpr float t = 8.27180613e-25f; // 2^-80
         if (again)
-            eps = 0.0f; // times 2^-160
+            eps = eps * t * t;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             const int k = c * step + k0;
@@ -286,7 +285,6 @@ __global__ void __launch_bounds__(kMost, kMin) rmsnorm_quant_kernel(const NormPa
             if (again) {
                 float v[8];
                 values8(h[c], v);
-                constexpr float t = 8.27180613e-25f; // 2^-80
                 h[c] = make_uint4(bf16x2_rn(v[0] * t, v[1] * t), bf16x2_rn(v[2] * t, v[3] * t),
                                   bf16x2_rn(v[4] * t, v[5] * t), bf16x2_rn(v[6] * t, v[7] * t));
             }
@@ -389,7 +387,7 @@ fp8bs_status rmsnorm_quant(const void *x, int ldx, const void *residual, int ldr
 {
     if (!x || !gamma || !xq || !scales || M < 1 || K < 1 || ldx < K || (residual == nullptr) != (residual_out == nullptr) ||
         (residual != nullptr && (ldr < K || ldo < K)) || (gamma_type != FP8BS_F32 && gamma_type != FP8BS_BF16) ||
-        !(eps >= 7.88860905e-31f) || !std::isfinite(eps) || (flags & ~FP8BS_FLAG_OVERLAP_PREV) != 0)
+        !(eps >= 7.88860905e-31f && eps <= 1.26765060e+30f) || (flags & ~FP8BS_FLAG_OVERLAP_PREV) != 0)
         return FP8BS_ERR_INVALID_ARG;
     if (K % 128 != 0 || K > kNormMaxK || (mx && M > kMaxTokens))
         return FP8BS_ERR_UNSUPPORTED_SHAPE;

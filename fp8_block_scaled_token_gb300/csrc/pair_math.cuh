@@ -84,19 +84,4 @@ __device__ __forceinline__ Pair divide(Pair a, Pair b)
     return fast_two_sum(q, __fdiv_rn(r, b.hi));
 }
 
-// exp(x) for x <= 0 (0 below -80); a whole warp calls it, `entry` the lane's of kPow32.
-__device__ __forceinline__ Pair exp_pair(Pair x, float2 entry)
-{
-    constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f; // log2(e)
-    const bool live = x.hi >= -80.0f;
-    const float a = live ? x.hi : 0.0f, b = live ? x.lo : 0.0f;
-    const float zh = a * kHi;
-    const float zl = fmaf(b, kHi, fmaf(a, kLo, fmaf(a, kHi, -zh)));
-    float th, rest;
-    const int n = pow_split(zh, zl, entry, th, rest);
-    th = __uint_as_float(__float_as_uint(th) + (static_cast<uint32_t>(n) << 23));
-    const Pair r = fast_two_sum(th, th * rest);
-    return {live ? r.hi : x.hi != x.hi ? x.hi : 0.0f, live ? r.lo : 0.0f};
-}
-
 } // namespace fp8bs

@@ -402,7 +402,7 @@ FP8BS_API fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, c
  * x, residual, residual_out: bf16, M rows of stride ldx, ldr, ldro (>= K, % 8 ==
  * 0), 16-byte aligned.  residual_out may be the residual itself, with the same
  * stride (the addition in place); otherwise no output overlaps an input.
- * gamma: fp32 or bf16 [K], 16-byte aligned.  2^-100 <= eps < infinity.
+ * gamma: fp32 or bf16 [K], 16-byte aligned.  2^-100 <= eps <= 2^100.
  * y: bf16 [M][K], 16-byte aligned, or NULL.  xq: u8 [M][K], 16-byte aligned.
  * xs: 4-byte aligned, xs_atoms: 16-byte aligned.
  * M >= 1 (MX: M <= 512), K % 128 == 0, K <= 32,768.

@@ -35,7 +35,7 @@ def test_norm_validation(L, name):
     assert call(res=NUL, out=NUL) not in (INVALID, SHAPE, MISALIGNED)
     assert call(M=0) == INVALID and call(K=0) == INVALID and call(gt=2) == INVALID
     assert call(ldx=256) == INVALID and call(ldr=256) == INVALID and call(ldo=256) == INVALID
-    for eps in (0.0, -1.0, 1e-31, float("nan"), float("inf")):
+    for eps in (0.0, -1.0, 1e-31, 1.3e30, float("nan"), float("inf")):
         assert call(eps=eps) == INVALID
     assert call(flags=2) == INVALID
     assert call(K=500, ldx=504, ldr=504, ldo=504) == SHAPE

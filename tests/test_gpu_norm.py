@@ -187,6 +187,17 @@ def test_the_ends_of_the_range(fmt, size):
         check(out, x, w, eps)
 
 
+def test_an_eps_that_counts_beside_squares_past_the_range():
+    """2^64 squared leaves fp32's range, and eps = 2^100 is 2^-13 of the mean over 32,768."""
+    eps, w = 2.0 ** 100, torch.ones((32768,), dtype=torch.bfloat16)
+    x = torch.zeros((1, 32768), dtype=torch.bfloat16)
+    x[0, 130] = 2.0 ** 64
+    out = fb.fp8_rmsnorm_quant_act(*_cuda(x, w), eps)
+    rs = 1.0 / torch.sqrt(x.double().square().mean() + eps)
+    want = 2.0 ** 64 / 448 * rs
+    assert abs(out[1].cpu().double()[0, 1] - want) <= RS_TOL * want
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("fmt", ["fp8", "mx"])
 def test_a_bad_value_stays_in_its_row(fmt, bad):
