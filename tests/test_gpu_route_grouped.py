@@ -74,6 +74,17 @@ SEEDS = {(64, 160, 2): 1802, (33, 512, 1): 4843, (33, 512, 2): 1844, (33, 512, 3
          (64, 512, 2): 3154, (64, 512, 3): 2155, (16, 31, 3): 1194}
 
 
+@pytest.mark.parametrize("M,E,H", [(3, 24, 20480), (64, 12, 12416)])
+def test_long_rows(M, E, H):
+    """Several turns of a warp over H.  Sums as above, six times sqrt(20,480) 2^-27: 6.4e-6 a logit."""
+    x, wr, b = _inputs(M, E, H, True, torch.bfloat16, seed=H + 1)
+    ids, w, gap = route(_logits(x, wr), 3, b.astype(np.float64), sigmoid=True, groups=4, top_groups=2, group_best=2)
+    assert gap > 1.3e-5, "the inputs have a choice at a border (%g): another seed" % gap
+    got = _call(x, wr, 3, b, groups=4, top_groups=2)
+    assert np.array_equal(got[0].cpu().numpy(), ids)
+    assert np.allclose(got[1].cpu().double().numpy(), w, rtol=1e-5, atol=0)
+
+
 def test_one_group_without_a_bias_is_the_plain_routing():
     x, wr, _ = _inputs(21, 70, 1024, False, torch.float32, seed=3)
     for renorm in (True, False):

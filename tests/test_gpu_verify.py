@@ -299,6 +299,34 @@ def test_calls_of_different_sizes_share_a_workspace():
             _check(c.run(workspace=work), c.want())
 
 
+@pytest.mark.parametrize("B,V,dtype", [(160, 60001, torch.bfloat16), (320, 60000, torch.bfloat16), (330, 59996, torch.float32)])
+def test_a_batch_that_fills_the_gpu_several_times_gives_the_bits_of_its_sequences(B, V, dtype):
+    """Several parts a warp, rows left out behind a stop: integer sums do not depend on it."""
+    L = 3
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn((B * (L + 1), V), generator=g, device="cuda").mul_(2.0)
+    x.scatter_add_(1, torch.randint(0, V, (B * (L + 1), 8), generator=g, device="cuda"),
+                   torch.rand((B * (L + 1), 8), generator=g, device="cuda") * 6 + 6)
+    x = x.to(dtype)
+    z = x.view(B, L + 1, V)[:, :L].float()
+    q = torch.softmax(z + 0.5 * torch.randn(z.shape, generator=g, device="cuda"), dim=2).view(B * L, V)
+    draft = torch.multinomial(q, 1, generator=g).view(B, L).to(torch.int32)
+    au, su = torch.rand((B, L), generator=g, device="cuda"), torch.rand((B,), generator=g, device="cuda")
+    temp = torch.rand((B,), generator=g, device="cuda") + 0.5
+    temp[::9] = 0.0
+    n = torch.randint(0, L + 1, (B,), generator=g, device="cuda").to(torch.int32)
+    for probs in (q, None):
+        all_of_them = fb.speculative_verify(x, su, draft, au, draft_probs=probs, draft_len=n, temperature=temp)
+        if probs is not None:
+            assert len(all_of_them[1].unique()) == L + 1, "the inputs have every number of accepted tokens"
+        for b in range(0, B, 5):
+            r = slice(b * (L + 1), (b + 5) * (L + 1))
+            one = fb.speculative_verify(x[r], su[b:b + 5], draft[b:b + 5], au[b:b + 5], draft_len=n[b:b + 5],
+                                        draft_probs=None if probs is None else probs[b * L:(b + 5) * L], temperature=temp[b:b + 5])
+            for a, o in zip(all_of_them, one):
+                assert torch.equal(a[b:b + 5], o)
+
+
 def test_a_long_vocabulary_and_rows_past_32_bit_offsets():
     """The largest vocabulary, and logits of more than 2^32 bytes of which only a
     view's rows are read."""
