@@ -79,7 +79,7 @@ __device__ __forceinline__ Pair exp_of(float x, float xl, float2 entry)
     const float th = __shfl_sync(0xffffffffu, entry.x, bits & 31u), tl = __shfl_sync(0xffffffffu, entry.y, bits & 31u);
     const float rest = fmaf(fmaf(fmaf(y, k3, k2), y, k1), y, tl);
     const float hi = __uint_as_float(__float_as_uint(th) + ((bits - static_cast<uint32_t>(kShiftBits)) >> 5 << 23));
-    return {hi, hi * rest};
+    return fast_two_sum(hi, hi * rest); // (rest is up to 2^-6: what divides by this takes low parts for small)
 }
 
 // 1 / (1 + a) for 0 <= a <= 2^10.

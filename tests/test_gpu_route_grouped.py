@@ -74,6 +74,29 @@ SEEDS = {(64, 160, 2): 1802, (33, 512, 1): 4843, (33, 512, 2): 1844, (33, 512, 3
          (64, 512, 2): 3154, (64, 512, 3): 2155, (16, 31, 3): 1194}
 
 
+@pytest.mark.parametrize("sigmoid,E", [(True, 512), (True, 45), (False, 24), (False, 512)])
+@pytest.mark.parametrize("seed", range(4))
+def test_scores_a_few_2_to_the_minus_24_apart(sigmoid, E, seed):
+    """Exact logits (one product each) up to 3 and biases that leave the scores plus
+    bias 4e-7 apart, two roundings of the bias (2^-25 each at most) aside, above the
+    3 * 2^-24 = 1.8e-7 from which the choice is that of exact arithmetic."""
+    rng = np.random.RandomState(seed)
+    l = (rng.rand(E) * 6 - 3).astype(np.float32)
+    wr = torch.zeros((E, 128))
+    wr[:, 5] = torch.from_numpy(l)
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    x[:, 5] = 1
+    l = l.astype(np.float64)
+    s = 1 / (1 + np.exp(-l)) if sigmoid else np.exp(l) / np.exp(l).sum()
+    b = (0.5 + 4e-7 * rng.permutation(E) - s).astype(np.float32)
+    k = min(E, 16)
+    ids, w, gap = route(np.stack([l, l]), k, b.astype(np.float64), sigmoid=sigmoid)
+    assert gap > 3.2e-7
+    got = _call(x, wr, k, b, sigmoid=sigmoid)
+    assert np.array_equal(got[0].cpu().numpy(), ids)
+    assert np.allclose(got[1].cpu().double().numpy(), w, rtol=W_TOL, atol=0)
+
+
 @pytest.mark.parametrize("M,E,H", [(3, 24, 20480), (64, 12, 12416)])
 def test_long_rows(M, E, H):
     """Several turns of a warp over H.  Sums as above, six times sqrt(20,480) 2^-27: 6.4e-6 a logit."""
