@@ -293,7 +293,7 @@ FP8BS_API fp8bs_status fp8_blockscaled_gemm_fused_greedy(const void *x, int ldx,
  * draft_len: int32 [B] or NULL, draft_probs: fp32, B*L rows of stride ldq >= V,
  * not negative, or NULL; with L = 0 all of draft, draft_len, draft_probs and
  * accept_u are NULL.  tokens: int32 [B][L+1], accepted: int32 [B], probs: fp32
- * [B][L+1].  All 4-byte aligned.
+ * [B][L+1].  All 4-byte aligned; no output overlaps an input.
  * B >= 1, 0 <= L <= 31, B * (L + 1) <= 4,096, 1 <= V <= 1,048,576.
  * workspace: 256-byte aligned, of speculative_verify_workspace_size; the same
  * contract as the GEMMs' workspace.  flags: 0 or FP8BS_FLAG_OVERLAP_PREV (waits
