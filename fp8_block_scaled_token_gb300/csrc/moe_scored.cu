@@ -66,12 +66,14 @@ __device__ __forceinline__ float sum_into(float a, float b, float &lo)
     return s;
 }
 
-// exp(x + xl) for x <= 0, that of -80 below it, as hi + lo (pow_split's steps with the
-// product held by an fma); a whole warp calls it, `entry` the lane's of kPow32.
+// exp(x + xl) for x <= 0 and |xl| <= 2^-23 |x|, that of -80 below it, as hi + lo
+// (pow_split's steps with the product held by an fma); a whole warp calls it, `entry`
+// the lane's of kPow32.
 __device__ __forceinline__ Pair exp_of(float x, float xl, float2 entry)
 {
     constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f; // log2(e)
     constexpr float k1 = 0x1.62e430p-1f, k2 = 0x1.ebfd1cp-3f, k3 = 0x1.c6b168p-5f; // nearest cubic to 2^y - 1 over y, |y| <= 2^-6
+    xl = x >= -80.0f ? xl : 0.0f; // a large number's low part is large, and y has to stay within 2^-6
     x = max_nan(x, -80.0f);
     const float u = fmaf(x, kHi, kShift);
     const uint32_t bits = __float_as_uint(u);
@@ -160,7 +162,7 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
     }
     copy_async_wait();
     __syncwarp();
-    float lmax = -INFINITY;
+    float lmax = -INFINITY, lmax_lo = 0.0f; // the largest logit, NaN aside
 #pragma unroll 1
     for (int e0 = lane; e0 < E; e0 += 128) {
         Pair s[4];
@@ -178,17 +180,20 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
             if (e < E) {
                 const bool finite = fabsf(s[i].hi) < INFINITY;
                 const float t = finite ? s[i].hi + s[i].lo : s[i].hi;
+                const float rest = finite ? s[i].lo - (t - s[i].hi) : 0.0f;
                 l[e] = t;
+                lmax_lo = t > lmax || (t == lmax && rest > lmax_lo) ? rest : lmax_lo;
                 lmax = fmaxf(lmax, t);
                 if (plain) {
-                    store_key({t, finite ? s[i].lo - (t - s[i].hi) : 0.0f}, e >> 5, key_hi + e, key_lo + e);
+                    store_key({t, rest}, e >> 5, key_hi + e, key_lo + e);
                 } else {
                     hi[e] = t;
-                    lo[e] = finite ? s[i].lo - (t - s[i].hi) : 0.0f;
+                    lo[e] = rest;
                 }
             }
         }
     }
+    const float lane_max = lmax;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         lmax = fmaxf(lmax, __shfl_xor_sync(0xffffffffu, lmax, o));
@@ -196,6 +201,11 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
     // through exp(-|l|), which cannot overflow.
     Pair inv = {1.0f, 0.0f};
     if (!plain && !sc.sigmoid) {
+        // l - lmax with both low parts: logits of 2^24 and more differ by units there
+        lmax_lo = lane_max == lmax ? lmax_lo : -INFINITY;
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1)
+            lmax_lo = fmaxf(lmax_lo, __shfl_xor_sync(0xffffffffu, lmax_lo, o));
         Pair all = {0.0f, 0.0f};
 #pragma unroll 1
         for (int e0 = 0; e0 < E; e0 += 64) {
@@ -203,9 +213,12 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
             for (int i = 0; i < 2; ++i) {
                 const int e = e0 + 32 * i + lane;
                 const bool there = e < E;
-                float dl = there ? lo[e] : 0.0f;
+                float dl = there ? lo[e] - lmax_lo : 0.0f;
                 const float d = sum_into(there ? hi[e] : lmax, -lmax, dl);
-                const Pair s = exp_of(d, fabsf(d) < INFINITY ? dl : 0.0f, entry);
+                Pair x = two_sum(d, fabsf(d) < INFINITY ? dl : 0.0f);
+                if (x.hi > 0.0f) // by a rounding of the low parts' difference
+                    x = {0.0f, 0.0f};
+                const Pair s = exp_of(x.hi, x.lo, entry);
                 if (there) {
                     all.hi = sum_into(all.hi, s.hi, all.lo);
                     all.lo += s.lo;

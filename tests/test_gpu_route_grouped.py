@@ -177,6 +177,52 @@ def test_large_and_hopeless_logits(sigmoid):
     assert np.allclose(got[1].cpu().numpy(), w / w.sum(), rtol=2e-5)
 
 
+def _in_two_parts(first, second):
+    """Three tokens whose logits are first + second, the parts from the two ends of a
+    long H, so that the second stays beside the first as a low part where H is split."""
+    x, wr = torch.zeros((3, 4096), dtype=torch.bfloat16), torch.zeros((len(first), 4096))
+    x[:, [5, 4000]] = 1
+    wr[:, 5], wr[:, 4000] = torch.from_numpy(first.astype(np.float32)), torch.from_numpy(second.astype(np.float32))
+    return x, wr
+
+
+@pytest.mark.parametrize("size", [1e5, 1e10, 1e18, 1e20, 1e25, 1e30])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("bias", [True, False])
+def test_logits_far_apart_have_scores_of_0_and_1(bias, sigmoid, size):
+    """Differences of 1,000 and more and low parts of any size: under softmax the
+    largest logit's score is 1 and the others' 0, under sigmoid they go by the sign.
+    With a bias its steps of 0.02 decide the rest, without one the groups' two best
+    scores, where the lowest of equal ones come first."""
+    rng = np.random.RandomState(3)
+    E = 24
+    x, wr = _in_two_parts(size * (1 + rng.permutation(E) / 64) * rng.choice([-1, 1], E), size * 2.0 ** -26 * rng.standard_normal(E))
+    b = (0.02 * rng.permutation(E)).astype(np.float32) if bias else None
+    kw = dict(sigmoid=sigmoid) if bias else dict(sigmoid=sigmoid, groups=6, top_groups=3, group_best=2)
+    ids, w, gap = route(_logits(x, wr), 6, None if b is None else b.astype(np.float64), **kw)
+    assert gap > 0.01 or not bias
+    got = _call(x, wr, 6, b, **kw)
+    assert np.array_equal(got[0].cpu().numpy(), ids)
+    assert np.allclose(got[1].cpu().double().numpy(), w, rtol=W_TOL, atol=1e-30)
+
+
+@pytest.mark.parametrize("size", [3e7, 1e10, 1e12, 1e30])
+def test_scores_of_logits_that_are_equal_in_fp32_lie_between_0_and_1(size):
+    """Sums of products of that size do not tell these logits apart for certain, so
+    any softmax may come of them: biases 2 apart decide all the same, and the weights
+    are positive parts of 1."""
+    rng = np.random.RandomState(4)
+    E = 20
+    x, wr = _in_two_parts(np.full(E, size) * np.where(np.arange(E) < 15, 1, -1), size * -4e-9 * rng.permutation(E))
+    b = (2.0 * rng.permutation(E)).astype(np.float32)
+    b[:15] += 40  # (the largest logits are among the chosen)
+    for sigmoid in (False, True):
+        ids, w = _call(x, wr, 8, b, sigmoid=sigmoid)
+        assert np.array_equal(ids.cpu().numpy(), np.tile(np.argsort(-b)[:8], (3, 1)))
+        w = w.cpu().double()
+        assert ((w >= 0) & (w <= 1)).all() and ((w.sum(dim=1) - 1).abs() <= 8 * 2.0 ** -24).all()
+
+
 def test_a_bad_token_stays_in_its_row():
     x, wr, b = _inputs(10, 64, 256, True, torch.bfloat16, seed=11)
     kw = dict(groups=8, top_groups=4)
