@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) moe_scored_kernel(const __gr
     __shared__ float part[kTG][kMostEx][kTG]; // [warp][expert][token]
     __shared__ unsigned arrived;
     __shared__ unsigned smask[kMoeMaxExperts / 32];
-    extern __shared__ float scratch[]; // kMoeMaxSplits planes of E numbers a warp
+    extern __shared__ __align__(16) float scratch[]; // kMoeMaxSplits planes of E numbers a warp; 16-byte copies go there
     const RouteParams &p = q.r;
     if (blockIdx.x == 0 && threadIdx.x == 0)
         atomicAdd(p.runs + FP8BS_RUNS_MOE_SCORED, 1ull);

@@ -3,6 +3,9 @@ verification of drafted tokens, routing with scores and groups) on
 the CPU: declared, and bad arguments rejected on the host before anything would
 reach a GPU.  Nothing here launches a kernel."""
 import ctypes
+import glob
+import os
+import re
 
 import numpy as np
 import pytest
@@ -144,3 +147,20 @@ def test_the_reference_of_the_routing():
     ids, w, _ = route(l, 1, sigmoid=False, renorm=False)                # 4 of 1 + 3 + 1/3 + 4
     assert ids.tolist() == [[3]] and np.allclose(w, [[4.0 / (25.0 / 3.0)]])
     assert route(np.array([[0.0, 0.0, np.nan, 0.0]]), 4)[0].tolist() == [[0, 1, 3, 2]]
+
+
+def test_dynamic_shared_memory_states_its_alignment():
+    """16-byte copies and loads go to it: declared with that alignment, or rounded up
+    by hand in the next lines; a plain element type promises no more than its own."""
+    csrc = os.path.join(os.path.dirname(fb.__file__), "csrc")
+    found = 0
+    for path in glob.glob(os.path.join(csrc, "*.cu*")):
+        with open(path) as f:
+            text = f.read()
+        for at in re.finditer(r"extern __shared__", text):
+            lines = text[at.start():].split("\n")[:3]
+            declared = re.search(r"__align__\((\d+)\)", lines[0])
+            rounded = re.search(r"\+ (\d+)u\) & ~\1u", " ".join(lines[1:]))
+            assert (declared and int(declared[1]) >= 16) or (rounded and int(rounded[1]) >= 15), "%s: %s" % (path, lines[0])
+            found += 1
+    assert found >= 3
