@@ -8,7 +8,7 @@
 
 namespace fp8bs {
 
-MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
+MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms, int planes)
 {
     auto up256 = [](size_t b) { return (b + 255) / 256 * 256; };
     const size_t npad = static_cast<size_t>(moe_token_pad(M));
@@ -20,7 +20,7 @@ MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms)
     w.counters_up_off = w.counters_down_off + static_cast<size_t>(H / 128) * 4;
     w.counters_bytes = static_cast<size_t>(H / 128) * 4 + active * (I / 128) * 4;
     w.logits_off = kCountersOff + counters_region(w.counters_bytes);
-    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4 * kMoeMaxSplits);
+    w.masks_off = w.logits_off + up256(static_cast<size_t>(M) * E * 4 * planes);
     w.ids_off = w.masks_off + static_cast<size_t>(kMoeMaxTokens / kMoeTokenGroup) * (kMoeMaxExperts / 32) * 4;
     w.topw_off = w.ids_off + up256(static_cast<size_t>(M) * top_k * 4);
     w.wtok_off = w.topw_off + up256(static_cast<size_t>(M) * top_k * 4);
@@ -76,7 +76,7 @@ fp8bs_status run_experts(MoeLaunch &L, size_t workspace_bytes)
     fp8bs_status st = current_device(&dev);
     if (st != FP8BS_OK)
         return st;
-    const MoeWorkspace w = moe_workspace(L.M, L.H, L.I, L.E, L.top_k, dev.sms);
+    const MoeWorkspace w = moe_workspace(L.M, L.H, L.I, L.E, L.top_k, dev.sms, L.scores.planes());
     if (workspace_bytes < w.total)
         return FP8BS_ERR_WORKSPACE_TOO_SMALL;
     if (L.ids == nullptr)
@@ -157,7 +157,8 @@ fp8bs_status run_route(const MoeLaunch &L, size_t workspace_bytes)
     fp8bs_status st = current_device(&dev);
     if (st != FP8BS_OK)
         return st;
-    const MoeWorkspace w = moe_workspace(L.M, 128, 128, L.E, 1, dev.sms); // the routing's part depends on M and E alone
+    // the routing's part depends on M, E and the planes alone
+    const MoeWorkspace w = moe_workspace(L.M, 128, 128, L.E, 1, dev.sms, L.scores.planes());
     if (workspace_bytes < w.masks_off)
         return FP8BS_ERR_WORKSPACE_TOO_SMALL;
     return launch_moe_route(L, w, dev);
@@ -195,7 +196,7 @@ fp8bs_status moe_route_workspace_size(int M, int E, size_t *bytes)
     fp8bs_status st = check_tokens(M, 128, E, 1);
     if (st != FP8BS_OK)
         return st;
-    *bytes = moe_workspace(M, 128, 128, E, 1, 1).masks_off;
+    *bytes = moe_workspace(M, 128, 128, E, 1, 1, kMoeMaxSplits).masks_off;
     return FP8BS_OK;
 }
 
@@ -239,7 +240,7 @@ fp8bs_status fp8_moe_workspace_size(int M, int H, int I, int E, int top_k, size_
     st = current_device(&dev);
     if (st != FP8BS_OK)
         return st;
-    *bytes = moe_workspace(M, H, I, E, top_k, dev.sms).total;
+    *bytes = moe_workspace(M, H, I, E, top_k, dev.sms, kMoeMaxSplits).total;
     return FP8BS_OK;
 }
 

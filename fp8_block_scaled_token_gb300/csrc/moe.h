@@ -41,6 +41,7 @@ struct MoeWorkspace {
 // How experts are scored and grouped; scored = false is the plain top_k of the logits.
 struct MoeScores {
     bool scored = false;
+    int planes() const { return scored ? kMoeMaxSplits : 1; }
     bool sigmoid = false;
     const float *bias = nullptr; // [E], or nullptr
     int groups = 1, top_groups = 1, group_best = 1;
@@ -68,7 +69,9 @@ struct MoeLaunch {
     int test_skip_phase = 0;  // 0 = gate/up, 1 = down
 };
 
-MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms);
+// planes: of [M][E] logits, 1 under the plain choice and kMoeMaxSplits under scores.  The size queries report the
+// larger layout, which both calls may use; each call asks for its own.
+MoeWorkspace moe_workspace(int M, int H, int I, int E, int top_k, int sms, int planes);
 fp8bs_status launch_moe_scored(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);
 fp8bs_status launch_moe_route(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);
 fp8bs_status launch_moe_up(const MoeLaunch &L, const MoeWorkspace &w, const DeviceInfo &dev);

@@ -454,9 +454,11 @@ FP8BS_API fp8bs_status fp8_mx_rmsnorm_quant_act(const void *x, int ldx, const vo
  * 1 <= M <= 64, 1 <= E <= 512, 1 <= top_k <= min(16, E), H and I multiples of
  * 128, E * 2I * H below 2^38.
  * workspace: 256-byte aligned, of moe_route_workspace_size (moe_route alone) or
- * fp8_moe_workspace_size; the same contract as the GEMMs' workspace (zero-filled
- * once, clean after every call, one call at a time; fp8bs_workspace_status
- * reports a time-out).
+ * fp8_moe_workspace_size, which cover the calls with scores below as well: those
+ * hold four planes of M x E fp32 numbers there, moe_route, fp8_moe_layer and
+ * fp8_moe_experts one, and these take a workspace that is smaller by the other
+ * three.  The same contract as the GEMMs' workspace (zero-filled once, clean after
+ * every call, one call at a time; fp8bs_workspace_status reports a time-out).
  * flags: FP8BS_FLAG_OVERLAP_PREV (the layer's first kernel may be set up while
  * the previous kernel on the stream finishes; it waits for it before reading
  * anything) and, for the layers, FP8BS_FLAG_WEIGHTS_TILED.

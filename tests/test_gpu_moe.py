@@ -314,3 +314,63 @@ def test_refusals():
                            *ops, experts=4)
     with pytest.raises(ValueError):
         fb.fp8_moe_layer(x.cpu(), wr, 2, *ops)
+
+
+@pytest.mark.parametrize("M,E,k,H,I", [(3, 40, 2, 256, 128), (64, 160, 6, 512, 128)])
+def test_a_workspace_with_one_plane_of_logits_is_enough(M, E, k, H, I):
+    """The size queries report what the calls with scores need, four planes of M x E
+    numbers; moe_route, fp8_moe_layer and fp8_moe_experts take one, leave what lies
+    behind alone, and refuse less."""
+    t = Layer(M, E, k, H, I, seed=M)
+    x, wr, ops = t.x.cuda(), t.wr.cuda(), t.operands()
+
+    def up256(n):
+        return (n + 255) // 256 * 256
+    spare = up256(16 * M * E) - up256(4 * M * E)
+
+    def run(route, layer):
+        ids, w = fb.moe_route(x, wr, k, workspace=route)
+        return (ids, w, *fb.fp8_moe_layer(x, wr, k, *ops, workspace=layer),
+                fb.fp8_moe_experts(x, ids, w, *ops, experts=E, workspace=layer))
+    want = run(None, None)
+    sizes = [fb.moe_route_workspace_size(M, E) - spare, fb.fp8_moe_workspace_size(M, H, I, E, k) - spare]
+    bufs = [torch.zeros(n + 512, dtype=torch.uint8, device="cuda") for n in sizes]
+    for b, n in zip(bufs, sizes):
+        b[n:] = 77
+    for _ in range(2):
+        for a, b in zip(run(*(b[:n] for b, n in zip(bufs, sizes))), want):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    for b, n in zip(bufs, sizes):
+        assert (b[n:] == 77).all() and not b[:1024 + 65536].any()
+    ids, w = want[:2]
+    for call in (lambda: fb.moe_route(x, wr, k, workspace=bufs[0][:sizes[0] - 256]),
+                 lambda: fb.moe_route_grouped(x, wr, k, workspace=bufs[0][:sizes[0]]),
+                 lambda: fb.fp8_moe_layer(x, wr, k, *ops, workspace=bufs[1][:sizes[1] - 256]),
+                 lambda: fb.fp8_moe_layer_grouped(x, wr, k, *ops, workspace=bufs[1][:sizes[1]]),
+                 lambda: fb.fp8_moe_experts(x, ids, w, *ops, experts=E, workspace=bufs[1][:sizes[1] - 256])):
+        with pytest.raises(fb.Fp8bsError) as e:
+            call()
+        assert e.value.code == 4
+
+
+def test_plain_and_scored_layers_take_turns_on_a_workspace():
+    """Their data lie at different places of it."""
+    M, E, k, H, I = 20, 96, 4, 512, 256
+    t = Layer(M, E, k, H, I, seed=2)
+    x, wr, ops = t.x.cuda(), t.wr.cuda(), t.operands()
+    bias = torch.rand(E, device="cuda") * 0.1
+
+    def run(work, flags=0):
+        out = []
+        for _ in range(3):
+            out += [*fb.fp8_moe_layer(x, wr, k, *ops, workspace=work(), flags=flags),
+                    *fb.fp8_moe_layer_grouped(x, wr, k, *ops, bias=bias, workspace=work(), flags=flags),
+                    *fb.moe_route(x, wr, k, workspace=work(), flags=flags),
+                    *fb.moe_route_grouped(x, wr, k, bias=bias, workspace=work(), flags=flags)]
+        torch.cuda.synchronize()
+        return out
+    want = run(lambda: None)
+    work = t.workspace()
+    for a, b in zip(run(lambda: work, fb.FLAG_OVERLAP_PREV), want):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    assert not work[:1024 + 65536].any()
