@@ -372,6 +372,8 @@ __device__ __forceinline__ void choose_scored(const ScoredParams &q, int m, floa
         w = __fdiv_rn(w, sum);
     }
     w *= sc.scale;
+    if (inv.hi != inv.hi)
+        w = inv.hi; // no score of the token is a number: a NaN or infinite logit is in the softmax's sum
     if (chosen) {
         p.ids[static_cast<long long>(m) * p.top_k + lane] = mine_e;
         p.topw[static_cast<long long>(m) * p.top_k + lane] = w;

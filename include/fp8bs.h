@@ -489,7 +489,11 @@ FP8BS_API fp8bs_status fp8_moe_layer(const void *x, int ldx, const void *wr, fp8
  *   ids[m]  = the top_k experts of largest c in the open groups, in descending
  *             order
  *   w[m,j]  = scale * s_j, divided by the sum of the chosen s where renormalize != 0
- * Ties go to the lowest group and expert; a NaN orders below every number.
+ * Ties go to the lowest group and expert; a NaN orders below every number.  Under
+ * softmax a NaN or +infinity among a token's logits leaves it without any score:
+ * its ids are then the first experts' and its weights NaN; without a bias, and with
+ * group_best = 1 or every group open, the order is that of the logits and ids and
+ * weights are those that moe_route's rule gives.
  * Logits and scores are held in two fp32 numbers until the choice is made, so
  * that it is the one of exact arithmetic unless two c lie within about 2^-24 of
  * the logits' size of each other.  A bias of -infinity makes an expert the last choice.

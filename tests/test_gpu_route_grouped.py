@@ -234,6 +234,34 @@ def test_a_bad_token_stays_in_its_row():
     assert got[0][6].tolist() == [0, 1, 2, 3] and torch.isnan(got[1][6]).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("kw", [dict(), dict(groups=6, top_groups=3, group_best=2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_an_expert_whose_logit_is_no_number(renorm, kw, bad):
+    """One expert's logit NaN or infinite in every token.  Sigmoid: its score is NaN
+    (last), 1 or 0, the others stay.  Softmax over all experts has no score for a token
+    with a NaN or +infinity: the first experts, whose weights say so."""
+    rng = np.random.RandomState(6)
+    E = 24
+    x = torch.ones((2, 128), dtype=torch.bfloat16)
+    x[:, 1:] = 0
+    wr = torch.zeros((E, 128))
+    wr[:, 0] = torch.from_numpy(np.float32(rng.permutation(E) * 0.25 - 3))
+    wr[9, 0] = bad
+    b = None if kw else np.float32(0.005 * rng.permutation(E))
+    logits = np.repeat(wr[:, 0].double().numpy()[None], 2, axis=0)
+    for sigmoid in (True, False):
+        with np.errstate(invalid="ignore"):
+            ids, w, gap = route(logits, 5, None if b is None else b.astype(np.float64), sigmoid=sigmoid, renorm=renorm, **kw)
+        if not sigmoid and bad != -float("inf"):
+            assert ids.tolist() == [[0, 1, 2, 3, 4]] * 2 and np.isnan(w).all()
+        elif sigmoid or not kw:
+            assert not gap < GAP
+        got = _call(x, wr, 5, b, sigmoid=sigmoid, renorm=renorm, **kw)
+        assert np.array_equal(got[0].cpu().numpy(), ids)
+        assert np.allclose(got[1].cpu().double().numpy(), w, rtol=W_TOL, atol=0, equal_nan=True)
+
+
 @pytest.mark.parametrize("tiled", [True, False])
 @pytest.mark.parametrize("M,E,k,H,I,G,tg", [(1, 16, 4, 256, 128, 4, 2), (9, 40, 6, 640, 256, 8, 3), (30, 24, 3, 1024, 128, 1, 1),
                                             (64, 128, 8, 384, 128, 16, 5)])
