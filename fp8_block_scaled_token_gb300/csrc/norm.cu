@@ -159,6 +159,111 @@ __device__ __forceinline__ float over_448(float a)
     return fmaf(fmaf(-q, kE4M3Max, a), y, q);
 }
 
+// Eight values of a row at k in the MX format; whole warps, K past the row's end stores nothing.
+__device__ __forceinline__ void store_mx8(const NormParams &p, int m, int k, int K, float (&v)[8])
+{
+    const int lane = threadIdx.x & 31;
+    float am = abs_max8(v);
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    const int e = mx_shared_exponent(am);
+    const float inv = mx_inv_scale(e);
+    uint32_t byte = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 2) & 3));
+    byte |= __shfl_xor_sync(0xffffffffu, byte, 4);
+    byte |= __shfl_xor_sync(0xffffffffu, byte, 8);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        mul2(v[i], v[i + 1], v[i], v[i + 1], inv);
+    if (k < K) {
+        *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) =
+            make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+        if ((lane & 15) == 0) {
+            const int r = m & 127;
+            reinterpret_cast<uint32_t *>(p.sf + (static_cast<long long>(m >> 7) * (p.K / 128) + (k >> 7)) * 512)
+                [4 * (r & 31) + (r >> 5)] = byte;
+        }
+    }
+}
+
+// A row whose sum of squares leaves fp32's range (a value above 2^64 / sqrt(K)): the sum
+// is taken of the row times 2^-80, in fp32, and everything else of the row as it is, so that
+// small values beside large ones keep their bits.  A product with gamma past the range is
+// taken times 2^-80 too, under fp32 scales with the rest of its group.  A row with an
+// infinity keeps an infinite sum.  Every thread of the CTA calls it, with mine = false
+// where its row is none of those; `h`: what this thread stored or read before.
+template <bool kMx, bool kBf16>
+__device__ __forceinline__ void far_row(const NormParams &p, const uint16_t *h, int m, bool mine, float *sum)
+{
+    constexpr float t = 0x1p-80f, t1 = 0x1p-56f, t2 = 0x1p-24f; // t = t1 t2: 1 / rms itself may be subnormal
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = static_cast<int>(blockDim.x >> 5);
+    const int K = mine ? p.K : 0, step = static_cast<int>(blockDim.x) * 8, k0 = static_cast<int>(threadIdx.x) * 8;
+    float ss = 0.0f;
+#pragma unroll 1
+    for (int k = k0; k < K; k += step) {
+        float v[8];
+        values8(*reinterpret_cast<const uint4 *>(h + k), v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            ss = fmaf(v[i] * t, v[i] * t, ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0)
+        sum[warp] = ss;
+    __syncthreads();
+    if (!mine)
+        return;
+    ss = lane < warps ? sum[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float rs = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(K)) + p.eps * t * t); // of the row times t
+    const float r1 = rs * t1;                                                           // r1 * t2: of the row
+#pragma unroll 1
+    for (int base = 0; base < K; base += step) {
+        const int k = base + k0;
+        Gamma8<kBf16> gamma = {};
+        float v[8] = {}, g[8], u[8], far[8], y[8];
+        if (k < K) {
+            gamma.load(p.gamma, k);
+            values8(*reinterpret_cast<const uint4 *>(h + k), v);
+        }
+        gamma.values(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            u[i] = v[i] * g[i];
+            far[i] = v[i] * t * g[i];
+            y[i] = fabsf(u[i]) < INFINITY ? u[i] * r1 * t2 : far[i] * rs;
+        }
+        if (p.y != nullptr && k < K)
+            *reinterpret_cast<uint4 *>(p.y + static_cast<long long>(m) * p.K + k) =
+                make_uint4(bf16x2_rn(y[0], y[1]), bf16x2_rn(y[2], y[3]), bf16x2_rn(y[4], y[5]), bf16x2_rn(y[6], y[7]));
+        if (kMx) {
+            store_mx8(p, m, k, K, y);
+        } else {
+            float am = abs_max8(u), am_far = abs_max8(far);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+                am_far = fmaxf(am_far, __shfl_xor_sync(0xffffffffu, am_far, o));
+            }
+            const bool over = am == INFINITY;
+            const float s = over_448(over ? am_far : am);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                u[i] = over ? far[i] : u[i];
+            const uint2 codes = codes8(u, s == 0.0f ? 1.0f : s);
+            if (k < K) {
+                *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) = codes;
+                if ((lane & 15) == 0)
+                    p.xs[p.kmajor ? static_cast<long long>(k >> 7) * p.M + m : static_cast<long long>(m) * (p.K / 128) + (k >> 7)] =
+                        s == 0.0f ? 1.0f : over ? s * rs : s * r1 * t2;
+            }
+        }
+    }
+}
+
 // A CTA: blockDim.y rows of blockDim.x threads; kMost threads at most, kMin CTAs to an SM.
 template <bool kMx, bool kBf16, int kChunks, int kMost, int kMin>
 __global__ void __launch_bounds__(kMost, kMin) rmsnorm_quant_kernel(const NormParams p)
@@ -225,71 +330,44 @@ __global__ void __launch_bounds__(kMost, kMin) rmsnorm_quant_kernel(const NormPa
                 *reinterpret_cast<uint4 *>(ro + k) = h[c];
         }
     }
-    // Squares past fp32's range (values above 2^64 / sqrt(K)) are summed again
-    // with the row times 2^-80; a row with an infinity or NaN keeps its sum.
     float u[kChunks][8];
     float sg[kChunks]; // fp32 scales of this thread's groups, before rs
-    float eps = p.eps, rs;
-#pragma unroll 1
-    for (int turn = 0;; ++turn) {
-        float s0 = 0.0f, s1 = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = c * step + k0;
-            float g[8];
-            values8(h[c], u[c]);
-            gamma[c].values(g);
+    for (int c = 0; c < kChunks; ++c) {
+        const int k = c * step + k0;
+        float g[8];
+        values8(h[c], u[c]);
+        gamma[c].values(g);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                fma2(s0, s1, u[c][i], u[c][i + 1], u[c][i], u[c][i + 1]);
-                mul2v(u[c][i], u[c][i + 1], u[c][i], u[c][i + 1], g[i], g[i + 1]);
-            }
-            if (!kMx) {
-                float am = abs_max8(u[c]);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                const float s = over_448(am);
-                sg[c] = s;
-                const uint2 codes = codes8(u[c], s == 0.0f ? 1.0f : s); // 0: zeros, or amax below 448 * 2^-150
-                if (k < K)
-                    *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) = codes;
-            }
+        for (int i = 0; i < 8; i += 2) {
+            fma2(s0, s1, u[c][i], u[c][i + 1], u[c][i], u[c][i + 1]);
+            mul2v(u[c][i], u[c][i + 1], u[c][i], u[c][i + 1], g[i], g[i + 1]);
         }
-        float ss = s0 + s1;
+        if (!kMx) {
+            float am = abs_max8(u[c]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (lane == 0)
-            sum[32 * turn + warp] = ss;
-        __syncthreads();
-        ss = lane < warps ? sum[32 * turn + lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rs = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.K)) + eps);
-        const bool again = turn == 0 && ss == INFINITY;
-        if (rows == 1 ? !again : !__syncthreads_or(again))
-            break;
-        const uint16_t *const hr = p.res != nullptr ? p.res_out + m * p.ldo : p.x + m * p.ldx; // what this thread summed
-        constexpr float t = 8.27180613e-25f; // 2^-80
-        if (again)
-            eps = eps * t * t;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int k = c * step + k0;
-            if (k >= K)
-                continue;
-            h[c] = *reinterpret_cast<const uint4 *>(hr + k);
-            gamma[c].load(p.gamma, k);
-            if (again) {
-                float v[8];
-                values8(h[c], v);
-                h[c] = make_uint4(bf16x2_rn(v[0] * t, v[1] * t), bf16x2_rn(v[2] * t, v[3] * t),
-                                  bf16x2_rn(v[4] * t, v[5] * t), bf16x2_rn(v[6] * t, v[7] * t));
-            }
+            for (int o = 8; o > 0; o >>= 1)
+                am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+            const float s = over_448(am);
+            sg[c] = s;
+            const uint2 codes = codes8(u[c], s == 0.0f ? 1.0f : s); // 0: zeros, or amax below 448 * 2^-150
+            if (k < K)
+                *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) = codes;
         }
     }
+    float ss = s0 + s1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0)
+        sum[warp] = ss;
+    __syncthreads();
+    ss = lane < warps ? sum[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float rs = __frsqrt_rn(__fdiv_rn(ss, static_cast<float>(p.K)) + p.eps);
     if (!kMx) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
@@ -298,42 +376,26 @@ __global__ void __launch_bounds__(kMost, kMin) rmsnorm_quant_kernel(const NormPa
                 p.xs[p.kmajor ? static_cast<long long>(k >> 7) * p.M + m : static_cast<long long>(m) * kg + (k >> 7)] =
                     sg[c] == 0.0f ? 1.0f : sg[c] * rs;
         }
-        if (p.y == nullptr)
-            return;
     }
+    if (kMx || p.y != nullptr) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int k = c * step + k0;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 2)
-            mul2(v[i], v[i + 1], u[c][i], u[c][i + 1], rs);
-        if (p.y != nullptr && k < K)
-            *reinterpret_cast<uint4 *>(p.y + static_cast<long long>(m) * p.K + k) =
-                make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
-        if (kMx) {
-            float am = abs_max8(v);
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            const int e = mx_shared_exponent(am);
-            const float inv = mx_inv_scale(e);
-            uint32_t byte = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 2) & 3));
-            byte |= __shfl_xor_sync(0xffffffffu, byte, 4);
-            byte |= __shfl_xor_sync(0xffffffffu, byte, 8);
+        for (int c = 0; c < kChunks; ++c) {
+            const int k = c * step + k0;
+            float v[8];
 #pragma unroll
             for (int i = 0; i < 8; i += 2)
-                mul2(v[i], v[i + 1], v[i], v[i + 1], inv);
-            if (k < K) {
-                *reinterpret_cast<uint2 *>(p.xq + static_cast<long long>(m) * p.K + k) =
-                    make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
-                if ((lane & 15) == 0) {
-                    const int r = m & 127;
-                    reinterpret_cast<uint32_t *>(p.sf + (static_cast<long long>(m >> 7) * kg + (k >> 7)) * 512)
-                        [4 * (r & 31) + (r >> 5)] = byte;
-                }
-            }
+                mul2(v[i], v[i + 1], u[c][i], u[c][i + 1], rs);
+            if (p.y != nullptr && k < K)
+                *reinterpret_cast<uint4 *>(p.y + static_cast<long long>(m) * p.K + k) =
+                    make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+            if (kMx)
+                store_mx8(p, m, k, K, v);
         }
     }
+    // Last, so that the usual row keeps nothing for it: each thread writes its own places once more.
+    const bool far = ss == INFINITY;
+    if (rows == 1 ? far : __syncthreads_or(far))
+        far_row<kMx, kBf16>(p, p.res != nullptr ? p.res_out + m * p.ldo : p.x + m * p.ldx, m, far, sum + 32);
 }
 
 namespace {

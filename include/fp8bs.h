@@ -386,7 +386,8 @@ FP8BS_API fp8bs_status fp8_mx_gemm(const uint8_t *aq, const uint8_t *as_atoms, c
  *   h  = bf16_rn(fl32(x + residual)), stored to residual_out; without a
  *        residual (both NULL) h = x
  *   rs = 1 / sqrt(mean(h^2) + eps)      (fp32 sums; no overflow at any finite h)
- *   u  = fl32(h * gamma)
+ *   u  = fl32(h * gamma)               (where that leaves fp32's range in a row whose
+ *        sum of squares does too, the product is taken times 2^-80, rs times 2^80)
  *   y  = bf16_rn(fl32(u * rs)), where y is not NULL
  * and, of the values u * rs (fp32, not y's bf16),
  * fp8_rmsnorm_quant_act: one fp32 scale per 128 consecutive values,

@@ -187,6 +187,52 @@ def test_the_ends_of_the_range(fmt, size):
         check(out, x, w, eps)
 
 
+def _sizes(rows, K, sizes, seed):
+    """Rows whose groups of 128 have values of 0.5 to 1 times the sizes, in turn."""
+    g = torch.Generator().manual_seed(seed)
+    v = (torch.rand((rows, K), generator=g) * 0.5 + 0.5) * (torch.randint(0, 2, (rows, K), generator=g) * 2 - 1)
+    return (v.view(rows, -1, 128) * torch.tensor(sizes).repeat(K // 128)[:K // 128, None]).view(rows, K).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("M,K", [(3, 1408), (150, 5120), (200, 5120), (300, 256), (160, 12288)])
+@pytest.mark.parametrize("fmt", ["fp8", "mx"])
+def test_small_values_beside_ones_whose_squares_leave_the_range(fmt, M, K):
+    """Groups of 1e-16 in a row with values of 1e20 (whose norm is about 1e-36 there, a
+    normal number): codes, scales and y by the same definition; the other rows too."""
+    call, check, _ = CALLS[fmt]
+    x, r, w = _inputs(M, K, True, "f32", seed=M)
+    w = w.abs() + 0.1
+    rows = torch.arange(0, M, 3)
+    x[rows] = _sizes(len(rows), K, [1e20, 1e-16, 1e-14, 1.0, 1e10], seed=K)
+    r[rows] = 0
+    out = call(*_cuda(x, w), EPS, residual=r.cuda(), store_y=True)
+    check(out, _h(x, r), w)
+    out = call(*_cuda(_h(x, r), w), EPS)
+    check(out, _h(x, r), w)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mx"])
+def test_products_past_the_range_of_a_row_whose_norm_is_not(fmt):
+    """h gamma leaves fp32's range, h / rms gamma does not: the norm stands, and so do the
+    small values beside."""
+    call, _, _ = CALLS[fmt]
+    K = 1152
+    x = _sizes(5, K, [3e38, 1e37, 1e25], seed=3)
+    w = torch.rand((K,), generator=torch.Generator().manual_seed(4)) * 2 + 2
+    xq, s, _, y = call(*_cuda(x, w), EPS, store_y=True)
+    v = _norm64(x, w)
+    assert ((y.cpu().double() - v).abs() <= (2.0 ** -8 + RS_TOL) * v.abs()).all()
+    q = xq.cpu().view(torch.float8_e4m3fn).double()
+    if fmt == "fp8":
+        s = s.cpu().double().repeat_interleave(128, dim=1)
+    else:
+        a = s.cpu().view(1, K // 128, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(128, K // 32)[:5]
+        s = torch.exp2(a.double() - 127.0).repeat_interleave(32, dim=1)
+        v = v.clamp(-448 * s, 448 * s)
+    # half a step of a code (2^-4, 2^-10 units of the scale below the normal codes), and fp8: two roundings of u / s
+    assert ((q * s - v).abs() <= (2.0 ** -4 + 2 * RS_TOL) * v.abs() + 2.0 ** -10 * s).all()
+
+
 def test_an_eps_that_counts_beside_squares_past_the_range():
     """2^64 squared leaves fp32's range, and eps = 2^100 is 2^-13 of the mean over 32,768."""
     eps, w = 2.0 ** 100, torch.ones((32768,), dtype=torch.bfloat16)
