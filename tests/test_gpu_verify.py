@@ -232,6 +232,51 @@ def test_random_numbers_at_and_past_their_ends():
     assert w[0].shape == tok.shape
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_random_numbers_at_their_ends_draw_the_first_and_last_tokens(dtype):
+    """0, what is not positive and NaN: the first token whose weight is one unit (2^-41 of
+    the largest) or more; the largest number below 1: the definition's token; 1 and more:
+    the last one with a unit.  The weights here are 2^-33 and more."""
+    V, ends = 30000, [0.0, -1.0, float("nan"), 1 - 2.0 ** -24, 1.0, 2.0, float("inf")]
+    t = Batch(1, 0, V, dtype, seed=8)
+    row = t.x[:1]
+    assert (row.double().max() - row.double().min()) * np.log2(np.e) < 33
+    x = row.repeat(len(ends), 1).cuda()
+    tok, _, p = fb.speculative_verify(x, torch.tensor(ends, device="cuda"))
+    near = verify(row.double().numpy(), np.array([1 - 2.0 ** -24]))
+    assert near[3] > MARGIN
+    want = [0, 0, 0, int(near[0][0, 0]), V - 1, V - 1, V - 1]
+    assert tok.cpu()[:, 0].tolist() == want
+    w = torch.softmax(row.double(), dim=1)[0, want]
+    assert ((p.cpu().double()[:, 0] - w).abs() <= P_TOL * w).all()
+
+
+@pytest.mark.parametrize("probs", [True, False])
+def test_random_numbers_at_their_ends_behind_a_rejected_draft(probs):
+    """The same over max(p - q, 0): its first and last tokens with a unit.  A drafted token
+    that all of q lies on has none."""
+    V, ends = 9000, [0.0, float("nan"), 1.0, 3.0]
+    B = len(ends)
+    t = Batch(1, 1, V, torch.float32, q=True, seed=12)
+    p = torch.softmax(t.x[:1].double(), dim=1)[0]
+    q = torch.zeros(V, dtype=torch.float64)
+    if probs:
+        q[:] = p * (1 + 2.0 ** -20)
+        q[100:8001:7] *= 0.5          # p - q is positive there alone
+        q = q.float().double()
+        r = p - q
+        assert torch.equal(torch.nonzero(r >= 0)[:, 0], torch.arange(100, 8001, 7)) and r[[100, 7996]].min() > 2.0 ** -36
+        first, last, draft = 100, 7996, 5
+    else:
+        first, last, draft = 0, V - 2, V - 1
+    d = torch.full((B, 1), draft, dtype=torch.int32, device="cuda")
+    au = torch.full((B, 1), 1.5, device="cuda")                # rejected: u q is above p
+    tok, acc, _ = fb.speculative_verify(t.x.repeat(B, 1).cuda(), torch.tensor(ends, device="cuda"), d, au,
+                                        draft_probs=q.float()[None].repeat(B, 1).cuda() if probs else None)
+    assert acc.tolist() == [0] * B and (tok[:, 1] == -1).all()
+    assert tok.cpu()[:, 0].tolist() == [first, first, last, last]
+
+
 def test_the_distribution_of_many_draws():
     """Draws at 4,096 evenly spaced numbers fall into each token's share."""
     V = 12
