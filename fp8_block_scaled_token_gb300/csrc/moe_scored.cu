@@ -8,10 +8,13 @@
 //   their one or two largest c; ids[m] = the top_k experts of largest c in those
 //   w = s of the chosen, over their sum where renormalised, times scale
 //
-// Logits and scores are pairs of fp32 numbers (pair_math.cuh) from the warps'
-// partial sums on: a sum of 5,120 products is then a few 2^-25 off, where fp32's own
-// step at a logit of 3 is 2^-22 and a score next to 1 has lost the difference of two
-// logits.  What is left decides.
+// A logit's products of 256 of H are added up in fp32 (ten roundings on a way: four
+// multiply-adds, a sum of two, five levels over the lanes), and so are a warp's turns
+// and a CTA's sum in the end: off by at most (10 + H / 256) 2^-24 of the sum of |x wr|, by
+// 1.2e-7 in the mean square for normal x and logits of deviation 1.5 (H = 2,048 to
+// 20,480).  From the CTAs' sums on logits and scores are pairs of fp32 numbers
+// (pair_math.cuh), where fp32 alone would lose more: its own step at a logit of 3 is
+// 2^-22, and a score next to 1 has lost the difference of two logits.
 //
 // Product: a warp holds 256 of H of eight tokens in registers and runs through up
 // to eight experts' rows; the eight sums are put together over the lanes by halving

@@ -108,6 +108,34 @@ def test_long_rows(M, E, H):
     assert np.allclose(got[1].cpu().double().numpy(), w, rtol=1e-5, atol=0)
 
 
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("E,H", [(256, 5120), (24, 20480)])
+def test_channels_far_above_the_others(E, H, sigmoid):
+    """Logits are off by (10 + H / 256) 2^-24 times the sum of |x wr| at most, scores by a
+    quarter of that (sigmoid) or half of it (softmax), weights by twice their logit's
+    error: no expert that is left out, or comes later, is better by more."""
+    rng = np.random.RandomState(H)
+    x, wr, b = _inputs(8, E, H, True, torch.float32, seed=H)
+    x = torch.where(torch.from_numpy(rng.rand(8, H) < 0.001), x * 1000, x)
+    logits = _logits(x, wr)
+    err = (10 + H / 256) * 2.0 ** -24 * (x.abs().double().numpy() @ wr.abs().double().numpy().T).max()
+    assert err < 1e-2
+    ids, w = [t.cpu().numpy() for t in _call(x, wr, 8, b, sigmoid=sigmoid, renorm=False)]
+    s = 1 / (1 + np.exp(-logits))
+    if not sigmoid:
+        s = np.exp(logits - logits.max(axis=1, keepdims=True))
+        s /= s.sum(axis=1, keepdims=True)
+    c = s + b.astype(np.float64)
+    for m in range(8):
+        left = np.ones(E, bool)
+        for e in ids[m]:
+            left[e] = False
+            assert c[m, e] >= c[m, left].max() - err
+    size = np.abs(logits).max() * 2.0 ** -23
+    # atol: softmax weights go down to e^-370 here, and below 2^-126 fp32 has no number that is right to 2^-24
+    assert np.allclose(w, np.take_along_axis(s, ids.astype(np.int64), axis=1), rtol=2 * err + size + W_TOL, atol=2.0 ** -126)
+
+
 def test_one_group_without_a_bias_is_the_plain_routing():
     x, wr, _ = _inputs(21, 70, 1024, False, torch.float32, seed=3)
     for renorm in (True, False):
