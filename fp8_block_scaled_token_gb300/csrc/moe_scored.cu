@@ -25,7 +25,7 @@
 // bandwidth, and much of it the fetching of instructions that run once: loops stay
 // rolled (the choice unrolled into registers, 74 KB of code, took 21.5 us in all for 8
 // tokens of 256 experts and H = 5,120, where its instructions alone would take 1.5;
-// this form 11.3, and 14.7 for 64 tokens of 160 experts).
+// this form 10.9, and 14.6 for 64 tokens of 160 experts).
 #include <cmath>
 
 #include "moe_route.cuh"
@@ -561,7 +561,9 @@ fp8bs_status launch_moe_scored(const MoeLaunch &L, const MoeWorkspace &w, const 
     const int units = (L.H + 255) / 256;
     const int groups = (L.M + kTG - 1) / kTG;
     // Warps that share H, CTAs that do, experts of a warp: the least of a wave's fixed time (about 2 us: launch, first
-    // loads, arrival) and a unit's (0.8 us and 0.2 for each expert), in fifths of a microsecond, two CTAs an SM.
+    // loads, arrival) and a unit's (0.8 us and 0.2 for each expert), in fifths of a microsecond, two CTAs an SM.  Of ten
+    // shapes from 1 x 64 to 64 x 512 it takes the best of the 30 to 48 choices, or one that is up to 4 % slower; the
+    // worst takes 2 to 16 times as long.
     long long best = 0;
     for (int hw = kWarps; hw >= 1; hw /= 2)
         for (int splits = 1; splits <= kMoeMaxSplits; ++splits)

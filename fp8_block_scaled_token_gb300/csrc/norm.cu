@@ -17,11 +17,11 @@
 // Eight consecutive values a thread and step, so that a group of 128 is 16 lanes
 // and a 16-byte access per lane is coalesced.  The row stays in registers between
 // the sum and what needs it: each input byte is read once and each output byte
-// written once.  16,384 rows of 5,120 with residual and y: 121 us, 6.2 TB/s (0.93 of
-// the measured copy bandwidth); 512 rows 5.6 us; up to 150 rows 2.1 to 2.7 us, which
-// is latency.  The first form took 255 us, bound by 45 instructions a value; it is
-// 15 with packed fp32, a bf16 addition and a corrected quotient (codes8) in place of
-// converting both ends of an interval.
+// written once.  16,384 rows of 5,120 with residual and y: 115 us, 6.6 TB/s (0.99 of
+// the measured copy bandwidth); 512 rows 5.1 us; up to 150 rows 2.1 to 2.7 us, which
+// is latency.  The first form took 255 us: packed fp32, a bf16 addition, a corrected
+// quotient (codes8) in place of converting both ends of an interval, and far_row apart
+// from the usual rows leave 30 instructions a value, 58 % of the issue slots.
 #include "fp8bs_testing.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -402,8 +402,10 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Registers for the values in flight against CTAs to an SM: four CTAs of 320 threads hold two steps (three: 130
-// us for 16,384 rows of 5,120, not 121; five spill, 210), two hold four (three: 63 us for 4,096 of 8,192, not 61).
+// Registers for the values in flight against CTAs to an SM: four CTAs of 320 threads hold two steps (three: 120
+// us for 16,384 rows of 5,120, not 115; five spill 240 bytes a thread, 162), two hold four (three: 53 us for 4,096
+// of 8,192, not 47.7).  Spills where the registers are few: 20 bytes of stores in two steps at 48 registers under
+// fp32 scales, 68 to 88 in four steps of 1,024 threads.
 template <bool kMx, bool kBf16> auto norm_kernel(int chunks, int threads)
 {
     if (threads <= kNormManyThreads)
@@ -420,9 +422,9 @@ template <bool kMx, bool kBf16> auto norm_kernel(int chunks, int threads)
 fp8bs_status launch_norm(const NormParams &p, bool mx, bool gamma_bf16, bool pdl, cudaStream_t stream, int sms)
 {
     const int words = p.K / 8;
-    // Up to a row an SM: the whole row's loads in flight at once, in one large CTA (152 rows of 5,120 2.7 us,
-    // 3.3 in small ones).  More: small CTAs, four to an SM (200 rows 3.9 us against 4.1, 16,384 rows 121 against
-    // 225), with several rows each where a row needs few threads (16,384 rows of 256: 9.6 us, 17.5 with one).
+    // Up to a row an SM: the whole row's loads in flight at once, in one large CTA (152 rows of 5,120 2.5 us,
+    // 2.9 in small ones).  More: small CTAs, four to an SM (200 rows 3.5 us against 3.8, 16,384 rows 115 against
+    // 224), with several rows each where a row needs few threads (16,384 rows of 256: 9.5 us, 17.4 with one).
     const int most = p.M <= sms ? kNormMaxThreads : kNormManyThreads;
     int chunks = 1;
     while (words > chunks * most && chunks < kNormMaxChunks)

@@ -32,10 +32,10 @@
 // a sequence's last CTA finds the 256 and looks through them.  Nothing waits.
 //
 // 64 sequences of 8 rows of 248,320 take 115 us (196 with a CTA's 8,192 logits and one
-// weight at a time, the token drawn by a second kernel): 13 fp32 operations and two
-// shuffles a logit, packed, at 60 % of the issue slots, 28 % of the memory's rate; 8
-// sequences 30 us, one 14.4, a row of 1,000 8.9, which are chains of loads, sums and
-// arrivals.
+// weight at a time, the token drawn by a second kernel), four times what their needed bytes
+// take: 19 instructions a logit, at 60 % of the issue slots with the barriers of the CTAs'
+// arrivals in between, and 28 % of the memory's rate; 8 sequences 30 us, one 14.5, a
+// row of 1,000 9.0, one of 248,320 9.6, which are chains of loads, sums and arrivals.
 #include <cmath>
 
 #include "fp8bs_testing.h"
@@ -47,7 +47,10 @@ namespace fp8bs {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyCtas = 5;      // to an SM (4: 64 rows of 248,320 at once 21.4 us, not 21.0)
+// CTAs to an SM.  4 instead: 64 rows of 248,320 at once 21.9 us, not 21.3, and 512 rows the same 115; but 5 rows 14.2,
+// not 14.5, 64 rows with the residual 29.7, not 30.3, and 256 fp32 rows of 128,000 52, not 57.5 (at 48 registers the
+// rows' kernel spills 128 bytes for fp32 logits, 24 for bf16)
+constexpr int kVerifyCtas = 5;
 constexpr int kPart = 1024;         // logits that a warp sums
 constexpr int kMostParts = 4;       // of a warp, one after the other
 constexpr int kBit = 256;           // logits that a warp sums for the residual
@@ -1152,14 +1155,14 @@ fp8bs_status speculative_verify(const void *logits, fp8bs_dtype logits_type, int
     p.L = L;
     p.V = V;
     // parts of a warp: more than one where the GPU is filled three times over all the same (512 rows of 248,320 in
-    // 131 us, 137 with one; two, for 5 rows, 18 us instead of 17)
+    // 115 us, 124 with one; two, for 64 rows, 31.7 us instead of 30.3; four, for 5 rows, 17.4 instead of 14.5)
     const long long rows = static_cast<long long>(B) * (L + 1);
     p.parts = w.parts;
     p.parts_each = 1;
     while (p.parts_each < kMostParts && rows * w.parts >= 2ll * p.parts_each * 3 * kVerifyWarps * kVerifyCtas * dev.sms)
         p.parts_each *= 2;
-    // the same for the residual, where a CTA's first loads and its arrival are most of its time (512 rows: 131 us with one
-    // run each, 118 with two, 116 with four; 64 rows 32, 33, 35)
+    // the same for the residual, where a CTA's first loads and its arrival are most of its time (512 rows: 130 us with one
+    // run each, 117 with two, 115 with four; 64 rows 30.3, 30.4, 32.9; 5 rows 14.5, 14.9, 16.3)
     p.bits = w.bits;
     p.runs_each = 1;
     const int runs = (w.bits + kVerifyWarps - 1) / kVerifyWarps;
